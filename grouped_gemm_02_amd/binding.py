@@ -59,6 +59,24 @@ class moe_kernel_time(ctypes.Structure):
                 ("total_ms", ctypes.c_double)]
 
 
+MOE_DT = {"bf16": 0, "f32": 1}
+# the usual quintic of the Newton-Schulz step: takes singular values in (0, 1]
+# to about [0.7, 1.2] in five steps
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+class moe_ortho_shape(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int64), ("R", ctypes.c_int64), ("C", ctypes.c_int64),
+                ("steps", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float),
+                ("num_cus", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class moe_muon_params(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("mu", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -83,6 +101,15 @@ _SIGS = {
     "moe_permute_noalloc": (ctypes.c_int, [ctypes.POINTER(moe_shape), _P, _P, _P, _P, _P, _P, _P]),
     "moe_route": (ctypes.c_int, [ctypes.POINTER(moe_shape), _P, ctypes.c_int32, _P, _P, _P]),
     "moe_route_bwd": (ctypes.c_int, [ctypes.POINTER(moe_shape), _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
+    "moe_balance_scratch_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_shape), ctypes.c_int64]),
+    "moe_balance": (ctypes.c_int, [ctypes.POINTER(moe_shape), _P, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _P,
+                                   _P, ctypes.c_size_t, _P]),
+    "moe_balance_bwd": (ctypes.c_int, [ctypes.POINTER(moe_shape), _P, _P, _P, _P, ctypes.c_int32, _P,
+                                       ctypes.c_int64, _P, _P, _P, _P, _P, _P]),
+    "moe_ortho_workspace_size": (ctypes.c_int, [ctypes.POINTER(moe_ortho_shape), ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_orthogonalize": (ctypes.c_int, [ctypes.POINTER(moe_ortho_shape), _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_muon_step": (ctypes.c_int, [ctypes.POINTER(moe_ortho_shape), ctypes.POINTER(moe_muon_params), _P, _P, _P, _P,
+                                     _P, ctypes.c_size_t, _P]),
     "moe_read_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_set_kernel_timing": (ctypes.c_int, [ctypes.c_int]),
@@ -142,6 +169,14 @@ def _want(t, name: str, dtype, numel: int | None = None, optional: bool = False)
         raise MoEError(MOE_ERR_SHAPE, f"{name} holds {t.numel()} elements, needs {numel}")
     if t.device.type != "cuda":
         raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, expected a GPU tensor")
+
+
+def _want_here(t, name: str, dtype, numel: int, optional: bool = False) -> None:
+    """As _want, and the tensor must be on the current device, whose stream the
+    call is enqueued on."""
+    _want(t, name, dtype, numel, optional)
+    if isinstance(t, torch.Tensor) and t.device.index != torch.cuda.current_device():
+        raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
@@ -332,6 +367,81 @@ def moe_route_bwd(shape, logits, topk_idx, topk_w, d_topk_w, renorm, d_logits, s
                                int(bool(renorm)), _ptr(d_logits), _stream(stream)), "moe_route_bwd")
 
 
+def make_ortho_shape(E, R, C, steps=5, grad="bf16", coeffs=NS_COEFFS, eps=1e-7, num_cus=0) -> moe_ortho_shape:
+    """E matrices [R, C]; grad: "bf16" or "f32", the type of what is orthogonalised."""
+    a, b, c = coeffs
+    g = MOE_DT[grad] if isinstance(grad, str) else int(grad)
+    return moe_ortho_shape(int(E), int(R), int(C), int(steps), g, float(a), float(b), float(c), float(eps),
+                           int(num_cus), 0)
+
+
+def moe_balance_scratch_bytes(shape: moe_shape, S: int) -> int:
+    return int(lib().moe_balance_scratch_bytes(ctypes.byref(shape), int(S)))
+
+
+def moe_balance(shape, logits, topk_idx, seq_offsets, S, mask, loss, counts, seq_counts, seq_probs, seq_scale, ws,
+                stream=None) -> None:
+    T, E, k, S = shape.T, shape.E, shape.k, int(S)
+    _want_here(logits, "logits", _F32, T * E)
+    _want_here(topk_idx, "topk_idx", _I32, T * k)
+    _want_here(seq_offsets, "seq_offsets", _I32, S + 1)
+    _want_here(mask, "mask", _U8, T)
+    _want_here(loss, "loss", _F32, 2)
+    _want_here(counts, "counts", _I32, E)
+    _want_here(seq_counts, "seq_counts", _I32, S * E)
+    _want_here(seq_probs, "seq_probs", _F32, S * E)
+    _want_here(seq_scale, "seq_scale", _F32, S + 1)
+    _want_here(ws, "ws", _U8, 0)
+    _check(lib().moe_balance(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), S, _ptr(mask),
+                             _ptr(loss), _ptr(counts), _ptr(seq_counts), _ptr(seq_probs), _ptr(seq_scale), _ptr(ws),
+                             ws.numel() * ws.element_size(), _stream(stream)), "moe_balance")
+
+
+def moe_balance_bwd(shape, logits, topk_idx, topk_w, d_topk_w, renorm, seq_offsets, S, mask, seq_counts, seq_scale,
+                    d_loss, d_logits, stream=None) -> None:
+    T, E, k, S = shape.T, shape.E, shape.k, int(S)
+    _want_here(logits, "logits", _F32, T * E)
+    _want_here(topk_idx, "topk_idx", _I32, T * k)
+    _want_here(topk_w, "topk_w", _F32, T * k)
+    _want_here(d_topk_w, "d_topk_w", _F32, T * k)
+    _want_here(seq_offsets, "seq_offsets", _I32, S + 1)
+    _want_here(mask, "mask", _U8, T)
+    _want_here(seq_counts, "seq_counts", _I32, S * E)
+    _want_here(seq_scale, "seq_scale", _F32, S + 1)
+    _want_here(d_loss, "d_loss", _F32, 2)
+    _want_here(d_logits, "d_logits", _F32, T * E)
+    _check(lib().moe_balance_bwd(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w),
+                                 int(bool(renorm)), _ptr(seq_offsets), S, _ptr(mask), _ptr(seq_counts),
+                                 _ptr(seq_scale), _ptr(d_loss), _ptr(d_logits), _stream(stream)), "moe_balance_bwd")
+
+
+def moe_ortho_workspace_size(shape: moe_ortho_shape) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_ortho_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_ortho_workspace_size")
+    return n.value
+
+
+def moe_orthogonalize(shape, G, U, ws, stream=None) -> None:
+    n = shape.E * shape.R * shape.C
+    _want_here(G, "G", _BF16 if shape.grad_dtype == 0 else _F32, n)
+    _want_here(U, "U", _BF16, n)
+    _want_here(ws, "ws", _U8, 0)
+    _check(lib().moe_orthogonalize(ctypes.byref(shape), _ptr(G), _ptr(U), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _stream(stream)), "moe_orthogonalize")
+
+
+def moe_muon_step(shape, params, grad, momentum, W, master, ws, stream=None) -> None:
+    n = shape.E * shape.R * shape.C
+    _want_here(grad, "grad", _BF16 if shape.grad_dtype == 0 else _F32, n)
+    _want_here(momentum, "momentum", _F32, n)
+    _want_here(W, "W", _BF16, n)
+    _want_here(master, "master", _F32, n)
+    _want_here(ws, "ws", _U8, 0)
+    _check(lib().moe_muon_step(ctypes.byref(shape), ctypes.byref(params), _ptr(grad), _ptr(momentum), _ptr(W),
+                               _ptr(master), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_muon_step")
+
+
 def moe_read_status(ws, stream=None) -> int:
     out = ctypes.c_int32()
     _check(lib().moe_read_status(_ptr(ws), ctypes.byref(out), _stream(stream)), "moe_read_status")
@@ -414,3 +524,70 @@ def backward(buf: LayerBuffers, dy, x, topk_idx, topk_w, W13, W2, grads=None, st
     dx, dw, dW13, dW2 = grads
     moe_bwd(s, dy, x, topk_idx, topk_w, W13, W2, buf.wq, buf.saved, dx, dw, dW13, dW2, buf.bwd_ws, stream)
     return grads
+
+
+@dataclasses.dataclass
+class BalanceBuffers:
+    """Outputs and scratch of the routing balance of one batch shape with S
+    sequences (allocated once with torch; see moe_balance for their meaning)."""
+    shape: moe_shape
+    S: int
+    loss: torch.Tensor
+    counts: torch.Tensor
+    seq_counts: torch.Tensor
+    seq_probs: torch.Tensor
+    seq_scale: torch.Tensor
+    ws: torch.Tensor
+
+    @classmethod
+    def allocate(cls, shape: moe_shape, S: int = 1, device="cuda") -> "BalanceBuffers":
+        E, S = shape.E, int(S)
+        mk = lambda n, dt: torch.empty(n, dtype=dt, device=device)  # noqa: E731
+        return cls(shape, S, mk((2,), _F32), mk((E,), _I32), mk((S, E), _I32), mk((S, E), _F32), mk((S + 1,), _F32),
+                   mk((max(moe_balance_scratch_bytes(shape, S), 256),), _U8))
+
+
+def balance(buf: BalanceBuffers, logits, topk_idx, seq_offsets=None, mask=None, stream=None) -> BalanceBuffers:
+    """Balance loss, z-loss and counts of a routed batch, into (and as) `buf`."""
+    moe_balance(buf.shape, logits, topk_idx, seq_offsets, buf.S, mask, buf.loss, buf.counts, buf.seq_counts,
+                buf.seq_probs, buf.seq_scale, buf.ws, stream)
+    return buf
+
+
+def balance_bwd(buf: BalanceBuffers, logits, topk_idx, topk_w, d_topk_w, renorm, d_loss, seq_offsets=None, mask=None,
+                seq_counts=None, seq_scale=None, d_logits=None, stream=None):
+    """d_logits of the balance losses and, with d_topk_w, of the routing
+    weights; seq_counts and seq_scale default to what balance left in `buf`."""
+    if d_logits is None:
+        d_logits = torch.empty((buf.shape.T, buf.shape.E), dtype=_F32, device=buf.loss.device)
+    moe_balance_bwd(buf.shape, logits, topk_idx, topk_w, d_topk_w, renorm, seq_offsets, buf.S, mask,
+                    buf.seq_counts if seq_counts is None else seq_counts,
+                    buf.seq_scale if seq_scale is None else seq_scale, d_loss, d_logits, stream)
+    return d_logits
+
+
+@dataclasses.dataclass
+class OrthoBuffers:
+    """Scratch of orthogonalize and muon_step for one stack of matrices."""
+    shape: moe_ortho_shape
+    ws: torch.Tensor
+
+    @classmethod
+    def allocate(cls, shape: moe_ortho_shape, device="cuda") -> "OrthoBuffers":
+        return cls(shape, torch.empty(max(moe_ortho_workspace_size(shape), 256), dtype=_U8, device=device))
+
+
+def orthogonalize(buf: OrthoBuffers, G, U=None, stream=None):
+    """The orthogonalised G (bf16); U may be a bf16 G itself."""
+    s = buf.shape
+    if U is None:
+        U = torch.empty((s.E, s.R, s.C), dtype=_BF16, device=G.device)
+    moe_orthogonalize(s, G, U, buf.ws, stream)
+    return U
+
+
+def muon_step(buf: OrthoBuffers, grad, momentum, W, *, lr, momentum_coef=0.95, weight_decay=0.0, scale=1.0,
+              nesterov=True, master=None, stream=None) -> None:
+    """One optimizer step on the weights W in place (see moe_muon_step)."""
+    p = moe_muon_params(float(lr), float(momentum_coef), float(weight_decay), float(scale), int(bool(nesterov)), 0)
+    moe_muon_step(buf.shape, p, grad, momentum, W, master, buf.ws, stream)

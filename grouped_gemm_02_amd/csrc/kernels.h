@@ -156,4 +156,45 @@ hipError_t launch_route_hist(const float* logits, int64_t T, int E, int k, int r
 hipError_t launch_route_bwd(const float* logits, int64_t T, int E, int k, int renorm, const int32_t* idx,
                             const float* w, const float* dw, float* dz, hipStream_t st, KernelTimer* timer);
 
+// ---------------------------------------------------------------- balance
+struct BalanceArgs {
+  const float* logits;
+  const int32_t* idx;
+  int64_t T;
+  int E, k;
+  const int32_t* off;  // sequence bounds [S + 1], or nullptr: one sequence
+  int64_t S;
+  const uint8_t* mask;  // nullptr: every token counts
+};
+size_t balance_scratch_bytes(int64_t T, int E, int64_t S);
+hipError_t launch_balance(const BalanceArgs& a, float* loss, int32_t* counts, int32_t* seq_counts, float* seq_probs,
+                          float* seq_scale, void* ws, hipStream_t st, KernelTimer* timer);
+// dw == nullptr: the balance's gradient alone
+hipError_t launch_balance_bwd(const BalanceArgs& a, const float* w, const float* dw, int renorm,
+                              const int32_t* seq_counts, const float* seq_scale, const float* d_loss, float* dz,
+                              hipStream_t st, KernelTimer* timer);
+
+// ---------------------------------------------------------------- orthogonalisation
+struct OrthoArgs {
+  int64_t E;
+  int R, C;
+  int steps;
+  bool grad_f32;
+  float a, b, c, eps;
+};
+// What is orthogonalised and where it goes: grad alone, or grad after a
+// momentum step; U written, or W (and master) updated by keep W - step U.
+struct OrthoTarget {
+  const void* grad;
+  float* momentum;
+  float mu;
+  bool nesterov;
+  uint16_t* U;
+  uint16_t* W;
+  float* master;
+  float keep, step;
+};
+size_t ortho_workspace_bytes(const OrthoArgs& a);
+hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipStream_t st, KernelTimer* timer);
+
 }  // namespace moe

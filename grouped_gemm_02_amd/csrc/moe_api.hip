@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -249,6 +250,35 @@ T* at(void* base, size_t off) {
 template <class T>
 const T* at(const void* base, size_t off) {
   return reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
+}
+
+// ------------------------------------------------------------ balance, orthogonalisation
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool sequences_fit(const moe_shape& s, int64_t S) {
+  return S >= 1 && S <= (int64_t(1) << 20) && S * s.E < (int64_t(1) << 28);
+}
+
+moe_status check_sequences(const moe_shape& s, const int32_t* seq_offsets, int64_t S) {
+  if (!sequences_fit(s, S)) return MOE_ERR_SHAPE;
+  if (!seq_offsets && S != 1) return MOE_ERR_NULL;
+  return MOE_OK;
+}
+
+moe_status check_ortho(const moe_ortho_shape* s) {
+  if (!s) return MOE_ERR_NULL;
+  if (s->grad_dtype != MOE_DT_BF16 && s->grad_dtype != MOE_DT_F32) return MOE_ERR_PRECISION;
+  if (s->E < 0 || s->R < 1 || s->C < 1 || s->R > 16384 || s->C > 16384) return MOE_ERR_SHAPE;
+  if (s->E >= (int64_t(1) << 40) / (s->R * s->C)) return MOE_ERR_SHAPE;
+  if (s->steps < 1 || s->steps > 32 || s->num_cus < 0 || s->reserved != 0) return MOE_ERR_SHAPE;
+  if (!std::isfinite(s->a) || !std::isfinite(s->b) || !std::isfinite(s->c)) return MOE_ERR_SHAPE;
+  if (!std::isfinite(s->eps) || s->eps < 0.f) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+OrthoArgs ortho_args(const moe_ortho_shape& s) {
+  return OrthoArgs{s.E, int(s.R), int(s.C), s.steps, s.grad_dtype == MOE_DT_F32, s.a, s.b, s.c, s.eps};
 }
 
 int effective_cus(const moe_shape& s, int dev_cus) {
@@ -663,6 +693,113 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
   std::lock_guard<std::mutex> lk(g_timer_mu);
   return launch_status(launch_route_bwd(logits, s->T, int(s->E), int(s->k), renorm != 0, topk_idx, topk_w, d_topk_w,
                                         d_logits, static_cast<hipStream_t>(stream), timer()));
+}
+
+size_t moe_balance_scratch_bytes(const moe_shape* s, int64_t S) {
+  if (check_shape(s) != MOE_OK || !sequences_fit(*s, S)) return 0;
+  return balance_scratch_bytes(s->T, int(s->E), S);
+}
+
+moe_status moe_balance(const moe_shape* s, const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
+                       int64_t S, const uint8_t* mask, float* loss, int32_t* counts, int32_t* seq_counts,
+                       float* seq_probs, float* seq_scale, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_sequences(*s, seq_offsets, S)) != MOE_OK) return st;
+  if (!loss || !counts || !seq_counts || !seq_probs || !seq_scale || !ws) return MOE_ERR_NULL;
+  if (s->T > 0 && (!logits || !topk_idx)) return MOE_ERR_NULL;
+  for (const void* p : {static_cast<const void*>(logits), static_cast<const void*>(topk_idx),
+                        static_cast<const void*>(seq_offsets), static_cast<const void*>(loss),
+                        static_cast<const void*>(counts), static_cast<const void*>(seq_counts),
+                        static_cast<const void*>(seq_probs), static_cast<const void*>(seq_scale)})
+    if (!aligned4(p)) return MOE_ERR_ALIGN;
+  if (!aligned16(ws)) return MOE_ERR_ALIGN;
+  if (ws_bytes < balance_scratch_bytes(s->T, int(s->E), S)) return MOE_ERR_WORKSPACE;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_balance(BalanceArgs{logits, topk_idx, s->T, int(s->E), int(s->k), seq_offsets, S, mask},
+                                      loss, counts, seq_counts, seq_probs, seq_scale, ws,
+                                      static_cast<hipStream_t>(stream), timer()));
+}
+
+moe_status moe_balance_bwd(const moe_shape* s, const float* logits, const int32_t* topk_idx, const float* topk_w,
+                           const float* d_topk_w, int32_t renorm, const int32_t* seq_offsets, int64_t S,
+                           const uint8_t* mask, const int32_t* seq_counts, const float* seq_scale,
+                           const float* d_loss, float* d_logits, void* stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_sequences(*s, seq_offsets, S)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;
+  if (!logits || !seq_counts || !seq_scale || !d_loss || !d_logits) return MOE_ERR_NULL;
+  if (d_topk_w && (!topk_idx || !topk_w)) return MOE_ERR_NULL;
+  for (const void* p : {static_cast<const void*>(logits), static_cast<const void*>(topk_idx),
+                        static_cast<const void*>(topk_w), static_cast<const void*>(d_topk_w),
+                        static_cast<const void*>(seq_offsets), static_cast<const void*>(seq_counts),
+                        static_cast<const void*>(seq_scale), static_cast<const void*>(d_loss),
+                        static_cast<const void*>(d_logits)})
+    if (!aligned4(p)) return MOE_ERR_ALIGN;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_balance_bwd(
+      BalanceArgs{logits, topk_idx, s->T, int(s->E), int(s->k), seq_offsets, S, mask}, topk_w, d_topk_w, renorm != 0,
+      seq_counts, seq_scale, d_loss, d_logits, static_cast<hipStream_t>(stream), timer()));
+}
+
+moe_status moe_ortho_workspace_size(const moe_ortho_shape* s, size_t* ws_bytes) {
+  const moe_status st = check_ortho(s);
+  if (st != MOE_OK) return st;
+  if (!ws_bytes) return MOE_ERR_NULL;
+  *ws_bytes = ortho_workspace_bytes(ortho_args(*s));
+  return MOE_OK;
+}
+
+moe_status moe_orthogonalize(const moe_ortho_shape* s, const void* G, void* U, void* ws, size_t ws_bytes,
+                             void* stream) {
+  moe_status st = check_ortho(s);
+  if (st != MOE_OK) return st;
+  if (s->E == 0) return MOE_OK;
+  if (!G || !U || !ws) return MOE_ERR_NULL;
+  if (!aligned16(G) || !aligned16(U) || !aligned16(ws)) return MOE_ERR_ALIGN;
+  const OrthoArgs a = ortho_args(*s);
+  if (ws_bytes < ortho_workspace_bytes(a)) return MOE_ERR_WORKSPACE;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  OrthoTarget t{};
+  t.grad = G;
+  t.U = static_cast<uint16_t*>(U);
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_ortho(a, t, ws, static_cast<hipStream_t>(stream), timer()));
+}
+
+moe_status moe_muon_step(const moe_ortho_shape* s, const moe_muon_params* p, const void* grad, float* momentum,
+                         void* W, float* master, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_ortho(s);
+  if (st != MOE_OK) return st;
+  if (!p) return MOE_ERR_NULL;
+  if (!std::isfinite(p->lr) || !std::isfinite(p->mu) || p->mu < 0.f || p->mu >= 1.f || !std::isfinite(p->weight_decay) ||
+      !std::isfinite(p->scale) || p->reserved != 0)
+    return MOE_ERR_SHAPE;
+  if (s->E == 0) return MOE_OK;
+  if (!grad || !momentum || !W || !ws) return MOE_ERR_NULL;
+  if (!aligned16(grad) || !aligned16(momentum) || !aligned16(W) || !aligned16(master) || !aligned16(ws))
+    return MOE_ERR_ALIGN;
+  const OrthoArgs a = ortho_args(*s);
+  if (ws_bytes < ortho_workspace_bytes(a)) return MOE_ERR_WORKSPACE;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  OrthoTarget t{};
+  t.grad = grad;
+  t.momentum = momentum;
+  t.mu = p->mu;
+  t.nesterov = p->nesterov != 0;
+  t.W = static_cast<uint16_t*>(W);
+  t.master = master;
+  t.keep = 1.f - p->lr * p->weight_decay;
+  t.step = p->lr * p->scale;
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_ortho(a, t, ws, static_cast<hipStream_t>(stream), timer()));
 }
 
 moe_status moe_read_status(const void* fwd_ws, int32_t* out, void* stream) {

@@ -290,6 +290,64 @@ moe_status moe_route(const moe_shape* s, const float* logits, int32_t renorm, in
 moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t* topk_idx, const float* topk_w,
                          const float* d_topk_w, int32_t renorm, float* d_logits, void* stream);
 
+/* Balance of the routing, per sequence: a load-balance loss, the router
+ * z-loss and the per-expert counts of a routed batch (not on the pages, which
+ * keep the router outside; they name skewed routing as what their benchmark
+ * leaves out: ic.work analysis, section on idealised assumptions). With
+ * p = softmax(logits[t]) over the E experts and lse its log-sum-exp, sequence
+ * q the tokens [seq_offsets[q], seq_offsets[q+1]), a token live when it is in
+ * a sequence and its mask byte is not 0, n_q the live tokens of q, S' the
+ * sequences with n_q > 0 and N = sum n_q:
+ *   c[q,e]  = #{(t,j) : t live in q, topk_idx[t,j] == e}
+ *   loss[0] = 1/S' sum_q E / (k n_q^2) sum_e c[q,e] sum_{t live in q} p[t,e]
+ *   loss[1] = 1/N sum_{t live} lse[t]^2
+ * (loss[0] is 1 for a perfectly balanced sequence; both are 0 when nothing is
+ * live.) Ids outside [0, E) are not counted. A logit of -inf gives
+ * probability 0; a row with nothing but -inf counts as live, gives p = 0 and
+ * nothing to the z-loss. NaN or +inf in a live row make the losses NaN (or
+ * +inf); rows that are not live are not read into any result.
+ *   logits      fp32  [T, E]   a row of E floats each, 4-byte aligned
+ *   topk_idx    int32 [T, k]   from moe_route or moe_fwd_logits
+ *   seq_offsets int32 [S+1]    ascending, within [0, T]; NULL: one sequence
+ *                              of all T tokens (S must be 1). Tokens before
+ *                              the first and behind the last belong to none
+ *   mask        uint8 [T]      NULL: every token counts
+ *   loss        fp32  [2]      written
+ *   counts      int32 [E]      written: sum over sequences of c
+ *   seq_counts  int32 [S, E]   written: c (for the backward)
+ *   seq_probs   fp32  [S, E]   written: mean of p over the live tokens (0
+ *                              for a sequence with none)
+ *   seq_scale   fp32  [S+1]    written (for the backward): per sequence
+ *                              E / (S' k n_q^2), 0 when n_q = 0; last 1 / N
+ *   ws          moe_balance_scratch_bytes(s, S) bytes, 16-byte aligned
+ * Uses s->T, E, k (check as moe_workspace_size); 1 <= S <= 2^20, S * E < 2^28.
+ * Sums run in a fixed order: results are reproducible bit for bit. With
+ * T == 0 every output is written as 0 (logits and topk_idx may be NULL).
+ * Calls that share `ws` must not overlap. */
+size_t moe_balance_scratch_bytes(const moe_shape* s, int64_t S);
+moe_status moe_balance(const moe_shape* s, const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
+                       int64_t S, const uint8_t* mask, float* loss, int32_t* counts, int32_t* seq_counts,
+                       float* seq_probs, float* seq_scale, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of moe_balance, joined with moe_route_bwd: d_logits fp32 [T, E]
+ * (every row written) = dL/dlogits given d_loss = dL/dloss (fp32 [2], device
+ * memory) and, unless d_topk_w is NULL, d_topk_w = dL/dtopk_w. Counts are
+ * piecewise constant and pass no gradient. With
+ * B[e] = d_loss[0] seq_scale[q] seq_counts[q,e] for a live token of sequence
+ * q (0 for any other token) and G = d_topk_w placed on the selected experts:
+ *   d_logits[t] = p (B - <p, B>) + 2 d_loss[1] seq_scale[S] lse p  [live]
+ *               + the gradient moe_route_bwd gives (with renorm as there)
+ * The mask and the sequences bear on the first two terms only. A row with
+ * nothing but -inf gets 0 from them. topk_idx, topk_w and d_topk_w are read
+ * only when d_topk_w is given (topk_idx and topk_w may be NULL otherwise);
+ * an expert named twice by one token takes the sum of both slots. The other
+ * arguments are as in moe_balance, with seq_counts and seq_scale as it wrote
+ * them. */
+moe_status moe_balance_bwd(const moe_shape* s, const float* logits, const int32_t* topk_idx, const float* topk_w,
+                           const float* d_topk_w, int32_t renorm, const int32_t* seq_offsets, int64_t S,
+                           const uint8_t* mask, const int32_t* seq_counts, const float* seq_scale,
+                           const float* d_loss, float* d_logits, void* stream);
+
 /* Forward of the layer (MarkTechPost article, "How does the fused kernel
  * work?"; kongchang.com explainer, grouped-GEMM note).
  *   x        bf16  [T, H]
@@ -359,6 +417,65 @@ moe_status moe_bwd(const moe_shape* s, const void* dy, const void* x, const int3
                    const float* topk_w, const void* W13, const void* W2, const void* wq,
                    const void* saved, void* dx, float* d_topk_w, void* dW13, void* dW2, void* ws,
                    size_t ws_bytes, void* stream);
+
+/* Orthogonalised updates of the expert weights, by Newton-Schulz products (the
+ * pages end at the weight gradients; this is the optimizer's step on them). For
+ * each of E matrices G [R, C]:
+ *   X = G / (|G| + eps)            |G| the Frobenius norm
+ *   steps times:  A = X X^T,  X <- a X + (b A + c A^2) X     (R <= C)
+ *                 A = X^T X,  X <- a X + X (b A + c A^2)     (R > C)
+ * which moves every singular value of X by a s + b s^3 + c s^5. A stack
+ * [E, 2I, H] of gate and up weights is also 2 E matrices [I, H].
+ * Arithmetic: the iterate is kept as an fp16 value plus an E4M3 remainder
+ * (about 15 significant bits) for the linear term, the products take its
+ * fp16 part, A and B = b A + c A^2 in fp16 with fp32 accumulation, and the
+ * rounding of B's diagonal is made good in fp32; norms are summed in 64
+ * bits. Iterates must stay below 63 in magnitude (they stay below 1.3 with
+ * the usual coefficients). A matrix of zeros gives zeros; a matrix with a
+ * NaN or an infinity gives NaN throughout, and leaves the others as they are.
+ *   grad_dtype   MOE_DT_BF16 or MOE_DT_F32: the type of G
+ *   num_cus      as in moe_shape
+ * Limits: 0 <= E, 1 <= R, C <= 16384, E R C < 2^40, 1 <= steps <= 32, a, b,
+ * c finite, eps >= 0 and finite, reserved 0. */
+typedef enum moe_dtype { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 } moe_dtype;
+
+typedef struct moe_ortho_shape {
+  int64_t E, R, C;
+  int32_t steps;
+  int32_t grad_dtype; /* moe_dtype */
+  float a, b, c, eps;
+  int32_t num_cus;
+  int32_t reserved;
+} moe_ortho_shape;
+
+/* Bytes of the scratch of moe_orthogonalize and moe_muon_step. It holds the
+ * state of a group of matrices at a time, not of all E. Pure host function. */
+moe_status moe_ortho_workspace_size(const moe_ortho_shape* s, size_t* ws_bytes);
+
+/* U bf16 [E, R, C] (written) = the orthogonalised G [E, R, C] (grad_dtype).
+ * U may be the very buffer of a bf16 G, but not overlap it otherwise. The
+ * caller owns every buffer; ws 16-byte aligned; enqueued on `stream`. Results
+ * do not depend on num_cus. Calls that share `ws` must not overlap. */
+moe_status moe_orthogonalize(const moe_ortho_shape* s, const void* G, void* U, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* One optimizer step with momentum on E weight matrices, in place:
+ *   momentum <- mu momentum + grad
+ *   u         = momentum, or with nesterov  grad + mu momentum
+ *   W        <- (1 - lr weight_decay) W - lr scale * orthogonalised(u)
+ *   grad     [E, R, C] of grad_dtype, momentum fp32 [E, R, C],
+ *   W        bf16 [E, R, C]
+ *   master   fp32 [E, R, C] or NULL: when given, the update is taken on it
+ *            and W becomes its bf16 rounding (W is not read)
+ * The parameters are host values, read at the call (a captured call replays
+ * them). lr, mu (0 <= mu < 1), weight_decay and scale finite. */
+typedef struct moe_muon_params {
+  float lr, mu, weight_decay, scale;
+  int32_t nesterov;
+  int32_t reserved; /* 0 */
+} moe_muon_params;
+moe_status moe_muon_step(const moe_ortho_shape* s, const moe_muon_params* p, const void* grad, float* momentum,
+                         void* W, float* master, void* ws, size_t ws_bytes, void* stream);
 
 /* Copies the routing status word that moe_fwd left in `fwd_ws` (or that
  * moe_permute left in its scratch) to *out (MOE_OK or MOE_ERR_ROUTING).
