@@ -45,6 +45,17 @@ constexpr float kLoScale = 1024.f;
 constexpr int kX0Exp = 14;
 constexpr float kLoScale0 = 16.f;
 
+// output tile of the products
+constexpr int kTM = 256;
+constexpr int kTN = 128;
+
+// The remainders are kept in the order in which the update's lanes hold a tile:
+// [tile][wave][sub-tile][lane][16 bytes], so they are read and written 16
+// bytes a lane.
+__device__ __forceinline__ int64_t lo_offset(int64_t tile, int wave, int sub, int lane) {
+  return (((tile * 4 + wave) * 8 + sub) * 64 + lane) * 16;
+}
+
 struct OrthoDims {
   int64_t E;   // matrices of the group
   int R, C;    // as given
@@ -96,18 +107,13 @@ __device__ __forceinline__ void matrix_scale(const double* __restrict__ part, fl
   if (!(norm < 1e300)) *s = NAN;
 }
 
+__device__ __forceinline__ uint32_t pack_halves(_Float16 a, _Float16 b) {
+  return uint32_t(__builtin_bit_cast(uint16_t, a)) | (uint32_t(__builtin_bit_cast(uint16_t, b)) << 16);
+}
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const _Float16 x = static_cast<_Float16>(a), y = static_cast<_Float16>(b);
-  return uint32_t(__builtin_bit_cast(uint16_t, x)) | (uint32_t(__builtin_bit_cast(uint16_t, y)) << 16);
+  return pack_halves(static_cast<_Float16>(a), static_cast<_Float16>(b));
 }
 
-__device__ __forceinline__ uint8_t e4m3_of(float v) {
-  const float c = fminf(fmaxf(v, -448.f), 448.f);
-  return uint8_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, 0.f, 0, false) & 0xff);
-}
-__device__ __forceinline__ float e4m3_to(uint8_t v) {
-  return __builtin_amdgcn_cvt_f32_fp8(int(v), 0);
-}
 
 // X0 and its remainder, 64 x 64 elements a workgroup, through LDS when G is
 // transposed.
@@ -140,135 +146,410 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(const void* __restrict_
     const int a = i / kLoadTile, b = i % kLoadTile;
     const float x = tile[a][b];
     const _Float16 h = static_cast<_Float16>(x);
-    const int64_t at = (int64_t(e) * d.mp + r0 + a) * d.np + c0 + b;
-    X[at] = h;
-    if (Xl) Xl[at] = e4m3_of((x - float(h)) * kLoScale0);
+    X[(int64_t(e) * d.mp + r0 + a) * d.np + c0 + b] = h;
+  }
+  if (Xl) {
+    // the 64 x 64 elements are half of a wave's part of an update tile: 2 x 2
+    // sub-tiles of 64 lanes of 16 bytes
+    const int lane = threadIdx.x & 63, sub = threadIdx.x >> 6;
+    const int r = 32 * (sub >> 1) + (lane & 31);
+    u32x4 v;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float q[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float x = tile[r][32 * (sub & 1) + 8 * g + 4 * (lane >> 5) + t];
+        q[t] = fminf(fmaxf((x - float(static_cast<_Float16>(x))) * kLoScale0, -448.f), 448.f);
+      }
+      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+      v[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true));
+    }
+    const int nrow = (d.mp + kTM - 1) / kTM;
+    const int64_t t = int64_t(c0 / kTN) * nrow + r0 / kTM;
+    const int wave = 2 * ((r0 / 128) & 1) + ((c0 / 64) & 1);
+    const int i = 2 * ((r0 / 64) & 1) + (sub >> 1);
+    *reinterpret_cast<u32x4*>(Xl + lo_offset(int64_t(e) * nrow * (d.np / kTN) + t, wave, 2 * i + (sub & 1), lane)) = v;
   }
 }
 
 // ------------------------------------------------------------------ products
+//
+// Every product is C = P Q^T (or P Q) in tiles of 256 x 128, 4 waves of
+// 128 x 64 in a 2 x 2 grid, v_mfma_f32_32x32x16_f16 with fp32 accumulators. The
+// k-slabs of 32 go straight into LDS (buffer_load ... lds), three stages, so
+// the loads of two slabs are in flight while one is multiplied. A stage is
+// 24 KiB: two workgroups share a CU, and the loads, barriers and epilogue of
+// one run under the other's products.
+//   * k-major slab (rows of 32 k, 64 bytes): 16-byte chunk c of row r at
+//     c ^ ((r / 2) % 4): eight rows' reads of one chunk fall in eight
+//     different slots of a 128-byte bank window.
+//   * mn-major slab (32 k-rows of 128 entities, 256 bytes): chunk c of k-row
+//     k at c ^ 4 (k % 4), read with the LDS transpose read
+//     ds_read_b64_tr_b16 (four consecutive k of one entity a lane).
+// The MFMA's A operand is the Q fragment, so a lane holds one row m and four
+// runs of four consecutive columns n of each 32 x 32 sub-tile.
+// The stages are separate LDS objects, named at compile time, so that the
+// compiler can tell a slab's reads from the loads in flight.
 
-// One 128 x 128 tile of P Q^T-like products on v_mfma_f32_32x32x16_f16: 4
-// waves of 64 x 64, k-slabs of 32 through registers into LDS.
-constexpr int kT = 128;
-constexpr int kK = 32;
-constexpr int kLd = kK + 8;
+constexpr int kBK = 32;
+constexpr int kSlabP = kTM * kBK;              // halves of the P part of a stage
+constexpr int kStage = (kTM + kTN) * kBK;      // halves of a stage
+__shared__ __attribute__((aligned(1024))) _Float16 g_s0[kStage];
+__shared__ __attribute__((aligned(1024))) _Float16 g_s1[kStage];
+__shared__ __attribute__((aligned(1024))) _Float16 g_s2[kStage];
+template <int S>
+__device__ __forceinline__ _Float16* stage() {
+  return S == 0 ? g_s0 : S == 1 ? g_s1 : g_s2;
+}
 
-struct TileAcc {
-  f32x16 c[2][2];
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef short v8i16 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+struct Acc {
+  f32x16 c[4][2];
 };
 
-// rows [e0, e0 + 128) of a k-contiguous operand
-__device__ __forceinline__ void stage_k(const _Float16* __restrict__ src, int64_t ld, int e0, int k0, _Float16* lds) {
-  for (int i = threadIdx.x; i < kT * kK / 8; i += 256) {
-    const int r = i / (kK / 8), c = i % (kK / 8);
-    *reinterpret_cast<f16x8*>(lds + r * kLd + 8 * c) =
-        *reinterpret_cast<const f16x8*>(src + int64_t(e0 + r) * ld + k0 + 8 * c);
-  }
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)); }
+__device__ __forceinline__ int wave_m() { return wave_id() >> 1; }
+__device__ __forceinline__ int wave_n() { return wave_id() & 1; }
+
+// One operand of a product: a matrix of `rows` rows of ld halves. Reads past
+// its end give zeros.
+struct Operand {
+  __amdgpu_buffer_rsrc_t rsrc;
+  uint32_t off;     // this lane's byte offset in its first load of slab 0
+  uint32_t row16;   // bytes from one load of a wave to its next
+  uint32_t slab;    // bytes from one slab to the next
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const _Float16* base, int64_t halves) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(base), 0, int(uint32_t(halves * 2)), 0x00020000);
 }
-// columns [e0, e0 + 128) of an operand whose rows are k
-__device__ __forceinline__ void stage_mn(const _Float16* __restrict__ src, int64_t ld, int e0, int k0, _Float16* lds) {
-  for (int i = threadIdx.x; i < kT * kK / 8; i += 256) {
-    const int k = i / (kT / 8), c = i % (kT / 8);
-    const f16x8 v = *reinterpret_cast<const f16x8*>(src + int64_t(k0 + k) * ld + e0 + 8 * c);
+
+// Rows [e0, ...) of a k-contiguous matrix: load i of wave w fills the 16 rows
+// from 64 i + 16 w on, lane l the slot l % 4 of row l / 4.
+__device__ __forceinline__ Operand operand_k(const _Float16* base, int rows, int ld, int e0) {
+  Operand o;
+  o.rsrc = rsrc_of(base, int64_t(rows) * ld);
+  const int r = 16 * wave_id() + (lane_id() >> 2);
+  const int c = (lane_id() & 3) ^ ((r >> 1) & 3);
+  o.off = uint32_t(e0 + r) * uint32_t(ld) * 2u + uint32_t(c) * 16u;
+  o.row16 = 64u * uint32_t(ld) * 2u;
+  o.slab = kBK * 2;
+  return o;
+}
+// Columns [e0, e0 + 128) of a matrix whose rows are k: load i of wave w fills
+// the 4 k-rows from 16 i + 4 w on, lane l the slot l % 16 of k-row l / 16.
+__device__ __forceinline__ Operand operand_mn(const _Float16* base, int rows, int ld, int e0) {
+  Operand o;
+  o.rsrc = rsrc_of(base, int64_t(rows) * ld);
+  const int r = 4 * wave_id() + (lane_id() >> 4);
+  const int c = (lane_id() & 15) ^ (4 * (r & 3));
+  o.off = uint32_t(r) * uint32_t(ld) * 2u + uint32_t(e0 + 8 * c) * 2u;
+  o.row16 = 16u * uint32_t(ld) * 2u;
+  o.slab = uint32_t(kBK) * uint32_t(ld) * 2u;
+  return o;
+}
+
+// N loads of 1 KiB a wave; both layouts fill 1 KiB from 64 i + 16 w rows of 64
+// bytes (k-major) or 16 i + 4 w rows of 256 bytes (mn-major) on: the same place.
+template <int N>
+__device__ __forceinline__ void load_slab(const Operand& o, int kt, _Float16* lds) {
+  const int w = wave_id();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) lds[(8 * c + j) * kLd + k] = v[j];
-  }
+  for (int i = 0; i < N; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(o.rsrc,
+                                             (__attribute__((address_space(3))) void*)(lds + (4 * i + w) * 512), 16,
+                                             o.off, kt * o.slab + i * o.row16, 0, 0);
+}
+
+// 32 entities x 16 k of a k-major slab, from entity ent0 and k = 16 kk on.
+__device__ __forceinline__ f16x8 frag_k(const _Float16* lds, int ent0, int kk) {
+  const int e = ent0 + (lane_id() & 31);
+  const int c = (2 * kk + (lane_id() >> 5)) ^ ((e >> 1) & 3);
+  return *reinterpret_cast<const f16x8*>(lds + e * kBK + c * 8);
+}
+// The same of an mn-major slab: in each 16-lane group the transpose read gives
+// lane p element p % 4 of the 8-byte pieces that lanes 4 j + p / 4 address. The
+// lane offset passes through an empty asm operand, or the compiler loses
+// which LDS object the read touches and waits for every load in flight.
+__device__ __forceinline__ f16x8 frag_mn(const _Float16* lds, int ent0, int kk) {
+  const int g = lane_id() >> 4, p = lane_id() & 15;
+  const int n = ent0 + 16 * (g & 1) + 4 * (p & 3);
+  const int k0 = 8 * (g >> 1) + (p >> 2);
+  int off = k0 * kTN + (((n >> 3) ^ (4 * (k0 & 3))) << 3) + (n & 7);
+  asm("" : "+v"(off));
+  const _Float16* a = lds + off + kk * 16 * kTN;
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a + 4 * kTN));
+  return __builtin_bit_cast(f16x8, v8i16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
 }
 
 template <bool Q_MN>
-__device__ __forceinline__ void tile_product(const _Float16* __restrict__ P, int64_t ldp, int p0,
-                                             const _Float16* __restrict__ Q, int64_t ldq, int q0, int K,
-                                             _Float16* lp, _Float16* lq, TileAcc& acc) {
-  const int wave = threadIdx.x >> 6, lane = lane_id();
-  const int pm = (wave >> 1) * 64, qn = (wave & 1) * 64;
+__device__ __forceinline__ void mma_slab(const _Float16* lds, Acc& acc) {
+  __builtin_amdgcn_iglp_opt(0);
+  const int pm = wave_m() * 128, qn = wave_n() * 64;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int kk = 0; kk < kBK / 16; ++kk) {
+    f16x8 pf[4], qf[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      qf[j] = Q_MN ? frag_mn(lds + kSlabP, qn + 32 * j, kk) : frag_k(lds + kSlabP, qn + 32 * j, kk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pf[i] = frag_k(lds, pm + 32 * i, kk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc.c[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[j], pf[i], acc.c[i][j], 0, 0, 0);
+  }
+}
+
+// s_waitcnt immediates: vmcnt(n), lgkmcnt(0) (a wave's LDS reads are done
+// before it lets the others overwrite the stage).
+constexpr int wait_imm(int vm) { return 0x0070 | (vm & 15) | ((vm >> 4) << 14); }
+
+// Slab kt out of stage S; the loads of slab kt + 2 go to the stage that slab
+// kt - 1 has left. `active` (uniform per wave) false: the wave only moves
+// data. `pass(kt, stage)` sees the slab while it is in LDS.
+template <int S, bool Q_MN, bool MMA, class Pass>
+__device__ __forceinline__ void slab_step(const Operand& P, const Operand& Q, int kt, int nk, bool active, Acc& acc,
+                                          Pass& pass) {
+  if (kt + 1 < nk) __builtin_amdgcn_s_waitcnt(wait_imm(6)); else __builtin_amdgcn_s_waitcnt(wait_imm(0));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  if (kt + 2 < nk) {
+    _Float16* nxt = stage<(S + 2) % 3>();
+    load_slab<4>(P, kt + 2, nxt);
+    load_slab<2>(Q, kt + 2, nxt + kSlabP);
+  }
+  if (active) {
+    if (MMA) mma_slab<Q_MN>(stage<S>(), acc);
+    pass(kt, stage<S>());
+  }
+}
+
+template <bool Q_MN, bool MMA = true, class Pass>
+__device__ __forceinline__ void product(const Operand& P, const Operand& Q, int nk, bool active, Acc& acc,
+                                        Pass& pass) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc.c[i][j][r] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += kK) {
-    __syncthreads();
-    stage_k(P, ldp, p0, k0, lp);
-    if (Q_MN) stage_mn(Q, ldq, q0, k0, lq); else stage_k(Q, ldq, q0, k0, lq);
-    __syncthreads();
+  load_slab<4>(P, 0, g_s0);
+  load_slab<2>(Q, 0, g_s0 + kSlabP);
+  load_slab<4>(P, 1, g_s1);
+  load_slab<2>(Q, 1, g_s1 + kSlabP);
+  int kt = 0;
+  for (; kt + 2 < nk; kt += 3) {
+    slab_step<0, Q_MN, MMA>(P, Q, kt, nk, active, acc, pass);
+    slab_step<1, Q_MN, MMA>(P, Q, kt + 1, nk, active, acc, pass);
+    slab_step<2, Q_MN, MMA>(P, Q, kt + 2, nk, active, acc, pass);
+  }
+  if (kt < nk) slab_step<0, Q_MN, MMA>(P, Q, kt, nk, active, acc, pass);
+  if (kt + 1 < nk) slab_step<1, Q_MN, MMA>(P, Q, kt + 1, nk, active, acc, pass);
+  __builtin_amdgcn_s_waitcnt(wait_imm(0));
+  __syncthreads();  // the stages are free for the epilogue's images
+}
+
+// Row and first of 4 columns, inside the tile, of registers 4g .. 4g+3 of
+// sub-tile (i, j).
+__device__ __forceinline__ int tile_row(int i) { return wave_m() * 128 + 32 * i + (lane_id() & 31); }
+__device__ __forceinline__ int tile_col(int j, int g) { return wave_n() * 64 + 32 * j + 8 * g + 4 * (lane_id() >> 5); }
+
+// ------------------------------------------------------------------ images
+//
+// A wave writes its results through LDS, 64 rows x 64 columns of 16-bit values
+// at a time (8 KiB of its own: no barrier): 16-byte chunk c of row r at
+// c ^ ((r / 2) % 8). Rows come out as 16-byte pieces, columns (the mirrored
+// half of a symmetric product, a tall matrix) through the transpose read.
+
+__device__ __forceinline__ uint16_t* image() {
+  const int w = wave_id();
+  return reinterpret_cast<uint16_t*>(w < 2 ? g_s0 : g_s1) + (w & 1) * 4096;
+}
+// four values of row r (0 .. 63), columns 4 q .. 4 q + 3
+__device__ __forceinline__ void image_put(uint16_t* im, int r, int q, uint32_t lo, uint32_t hi) {
+  u32x2 v = {lo, hi};
+  *reinterpret_cast<u32x2*>(im + r * 64 + (((q >> 1) ^ ((r >> 1) & 7)) << 3) + (q & 1) * 4) = v;
+}
+// eight values of row r, columns 8 c .. 8 c + 7
+__device__ __forceinline__ u32x4 image_row(const uint16_t* im, int r, int c) {
+  return *reinterpret_cast<const u32x4*>(im + r * 64 + ((c ^ ((r >> 1) & 7)) << 3));
+}
+// Every lane: eight values of one column, rows r0 .. r0 + 7, for the 16
+// columns from n0 on (column n0 + lane % 16; r0 may differ from one 16-lane
+// group to another).
+__device__ __forceinline__ u32x4 image_col(const uint16_t* im, int r0, int n0) {
+  const int p = lane_id() & 15;
+  const int r = r0 + (p >> 2), n = n0 + 4 * (p & 3);
+  // rows r and r + 4 differ in the chunk's position
+  const uint16_t* a = im + r * 64 + (((n >> 3) ^ ((r >> 1) & 7)) << 3) + (n & 7);
+  const uint16_t* b = im + (r + 4) * 64 + (((n >> 3) ^ (((r + 4) >> 1) & 7)) << 3) + (n & 7);
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(b));
+  return __builtin_bit_cast(u32x4, v8i16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
+}
+// LDS writes of the wave are visible to its own reads
+__device__ __forceinline__ void image_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------------------ tiles
+//
+// Workgroups of one launch are dealt to the eight XCDs in turn (blockIdx % 8);
+// each XCD takes a contiguous range of (matrix, tile), so that the tiles of a
+// matrix share its operands in that XCD's L2.
+
+__device__ __forceinline__ bool take_tile(int64_t total, int tiles, int64_t* e, int* t) {
+  const int64_t per = (total + 7) / 8;
+  const int64_t id = int64_t(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || id >= total) return false;
+  *e = id / tiles;
+  *t = int(id % tiles);
+  return true;
+}
+unsigned grid_of(int64_t total) { return unsigned((total + 7) / 8 * 8); }
+
+// The tiles of a symmetric product: 256 x 128, the blocks of 128 x 128 on and
+// below the diagonal. Row bi holds column tiles 0 .. 2 bi + 1.
+int sym_tiles(int mp) {
+  const int nb = mp / 128, h = nb / 2;
+  return h * (h + 1) + (nb & 1 ? 2 * h + 1 : 0);
+}
+__device__ __forceinline__ void sym_tile(int t, int* bi, int* bj) {
+  int b = int((sqrtf(4.f * float(t) + 1.f) - 1.f) * 0.5f);
+  while (b * (b + 1) > t) --b;
+  while ((b + 1) * (b + 2) <= t) ++b;
+  *bi = b;
+  *bj = t - b * (b + 1);
+}
+
+struct NoPass {
+  __device__ __forceinline__ void operator()(int, const _Float16*) const {}
+};
+
+// The blocks of a symmetric result, fp16, times f, and their mirror images.
+// diag (or NULL): what the rounding of the diagonal lost.
+__device__ __forceinline__ void store_symmetric(const Acc& acc, float f, _Float16* __restrict__ out, int mp, int bi,
+                                                int bj, float* __restrict__ diag) {
+  uint16_t* im = image();
+  const int rb = 2 * bi + wave_m();                 // 128-row block of this wave
+  const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
+  const int lane = lane_id();
 #pragma unroll
-    for (int kk = 0; kk < kK; kk += 16) {
-      f16x8 pf[2], qf[2];
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        pf[i] = *reinterpret_cast<const f16x8*>(lp + (pm + 32 * i + (lane & 31)) * kLd + kk + 8 * (lane >> 5));
-        qf[i] = *reinterpret_cast<const f16x8*>(lq + (qn + 32 * i + (lane & 31)) * kLd + kk + 8 * (lane >> 5));
-      }
+    for (int ii = 0; ii < 2; ++ii) {
+      const int i = 2 * h + ii;
+      const int r = 32 * ii + (lane & 31);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc.c[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[j], pf[i], acc.c[i][j], 0, 0, 0);
+        for (int g = 0; g < 4; ++g) {
+          const f32x16& c = acc.c[i][j];
+          image_put(im, r, 8 * j + 2 * g + (lane >> 5), pack_f16(c[4 * g] * f, c[4 * g + 1] * f),
+                    pack_f16(c[4 * g + 2] * f, c[4 * g + 3] * f));
+          if (diag) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              if (row0 + 64 * h + r == col0 + 32 * j + 8 * g + 4 * (lane >> 5) + t) {
+                const float x = c[4 * g + t] * f;
+                diag[row0 + 64 * h + r] = x - float(static_cast<_Float16>(x));
+              }
+          }
+        }
     }
+    image_sync();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int r = 8 * q + (lane >> 3), c = lane & 7;
+      *reinterpret_cast<u32x4*>(out + int64_t(row0 + 64 * h + r) * mp + col0 + 8 * c) = image_row(im, r, c);
+    }
+    if (bj != rb) {
+      // column n of the image is row col0 + n of the mirror; 4 groups of 16
+      // lanes take 16 columns each, 8 rows at a time
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const u32x4 v = image_col(im, 8 * q, 16 * (lane >> 4));
+        *reinterpret_cast<u32x4*>(out + int64_t(col0 + lane) * mp + row0 + 64 * h + 8 * q) = v;
+      }
+    }
+    image_sync();
   }
 }
 
-// Row and first of 4 columns, inside the tile, of registers 4g .. 4g+3 of sub-tile (i, j).
-__device__ __forceinline__ int tile_row(int i) { return ((threadIdx.x >> 7) * 64) + 32 * i + (lane_id() & 31); }
-__device__ __forceinline__ int tile_col(int j, int g) {
-  return ((threadIdx.x >> 6) & 1) * 64 + 32 * j + 8 * g + 4 * (lane_id() >> 5);
-}
-
-// A = X X^T times the square of the iterate's scale. Symmetric: tiles (bi, bj)
-// with bj <= bi only, each also written transposed.
-__global__ __launch_bounds__(256) void ortho_gram_kernel(const _Float16* __restrict__ X, OrthoDims d,
-                                                         const float* __restrict__ scale, _Float16* __restrict__ A) {
-  __shared__ __attribute__((aligned(16))) _Float16 lp[kT * kLd], lq[kT * kLd];
-  const int bi = blockIdx.y, bj = blockIdx.x, e = blockIdx.z;
-  if (bj > bi) return;
-  const _Float16* Xe = X + int64_t(e) * d.mp * d.np;
-  _Float16* Ae = A + int64_t(e) * d.mp * d.mp;
-  TileAcc acc;
-  tile_product<false>(Xe, d.np, bi * kT, Xe, d.np, bj * kT, d.np, lp, lq, acc);
+// A = X X^T times the square of the iterate's scale.
+__global__ __launch_bounds__(256, 2) void ortho_gram_kernel(const _Float16* __restrict__ X, OrthoDims d, int tiles,
+                                                            const float* __restrict__ scale,
+                                                            _Float16* __restrict__ A) {
+  int64_t e;
+  int t, bi, bj;
+  if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
+  sym_tile(t, &bi, &bj);
+  const _Float16* Xe = X + e * d.mp * d.np;
+  const int rb = 2 * bi + wave_m();
+  const bool active = bj <= rb && rb * 128 < d.mp;
+  Acc acc;
+  NoPass pass;
+  product<false>(operand_k(Xe, d.mp, d.np, bi * kTM), operand_k(Xe, d.mp, d.np, bj * kTN), d.np / kBK, active, acc,
+                 pass);
+  if (!active) return;
   const float s = scale ? scale[e] : 1.f / kXScale;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int r = bi * kT + tile_row(i), c = bj * kT + tile_col(j, g) + t;
-          const _Float16 v = static_cast<_Float16>(acc.c[i][j][4 * g + t] * s * s);
-          Ae[int64_t(r) * d.mp + c] = v;
-          if (bi != bj) Ae[int64_t(c) * d.mp + r] = v;
-        }
+  store_symmetric(acc, s * s, A + e * d.mp * d.mp, d.mp, bi, bj, nullptr);
 }
 
-// B = b A + c A A in fp16, and what the rounding of its diagonal lost.
-__global__ __launch_bounds__(256) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d, float cb,
-                                                           float cc, _Float16* __restrict__ B,
-                                                           float* __restrict__ diag) {
-  __shared__ __attribute__((aligned(16))) _Float16 lp[kT * kLd], lq[kT * kLd];
-  const int bi = blockIdx.y, bj = blockIdx.x, e = blockIdx.z;
-  if (bj > bi) return;
-  const _Float16* Ae = A + int64_t(e) * d.mp * d.mp;
-  _Float16* Be = B + int64_t(e) * d.mp * d.mp;
-  TileAcc acc;
-  tile_product<false>(Ae, d.mp, bi * kT, Ae, d.mp, bj * kT, d.mp, lp, lq, acc);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
+// While the slab passes whose k are the columns of this wave's sub-tiles j, the
+// P rows hold the tile of A itself: acc += ratio A.
+struct AddTile {
+  int kt0;      // slab of the wave's sub-tile j = 0
+  float ratio;
+  Acc& acc;
+  __device__ __forceinline__ void operator()(int kt, const _Float16* lds) const {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
+      if (kt == kt0 + j) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int r = bi * kT + tile_row(i), c = bj * kT + tile_col(j, g) + t;
-          const float x = cb * float(Ae[int64_t(r) * d.mp + c]) + cc * acc.c[i][j][4 * g + t];
-          const _Float16 v = static_cast<_Float16>(x);
-          Be[int64_t(r) * d.mp + c] = v;
-          if (bi != bj) Be[int64_t(c) * d.mp + r] = v;
-          if (r == c) diag[int64_t(e) * d.mp + r] = x - float(v);
-        }
+          for (int g = 0; g < 4; ++g) {
+            const int r = tile_row(i);
+            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + r * kBK + ((g ^ ((r >> 1) & 3)) << 3) +
+                                                           4 * (lane_id() >> 5));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] += ratio * float(v[t]);
+            __builtin_amdgcn_sched_barrier(0);  // few reads at a time: registers
+          }
+      }
+  }
+};
+
+// B = b A + c A A = f (A A + ratio A) in fp16 (or, c negligible, f ratio A),
+// and what the rounding of its diagonal lost.
+template <bool MMA>
+__global__ __launch_bounds__(256, 2) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d, int tiles,
+                                                              float f, float ratio, _Float16* __restrict__ B,
+                                                              float* __restrict__ diag) {
+  int64_t e;
+  int t, bi, bj;
+  if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
+  sym_tile(t, &bi, &bj);
+  const _Float16* Ae = A + e * d.mp * d.mp;
+  const int rb = 2 * bi + wave_m();
+  const bool active = bj <= rb && rb * 128 < d.mp;
+  Acc acc;
+  AddTile pass{(bj * kTN + wave_n() * 64) / kBK, ratio, acc};
+  product<false, MMA>(operand_k(Ae, d.mp, d.mp, bi * kTM), operand_k(Ae, d.mp, d.mp, bj * kTN), d.mp / kBK, active,
+                      acc, pass);
+  if (!active) return;
+  store_symmetric(acc, f, B + e * d.mp * d.mp, d.mp, bi, bj, diag + e * d.mp);
 }
 
 struct OrthoOut {
@@ -280,49 +561,194 @@ struct OrthoOut {
   float keep, step;  // W keep - step U
 };
 
-__global__ __launch_bounds__(256) void ortho_update_kernel(const _Float16* __restrict__ X,
-                                                           const uint8_t* __restrict__ Xl, float lo_inv,
-                                                           const _Float16* __restrict__ B,
-                                                           const float* __restrict__ diag, OrthoDims d, float ca,
-                                                           const float* __restrict__ scale, OrthoOut out) {
-  __shared__ __attribute__((aligned(16))) _Float16 lp[kT * kLd], lq[kT * kLd];
-  const int bi = blockIdx.y, bj = blockIdx.x, e = blockIdx.z;
-  const int64_t xo = int64_t(e) * d.mp * d.np;
-  TileAcc acc;
-  tile_product<true>(B + int64_t(e) * d.mp * d.mp, d.mp, bi * kT, X + xo, d.np, bj * kT, d.mp, lp, lq, acc);
-  const float s = scale ? scale[e] : 1.f / kXScale;  // takes a stored iterate to its value
+// While the slab passes whose k are the rows of this wave's sub-tiles i, the Q
+// rows hold the tile of X itself: acc += (a + diag) X.
+struct AddLinear {
+  int kt0;          // slab of the wave's sub-tile i = 0
+  const float* lin;  // a + diag of the lane's row in sub-tile i
+  Acc& acc;
+  __device__ __forceinline__ void operator()(int kt, const _Float16* lds) const {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = bi * kT + tile_row(i);
-    const float lin = ca + diag[int64_t(e) * d.mp + r];
+    for (int i = 0; i < 4; ++i)
+      if (kt == kt0 + i) {
+        const int k = lane_id() & 31;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+          for (int g = 0; g < 4; ++g) {
+            const int n = tile_col(j, g);
+            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + kSlabP + k * kTN +
+                                                           (((n >> 3) ^ (4 * (k & 3))) << 3) + (n & 7));
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int c = bj * kT + tile_col(j, g) + t;
-          const int64_t at = xo + int64_t(r) * d.np + c;
-          float x = float(X[at]);
-          if (Xl) x += e4m3_to(Xl[at]) * lo_inv;
-          const float y = (lin * x + acc.c[i][j][4 * g + t]) * s;
-          if (out.X) {
-            const float z = y * kXScale;
-            const _Float16 h = static_cast<_Float16>(z);
-            out.X[at] = h;
-            if (out.Xl) out.Xl[at] = e4m3_of((z - float(h)) * kLoScale);
-          } else if (r < d.m && c < d.n) {
-            const int64_t o = int64_t(e) * d.R * d.C + (d.tall ? int64_t(c) * d.C + r : int64_t(r) * d.C + c);
-            if (out.U) {
-              out.U[o] = uint16_t(pack_bf16x2(y, 0.f));
-            } else {
-              const float w = out.master ? out.master[o] : __uint_as_float(uint32_t(out.W[o]) << 16);
-              const float v = out.keep * w - out.step * y;
-              if (out.master) out.master[o] = v;
-              out.W[o] = uint16_t(pack_bf16x2(v, 0.f));
-            }
+            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] += lin[i] * float(v[t]);
           }
+      }
+  }
+};
+
+__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
+__device__ __forceinline__ float half_of(uint32_t w, int t) {
+  return float(__builtin_bit_cast(_Float16, uint16_t(t ? w >> 16 : w)));
+}
+
+// Eight consecutive elements of the result at element `at` of matrix storage:
+// v holds bf16 values (U) or fp16 values (the step of W). Only `count` of
+// them exist; rows of whole 16-byte pieces (vec) go at once.
+__device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, const u32x4& v, int count, bool vec) {
+  if (out.U) {
+    if (vec) {
+      *reinterpret_cast<u32x4*>(out.U + at) = v;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (t < count) out.U[at + t] = uint16_t(v[t >> 1] >> (16 * (t & 1)));
+    }
+    return;
+  }
+  float w[8];
+  if (vec) {
+    if (out.master) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(out.master + at);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(out.master + at + 4);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        w[t] = a[t];
+        w[4 + t] = b[t];
+      }
+    } else {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(out.W + at);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        w[2 * t] = bf16_lo(a[t]);
+        w[2 * t + 1] = bf16_hi(a[t]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) w[t] = t < count ? (out.master ? out.master[at + t] : bf16_at(out.W + at + t)) : 0.f;
+  }
+#pragma unroll
+  for (int t = 0; t < 8; ++t) w[t] = out.keep * w[t] - out.step * half_of(v[t >> 1], t & 1);
+  if (vec) {
+    if (out.master) {
+      *reinterpret_cast<f32x4*>(out.master + at) = f32x4{w[0], w[1], w[2], w[3]};
+      *reinterpret_cast<f32x4*>(out.master + at + 4) = f32x4{w[4], w[5], w[6], w[7]};
+    }
+    *reinterpret_cast<u32x4*>(out.W + at) = u32x4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
+                                                  pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
+  } else {
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (t < count) {
+        if (out.master) out.master[at + t] = w[t];
+        out.W[at + t] = uint16_t(pack_bf16x2(w[t], 0.f));
+      }
+  }
+}
+
+// X' = (a + diag) X + B X; the last step writes the result instead. U leaves
+// as bf16; the step of the weights goes through LDS as fp16 (2^-12 of the
+// update, an eighth of what the products' roundings leave).
+template <bool LAST>
+__global__ __launch_bounds__(256, 2) void ortho_update_kernel(const _Float16* __restrict__ X,
+                                                              const uint8_t* __restrict__ Xl, float lo_inv,
+                                                              const _Float16* __restrict__ B,
+                                                              const float* __restrict__ diag, OrthoDims d, int tiles,
+                                                              float ca, const float* __restrict__ scale,
+                                                              OrthoOut out) {
+  int64_t e;
+  int t;
+  if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
+  const int nrow = (d.mp + kTM - 1) / kTM;
+  const int bi = t % nrow, bj = t / nrow;  // the row tiles of a column panel follow each other
+  const bool active = bi * kTM + wave_m() * 128 < d.mp;
+  const int64_t xo = e * d.mp * d.np;
+  const int lane = lane_id();
+  float lin[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) lin[i] = active ? ca + diag[e * d.mp + bi * kTM + tile_row(i)] : 0.f;
+  Acc acc;
+  AddLinear pass{(bi * kTM + wave_m() * 128) / kBK, lin, acc};
+  product<true>(operand_k(B + e * d.mp * d.mp, d.mp, d.mp, bi * kTM), operand_mn(X + xo, d.mp, d.np, bj * kTN),
+                d.mp / kBK, active, acc, pass);
+  if (!active) return;
+  const float s = scale ? scale[e] : 1.f / kXScale;  // takes a stored iterate to its value
+  uint16_t* im = image();
+  const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
+  const int64_t ltile = e * tiles + t;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int ii = 0; ii < 2; ++ii) {
+      const int i = 2 * h + ii;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        u32x4 lo = {0u, 0u, 0u, 0u}, nlo;
+        if (Xl) lo = *reinterpret_cast<const u32x4*>(Xl + lo_offset(ltile, wave_id(), 2 * i + j, lane));
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = acc.c[i][j][4 * g + q];
+          if (Xl) {
+            const float f = lin[i] * lo_inv;
+            const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[g]), false);
+            const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[g]), true);
+            y[0] += f * a[0];
+            y[1] += f * a[1];
+            y[2] += f * b[0];
+            y[3] += f * b[1];
+          }
+          uint32_t p0, p1;
+          if (!LAST) {
+            const float sz = s * kXScale;
+            float r[4];
+            _Float16 hv[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float z = y[q] * sz;
+              hv[q] = static_cast<_Float16>(z);
+              r[q] = fminf(fmaxf((z - float(hv[q])) * kLoScale, -448.f), 448.f);
+            }
+            p0 = pack_halves(hv[0], hv[1]);
+            p1 = pack_halves(hv[2], hv[3]);
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
+            nlo[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], w, true));
+          } else if (out.U) {
+            p0 = pack_bf16x2(y[0] * s, y[1] * s);
+            p1 = pack_bf16x2(y[2] * s, y[3] * s);
+          } else {
+            p0 = pack_f16(y[0] * s, y[1] * s);
+            p1 = pack_f16(y[2] * s, y[3] * s);
+          }
+          image_put(im, 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), p0, p1);
         }
+        if (!LAST) *reinterpret_cast<u32x4*>(out.Xl + lo_offset(ltile, wave_id(), 2 * i + j, lane)) = nlo;
+      }
+    }
+    image_sync();
+    if (!LAST) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int r = 8 * q + (lane >> 3), c = lane & 7;
+        *reinterpret_cast<u32x4*>(out.X + xo + int64_t(row0 + 64 * h + r) * d.np + col0 + 8 * c) = image_row(im, r, c);
+      }
+    } else if (!d.tall) {
+      for (int q = 0; q < 8; ++q) {
+        const int r = row0 + 64 * h + 8 * q + (lane >> 3), c = col0 + 8 * (lane & 7);
+        const u32x4 v = image_row(im, 8 * q + (lane >> 3), lane & 7);
+        if (r < d.m && c < d.n)
+          put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c, (d.C & 7) == 0);
+      }
+    } else {
+      for (int q = 0; q < 8; ++q) {
+        const int r = row0 + 64 * h + 8 * q, c = col0 + lane;
+        const u32x4 v = image_col(im, 8 * q, 16 * (lane >> 4));
+        if (r < d.m && c < d.n)
+          put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r, (d.C & 7) == 0);
+      }
+    }
+    image_sync();
   }
 }
 
@@ -344,24 +770,27 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   d.tall = a.R > a.C;
   d.m = d.tall ? a.C : a.R;
   d.n = d.tall ? a.R : a.C;
-  d.mp = (d.m + kT - 1) / kT * kT;
-  d.np = (d.n + kT - 1) / kT * kT;
+  d.mp = (d.m + 127) / 128 * 128;
+  d.np = (d.n + 127) / 128 * 128;
   const int64_t x = int64_t(d.mp) * d.np, q = int64_t(d.mp) * d.mp;
+  const int64_t xl = int64_t((d.mp + kTM - 1) / kTM * kTM) * d.np;  // whole tiles
   // at most about 4 GiB of state
   const int64_t bytes = 6 * x + 4 * q;
   int64_t g = (int64_t(4) << 30) / bytes;
   g = g < 1 ? 1 : (g > 4096 ? 4096 : g);
   p.group = a.E < g ? (a.E > 0 ? a.E : 1) : g;
   size_t o = 0;
+  // The products read up to 128 rows past a matrix (as zeros: the buffer
+  // resource ends with it); B is followed by X, each X by its remainders.
   p.part = o;  o = up256(o + size_t(p.group) * kNormParts * 8);
   p.scale = o; o = up256(o + size_t(p.group) * 4);
   p.diag = o;  o = up256(o + size_t(p.group) * d.mp * 4);
+  p.A = o;     o = up256(o + size_t(p.group) * q * 2);
+  p.B = o;     o = up256(o + size_t(p.group) * q * 2);
   for (int i = 0; i < 2; ++i) {
     p.X[i] = o;  o = up256(o + size_t(p.group) * x * 2);
-    p.Xl[i] = o; o = up256(o + size_t(p.group) * x);
+    p.Xl[i] = o; o = up256(o + size_t(p.group) * xl);
   }
-  p.A = o; o = up256(o + size_t(p.group) * q * 2);
-  p.B = o; o = up256(o + size_t(p.group) * q * 2);
   p.total = o;
   return p;
 }
@@ -398,34 +827,45 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
                          a.grad_f32, mom, t.mu, t.nesterov, d, part, a.eps, f16(p.X[0]), lo0 ? u8(p.Xl[0]) : nullptr,
                          f32(p.scale));
     }
+    const int st_tiles = sym_tiles(d.mp);
+    const int up_tiles = (d.mp + kTM - 1) / kTM * (d.np / kTN);
+    // B = f (A A + ratio A); a c below 2^-20 of b adds nothing that fp16 holds
+    const bool square = std::fabs(a.c) > 1e-6f * std::fabs(a.b);
+    const float f = square ? a.c : 1.f, ratio = square ? a.b / a.c : a.b;
     for (int k = 0; k < a.steps; ++k) {
       const int in = k & 1;
       const float* scale = k == 0 ? f32(p.scale) : nullptr;
-      const dim3 sym(d.mp / kT, d.mp / kT, ge);
       {
         TimedLaunch tl(timer, "ortho_gram", st);
-        hipLaunchKernelGGL(ortho_gram_kernel, sym, dim3(256), 0, st, f16(p.X[in]), d, scale, f16(p.A));
+        hipLaunchKernelGGL(ortho_gram_kernel, dim3(grid_of(d.E * st_tiles)), dim3(256), 0, st, f16(p.X[in]), d,
+                           st_tiles, scale, f16(p.A));
       }
       {
         TimedLaunch tl(timer, "ortho_square", st);
-        hipLaunchKernelGGL(ortho_square_kernel, sym, dim3(256), 0, st, f16(p.A), d, a.b, a.c, f16(p.B), f32(p.diag));
+        hipLaunchKernelGGL(square ? ortho_square_kernel<true> : ortho_square_kernel<false>,
+                           dim3(grid_of(d.E * st_tiles)), dim3(256), 0, st, f16(p.A), d, st_tiles, f, ratio, f16(p.B),
+                           f32(p.diag));
       }
+      const bool lo = k > 0 || lo0;
+      const uint8_t* xl = lo ? u8(p.Xl[in]) : nullptr;
+      const float lo_inv = 1.f / (k == 0 ? kLoScale0 : kLoScale);
+      const dim3 grid(grid_of(d.E * up_tiles));
       OrthoOut out{};
+      TimedLaunch tl(timer, "ortho_update", st);
       if (k + 1 < a.steps) {
         out.X = f16(p.X[1 - in]);
         out.Xl = u8(p.Xl[1 - in]);
+        hipLaunchKernelGGL(ortho_update_kernel<false>, grid, dim3(256), 0, st, f16(p.X[in]), xl, lo_inv, f16(p.B),
+                           f32(p.diag), d, up_tiles, a.a, scale, out);
       } else {
         out.U = t.U ? t.U + e0 * count : nullptr;
         out.W = t.W ? t.W + e0 * count : nullptr;
         out.master = t.master ? t.master + e0 * count : nullptr;
         out.keep = t.keep;
         out.step = t.step;
+        hipLaunchKernelGGL(ortho_update_kernel<true>, grid, dim3(256), 0, st, f16(p.X[in]), xl, lo_inv, f16(p.B),
+                           f32(p.diag), d, up_tiles, a.a, scale, out);
       }
-      const bool lo = k > 0 || lo0;
-      TimedLaunch tl(timer, "ortho_update", st);
-      hipLaunchKernelGGL(ortho_update_kernel, dim3(d.np / kT, d.mp / kT, ge), dim3(256), 0, st, f16(p.X[in]),
-                         lo ? u8(p.Xl[in]) : nullptr, 1.f / (k == 0 ? kLoScale0 : kLoScale), f16(p.B), f32(p.diag), d,
-                         a.a, scale, out);
     }
   }
   return hipGetLastError();
