@@ -171,12 +171,20 @@ def _want(t, name: str, dtype, numel: int | None = None, optional: bool = False)
         raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, expected a GPU tensor")
 
 
-def _want_here(t, name: str, dtype, numel: int, optional: bool = False) -> None:
-    """As _want, and the tensor must be on the current device, whose stream the
-    call is enqueued on."""
-    _want(t, name, dtype, numel, optional)
-    if isinstance(t, torch.Tensor) and t.device.index != torch.cuda.current_device():
-        raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _here(*wanted) -> None:
+    """_want for each (tensor, name, dtype, numel), and the tensor must be on the
+    current device, whose stream the call is enqueued on."""
+    dev = None
+    for t, name, dtype, numel in wanted:
+        if not isinstance(t, torch.Tensor):
+            continue
+        if t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
+            if dev is None:
+                dev = torch.cuda.current_device()
+            if t.get_device() == dev:
+                continue
+            raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{dev}")
+        _want(t, name, dtype, numel)
 
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
@@ -185,7 +193,8 @@ _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 def _stream(stream) -> int | None:
     if stream is None:
         if torch.cuda.is_available():
-            return torch.cuda.current_stream().cuda_stream
+            # the current stream's handle without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         return None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -382,16 +391,16 @@ def moe_balance_scratch_bytes(shape: moe_shape, S: int) -> int:
 def moe_balance(shape, logits, topk_idx, seq_offsets, S, mask, loss, counts, seq_counts, seq_probs, seq_scale, ws,
                 stream=None) -> None:
     T, E, k, S = shape.T, shape.E, shape.k, int(S)
-    _want_here(logits, "logits", _F32, T * E)
-    _want_here(topk_idx, "topk_idx", _I32, T * k)
-    _want_here(seq_offsets, "seq_offsets", _I32, S + 1)
-    _want_here(mask, "mask", _U8, T)
-    _want_here(loss, "loss", _F32, 2)
-    _want_here(counts, "counts", _I32, E)
-    _want_here(seq_counts, "seq_counts", _I32, S * E)
-    _want_here(seq_probs, "seq_probs", _F32, S * E)
-    _want_here(seq_scale, "seq_scale", _F32, S + 1)
-    _want_here(ws, "ws", _U8, 0)
+    _here((logits, "logits", _F32, T * E),
+          (topk_idx, "topk_idx", _I32, T * k),
+          (seq_offsets, "seq_offsets", _I32, S + 1),
+          (mask, "mask", _U8, T),
+          (loss, "loss", _F32, 2),
+          (counts, "counts", _I32, E),
+          (seq_counts, "seq_counts", _I32, S * E),
+          (seq_probs, "seq_probs", _F32, S * E),
+          (seq_scale, "seq_scale", _F32, S + 1),
+          (ws, "ws", _U8, 0))
     _check(lib().moe_balance(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), S, _ptr(mask),
                              _ptr(loss), _ptr(counts), _ptr(seq_counts), _ptr(seq_probs), _ptr(seq_scale), _ptr(ws),
                              ws.numel() * ws.element_size(), _stream(stream)), "moe_balance")
@@ -400,16 +409,16 @@ def moe_balance(shape, logits, topk_idx, seq_offsets, S, mask, loss, counts, seq
 def moe_balance_bwd(shape, logits, topk_idx, topk_w, d_topk_w, renorm, seq_offsets, S, mask, seq_counts, seq_scale,
                     d_loss, d_logits, stream=None) -> None:
     T, E, k, S = shape.T, shape.E, shape.k, int(S)
-    _want_here(logits, "logits", _F32, T * E)
-    _want_here(topk_idx, "topk_idx", _I32, T * k)
-    _want_here(topk_w, "topk_w", _F32, T * k)
-    _want_here(d_topk_w, "d_topk_w", _F32, T * k)
-    _want_here(seq_offsets, "seq_offsets", _I32, S + 1)
-    _want_here(mask, "mask", _U8, T)
-    _want_here(seq_counts, "seq_counts", _I32, S * E)
-    _want_here(seq_scale, "seq_scale", _F32, S + 1)
-    _want_here(d_loss, "d_loss", _F32, 2)
-    _want_here(d_logits, "d_logits", _F32, T * E)
+    _here((logits, "logits", _F32, T * E),
+          (topk_idx, "topk_idx", _I32, T * k),
+          (topk_w, "topk_w", _F32, T * k),
+          (d_topk_w, "d_topk_w", _F32, T * k),
+          (seq_offsets, "seq_offsets", _I32, S + 1),
+          (mask, "mask", _U8, T),
+          (seq_counts, "seq_counts", _I32, S * E),
+          (seq_scale, "seq_scale", _F32, S + 1),
+          (d_loss, "d_loss", _F32, 2),
+          (d_logits, "d_logits", _F32, T * E))
     _check(lib().moe_balance_bwd(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w),
                                  int(bool(renorm)), _ptr(seq_offsets), S, _ptr(mask), _ptr(seq_counts),
                                  _ptr(seq_scale), _ptr(d_loss), _ptr(d_logits), _stream(stream)), "moe_balance_bwd")
@@ -423,20 +432,20 @@ def moe_ortho_workspace_size(shape: moe_ortho_shape) -> int:
 
 def moe_orthogonalize(shape, G, U, ws, stream=None) -> None:
     n = shape.E * shape.R * shape.C
-    _want_here(G, "G", _BF16 if shape.grad_dtype == 0 else _F32, n)
-    _want_here(U, "U", _BF16, n)
-    _want_here(ws, "ws", _U8, 0)
+    _here((G, "G", _BF16 if shape.grad_dtype == 0 else _F32, n),
+          (U, "U", _BF16, n),
+          (ws, "ws", _U8, 0))
     _check(lib().moe_orthogonalize(ctypes.byref(shape), _ptr(G), _ptr(U), _ptr(ws), ws.numel() * ws.element_size(),
                                    _stream(stream)), "moe_orthogonalize")
 
 
 def moe_muon_step(shape, params, grad, momentum, W, master, ws, stream=None) -> None:
     n = shape.E * shape.R * shape.C
-    _want_here(grad, "grad", _BF16 if shape.grad_dtype == 0 else _F32, n)
-    _want_here(momentum, "momentum", _F32, n)
-    _want_here(W, "W", _BF16, n)
-    _want_here(master, "master", _F32, n)
-    _want_here(ws, "ws", _U8, 0)
+    _here((grad, "grad", _BF16 if shape.grad_dtype == 0 else _F32, n),
+          (momentum, "momentum", _F32, n),
+          (W, "W", _BF16, n),
+          (master, "master", _F32, n),
+          (ws, "ws", _U8, 0))
     _check(lib().moe_muon_step(ctypes.byref(shape), ctypes.byref(params), _ptr(grad), _ptr(momentum), _ptr(W),
                                _ptr(master), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
            "moe_muon_step")

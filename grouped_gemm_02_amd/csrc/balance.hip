@@ -4,7 +4,8 @@
 // A token's row of E logits is held by LPT = 4 .. 64 neighbouring lanes, four
 // consecutive experts a lane and V such chunks (E <= 4 LPT V), so a wave
 // works on 64 / LPT tokens at once and reads 16 bytes a lane. Row maxima and
-// sums are butterflies over the LPT lanes.
+// sums are butterflies over the LPT lanes in DPP and permlane swaps, and every
+// group of lanes has the rows of several tokens in flight.
 //
 // Forward, in a fixed order without float atomics:
 //   balance_partial  a workgroup per chunk of tokens. The part of sequence q
@@ -13,8 +14,8 @@
 //                    and at most chunks + S of them exist, without a scan.
 //                    Each piece gets its sums of p and lse^2, its counts
 //                    (integer atomics in LDS) and its live tokens.
-//   balance_seq      a workgroup per sequence adds its pieces.
-//   balance_finish   one workgroup adds the sequences.
+//   balance_seq      a workgroup per sequence and 32 experts adds its pieces.
+//   balance_finish   adds the sequences.
 #include "device_common.h"
 #include "kernels.h"
 
@@ -23,8 +24,12 @@ namespace moe {
 namespace {
 
 constexpr int kBalThreads = 256;
+constexpr int kBalRows = 4;  // 16-byte loads of logits a lane has in flight
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// T * E up to which one workgroup does the whole forward
+constexpr int64_t kSmallWork = 32768;
 
 int balance_chunk_tokens(int64_t T) {
   // 32 tokens a workgroup until 1024 workgroups are reached, then more
@@ -42,42 +47,73 @@ __device__ __forceinline__ f32x4 load4(const float* __restrict__ row, int e0, in
   return v;
 }
 
+// One step of a butterfly over 2, 4, 8, 16, 32, 64 lanes: the value that meets
+// this lane's. The mirrors do for lanes that already agree in 4s and 8s what
+// xor 4 and 8 would; the swaps give both halves at once.
+template <int W, class Op>
+__device__ __forceinline__ float butterfly(float v, Op op) {
+  if constexpr (W == 2) return op(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 15, 15, true)));
+  if constexpr (W == 4) return op(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 15, 15, true)));
+  if constexpr (W == 8) return op(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 15, 15, true)));
+  if constexpr (W == 16)
+    return op(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 15, 15, true)));
+  if constexpr (W == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (W == 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return v;
+}
+template <int LPT, class Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+  if constexpr (LPT >= 2) v = butterfly<2>(v, op);
+  if constexpr (LPT >= 4) v = butterfly<4>(v, op);
+  if constexpr (LPT >= 8) v = butterfly<8>(v, op);
+  if constexpr (LPT >= 16) v = butterfly<16>(v, op);
+  if constexpr (LPT >= 32) v = butterfly<32>(v, op);
+  if constexpr (LPT >= 64) v = butterfly<64>(v, op);
+  return v;
+}
 template <int LPT>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int off = LPT / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+  return group_reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int off = LPT / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+  return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
 }
 
-// The softmax of one row: v becomes exp(v - max), sum its sum, lse the
-// log-sum-exp. fmaxf drops a NaN, so a NaN reaches the sum through exp. A row
-// of -inf alone gives v = 0 and sum = 0 (and lse = -inf).
+// The softmax of one row, in powers of two on the transcendental unit: v
+// becomes 2^(v log2(e) - c) with c = max log2(e) (c's rounding cancels between
+// v and sum, the product's is inside the fma), sum its sum, lse the log-sum-
+// exp. fmaxf drops a NaN, so a NaN reaches the sum through the power. A row of
+// -inf alone gives v = 0 and sum = 0 (and lse = -inf).
 template <int LPT, int V>
 __device__ __forceinline__ void row_softmax(f32x4 (&v)[V], float& sum, float& lse) {
+  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i][j]);
   m = group_max<LPT>(m);
-  const float ref = m == -INFINITY ? 0.f : m;
+  const float c = m == -INFINITY ? 0.f : m * kLog2e;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[i][j] = expf(v[i][j] - ref);
+      v[i][j] = __builtin_amdgcn_exp2f(fmaf(v[i][j], kLog2e, -c));
       s += v[i][j];
     }
   sum = group_sum<LPT>(s);
-  lse = m + logf(sum);
+  lse = (c + __builtin_amdgcn_logf(sum)) * kLn2;
 }
+// 1 / sum; 0 for a row of -inf alone, NaN stays
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum); }
 
 // The last sequence that starts at or before t, in [0, S).
 __device__ __forceinline__ int seq_of(const int32_t* __restrict__ off, int S, int64_t t) {
@@ -96,16 +132,74 @@ struct BalancePieces {
   int32_t* n;      // [pieces]
 };
 
+// Sums over the tokens [lo, hi), by a workgroup of kGroups groups of LPT lanes:
+// on return (after a barrier by the caller) sp[group][e] holds the sums of p,
+// sc[e] the counts, sz and sn each group's sum of lse^2 and live tokens.
+template <int LPT, int V, int kGroups>
+__device__ __forceinline__ void sum_tokens(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                                           int64_t lo, int64_t hi, int E, int k, const uint8_t* __restrict__ mask,
+                                           float* sp, int32_t* sc, float* sz, int32_t* sn) {
+  constexpr int U = kBalRows / V;
+  const int grp = threadIdx.x / LPT, l = threadIdx.x % LPT;
+  f32x4 acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float z = 0.f;
+  int32_t n = 0;
+  // the trip count is the same for a whole wave: the butterflies stay converged
+  for (int64_t b = lo; b < hi; b += kGroups * U) {
+    f32x4 v[U][V];
+    bool live[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t tt = b + u * kGroups + grp;
+      live[u] = tt < hi && (!mask || mask[tt] != 0);
+      const int64_t tr = live[u] ? tt : lo;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[u][i] = load4(logits + tr * E, 4 * (l + LPT * i), E);
+    }
+    for (int j0 = 0; j0 < k; j0 += LPT) {
+      int e[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        e[u] = live[u] && j0 + l < k ? idx[(b + u * kGroups + grp) * k + j0 + l] : -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (e[u] >= 0 && e[u] < E) atomicAdd(&sc[e[u]], 1);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float sum, lse;
+      row_softmax<LPT, V>(v[u], sum, lse);
+      if (live[u]) {
+        const float inv = inverse_of(sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] += v[u][i][j] * inv;
+        z += sum == 0.f ? 0.f : lse * lse;
+        ++n;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) *reinterpret_cast<f32x4*>(sp + grp * 4 * LPT * V + 4 * (l + LPT * i)) = acc[i];
+  if (l == 0) {
+    sz[grp] = z;
+    sn[grp] = n;
+  }
+}
+
 template <int LPT, int V>
 __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t T, int E, int k,
     const int32_t* __restrict__ off, int S, const uint8_t* __restrict__ mask, int chunk, BalancePieces out) {
   constexpr int kGroups = kBalThreads / LPT;
-  __shared__ float sp[kGroups * 4 * LPT * V];
+  __shared__ __attribute__((aligned(16))) float sp[kGroups * 4 * LPT * V];
   __shared__ int32_t sc[4 * LPT * V];
   __shared__ float sz[kGroups];
   __shared__ int32_t sn[kGroups];
-  const int tid = threadIdx.x, grp = tid / LPT, l = tid % LPT;
+  const int tid = threadIdx.x;
   const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(T, t0 + chunk);
   int q = off ? seq_of(off, S, t0) : 0;
   for (int64_t t = t0; t < t1 && q < S; ++q) {
@@ -116,45 +210,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
     t = hi;
     for (int i = tid; i < E; i += kBalThreads) sc[i] = 0;
     __syncthreads();
-    f32x4 acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float z = 0.f;
-    int32_t n = 0;
-    // the trip count is the same for a whole wave: shuffles stay converged
-    for (int64_t b = lo; b < hi; b += kGroups) {
-      const int64_t tt = b + grp;
-      const bool in = tt < hi;
-      const bool live = in && (!mask || mask[tt] != 0);
-      if (!__any(live)) continue;
-      const int64_t tr = live ? tt : lo;
-      f32x4 v[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = load4(logits + tr * E, 4 * (l + LPT * i), E);
-      float sum, lse;
-      row_softmax<LPT, V>(v, sum, lse);
-      if (live) {
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] += v[i][j] * inv;
-        z += sum == 0.f ? 0.f : lse * lse;
-        ++n;
-        for (int j = l; j < k; j += LPT) {
-          const int e = idx[tt * k + j];
-          if (e >= 0 && e < E) atomicAdd(&sc[e], 1);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sp[grp * 4 * LPT * V + 4 * (l + LPT * i) + j] = acc[i][j];
-    if (l == 0) {
-      sz[grp] = z;
-      sn[grp] = n;
-    }
+    sum_tokens<LPT, V, kGroups>(logits, idx, lo, hi, E, k, mask, sp, sc, sz, sn);
     __syncthreads();
     const int64_t piece = int64_t(blockIdx.x) + q;
     for (int e = tid; e < E; e += kBalThreads) {
@@ -164,15 +220,15 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
       out.p[piece * E + e] = s;
       out.c[piece * E + e] = sc[e];
     }
-    if (tid == 0) {
-      float s = 0.f;
-      int32_t m = 0;
-      for (int g = 0; g < kGroups; ++g) {
-        s += sz[g];
-        m += sn[g];
+    if (tid < 64) {  // kGroups <= 64
+      float s = tid < kGroups ? sz[tid] : 0.f;
+      int32_t m = tid < kGroups ? sn[tid] : 0;
+      s = group_sum<64>(s);
+      for (int o = 32; o > 0; o >>= 1) m += __shfl_xor(m, o);
+      if (tid == 0) {
+        out.z[piece] = s;
+        out.n[piece] = m;
       }
-      out.z[piece] = s;
-      out.n[piece] = m;
     }
     __syncthreads();
   }
@@ -180,74 +236,118 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
 
 // What balance_finish needs of each sequence.
 struct BalanceSeq {
-  double* term;  // [S] sum_e c P
+  double* term;  // [S][blocks of 32 experts] sum_e c P
   double* z;     // [S] sum of lse^2
   int32_t* n;    // [S] live tokens
 };
 
+// Sum over the workgroup's 1024 threads, in every thread.
 __device__ __forceinline__ double block_sum(double v, double* sm) {
   const int tid = threadIdx.x;
-  sm[tid] = v;
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if ((tid & 63) == 0) sm[tid >> 6] = v;
   __syncthreads();
-  for (int o = blockDim.x / 2; o > 0; o >>= 1) {
-    if (tid < o) sm[tid] += sm[tid + o];
-    __syncthreads();
-  }
-  const double r = sm[0];
+  double r = 0.0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r += sm[i];
   __syncthreads();
   return r;
 }
 
-__global__ __launch_bounds__(kBalThreads) void balance_seq_kernel(int64_t T, int E, const int32_t* __restrict__ off,
-                                                                  int chunk, BalancePieces in,
-                                                                  int32_t* __restrict__ seq_counts,
-                                                                  float* __restrict__ seq_probs, BalanceSeq out) {
-  __shared__ double sm[kBalThreads];
+constexpr int kSeqExperts = 32;
+constexpr int kSmallSeqs = 16;
+
+// 32 experts x 32 pieces at a time.
+__global__ __launch_bounds__(1024) void balance_seq_kernel(int64_t T, int E, const int32_t* __restrict__ off,
+                                                           int chunk, BalancePieces in,
+                                                           int32_t* __restrict__ seq_counts,
+                                                           float* __restrict__ seq_probs, BalanceSeq out) {
+  __shared__ double sm[16];
+  __shared__ double sP[32][kSeqExperts + 1];
+  __shared__ int32_t sC[32][kSeqExperts + 1];
   const int q = blockIdx.x, tid = threadIdx.x;
   const int64_t lo = off ? max(int64_t(0), int64_t(off[q])) : 0;
   const int64_t hi = off ? min(T, int64_t(off[q + 1])) : T;
   const int64_t p0 = lo / chunk + q, p1 = hi > lo ? (hi - 1) / chunk + q + 1 : p0;
+  const int e = blockIdx.y * kSeqExperts + (tid & 31);
+  const int pl = tid >> 5;
+  double P = 0.0;
+  int32_t c = 0;
+  if (e < E) {
+#pragma unroll 4
+    for (int64_t p = p0 + pl; p < p1; p += 32) {
+      P += in.p[p * E + e];
+      c += in.c[p * E + e];
+    }
+  }
+  sP[pl][tid & 31] = P;
+  sC[pl][tid & 31] = c;
   double z = 0.0, n = 0.0;
-  for (int64_t p = p0 + tid; p < p1; p += kBalThreads) {
+  for (int64_t p = p0 + tid; p < p1; p += 1024) {
     z += in.z[p];
     n += in.n[p];
   }
   z = block_sum(z, sm);
   n = block_sum(n, sm);
   double term = 0.0;
-  for (int e = tid; e < E; e += kBalThreads) {
-    double P = 0.0;
-    int32_t c = 0;
-    for (int64_t p = p0; p < p1; ++p) {
-      P += in.p[p * E + e];
-      c += in.c[p * E + e];
+  if (tid < kSeqExperts) {
+    P = 0.0;
+    c = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      P += sP[i][tid];
+      c += sC[i][tid];
     }
-    seq_counts[int64_t(q) * E + e] = c;
-    seq_probs[int64_t(q) * E + e] = n > 0.0 ? float(P / n) : 0.f;
-    term += double(c) * P;
-  }
-  term = block_sum(term, sm);
-  if (tid == 0) {
-    out.term[q] = term;
-    out.z[q] = z;
-    out.n[q] = int32_t(n);
+    if (e < E) {
+      seq_counts[int64_t(q) * E + e] = c;
+      seq_probs[int64_t(q) * E + e] = n > 0.0 ? float(P / n) : 0.f;
+    }
+    term = double(c) * P;
+    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor(term, o, 32);
+    if (tid == 0) {
+      out.term[int64_t(q) * gridDim.y + blockIdx.y] = term;
+      if (blockIdx.y == 0) {
+        out.z[q] = z;
+        out.n[q] = int32_t(n);
+      }
+    }
   }
 }
 
-__global__ __launch_bounds__(kBalThreads) void balance_finish_kernel(int E, int k, int S, BalanceSeq in,
-                                                                     const int32_t* __restrict__ seq_counts,
-                                                                     float* __restrict__ loss,
-                                                                     int32_t* __restrict__ counts,
-                                                                     float* __restrict__ seq_scale) {
-  __shared__ double sm[kBalThreads];
+// Workgroup 0: the losses and the factors; the others 64 experts' counts each.
+__global__ __launch_bounds__(1024) void balance_finish_kernel(int E, int k, int S, int blocks, BalanceSeq in,
+                                                              const int32_t* __restrict__ seq_counts,
+                                                              float* __restrict__ loss, int32_t* __restrict__ counts,
+                                                              float* __restrict__ seq_scale) {
+  __shared__ double sm[16];
+  __shared__ int32_t sC[16][64];
   const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    const int e = (blockIdx.x - 1) * 64 + (tid & 63);
+    int32_t c = 0;
+    if (e < E) {
+#pragma unroll 4
+      for (int q = tid >> 6; q < S; q += 16) c += seq_counts[int64_t(q) * E + e];
+    }
+    sC[tid >> 6][tid & 63] = c;
+    __syncthreads();
+    if (tid < 64 && e < E) {
+      c = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) c += sC[i][tid];
+      counts[e] = c;
+    }
+    return;
+  }
   double term = 0.0, z = 0.0, n = 0.0, used = 0.0;
-  for (int q = tid; q < S; q += kBalThreads) {
+  for (int q = tid; q < S; q += 1024) {
     const double nq = in.n[q];
     z += in.z[q];
     n += nq;
     if (nq > 0.0) {
-      term += in.term[q] * double(E) / (double(k) * nq * nq);
+      double t = 0.0;
+      for (int b = 0; b < blocks; ++b) t += in.term[int64_t(q) * blocks + b];
+      term += t * double(E) / (double(k) * nq * nq);
       used += 1.0;
     }
   }
@@ -255,20 +355,84 @@ __global__ __launch_bounds__(kBalThreads) void balance_finish_kernel(int E, int 
   z = block_sum(z, sm);
   n = block_sum(n, sm);
   used = block_sum(used, sm);
-  for (int q = tid; q < S; q += kBalThreads) {
+  for (int q = tid; q < S; q += 1024) {
     const double nq = in.n[q];
     seq_scale[q] = nq > 0.0 ? float(double(E) / (used * double(k) * nq * nq)) : 0.f;
-  }
-  for (int e = tid; e < E; e += kBalThreads) {
-    int32_t c = 0;
-    for (int q = 0; q < S; ++q) c += seq_counts[int64_t(q) * E + e];
-    counts[e] = c;
   }
   if (tid == 0) {
     loss[0] = used > 0.0 ? float(term / used) : 0.f;
     loss[1] = n > 0.0 ? float(z / n) : 0.f;
     seq_scale[S] = n > 0.0 ? float(1.0 / n) : 0.f;
   }
+}
+
+// The whole forward in one workgroup, for batches whose three launches would
+// cost more than their work (see launch_balance).
+template <int LPT, int V>
+__global__ __launch_bounds__(1024) void balance_small_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t T, int E, int k,
+    const int32_t* __restrict__ off, int S, const uint8_t* __restrict__ mask, float* __restrict__ loss,
+    int32_t* __restrict__ counts, int32_t* __restrict__ seq_counts, float* __restrict__ seq_probs,
+    float* __restrict__ seq_scale) {
+  constexpr int kGroups = 1024 / LPT;
+  __shared__ __attribute__((aligned(16))) float sp[kGroups * 4 * LPT * V];
+  __shared__ int32_t sc[4 * LPT * V];
+  __shared__ float sz[kGroups];
+  __shared__ int32_t sn[kGroups];
+  __shared__ double sm[16];
+  __shared__ int32_t live_of[kSmallSeqs];
+  const int tid = threadIdx.x;
+  double term = 0.0, z = 0.0, n = 0.0, used = 0.0;
+  int32_t total = 0;  // expert tid's count over the sequences (E <= 1024)
+  for (int q = 0; q < S; ++q) {
+    const int64_t lo = off ? max(int64_t(0), int64_t(off[q])) : 0;
+    const int64_t hi = off ? min(T, int64_t(off[q + 1])) : T;
+    if (tid < E) sc[tid] = 0;
+    __syncthreads();
+    sum_tokens<LPT, V, kGroups>(logits, idx, lo, hi, E, k, mask, sp, sc, sz, sn);
+    __syncthreads();
+    const double zq = block_sum(tid < kGroups ? double(sz[tid]) : 0.0, sm);
+    const double nq = block_sum(tid < kGroups ? double(sn[tid]) : 0.0, sm);
+    double P = 0.0;
+    int32_t c = 0;
+    if (tid < E) {
+#pragma unroll 8
+      for (int g = 0; g < kGroups; ++g) P += sp[g * 4 * LPT * V + tid];
+      c = sc[tid];
+      seq_counts[int64_t(q) * E + tid] = c;
+      seq_probs[int64_t(q) * E + tid] = nq > 0.0 ? float(P / nq) : 0.f;
+      total += c;
+    }
+    const double t = block_sum(double(c) * P, sm);
+    if (nq > 0.0) {
+      term += t * double(E) / (double(k) * nq * nq);
+      used += 1.0;
+    }
+    z += zq;
+    n += nq;
+    if (tid == 0) live_of[q] = int32_t(nq);
+  }
+  if (tid < E) counts[tid] = total;
+  __syncthreads();
+  if (tid < S) {
+    const double nq = live_of[tid];
+    seq_scale[tid] = nq > 0.0 ? float(double(E) / (used * double(k) * nq * nq)) : 0.f;
+  }
+  if (tid == 0) {
+    loss[0] = used > 0.0 ? float(term / used) : 0.f;
+    loss[1] = n > 0.0 ? float(z / n) : 0.f;
+    seq_scale[S] = n > 0.0 ? float(1.0 / n) : 0.f;
+  }
+}
+
+// Rows a group of the backward has in flight, and the tokens of a workgroup.
+// 131,072 x 256: two rows and 32 tokens 71 us, four rows 83, two rows and 64
+// tokens 85, four rows and 128 tokens 113 (fewer registers and more
+// workgroups: more loads in flight); 16,384 x 128: 16 tokens 9.6 us, 32 10.6.
+constexpr int bwd_rows(int V) { return V == 1 ? 2 : 1; }
+int bwd_chunk(int64_t T, int groups, int V) {
+  const int base = T >= 65536 ? 32 : 16, batch = groups * bwd_rows(V);
+  return base > batch ? base : batch;
 }
 
 // One pass over the logits. HBM-bound for long batches (reads and writes a
@@ -280,6 +444,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
     const uint8_t* __restrict__ mask, const int32_t* __restrict__ seq_counts, const float* __restrict__ seq_scale,
     const float* __restrict__ d_loss, int chunk, float* __restrict__ dz) {
   constexpr int kGroups = kBalThreads / LPT;
+  constexpr int U = bwd_rows(V);
+  __shared__ __attribute__((aligned(16))) float sel[U * kGroups * 4 * LPT * V];
   const int tid = threadIdx.x, grp = tid / LPT, l = tid % LPT;
   const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(T, t0 + chunk);
   const float gb = d_loss[0], gz = 2.f * d_loss[1] * seq_scale[S];
@@ -288,87 +454,117 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
   f32x4 bal[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) bal[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t b = t0; b < t1; b += kGroups) {
-    const int64_t t = b + grp;
-    const bool in = t < t1;
-    const int64_t tr = in ? t : t0;
-    f32x4 v[V];
+  float* const row = sel + grp * 4 * LPT * V;  // the group's selected experts' values, kRow apart
+  constexpr int kRow = kGroups * 4 * LPT * V;
+  for (int64_t b = t0; b < t1; b += kGroups * U) {
+    f32x4 v[U][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = load4(logits + tr * E, 4 * (l + LPT * i), E);
-    if (in && (q < 0 || t >= qe || t < qb)) {
-      q = off ? seq_of(off, S, t) : 0;
-      qb = off ? int64_t(off[q]) : 0;
-      qe = off ? int64_t(off[q + 1]) : T;
-      const float sc = gb * seq_scale[q];
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = b + u * kGroups + grp;
+      const int64_t tr = t < t1 ? t : t0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[u][i] = load4(logits + tr * E, 4 * (l + LPT * i), E);
+    }
+    // the first LPT slots of each row; more are read below
+    int ej[U];
+    float dj[U], wj[U];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = b + u * kGroups + grp;
+      const bool has = dw && t < t1 && l < k;
+      ej[u] = has ? idx[t * k + l] : -1;
+      dj[u] = has ? dw[t * k + l] : 0.f;
+      wj[u] = has && renorm ? w[t * k + l] : 0.f;
+      on[u] = t < t1 && (!mask || mask[t] != 0);
+    }
+    if (dw) {
+      // the slots' values to their experts through LDS; the lanes of a group
+      // are in one wave, whose LDS operations are in order
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          *reinterpret_cast<f32x4*>(row + u * kRow + 4 * (l + LPT * i)) = f32x4{0.f, 0.f, 0.f, 0.f};
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t t = b + u * kGroups + grp;
+        const int kt = t < t1 ? k : 0;
+        float c = 0.f;
+        if (renorm) {
+          c = wj[u] * dj[u];
+          for (int j = l + LPT; j < kt; j += LPT) c += w[t * k + j] * dw[t * k + j];
+          c = group_sum<LPT>(c);
+        }
+        if (ej[u] >= 0 && ej[u] < E) atomicAdd(row + u * kRow + ej[u], renorm ? wj[u] * (dj[u] - c) : dj[u]);
+        for (int j = l + LPT; j < kt; j += LPT) {
+          const int e = idx[t * k + j];
+          const float d = dw[t * k + j];
+          if (e >= 0 && e < E) atomicAdd(row + u * kRow + e, renorm ? w[t * k + j] * (d - c) : d);
+        }
+      }
+      asm volatile("" ::: "memory");
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = b + u * kGroups + grp;
+      const bool in = t < t1;
+      if (in && (q < 0 || t >= qe || t < qb)) {
+        q = off ? seq_of(off, S, t) : 0;
+        qb = off ? int64_t(off[q]) : 0;
+        qe = off ? int64_t(off[q + 1]) : T;
+        const float sc = gb * seq_scale[q];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * (l + LPT * i) + j;
+            bal[i][j] = e < E ? sc * float(seq_counts[int64_t(q) * E + e]) : 0.f;
+          }
+      }
+      const bool live = on[u] && t >= qb && t < qe;
+      float sum, lse;
+      row_softmax<LPT, V>(v[u], sum, lse);
+      const float inv = inverse_of(sum);
+      // G: what is weighted by p; H: the renormalised weights' gradient, added as it is
+      f32x4 G[V], H[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[u][i] *= inv;
+        H[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        G[i] = live ? bal[i] : H[i];
+        if (dw) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(row + u * kRow + 4 * (l + LPT * i));
+          if (renorm) H[i] = x; else G[i] += x;
+        }
+      }
+      float pg = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = 4 * (l + LPT * i) + j;
-          bal[i][j] = e < E ? sc * float(seq_counts[int64_t(q) * E + e]) : 0.f;
-        }
-    }
-    const bool live = in && t >= qb && t < qe && (!mask || mask[t] != 0);
-    float sum, lse;
-    row_softmax<LPT, V>(v, sum, lse);
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    // G: what is weighted by p; H: the renormalised weights' gradient, added as it is
-    f32x4 G[V], H[V];
+        for (int j = 0; j < 4; ++j) pg += v[u][i][j] * G[i][j];
+      pg = group_sum<LPT>(pg);
+      const float zt = live && sum != 0.f ? gz * lse : 0.f;
+      if (in) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] *= inv;
-      H[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      G[i] = live ? bal[i] : H[i];
-    }
-    if (dw) {
-      float c = 0.f;
-      if (renorm) {
-        for (int j = l; j < k; j += LPT) c += w[tr * k + j] * dw[tr * k + j];
-        c = group_sum<LPT>(c);
-      }
-      for (int j0 = 0; j0 < k; j0 += LPT) {
-        const int j = j0 + l;
-        const int ej = j < k ? idx[tr * k + j] : -1;
-        const float dj = j < k ? dw[tr * k + j] : 0.f;
-        const float xj = renorm && j < k ? w[tr * k + j] * (dj - c) : dj;
-        const int nj = min(LPT, k - j0);
-        for (int s = 0; s < nj; ++s) {
-          const int e = __shfl(ej, s, LPT);
-          const float x = __shfl(xj, s, LPT);
+        for (int i = 0; i < V; ++i) {
+          const int e0 = 4 * (l + LPT * i);
+          f32x4 o;
 #pragma unroll
-          for (int i = 0; i < V; ++i)
+          for (int j = 0; j < 4; ++j) o[j] = v[u][i][j] * (G[i][j] - pg + zt) + H[i][j];
+          float* dst = dz + t * E + e0;
+          if (e0 + 4 <= E) {
+            *reinterpret_cast<f32x4u*>(dst) = o;
+          } else {
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
-              if (e == 4 * (l + LPT * i) + jj) {
-                if (renorm) H[i][jj] += x; else G[i][jj] += x;
-              }
+            for (int j = 0; j < 4; ++j)
+              if (e0 + j < E) dst[j] = o[j];
+          }
         }
       }
     }
-    float pg = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) pg += v[i][j] * G[i][j];
-    pg = group_sum<LPT>(pg);
-    const float zt = live && sum != 0.f ? gz * lse : 0.f;
-    if (in) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e0 = 4 * (l + LPT * i);
-        f32x4 o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = v[i][j] * (G[i][j] - pg + zt) + H[i][j];
-        float* dst = dz + t * E + e0;
-        if (e0 + 4 <= E) {
-          *reinterpret_cast<f32x4u*>(dst) = o;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (e0 + j < E) dst[j] = o[j];
-        }
-      }
-    }
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -387,6 +583,7 @@ void with_layout(int E, F f) {
 struct BalanceWs {
   size_t p, c, z, n, term, qz, qn, total;
 };
+int seq_blocks(int E) { return (E + kSeqExperts - 1) / kSeqExperts; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 BalanceWs balance_ws(int64_t T, int E, int64_t S) {
   const int chunk = balance_chunk_tokens(T);
@@ -397,7 +594,7 @@ BalanceWs balance_ws(int64_t T, int E, int64_t S) {
   L.c = o;    o = up256(o + pieces * size_t(E) * 4);
   L.z = o;    o = up256(o + pieces * 4);
   L.n = o;    o = up256(o + pieces * 4);
-  L.term = o; o = up256(o + size_t(S) * 8);
+  L.term = o; o = up256(o + size_t(S) * seq_blocks(E) * 8);
   L.qz = o;   o = up256(o + size_t(S) * 8);
   L.qn = o;   o = up256(o + size_t(S) * 4);
   L.total = o;
@@ -417,6 +614,19 @@ struct PartialLaunch {
   }
 };
 
+struct SmallLaunch {
+  const BalanceArgs& a;
+  float* loss;
+  int32_t *counts, *seq_counts;
+  float *seq_probs, *seq_scale;
+  hipStream_t st;
+  template <int LPT, int V>
+  void operator()() const {
+    hipLaunchKernelGGL((balance_small_kernel<LPT, V>), dim3(1), dim3(1024), 0, st, a.logits, a.idx, a.T, a.E, a.k, a.off,
+                       int(a.S), a.mask, loss, counts, seq_counts, seq_probs, seq_scale);
+  }
+};
+
 struct BwdLaunch {
   const BalanceArgs& a;
   const float *w, *dw;
@@ -424,11 +634,11 @@ struct BwdLaunch {
   const int32_t* seq_counts;
   const float *seq_scale, *d_loss;
   float* dz;
-  int chunk;
-  dim3 grid;
   hipStream_t st;
   template <int LPT, int V>
   void operator()() const {
+    const int chunk = bwd_chunk(a.T, kBalThreads / LPT, V);
+    const dim3 grid(unsigned((a.T + chunk - 1) / chunk));
     hipLaunchKernelGGL((balance_bwd_kernel<LPT, V>), grid, dim3(kBalThreads), 0, st, a.logits, a.idx, w, dw, a.T, a.E,
                        a.k, renorm, a.off, int(a.S), a.mask, seq_counts, seq_scale, d_loss, chunk, dz);
   }
@@ -440,6 +650,11 @@ size_t balance_scratch_bytes(int64_t T, int E, int64_t S) { return balance_ws(T,
 
 hipError_t launch_balance(const BalanceArgs& a, float* loss, int32_t* counts, int32_t* seq_counts, float* seq_probs,
                           float* seq_scale, void* ws, hipStream_t st, KernelTimer* timer) {
+  if (a.S <= kSmallSeqs && a.T * a.E <= kSmallWork) {
+    TimedLaunch tl(timer, "balance_small", st);
+    with_layout(a.E, SmallLaunch{a, loss, counts, seq_counts, seq_probs, seq_scale, st});
+    return hipGetLastError();
+  }
   const BalanceWs L = balance_ws(a.T, a.E, a.S);
   char* base = static_cast<char*>(ws);
   const BalancePieces pc{reinterpret_cast<float*>(base + L.p), reinterpret_cast<int32_t*>(base + L.c),
@@ -451,15 +666,16 @@ hipError_t launch_balance(const BalanceArgs& a, float* loss, int32_t* counts, in
     TimedLaunch tl(timer, "balance_partial", st);
     with_layout(a.E, PartialLaunch{a, pc, chunk, dim3(unsigned((a.T + chunk - 1) / chunk)), st});
   }
+  const int blocks = seq_blocks(a.E);
   {
     TimedLaunch tl(timer, "balance_seq", st);
-    hipLaunchKernelGGL(balance_seq_kernel, dim3(unsigned(a.S)), dim3(kBalThreads), 0, st, a.T, a.E, a.off, chunk, pc,
-                       seq_counts, seq_probs, sq);
+    hipLaunchKernelGGL(balance_seq_kernel, dim3(unsigned(a.S), unsigned(blocks)), dim3(1024), 0, st, a.T, a.E, a.off,
+                       chunk, pc, seq_counts, seq_probs, sq);
   }
   {
     TimedLaunch tl(timer, "balance_finish", st);
-    hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(kBalThreads), 0, st, a.E, a.k, int(a.S), sq, seq_counts,
-                       loss, counts, seq_scale);
+    hipLaunchKernelGGL(balance_finish_kernel, dim3(unsigned(1 + (a.E + 63) / 64)), dim3(1024), 0, st, a.E, a.k, int(a.S),
+                       blocks, sq, seq_counts, loss, counts, seq_scale);
   }
   return hipGetLastError();
 }
@@ -469,9 +685,7 @@ hipError_t launch_balance_bwd(const BalanceArgs& a, const float* w, const float*
                               hipStream_t st, KernelTimer* timer) {
   if (a.T <= 0) return hipSuccess;
   TimedLaunch tl(timer, "balance_bwd", st);
-  const int chunk = balance_chunk_tokens(a.T);
-  with_layout(a.E, BwdLaunch{a, w, dw, renorm, seq_counts, seq_scale, d_loss, dz, chunk,
-                             dim3(unsigned((a.T + chunk - 1) / chunk)), st});
+  with_layout(a.E, BwdLaunch{a, w, dw, renorm, seq_counts, seq_scale, d_loss, dz, st});
   return hipGetLastError();
 }
 
