@@ -84,35 +84,109 @@ __device__ __forceinline__ float grad_at(const void* g, bool f32, int64_t i) {
              : __uint_as_float(uint32_t(static_cast<const uint16_t*>(g)[i]) << 16);
 }
 
-// Partial sums of squares, after the momentum step if there is one.
-__global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(const void* __restrict__ grad, bool f32,
-                                                                  float* __restrict__ mom, float mu, bool nesterov,
-                                                                  int64_t count, double* __restrict__ part) {
-  __shared__ double sm[kNormThreads];
-  const int64_t base = int64_t(blockIdx.y) * count;
-  double s = 0.0;
-  for (int64_t i = int64_t(blockIdx.x) * kNormThreads + threadIdx.x; i < count; i += int64_t(kNormParts) * kNormThreads) {
-    float x = grad_at(grad, f32, base + i);
-    if (mom) {
-      const float m = mu * mom[base + i] + x;
-      mom[base + i] = m;
-      x = nesterov ? x + mu * m : m;
+// What is orthogonalised.
+struct OrthoIn {
+  const void* grad;
+  bool f32;
+  float* mom;  // NULL: the gradient itself
+  float mu;
+  bool nesterov;
+};
+
+// Eight neighbouring gradient values (16-byte aligned).
+__device__ __forceinline__ void grad8(const OrthoIn& in, int64_t i, float (&x)[8]) {
+  if (in.f32) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(in.grad) + i);
+    const f32x4 a = p[0], b = p[1];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      x[t] = a[t];
+      x[4 + t] = b[t];
     }
-    s += double(x) * double(x);
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(in.grad) + i);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      x[2 * t] = bf16_lo(a[t]);
+      x[2 * t + 1] = bf16_hi(a[t]);
+    }
   }
-  sm[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = kNormThreads / 2; o > 0; o >>= 1) {
-    if (int(threadIdx.x) < o) sm[threadIdx.x] += sm[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) part[int64_t(blockIdx.y) * kNormParts + blockIdx.x] = sm[0];
 }
 
-// The exponent p of X0 = G 2^p, and s = 1 / ((|G| + eps) 2^p).
+// One element of what is orthogonalised, the momentum being up to date.
+__device__ __forceinline__ float input_at(const OrthoIn& in, int64_t i) {
+  if (!in.mom) return grad_at(in.grad, in.f32, i);
+  return in.nesterov ? grad_at(in.grad, in.f32, i) + in.mu * in.mom[i] : in.mom[i];
+}
+__device__ __forceinline__ void input8(const OrthoIn& in, int64_t i, float (&x)[8]) {
+  if (!in.mom || in.nesterov) grad8(in, i, x);
+  if (in.mom) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(in.mom + i);
+    const f32x4 a = p[0], b = p[1];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const float m = t < 4 ? a[t & 3] : b[t & 3];
+      x[t] = in.nesterov ? x[t] + in.mu * m : m;
+    }
+  }
+}
+
+// Partial sums of squares, after the momentum step if there is one. HBM-bound:
+// 16-byte accesses where a matrix is a whole number of them.
+__global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(OrthoIn in, int64_t count,
+                                                                  double* __restrict__ part) {
+  __shared__ double sm[kNormThreads / 64];
+  const int64_t base = int64_t(blockIdx.y) * count;
+  const int64_t first = int64_t(blockIdx.x) * kNormThreads + threadIdx.x;
+  constexpr int64_t kStep = int64_t(kNormParts) * kNormThreads;
+  double s = 0.0;
+  if ((count & 7) == 0) {
+#pragma unroll 2
+    for (int64_t i = first * 8; i < count; i += kStep * 8) {
+      float x[8];
+      grad8(in, base + i, x);
+      if (in.mom) {
+        f32x4* p = reinterpret_cast<f32x4*>(in.mom + base + i);
+        f32x4 a = p[0], b = p[1];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          a[t] = in.mu * a[t] + x[t];
+          b[t] = in.mu * b[t] + x[4 + t];
+          x[t] = in.nesterov ? x[t] + in.mu * a[t] : a[t];
+          x[4 + t] = in.nesterov ? x[4 + t] + in.mu * b[t] : b[t];
+        }
+        p[0] = a;
+        p[1] = b;
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) s += double(x[t]) * double(x[t]);
+    }
+  } else {
+    for (int64_t i = first; i < count; i += kStep) {
+      float x = grad_at(in.grad, in.f32, base + i);
+      if (in.mom) {
+        const float m = in.mu * in.mom[base + i] + x;
+        in.mom[base + i] = m;
+        x = in.nesterov ? x + in.mu * m : m;
+      }
+      s += double(x) * double(x);
+    }
+  }
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int i = 0; i < kNormThreads / 64; ++i) s += sm[i];
+    part[int64_t(blockIdx.y) * kNormParts + blockIdx.x] = s;
+  }
+}
+
+// The exponent p of X0 = G 2^p, and s = 1 / ((|G| + eps) 2^p), in every lane.
+static_assert(kNormParts == 64, "a lane per partial sum");
 __device__ __forceinline__ void matrix_scale(const double* __restrict__ part, float eps, int* p, float* s) {
-  double q = 0.0;
-  for (int i = 0; i < kNormParts; ++i) q += part[i];
+  double q = part[lane_id()];
+  for (int o = 32; o > 0; o >>= 1) q += __shfl_xor(q, o);
   const double norm = sqrt(q);
   const bool plain = norm > 0.0 && norm < 1e300;
   *p = plain ? kX0Exp - ilogb(norm) : 0;
@@ -127,32 +201,44 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return pack_halves(static_cast<_Float16>(a), static_cast<_Float16>(b));
 }
 
-
-// X0 and its remainder, 64 x 64 elements a workgroup, through LDS when G is
-// transposed.
-__global__ __launch_bounds__(256) void ortho_load_kernel(const void* __restrict__ grad, bool f32,
-                                                         const float* __restrict__ mom, float mu, bool nesterov,
-                                                         OrthoDims d, const double* __restrict__ part, float eps,
-                                                         _Float16* __restrict__ X, uint8_t* __restrict__ Xl,
-                                                         float* __restrict__ scale) {
+// X0 and its remainder, 64 x 64 elements a workgroup, through LDS (transposed
+// when G is tall). HBM-bound.
+__global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d, const double* __restrict__ part,
+                                                         float eps, _Float16* __restrict__ X,
+                                                         uint8_t* __restrict__ Xl, float* __restrict__ scale) {
   __shared__ float tile[kLoadTile][kLoadTile + 1];
   const int e = blockIdx.z, r0 = blockIdx.y * kLoadTile, c0 = blockIdx.x * kLoadTile;
   int p;
   float s;
   matrix_scale(part + int64_t(e) * kNormParts, eps, &p, &s);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) scale[e] = s;
-  // r, c: position in X
-  for (int i = threadIdx.x; i < kLoadTile * kLoadTile; i += 256) {
-    const int a = i / kLoadTile, b = i % kLoadTile;
-    const int gr = d.tall ? c0 + a : r0 + a, gc = d.tall ? r0 + b : c0 + b;
-    float x = 0.f;
-    if (gr < d.R && gc < d.C) {
-      const int64_t at = (int64_t(e) * d.R + gr) * d.C + gc;
-      x = grad_at(grad, f32, at);
-      if (mom) x = nesterov ? x + mu * mom[at] : mom[at];
-      x = s == s ? ldexpf(x, p) : NAN;
+  // a, b: row and column of G inside the tile
+  const int g0 = d.tall ? c0 : r0, h0 = d.tall ? r0 : c0;
+  if ((d.C & 7) == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int a = 32 * i + int(threadIdx.x >> 3), b = int(threadIdx.x & 7) * 8;
+      float x[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) x[t] = 0.f;
+      if (g0 + a < d.R && h0 + b < d.C) {
+        input8(in, (int64_t(e) * d.R + g0 + a) * d.C + h0 + b, x);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) x[t] = s == s ? ldexpf(x[t], p) : NAN;
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) tile[d.tall ? b + t : a][d.tall ? a : b + t] = x[t];
     }
-    tile[d.tall ? b : a][d.tall ? a : b] = x;
+  } else {
+    for (int i = threadIdx.x; i < kLoadTile * kLoadTile; i += 256) {
+      const int a = i / kLoadTile, b = i % kLoadTile;
+      float x = 0.f;
+      if (g0 + a < d.R && h0 + b < d.C) {
+        x = input_at(in, (int64_t(e) * d.R + g0 + a) * d.C + h0 + b);
+        x = s == s ? ldexpf(x, p) : NAN;
+      }
+      tile[d.tall ? b : a][d.tall ? a : b] = x;
+    }
   }
   __syncthreads();
 #pragma unroll
@@ -841,19 +927,17 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
     OrthoDims d = p.d;
     d.E = a.E - e0 < p.group ? a.E - e0 : p.group;
     const unsigned ge = unsigned(d.E);
-    const void* grad = static_cast<const char*>(t.grad) + size_t(e0) * count * gsize;
-    float* mom = t.momentum ? t.momentum + e0 * count : nullptr;
+    const OrthoIn in{static_cast<const char*>(t.grad) + size_t(e0) * count * gsize, a.grad_f32,
+                     t.momentum ? t.momentum + e0 * count : nullptr, t.mu, t.nesterov};
     {
       TimedLaunch tl(timer, "ortho_norm", st);
-      hipLaunchKernelGGL(ortho_norm_kernel, dim3(kNormParts, ge), dim3(kNormThreads), 0, st, grad, a.grad_f32, mom, t.mu,
-                         t.nesterov, count, part);
+      hipLaunchKernelGGL(ortho_norm_kernel, dim3(kNormParts, ge), dim3(kNormThreads), 0, st, in, count, part);
     }
-    const bool lo0 = a.grad_f32 || mom;  // a bf16 G is exact in fp16
+    const bool lo0 = a.grad_f32 || in.mom;  // a bf16 G is exact in fp16
     {
       TimedLaunch tl(timer, "ortho_load", st);
-      hipLaunchKernelGGL(ortho_load_kernel, dim3(d.np / kLoadTile, d.mp / kLoadTile, ge), dim3(256), 0, st, grad,
-                         a.grad_f32, mom, t.mu, t.nesterov, d, part, a.eps, f16(p.X[0]), lo0 ? u8(p.Xl[0]) : nullptr,
-                         f32(p.scale));
+      hipLaunchKernelGGL(ortho_load_kernel, dim3(d.np / kLoadTile, d.mp / kLoadTile, ge), dim3(256), 0, st, in, d, part,
+                         a.eps, f16(p.X[0]), lo0 ? u8(p.Xl[0]) : nullptr, f32(p.scale));
     }
     const int st_tiles = sym_tiles(d.mp);
     const int up_tiles = (d.mp + kTM - 1) / kTM * (d.np / kTN);
@@ -861,11 +945,11 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
     const bool square = std::fabs(a.c) > 1e-6f * std::fabs(a.b);
     const float f = square ? a.c : 1.f, ratio = square ? a.b / a.c : a.b;
     for (int k = 0; k < a.steps; ++k) {
-      const int in = k & 1;
+      const int cur = k & 1;
       const float* scale = k == 0 ? f32(p.scale) : nullptr;
       {
         TimedLaunch tl(timer, "ortho_gram", st);
-        hipLaunchKernelGGL(ortho_gram_kernel, dim3(grid_of(d.E * st_tiles)), dim3(256), 0, st, f16(p.X[in]), d,
+        hipLaunchKernelGGL(ortho_gram_kernel, dim3(grid_of(d.E * st_tiles)), dim3(256), 0, st, f16(p.X[cur]), d,
                            st_tiles, scale, f16(p.A));
       }
       {
@@ -875,15 +959,15 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
                            f32(p.diag));
       }
       const bool lo = k > 0 || lo0;
-      const uint8_t* xl = lo ? u8(p.Xl[in]) : nullptr;
+      const uint8_t* xl = lo ? u8(p.Xl[cur]) : nullptr;
       const float lo_inv = 1.f / (k == 0 ? kLoScale0 : kLoScale);
       const dim3 grid(grid_of(d.E * up_tiles));
       OrthoOut out{};
       TimedLaunch tl(timer, "ortho_update", st);
       if (k + 1 < a.steps) {
-        out.X = f16(p.X[1 - in]);
-        out.Xl = u8(p.Xl[1 - in]);
-        hipLaunchKernelGGL(ortho_update_kernel<false>, grid, dim3(256), 0, st, f16(p.X[in]), xl, lo_inv, f16(p.B),
+        out.X = f16(p.X[1 - cur]);
+        out.Xl = u8(p.Xl[1 - cur]);
+        hipLaunchKernelGGL(ortho_update_kernel<false>, grid, dim3(256), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
                            f32(p.diag), d, up_tiles, a.a, scale, out);
       } else {
         out.U = t.U ? t.U + e0 * count : nullptr;
@@ -891,7 +975,7 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
         out.master = t.master ? t.master + e0 * count : nullptr;
         out.keep = t.keep;
         out.step = t.step;
-        hipLaunchKernelGGL(ortho_update_kernel<true>, grid, dim3(256), 0, st, f16(p.X[in]), xl, lo_inv, f16(p.B),
+        hipLaunchKernelGGL(ortho_update_kernel<true>, grid, dim3(256), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
                            f32(p.diag), d, up_tiles, a.a, scale, out);
       }
     }
