@@ -47,27 +47,29 @@ constexpr float kLoScale0 = 16.f;
 
 // output tile of the products
 constexpr int kTM = 256;
-constexpr int kTN = 128;
+constexpr int kTN = 256;
+constexpr int kThreads = 512;  // 8 waves of 128 x 64, 2 x 4
 
 // The remainders are kept in the order in which the update's lanes hold a tile:
 // [tile][wave][sub-tile][lane][16 bytes], so they are read and written 16
 // bytes a lane.
 __device__ __forceinline__ int64_t lo_offset(int64_t tile, int wave, int sub, int lane) {
-  return (((tile * 4 + wave) * 8 + sub) * 64 + lane) * 16;
+  return (((tile * 8 + wave) * 8 + sub) * 64 + lane) * 16;
 }
 
-// X, A and B live in the workspace in blocks of 16 rows x 32 columns (1 KiB, 64
-// lanes of 16 bytes: one load of a wave), the row blocks of a column block one
-// after the other. Inside a block 16-byte chunk c of row r is at slot
-// c ^ ((r / 4) % 4), the order in which the blocks lie in LDS: rows read with
-// k along them (sixteen rows' reads of one chunk fall in sixteen slots of a
-// 256-byte bank window) as well as across them (the transpose read takes 32
-// bytes of four rows). Against row-major matrices, whose loads are 64-byte
-// pieces of 16 rows, the products take 13 to 25 % less time.
+// X, A and B live in the workspace in blocks of 32 rows x 16 columns (1 KiB), the
+// row blocks of a column block one after the other. A block is an MFMA fragment
+// in the order of its lanes: 16-byte chunk h (columns 8 h .. 8 h + 7) of row r
+// at slot 32 h + (r ^ 4 h). So a load of a wave moves a block into LDS as it
+// lies, a fragment with k along the rows is one linear LDS read, a store of a
+// 32 x 16 result is one linear 1 KiB, and the transpose read (two chunks of
+// four rows) finds its four rows of both chunks in different banks (the xor).
+// Row-major matrices (64-byte pieces of 16 rows a load) cost 13 to 25 % of the
+// products' time.
 constexpr int kBlock = 512;  // halves
-__device__ __forceinline__ int64_t block_at(int rows, int rb, int cb) { return (int64_t(cb) * (rows / 16) + rb) * kBlock; }
-// element (r, 8 c ..) inside a block
-__device__ __forceinline__ int in_block(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 3)) << 3); }
+__device__ __forceinline__ int64_t block_at(int rows, int rb, int cb) { return (int64_t(cb) * (rows / 32) + rb) * kBlock; }
+// element (r, 8 h ..) inside a block
+__device__ __forceinline__ int in_block(int r, int h) { return (32 * h + (r ^ (4 * h))) * 8; }
 
 struct OrthoDims {
   int64_t E;   // matrices of the group
@@ -194,11 +196,10 @@ __device__ __forceinline__ void matrix_scale(const double* __restrict__ part, fl
   if (!(norm < 1e300)) *s = NAN;
 }
 
-__device__ __forceinline__ uint32_t pack_halves(_Float16 a, _Float16 b) {
-  return uint32_t(__builtin_bit_cast(uint16_t, a)) | (uint32_t(__builtin_bit_cast(uint16_t, b)) << 16);
-}
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  return pack_halves(static_cast<_Float16>(a), static_cast<_Float16>(b));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {  // v_cvt_pk_f16_f32, nearest even
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
 // X0 and its remainder, 64 x 64 elements a workgroup, through LDS (transposed
@@ -243,14 +244,14 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int blk = 4 * q + int(threadIdx.x >> 6), lane = lane_id();  // 4 x 2 blocks
-    const int r = lane >> 2, c = (lane & 3) ^ ((r >> 2) & 3);
-    const float* src = &tile[16 * (blk & 3) + r][32 * (blk >> 2) + 8 * c];
+    const int blk = 4 * q + int(threadIdx.x >> 6), lane = lane_id();  // 2 x 4 blocks
+    const int h = lane >> 5, r = (lane & 31) ^ (4 * h);
+    const float* src = &tile[32 * (blk & 1) + r][16 * (blk >> 1) + 8 * h];
     u32x4 v;
 #pragma unroll
     for (int t = 0; t < 4; ++t) v[t] = pack_f16(src[2 * t], src[2 * t + 1]);
     *reinterpret_cast<u32x4*>(X + int64_t(e) * d.mp * d.np +
-                              block_at(d.mp, r0 / 16 + (blk & 3), c0 / 32 + (blk >> 2)) + 8 * lane) = v;
+                              block_at(d.mp, r0 / 32 + (blk & 1), c0 / 16 + (blk >> 1)) + 8 * lane) = v;
   }
   if (Xl) {
     // the 64 x 64 elements are half of a wave's part of an update tile: 2 x 2
@@ -269,27 +270,30 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d
       const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
       v[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true));
     }
-    const int nrow = (d.mp + kTM - 1) / kTM;
+    const int nrow = (d.mp + kTM - 1) / kTM, ncol = (d.np + kTN - 1) / kTN;
     const int64_t t = int64_t(c0 / kTN) * nrow + r0 / kTM;
-    const int wave = 2 * ((r0 / 128) & 1) + ((c0 / 64) & 1);
+    const int wave = 4 * ((r0 / 128) & 1) + ((c0 / 64) & 3);
     const int i = 2 * ((r0 / 64) & 1) + (sub >> 1);
-    *reinterpret_cast<u32x4*>(Xl + lo_offset(int64_t(e) * nrow * (d.np / kTN) + t, wave, 2 * i + (sub & 1), lane)) = v;
+    *reinterpret_cast<u32x4*>(Xl + lo_offset(int64_t(e) * nrow * ncol + t, wave, 2 * i + (sub & 1), lane)) = v;
   }
 }
 
 // ------------------------------------------------------------------ products
 //
-// Every product is C = P Q^T (or P Q) in tiles of 256 x 128, 4 waves of
-// 128 x 64 in a 2 x 2 grid, v_mfma_f32_32x32x16_f16 with fp32 accumulators. The
-// k-slabs of 32 go straight into LDS (buffer_load ... lds), three stages, so
-// the loads of two slabs are in flight while one is multiplied. A stage is
-// 24 KiB: two workgroups share a CU, and the loads, barriers and epilogue of
-// one run under the other's products.
-//   * k-major slab (P, and Q of the symmetric products): blocks of 16
-//     entities x 32 k, fragments with ds_read_b128.
-//   * mn-major slab (Q of the update): 32 k-rows x 128 columns in blocks of
-//     16 k-rows x 32 columns, read with the LDS transpose read
-//     ds_read_b64_tr_b16 (four consecutive k of one entity a lane).
+// Every product is C = P Q^T (or P Q) in tiles of 256 x 256, 8 waves of
+// 128 x 64 in a 2 x 4 grid (two a SIMD), v_mfma_f32_32x32x16_f16 with fp32
+// accumulators. The k-slabs of 32 go straight into LDS (buffer_load ... lds),
+// four stages of 32 KiB: while a slab is multiplied, the next two are on their
+// way and the loads of a third are issued. What bounds the loop is moving the
+// slabs into LDS (20 TB/s from L2 over the chip with no products at all), so
+// the tile is as large as the registers allow: 256 x 128 tiles, two workgroups
+// a CU, move half as much again per product and their epilogues did not
+// overlap the other workgroup's products.
+//   * k-major slab (P, and Q of the symmetric products): 8 blocks of 32
+//     entities for each 16 k, fragments with one ds_read_b128.
+//   * mn-major slab (Q of the update): 16 blocks of 32 k-rows x 16 columns,
+//     read with the LDS transpose read ds_read_b64_tr_b16 (four consecutive k
+//     of one entity a lane).
 // The MFMA's A operand is the Q fragment, so a lane holds one row m and four
 // runs of four consecutive columns n of each 32 x 32 sub-tile.
 // The stages are separate LDS objects, named at compile time, so that the
@@ -301,9 +305,10 @@ constexpr int kStage = (kTM + kTN) * kBK;      // halves of a stage
 __shared__ __attribute__((aligned(1024))) _Float16 g_s0[kStage];
 __shared__ __attribute__((aligned(1024))) _Float16 g_s1[kStage];
 __shared__ __attribute__((aligned(1024))) _Float16 g_s2[kStage];
+__shared__ __attribute__((aligned(1024))) _Float16 g_s3[kStage];
 template <int S>
 __device__ __forceinline__ _Float16* stage() {
-  return S == 0 ? g_s0 : S == 1 ? g_s1 : g_s2;
+  return S == 0 ? g_s0 : S == 1 ? g_s1 : S == 2 ? g_s2 : g_s3;
 }
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -315,15 +320,15 @@ struct Acc {
 };
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)); }
-__device__ __forceinline__ int wave_m() { return wave_id() >> 1; }
-__device__ __forceinline__ int wave_n() { return wave_id() & 1; }
+__device__ __forceinline__ int wave_m() { return wave_id() >> 2; }
+__device__ __forceinline__ int wave_n() { return wave_id() & 3; }
 
-// One operand of a product: load i of wave w moves block 4 i + w of a slab (N
-// loads: the slab has 4 N blocks). Reads past the matrix give zeros.
+// One operand of a product: load i (0, 1) of wave w moves block 8 i + w of a
+// slab's 16. Reads past the matrix give zeros.
 struct Operand {
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t blk;    // byte offset of block w of slab 0
-  uint32_t next;   // bytes from block 4 i + w to block 4 (i + 1) + w
+  uint32_t next;   // bytes from block w to block 8 + w
   uint32_t slab;   // bytes from one slab to the next
 };
 
@@ -331,48 +336,45 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const _Float16* base, 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(base), 0, int(uint32_t(halves * 2)), 0x00020000);
 }
 
-// Rows [e0, ...) of a matrix, k along its columns: block j is row block j.
+// Rows [e0, e0 + 256) of a matrix, k along its columns: block j is row block
+// j % 8 of column block j / 8.
 __device__ __forceinline__ Operand operand_k(const _Float16* base, int rows, int cols, int e0) {
   Operand o;
   o.rsrc = rsrc_of(base, int64_t(rows) * cols);
-  o.blk = uint32_t(block_at(rows, e0 / 16 + wave_id(), 0)) * 2u;
-  o.next = 4 * kBlock * 2;
-  o.slab = uint32_t(rows / 16) * kBlock * 2u;
+  o.blk = uint32_t(block_at(rows, e0 / 32 + wave_id(), 0)) * 2u;
+  o.next = uint32_t(rows / 32) * kBlock * 2u;
+  o.slab = uint32_t(rows / 32) * 2u * kBlock * 2u;
   return o;
 }
-// Columns [e0, e0 + 128) of a matrix, k along its rows: block j is row block
-// j % 2 of column block j / 2.
+// Columns [e0, e0 + 256) of a matrix, k along its rows: block j is column block j.
 __device__ __forceinline__ Operand operand_mn(const _Float16* base, int rows, int cols, int e0) {
   Operand o;
   o.rsrc = rsrc_of(base, int64_t(rows) * cols);
-  o.blk = uint32_t(block_at(rows, wave_id() & 1, e0 / 32 + (wave_id() >> 1))) * 2u;
-  o.next = uint32_t(rows / 16) * 2u * kBlock * 2u;
-  o.slab = 2 * kBlock * 2;
+  o.blk = uint32_t(block_at(rows, 0, e0 / 16 + wave_id())) * 2u;
+  o.next = uint32_t(rows / 32) * 8u * kBlock * 2u;
+  o.slab = kBlock * 2;
   return o;
 }
 
-template <int N>
-__device__ __forceinline__ void load_slab(const Operand& o, int kt, int nk, _Float16* lds) {
+__device__ __forceinline__ void load_slab(const Operand& o, int kt, _Float16* lds) {
   const int w = wave_id();
-  // a slab past the end gets an offset past every matrix (512 MiB at most)
-  const uint32_t off = uint32_t(lane_id()) * 16u + (kt < nk ? 0u : 0x80000000u);
+  const uint32_t off = uint32_t(lane_id()) * 16u;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int i = 0; i < 2; ++i)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(o.rsrc,
-                                             (__attribute__((address_space(3))) void*)(lds + (4 * i + w) * kBlock), 16,
+                                             (__attribute__((address_space(3))) void*)(lds + (8 * i + w) * kBlock), 16,
                                              off, int(o.blk + kt * o.slab + i * o.next), 0, 0);
 }
-// Slab kt of both operands; zeros for one past the end.
+// Slab kt of both operands; past the last one, the last one again.
 __device__ __forceinline__ void load_stage(const Operand& P, const Operand& Q, int kt, int nk, _Float16* lds) {
-  load_slab<4>(P, kt, nk, lds);
-  load_slab<2>(Q, kt, nk, lds + kSlabP);
+  kt = kt < nk ? kt : nk - 1;
+  load_slab(P, kt, lds);
+  load_slab(Q, kt, lds + kSlabP);
 }
 
 // 32 entities x 16 k of a k-major slab, from entity ent0 and k = 16 kk on.
 __device__ __forceinline__ f16x8 frag_k(const _Float16* lds, int ent0, int kk) {
-  const int e = ent0 + (lane_id() & 31);
-  const int c = (2 * kk + (lane_id() >> 5)) ^ ((e >> 2) & 3);
-  return *reinterpret_cast<const f16x8*>(lds + e * kBK + c * 8);
+  return *reinterpret_cast<const f16x8*>(lds + (kk * 8 + (ent0 >> 5)) * kBlock + in_block(lane_id() & 31, lane_id() >> 5));
 }
 // The same of an mn-major slab: in each 16-lane group the transpose read gives
 // lane p element p % 4 of the 8-byte pieces that lanes 4 j + p / 4 address. The
@@ -380,11 +382,11 @@ __device__ __forceinline__ f16x8 frag_k(const _Float16* lds, int ent0, int kk) {
 // which LDS object the read touches and waits for every load in flight.
 __device__ __forceinline__ f16x8 frag_mn(const _Float16* lds, int ent0, int kk) {
   const int g = lane_id() >> 4, p = lane_id() & 15;
-  const int n = 16 * (g & 1) + 4 * (p & 3);  // inside the 32 columns of a block
-  const int k = 8 * (g >> 1) + (p >> 2);     // k + 4 too is in the block's 16 rows
-  int lo = in_block(k, n >> 3) + (n & 7), hi = in_block(k + 4, n >> 3) + (n & 7);
+  const int k = 8 * (g >> 1) + (p >> 2);
+  const int at = (g & 1) * kBlock + 4 * (p & 1);  // 16 columns on, 4 columns on
+  int lo = at + in_block(k, (p & 3) >> 1), hi = at + in_block(k + 4, (p & 3) >> 1);
   asm("" : "+v"(lo), "+v"(hi));
-  const _Float16* a = lds + ((ent0 >> 5) * 2 + kk) * kBlock;
+  const _Float16* a = lds + (ent0 >> 4) * kBlock + kk * 16 * 8;
   const v4i16 l = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a + lo));
   const v4i16 h = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a + hi));
   return __builtin_bit_cast(f16x8, v8i16(__builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7)));
@@ -414,34 +416,37 @@ __device__ __forceinline__ void mma_slab(const _Float16* lds, Acc& acc) {
 // before it lets the others overwrite the stage).
 constexpr int wait_imm(int vm) { return 0x0070 | (vm & 15) | ((vm >> 4) << 14); }
 
-// Slab kt out of stage S, while slab kt + 1 is on its way and the loads of slab
-// kt + 2 go to the stage that slab kt - 1 has left. ACTIVE false: the wave
-// only moves data. `pass(kt, stage)` sees the slab while it is in LDS.
+// Slab kt out of stage S, while slabs kt + 1 and kt + 2 are on their way and the
+// loads of slab kt + 3 go to the stage that slab kt - 1 has left. ACTIVE
+// false: the wave only moves data. `pass(kt, stage)` sees the slab while it is
+// in LDS.
 template <int S, bool Q_MN, bool MMA, bool ACTIVE, class Pass>
 __device__ __forceinline__ void slab_step(const Operand& P, const Operand& Q, int kt, int nk, Acc& acc, Pass& pass) {
-  __builtin_amdgcn_s_waitcnt(wait_imm(6));
+  __builtin_amdgcn_s_waitcnt(wait_imm(8));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  load_stage(P, Q, kt + 2, nk, stage<(S + 2) % 3>());
+  load_stage(P, Q, kt + 3, nk, stage<(S + 3) % 4>());
   if constexpr (ACTIVE) {
     if constexpr (MMA) mma_slab<Q_MN>(stage<S>(), acc);
     pass(kt, stage<S>());
   }
 }
 
-// The k loop, three slabs a turn: one body and one exit (more exits made the
-// compiler keep copies of the accumulators), and no branch around the loads,
-// so that it counts them and waits for a slab's own loads only. Slabs past the
-// last one are zeros.
+// The k loop, four slabs a turn (nk is a multiple of four: matrices are padded
+// to 128): one body and one exit (more exits made the compiler keep copies of
+// the accumulators), and no branch around the loads, so that it counts them
+// and waits for a slab's own loads only.
 template <bool Q_MN, bool MMA, bool ACTIVE, class Pass>
 __device__ __forceinline__ void slabs(const Operand& P, const Operand& Q, int nk, Acc& acc, Pass& pass) {
   load_stage(P, Q, 0, nk, g_s0);
   load_stage(P, Q, 1, nk, g_s1);
-  for (int kt = 0; kt < nk; kt += 3) {
+  load_stage(P, Q, 2, nk, g_s2);
+  for (int kt = 0; kt < nk; kt += 4) {
     slab_step<0, Q_MN, MMA, ACTIVE>(P, Q, kt, nk, acc, pass);
     slab_step<1, Q_MN, MMA, ACTIVE>(P, Q, kt + 1, nk, acc, pass);
     slab_step<2, Q_MN, MMA, ACTIVE>(P, Q, kt + 2, nk, acc, pass);
+    slab_step<3, Q_MN, MMA, ACTIVE>(P, Q, kt + 3, nk, acc, pass);
   }
   __builtin_amdgcn_s_waitcnt(wait_imm(0));
   __syncthreads();  // the stages are free for the epilogue's images
@@ -480,7 +485,7 @@ __device__ __forceinline__ int tile_col(int j, int g) { return wave_n() * 64 + 3
 
 __device__ __forceinline__ uint16_t* image() {
   const int w = wave_id();
-  return reinterpret_cast<uint16_t*>(w < 2 ? g_s0 : g_s1) + (w & 1) * 4096;
+  return reinterpret_cast<uint16_t*>(w < 4 ? g_s0 : g_s1) + (w & 3) * 4096;
 }
 // four values of row r (0 .. 63), columns 4 q .. 4 q + 3
 __device__ __forceinline__ void image_put(uint16_t* im, int r, int q, uint32_t lo, uint32_t hi) {
@@ -504,25 +509,31 @@ __device__ __forceinline__ u32x4 image_col(const uint16_t* im, int r0, int n0) {
   const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(b));
   return __builtin_bit_cast(u32x4, v8i16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
 }
-// The image's 64 x 64 values to rows row0 .., columns col0 .. of a matrix of
-// blocks: 4 x 2 blocks of 1 KiB.
-__device__ __forceinline__ void put_blocks(const uint16_t* im, _Float16* __restrict__ out, int rows, int row0,
-                                           int col0) {
-  const int r = lane_id() >> 2, c = (lane_id() & 3) ^ ((r >> 2) & 3);
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    *reinterpret_cast<u32x4*>(out + block_at(rows, row0 / 16 + (q & 3), col0 / 32 + (q >> 2)) + 8 * lane_id()) =
-        image_row(im, 16 * (q & 3) + r, 4 * (q >> 2) + c);
-}
-// The same transposed: image column n is row col0 + n. Each 16-lane group takes
-// 16 columns (a row block), 8 image rows at a time (a chunk).
+// The image's 64 x 64 values transposed into a matrix of blocks: image column n
+// is row col0 + n, image row r column row0 + r. Lane n takes column n, 8 image
+// rows (a chunk) at a time.
 __device__ __forceinline__ void put_blocks_mirrored(const uint16_t* im, _Float16* __restrict__ out, int rows, int row0,
                                                     int col0) {
-  const int g = lane_id() >> 4, r = lane_id() & 15;
+  const int n = lane_id();
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const u32x4 v = image_col(im, 8 * q, 16 * g);
-    *reinterpret_cast<u32x4*>(out + block_at(rows, col0 / 16 + g, row0 / 32 + (q >> 2)) + in_block(r, q & 3)) = v;
+    const u32x4 v = image_col(im, 8 * q, 16 * (n >> 4));
+    *reinterpret_cast<u32x4*>(out + block_at(rows, col0 / 32 + (n >> 5), row0 / 16 + (q >> 1)) +
+                              in_block(n & 31, q & 1)) = v;
+  }
+}
+// A 32 x 32 sub-tile (rows row0 .., columns col0 ..) straight from the MFMA's
+// registers: w[g] holds the lane's row lane % 32, columns 8 g + 4 (lane / 32) ..
+// + 3. The swap of the upper half of one run with the lower half of the next
+// gives every lane a whole 16-byte chunk.
+__device__ __forceinline__ void put_subtile(const u32x2 (&w)[4], _Float16* __restrict__ out, int rows, int row0,
+                                            int col0) {
+  const int at = in_block(lane_id() & 31, lane_id() >> 5);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[2 * p][0], w[2 * p + 1][0], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[2 * p][1], w[2 * p + 1][1], false, false);
+    *reinterpret_cast<u32x4*>(out + block_at(rows, row0 / 32, col0 / 16 + p) + at) = u32x4{a[0], b[0], a[1], b[1]};
   }
 }
 // LDS writes of the wave are visible to its own reads
@@ -548,18 +559,23 @@ __device__ __forceinline__ bool take_tile(int64_t total, int tiles, int64_t* e, 
 }
 unsigned grid_of(int64_t total) { return unsigned((total + 7) / 8 * 8); }
 
-// The tiles of a symmetric product: 256 x 128, the blocks of 128 x 128 on and
-// below the diagonal. Row bi holds column tiles 0 .. 2 bi + 1.
+// The tiles of a symmetric product: 256 x 256 on and below the diagonal; of a
+// tile, the 128 x 128 blocks on and below it.
 int sym_tiles(int mp) {
-  const int nb = mp / 128, h = nb / 2;
-  return h * (h + 1) + (nb & 1 ? 2 * h + 1 : 0);
+  const int h = (mp + kTM - 1) / kTM;
+  return h * (h + 1) / 2;
 }
 __device__ __forceinline__ void sym_tile(int t, int* bi, int* bj) {
-  int b = int((sqrtf(4.f * float(t) + 1.f) - 1.f) * 0.5f);
-  while (b * (b + 1) > t) --b;
-  while ((b + 1) * (b + 2) <= t) ++b;
+  int b = int((sqrtf(8.f * float(t) + 1.f) - 1.f) * 0.5f);
+  while (b * (b + 1) / 2 > t) --b;
+  while ((b + 1) * (b + 2) / 2 <= t) ++b;
   *bi = b;
-  *bj = t - b * (b + 1);
+  *bj = t - b * (b + 1) / 2;
+}
+// Whether this wave's 128 x 64 are part of it.
+__device__ __forceinline__ bool sym_active(int bi, int bj, int mp) {
+  const int rb = 2 * bi + wave_m(), cb = 2 * bj + (wave_n() >> 1);
+  return rb * 128 < mp && cb <= rb;
 }
 
 struct NoPass {
@@ -571,7 +587,7 @@ struct NoPass {
 __device__ __forceinline__ void store_symmetric(const Acc& acc, float f, _Float16* __restrict__ out, int rows, int bi,
                                                 int bj, float* __restrict__ diag) {
   uint16_t* im = image();
-  const int rb = 2 * bi + wave_m();                 // 128-row block of this wave
+  const bool mirror = 2 * bi + wave_m() != 2 * bj + (wave_n() >> 1);  // blocks of 128
   const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
   const int lane = lane_id();
 #pragma unroll
@@ -579,33 +595,38 @@ __device__ __forceinline__ void store_symmetric(const Acc& acc, float f, _Float1
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii) {
       const int i = 2 * h + ii;
-      const int r = 32 * ii + (lane & 31);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        const f32x16& c = acc.c[i][j];
+        u32x2 w[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x16& c = acc.c[i][j];
-          image_put(im, r, 8 * j + 2 * g + (lane >> 5), pack_f16(c[4 * g] * f, c[4 * g + 1] * f),
-                    pack_f16(c[4 * g + 2] * f, c[4 * g + 3] * f));
-          if (diag) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-              if (row0 + 64 * h + r == col0 + 32 * j + 8 * g + 4 * (lane >> 5) + t) {
-                const float x = c[4 * g + t] * f;
-                diag[row0 + 64 * h + r] = x - float(static_cast<_Float16>(x));
-              }
-          }
+          w[g] = u32x2{pack_f16(c[4 * g] * f, c[4 * g + 1] * f), pack_f16(c[4 * g + 2] * f, c[4 * g + 3] * f)};
+          if (mirror) image_put(im, 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), w[g][0], w[g][1]);
         }
+        put_subtile(w, out, rows, row0 + 32 * i, col0 + 32 * j);
+        if (diag && !mirror && row0 + 32 * i == col0 + 32 * j) {
+          // register q of the lane is row lane % 32, column 8 (q / 4) + 4 (lane / 32) + q % 4
+          const int n = lane & 31;
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (n == 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) {
+              const float x = c[q] * f;
+              diag[row0 + 32 * i + n] = x - float(static_cast<_Float16>(x));
+            }
+        }
+      }
     }
-    image_sync();
-    put_blocks(im, out, rows, row0 + 64 * h, col0);
-    if (bj != rb) put_blocks_mirrored(im, out, rows, row0 + 64 * h, col0);
-    image_sync();
+    if (mirror) {
+      image_sync();
+      put_blocks_mirrored(im, out, rows, row0 + 64 * h, col0);
+      image_sync();
+    }
   }
 }
 
 // A = X X^T times the square of the iterate's scale.
-__global__ __launch_bounds__(256, 2) void ortho_gram_kernel(const _Float16* __restrict__ X, OrthoDims d, int tiles,
+__global__ __launch_bounds__(kThreads) void ortho_gram_kernel(const _Float16* __restrict__ X, OrthoDims d, int tiles,
                                                             const float* __restrict__ scale,
                                                             _Float16* __restrict__ A) {
   int64_t e;
@@ -613,8 +634,7 @@ __global__ __launch_bounds__(256, 2) void ortho_gram_kernel(const _Float16* __re
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
   sym_tile(t, &bi, &bj);
   const _Float16* Xe = X + e * d.mp * d.np;
-  const int rb = 2 * bi + wave_m();
-  const bool active = bj <= rb && rb * 128 < d.mp;
+  const bool active = sym_active(bi, bj, d.mp);
   Acc acc;
   NoPass pass;
   if (!product<false>(operand_k(Xe, d.mp, d.np, bi * kTM), operand_k(Xe, d.mp, d.np, bj * kTN), d.np / kBK, active, acc,
@@ -638,11 +658,10 @@ struct AddTile {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int r = tile_row(i);
-            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + r * kBK + ((g ^ ((r >> 2) & 3)) << 3) +
-                                                           4 * (lane_id() >> 5));
+            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + ((g >> 1) * 8 + wave_m() * 4 + i) * kBlock +
+                                                           in_block(lane_id() & 31, g & 1) + 4 * (lane_id() >> 5));
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] += ratio * float(v[t]);
+            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] = fmaf(float(v[t]), ratio, acc.c[i][j][4 * g + t]);
             __builtin_amdgcn_sched_barrier(0);  // few reads at a time: registers
           }
       }
@@ -652,7 +671,7 @@ struct AddTile {
 // B = b A + c A A = f (A A + ratio A) in fp16 (or, c negligible, f ratio A),
 // and what the rounding of its diagonal lost.
 template <bool MMA>
-__global__ __launch_bounds__(256, 2) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d, int tiles,
+__global__ __launch_bounds__(kThreads) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d, int tiles,
                                                               float f, float ratio, _Float16* __restrict__ B,
                                                               float* __restrict__ diag) {
   int64_t e;
@@ -660,8 +679,7 @@ __global__ __launch_bounds__(256, 2) void ortho_square_kernel(const _Float16* __
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
   sym_tile(t, &bi, &bj);
   const _Float16* Ae = A + e * d.mp * d.mp;
-  const int rb = 2 * bi + wave_m();
-  const bool active = bj <= rb && rb * 128 < d.mp;
+  const bool active = sym_active(bi, bj, d.mp);
   Acc acc;
   AddTile pass{(bj * kTN + wave_n() * 64) / kBK, ratio, acc};
   if (!product<false, MMA>(operand_k(Ae, d.mp, d.mp, bi * kTM), operand_k(Ae, d.mp, d.mp, bj * kTN), d.mp / kBK, active,
@@ -689,16 +707,14 @@ struct AddLinear {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (kt == kt0 + i) {
-        const int k = lane_id() & 31;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int n = tile_col(j, g);
-            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + kSlabP + ((n >> 5) * 2 + (k >> 4)) * kBlock +
-                                                           in_block(k & 15, (n >> 3) & 3) + (n & 7));
+            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + kSlabP + (wave_n() * 4 + 2 * j + (g >> 1)) * kBlock +
+                                                           in_block(lane_id() & 31, g & 1) + 4 * (lane_id() >> 5));
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] += lin[i] * float(v[t]);
+            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] = fmaf(float(v[t]), lin[i], acc.c[i][j][4 * g + t]);
           }
       }
   }
@@ -768,7 +784,7 @@ __device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, cons
 // as bf16; the step of the weights goes through LDS as fp16 (2^-12 of the
 // update, an eighth of what the products' roundings leave).
 template <bool LAST>
-__global__ __launch_bounds__(256, 2) void ortho_update_kernel(const _Float16* __restrict__ X,
+__global__ __launch_bounds__(kThreads) void ortho_update_kernel(const _Float16* __restrict__ X,
                                                               const uint8_t* __restrict__ Xl, float lo_inv,
                                                               const _Float16* __restrict__ B,
                                                               const float* __restrict__ diag, OrthoDims d, int tiles,
@@ -779,90 +795,90 @@ __global__ __launch_bounds__(256, 2) void ortho_update_kernel(const _Float16* __
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
   const int nrow = (d.mp + kTM - 1) / kTM;
   const int bi = t % nrow, bj = t / nrow;  // the row tiles of a column panel follow each other
-  const bool active = bi * kTM + wave_m() * 128 < d.mp;
+  const bool active = bi * kTM + wave_m() * 128 < d.mp && bj * kTN + wave_n() * 64 < d.np;
   const int64_t xo = e * d.mp * d.np;
   const int lane = lane_id();
   float lin[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) lin[i] = active ? ca + diag[e * d.mp + bi * kTM + tile_row(i)] : 0.f;
+  // the remainders, read ahead of the products
+  const int64_t ltile = e * tiles + t;
+  u32x4 lo[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    lo[q] = u32x4{0u, 0u, 0u, 0u};
+    if (Xl && active) lo[q] = *reinterpret_cast<const u32x4*>(Xl + lo_offset(ltile, wave_id(), q, lane));
+  }
   Acc acc;
   AddLinear pass{(bi * kTM + wave_m() * 128) / kBK, lin, acc};
   if (!product<true>(operand_k(B + e * d.mp * d.mp, d.mp, d.mp, bi * kTM), operand_mn(X + xo, d.mp, d.np, bj * kTN),
                      d.mp / kBK, active, acc, pass))
     return;
   const float s = scale ? scale[e] : 1.f / kXScale;  // takes a stored iterate to its value
-  uint16_t* im = image();
   const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
-  const int64_t ltile = e * tiles + t;
+  const float sz = s * kXScale;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii) {
       const int i = 2 * h + ii;
+      const float f = lin[i] * lo_inv;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        u32x4 lo = {0u, 0u, 0u, 0u}, nlo;
-        if (Xl) lo = *reinterpret_cast<const u32x4*>(Xl + lo_offset(ltile, wave_id(), 2 * i + j, lane));
+        u32x4 nlo;
+        u32x2 w[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           float y[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) y[q] = acc.c[i][j][4 * g + q];
-          if (Xl) {
-            const float f = lin[i] * lo_inv;
-            const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[g]), false);
-            const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[g]), true);
-            y[0] += f * a[0];
-            y[1] += f * a[1];
-            y[2] += f * b[0];
-            y[3] += f * b[1];
-          }
-          uint32_t p0, p1;
+          // no remainder: lo is zero, and so is what it adds
+          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[2 * i + j][g]), false);
+          const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[2 * i + j][g]), true);
+          y[0] = fmaf(f, a[0], acc.c[i][j][4 * g]);
+          y[1] = fmaf(f, a[1], acc.c[i][j][4 * g + 1]);
+          y[2] = fmaf(f, b[0], acc.c[i][j][4 * g + 2]);
+          y[3] = fmaf(f, b[1], acc.c[i][j][4 * g + 3]);
           if (!LAST) {
-            const float sz = s * kXScale;
             float r[4];
-            _Float16 hv[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float z = y[q] * sz;
-              hv[q] = static_cast<_Float16>(z);
-              r[q] = fminf(fmaxf((z - float(hv[q])) * kLoScale, -448.f), 448.f);
-            }
-            p0 = pack_halves(hv[0], hv[1]);
-            p1 = pack_halves(hv[2], hv[3]);
-            int w = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
-            nlo[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], w, true));
+            for (int q = 0; q < 4; ++q) y[q] *= sz;
+            w[g] = u32x2{pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              r[q] = __builtin_amdgcn_fmed3f((y[q] - half_of(w[g][q >> 1], q & 1)) * kLoScale, -448.f, 448.f);
+            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
+            nlo[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], v, true));
           } else if (out.U) {
-            p0 = pack_bf16x2(y[0] * s, y[1] * s);
-            p1 = pack_bf16x2(y[2] * s, y[3] * s);
+            w[g] = u32x2{pack_bf16x2(y[0] * s, y[1] * s), pack_bf16x2(y[2] * s, y[3] * s)};
           } else {
-            p0 = pack_f16(y[0] * s, y[1] * s);
-            p1 = pack_f16(y[2] * s, y[3] * s);
+            w[g] = u32x2{pack_f16(y[0] * s, y[1] * s), pack_f16(y[2] * s, y[3] * s)};
           }
-          image_put(im, 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), p0, p1);
         }
-        if (!LAST) *reinterpret_cast<u32x4*>(out.Xl + lo_offset(ltile, wave_id(), 2 * i + j, lane)) = nlo;
+        if constexpr (!LAST) {
+          put_subtile(w, out.X + xo, d.mp, row0 + 32 * i, col0 + 32 * j);
+          *reinterpret_cast<u32x4*>(out.Xl + lo_offset(ltile, wave_id(), 2 * i + j, lane)) = nlo;
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            image_put(image(), 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), w[g][0], w[g][1]);
+        }
       }
     }
-    image_sync();
-    if (!LAST) {
-      put_blocks(im, out.X + xo, d.mp, row0 + 64 * h, col0);
-    } else if (!d.tall) {
+    if constexpr (LAST) {
+      const uint16_t* im = image();
+      image_sync();
       for (int q = 0; q < 8; ++q) {
-        const int r = row0 + 64 * h + 8 * q + (lane >> 3), c = col0 + 8 * (lane & 7);
-        const u32x4 v = image_row(im, 8 * q + (lane >> 3), lane & 7);
-        if (r < d.m && c < d.n)
-          put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c, (d.C & 7) == 0);
+        if (!d.tall) {
+          const int r = row0 + 64 * h + 8 * q + (lane >> 3), c = col0 + 8 * (lane & 7);
+          const u32x4 v = image_row(im, 8 * q + (lane >> 3), lane & 7);
+          if (r < d.m && c < d.n) put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c, (d.C & 7) == 0);
+        } else {
+          const int r = row0 + 64 * h + 8 * q, c = col0 + lane;
+          const u32x4 v = image_col(im, 8 * q, 16 * (lane >> 4));
+          if (r < d.m && c < d.n) put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r, (d.C & 7) == 0);
+        }
       }
-    } else {
-      for (int q = 0; q < 8; ++q) {
-        const int r = row0 + 64 * h + 8 * q, c = col0 + lane;
-        const u32x4 v = image_col(im, 8 * q, 16 * (lane >> 4));
-        if (r < d.m && c < d.n)
-          put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r, (d.C & 7) == 0);
-      }
+      image_sync();
     }
-    image_sync();
   }
 }
 
@@ -887,7 +903,7 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   d.mp = (d.m + 127) / 128 * 128;
   d.np = (d.n + 127) / 128 * 128;
   const int64_t x = int64_t(d.mp) * d.np, q = int64_t(d.mp) * d.mp;
-  const int64_t xl = int64_t((d.mp + kTM - 1) / kTM * kTM) * d.np;  // whole tiles
+  const int64_t xl = int64_t((d.mp + kTM - 1) / kTM * kTM) * ((d.np + kTN - 1) / kTN * kTN);  // whole tiles
   // at most about 4 GiB of state
   const int64_t bytes = 6 * x + 4 * q;
   int64_t g = (int64_t(4) << 30) / bytes;
@@ -940,7 +956,7 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
                          a.eps, f16(p.X[0]), lo0 ? u8(p.Xl[0]) : nullptr, f32(p.scale));
     }
     const int st_tiles = sym_tiles(d.mp);
-    const int up_tiles = (d.mp + kTM - 1) / kTM * (d.np / kTN);
+    const int up_tiles = (d.mp + kTM - 1) / kTM * ((d.np + kTN - 1) / kTN);
     // B = f (A A + ratio A); a c below 2^-20 of b adds nothing that fp16 holds
     const bool square = std::fabs(a.c) > 1e-6f * std::fabs(a.b);
     const float f = square ? a.c : 1.f, ratio = square ? a.b / a.c : a.b;
@@ -949,13 +965,13 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
       const float* scale = k == 0 ? f32(p.scale) : nullptr;
       {
         TimedLaunch tl(timer, "ortho_gram", st);
-        hipLaunchKernelGGL(ortho_gram_kernel, dim3(grid_of(d.E * st_tiles)), dim3(256), 0, st, f16(p.X[cur]), d,
+        hipLaunchKernelGGL(ortho_gram_kernel, dim3(grid_of(d.E * st_tiles)), dim3(kThreads), 0, st, f16(p.X[cur]), d,
                            st_tiles, scale, f16(p.A));
       }
       {
         TimedLaunch tl(timer, "ortho_square", st);
         hipLaunchKernelGGL(square ? ortho_square_kernel<true> : ortho_square_kernel<false>,
-                           dim3(grid_of(d.E * st_tiles)), dim3(256), 0, st, f16(p.A), d, st_tiles, f, ratio, f16(p.B),
+                           dim3(grid_of(d.E * st_tiles)), dim3(kThreads), 0, st, f16(p.A), d, st_tiles, f, ratio, f16(p.B),
                            f32(p.diag));
       }
       const bool lo = k > 0 || lo0;
@@ -967,7 +983,7 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
       if (k + 1 < a.steps) {
         out.X = f16(p.X[1 - cur]);
         out.Xl = u8(p.Xl[1 - cur]);
-        hipLaunchKernelGGL(ortho_update_kernel<false>, grid, dim3(256), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
+        hipLaunchKernelGGL(ortho_update_kernel<false>, grid, dim3(kThreads), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
                            f32(p.diag), d, up_tiles, a.a, scale, out);
       } else {
         out.U = t.U ? t.U + e0 * count : nullptr;
@@ -975,7 +991,7 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
         out.master = t.master ? t.master + e0 * count : nullptr;
         out.keep = t.keep;
         out.step = t.step;
-        hipLaunchKernelGGL(ortho_update_kernel<true>, grid, dim3(256), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
+        hipLaunchKernelGGL(ortho_update_kernel<true>, grid, dim3(kThreads), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
                            f32(p.diag), d, up_tiles, a.a, scale, out);
       }
     }
