@@ -35,15 +35,14 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kNormThreads = 256;
-constexpr int kNormParts = 64;      // partial sums per matrix
+constexpr int kNormParts = 64;      // partial sums (and maxima) per matrix
 constexpr int kLoadTile = 64;
-// iterates after the first step are stored times 2^10 (so that rows far below
-// the norm keep their bits in fp16); their remainder times another 2^10
-constexpr float kXScale = 1024.f;
-constexpr float kLoScale = 1024.f;
-// X0 has a norm in [2^14, 2^15): a remainder is below 2^4
+// An iterate is stored times 2^15 (iterates stay below 2, fp16 ends at 65504),
+// X0 times the power of two that takes its largest element to [2^14, 2^15):
+// then the remainders need no scale of their own to lie in E4M3's range
+// (16 at most), and elements 2^-20 of the largest still have theirs.
+constexpr float kXScale = 32768.f;
 constexpr int kX0Exp = 14;
-constexpr float kLoScale0 = 16.f;
 
 // output tile of the products
 constexpr int kTM = 256;
@@ -133,15 +132,24 @@ __device__ __forceinline__ void input8(const OrthoIn& in, int64_t i, float (&x)[
   }
 }
 
-// Partial sums of squares, after the momentum step if there is one. HBM-bound:
-// 16-byte accesses where a matrix is a whole number of them.
+// What the norm pass leaves of a part of a matrix.
+struct NormPart {
+  double sum;  // of squares
+  float amax;  // largest magnitude
+  float pad;
+};
+
+// Partial sums of squares and maxima, after the momentum step if there is one.
+// HBM-bound: 16-byte accesses where a matrix is a whole number of them.
 __global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(OrthoIn in, int64_t count,
-                                                                  double* __restrict__ part) {
+                                                                  NormPart* __restrict__ part) {
   __shared__ double sm[kNormThreads / 64];
+  __shared__ float mx[kNormThreads / 64];
   const int64_t base = int64_t(blockIdx.y) * count;
   const int64_t first = int64_t(blockIdx.x) * kNormThreads + threadIdx.x;
   constexpr int64_t kStep = int64_t(kNormParts) * kNormThreads;
   double s = 0.0;
+  float m = 0.f;  // fmaxf drops a NaN; the sum keeps it
   if ((count & 7) == 0) {
 #pragma unroll 2
     for (int64_t i = first * 8; i < count; i += kStep * 8) {
@@ -161,39 +169,55 @@ __global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(OrthoIn in, in
         p[1] = b;
       }
 #pragma unroll
-      for (int t = 0; t < 8; ++t) s += double(x[t]) * double(x[t]);
+      for (int t = 0; t < 8; ++t) {
+        s += double(x[t]) * double(x[t]);
+        m = fmaxf(m, fabsf(x[t]));
+      }
     }
   } else {
     for (int64_t i = first; i < count; i += kStep) {
       float x = grad_at(in.grad, in.f32, base + i);
       if (in.mom) {
-        const float m = in.mu * in.mom[base + i] + x;
-        in.mom[base + i] = m;
-        x = in.nesterov ? x + in.mu * m : m;
+        const float v = in.mu * in.mom[base + i] + x;
+        in.mom[base + i] = v;
+        x = in.nesterov ? x + in.mu * v : v;
       }
       s += double(x) * double(x);
+      m = fmaxf(m, fabsf(x));
     }
   }
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
+  for (int o = 32; o > 0; o >>= 1) {
+    s += __shfl_xor(s, o);
+    m = fmaxf(m, __shfl_xor(m, o));
+  }
+  if ((threadIdx.x & 63) == 0) {
+    sm[threadIdx.x >> 6] = s;
+    mx[threadIdx.x >> 6] = m;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     s = 0.0;
-    for (int i = 0; i < kNormThreads / 64; ++i) s += sm[i];
-    part[int64_t(blockIdx.y) * kNormParts + blockIdx.x] = s;
+    for (int i = 0; i < kNormThreads / 64; ++i) {
+      s += sm[i];
+      m = fmaxf(m, mx[i]);
+    }
+    part[int64_t(blockIdx.y) * kNormParts + blockIdx.x] = NormPart{s, m, 0.f};
   }
 }
 
 // The exponent p of X0 = G 2^p, and s = 1 / ((|G| + eps) 2^p), in every lane.
 static_assert(kNormParts == 64, "a lane per partial sum");
-__device__ __forceinline__ void matrix_scale(const double* __restrict__ part, float eps, int* p, float* s) {
-  double q = part[lane_id()];
-  for (int o = 32; o > 0; o >>= 1) q += __shfl_xor(q, o);
+__device__ __forceinline__ void matrix_scale(const NormPart* __restrict__ part, float eps, int* p, float* s) {
+  double q = part[lane_id()].sum;
+  float m = part[lane_id()].amax;
+  for (int o = 32; o > 0; o >>= 1) {
+    q += __shfl_xor(q, o);
+    m = fmaxf(m, __shfl_xor(m, o));
+  }
   const double norm = sqrt(q);
-  const bool plain = norm > 0.0 && norm < 1e300;
-  *p = plain ? kX0Exp - ilogb(norm) : 0;
-  *s = norm == 0.0 ? 0.f : float(ldexp(1.0 / (norm + double(eps)), -*p));
-  if (!(norm < 1e300)) *s = NAN;
+  const bool finite = norm < 1e300;
+  *p = finite && m > 0.f ? kX0Exp - ilogbf(m) : 0;
+  *s = !finite ? NAN : norm == 0.0 ? 0.f : float(ldexp(1.0 / (norm + double(eps)), -*p));
 }
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -204,7 +228,7 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {  // v_cvt_pk_f1
 
 // X0 and its remainder, 64 x 64 elements a workgroup, through LDS (transposed
 // when G is tall). HBM-bound.
-__global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d, const double* __restrict__ part,
+__global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d, const NormPart* __restrict__ part,
                                                          float eps, _Float16* __restrict__ X,
                                                          uint8_t* __restrict__ Xl, float* __restrict__ scale) {
   __shared__ float tile[kLoadTile][kLoadTile + 1];
@@ -265,7 +289,7 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const float x = tile[r][32 * (sub & 1) + 8 * g + 4 * (lane >> 5) + t];
-        q[t] = fminf(fmaxf((x - float(static_cast<_Float16>(x))) * kLoScale0, -448.f), 448.f);
+        q[t] = x - float(static_cast<_Float16>(x));
       }
       const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
       v[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true));
@@ -318,6 +342,14 @@ typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 struct Acc {
   f32x16 c[4][2];
 };
+__device__ __forceinline__ void zero(Acc& acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc.c[i][j][r] = 0.f;
+}
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)); }
 __device__ __forceinline__ int wave_m() { return wave_id() >> 2; }
@@ -418,63 +450,70 @@ constexpr int wait_imm(int vm) { return 0x0070 | (vm & 15) | ((vm >> 4) << 14); 
 
 // Slab kt out of stage S, while slabs kt + 1 and kt + 2 are on their way and the
 // loads of slab kt + 3 go to the stage that slab kt - 1 has left. ACTIVE
-// false: the wave only moves data. `pass(kt, stage)` sees the slab while it is
-// in LDS.
-template <int S, bool Q_MN, bool MMA, bool ACTIVE, class Pass>
-__device__ __forceinline__ void slab_step(const Operand& P, const Operand& Q, int kt, int nk, Acc& acc, Pass& pass) {
+// false: the wave only moves data.
+template <int S, bool Q_MN, bool ACTIVE>
+__device__ __forceinline__ void slab_step(const Operand& P, const Operand& Q, int kt, int nk, Acc& acc) {
   __builtin_amdgcn_s_waitcnt(wait_imm(8));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   load_stage(P, Q, kt + 3, nk, stage<(S + 3) % 4>());
-  if constexpr (ACTIVE) {
-    if constexpr (MMA) mma_slab<Q_MN>(stage<S>(), acc);
-    pass(kt, stage<S>());
-  }
+  if constexpr (ACTIVE) mma_slab<Q_MN>(stage<S>(), acc);
 }
 
-// The k loop, four slabs a turn (nk is a multiple of four: matrices are padded
-// to 128): one body and one exit (more exits made the compiler keep copies of
-// the accumulators), and no branch around the loads, so that it counts them
-// and waits for a slab's own loads only.
-template <bool Q_MN, bool MMA, bool ACTIVE, class Pass>
-__device__ __forceinline__ void slabs(const Operand& P, const Operand& Q, int nk, Acc& acc, Pass& pass) {
+// The loads of the first three slabs; between them and slabs() a kernel reads
+// what its accumulators start from.
+__device__ __forceinline__ void first_slabs(const Operand& P, const Operand& Q, int nk) {
   load_stage(P, Q, 0, nk, g_s0);
   load_stage(P, Q, 1, nk, g_s1);
   load_stage(P, Q, 2, nk, g_s2);
-  for (int kt = 0; kt < nk; kt += 4) {
-    slab_step<0, Q_MN, MMA, ACTIVE>(P, Q, kt, nk, acc, pass);
-    slab_step<1, Q_MN, MMA, ACTIVE>(P, Q, kt + 1, nk, acc, pass);
-    slab_step<2, Q_MN, MMA, ACTIVE>(P, Q, kt + 2, nk, acc, pass);
-    slab_step<3, Q_MN, MMA, ACTIVE>(P, Q, kt + 3, nk, acc, pass);
+}
+
+// The k loop, four slabs a turn (nk is a multiple of four: matrices are padded
+// to 128): one body and no branch in it (more exits, or work on the
+// accumulators under a condition, made the compiler copy them), so that it
+// also counts the loads and waits for a slab's own only.
+template <bool Q_MN, bool ACTIVE>
+__device__ __forceinline__ void turns(const Operand& P, const Operand& Q, int from, int to, int nk, Acc& acc) {
+  for (int kt = from; kt < to; kt += 4) {
+    slab_step<0, Q_MN, ACTIVE>(P, Q, kt, nk, acc);
+    slab_step<1, Q_MN, ACTIVE>(P, Q, kt + 1, nk, acc);
+    slab_step<2, Q_MN, ACTIVE>(P, Q, kt + 2, nk, acc);
+    slab_step<3, Q_MN, ACTIVE>(P, Q, kt + 3, nk, acc);
   }
+}
+__device__ __forceinline__ void slabs_end() {
   __builtin_amdgcn_s_waitcnt(wait_imm(0));
   __syncthreads();  // the stages are free for the epilogue's images
 }
-
-// Returns false for a wave that is not `active` (uniform per wave): it has
-// only moved data.
-template <bool Q_MN, bool MMA = true, class Pass>
-__device__ __forceinline__ bool product(const Operand& P, const Operand& Q, int nk, bool active, Acc& acc,
-                                        Pass& pass) {
-  if (!active) {
-    slabs<Q_MN, MMA, false>(P, Q, nk, acc, pass);
-    return false;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc.c[i][j][r] = 0.f;
-  slabs<Q_MN, MMA, true>(P, Q, nk, acc, pass);
-  return true;
+template <bool Q_MN, bool ACTIVE>
+__device__ __forceinline__ void slabs(const Operand& P, const Operand& Q, int nk, Acc& acc) {
+  turns<Q_MN, ACTIVE>(P, Q, 0, nk, nk, acc);
+  slabs_end();
 }
 
 // Row and first of 4 columns, inside the tile, of registers 4g .. 4g+3 of
 // sub-tile (i, j).
 __device__ __forceinline__ int tile_row(int i) { return wave_m() * 128 + 32 * i + (lane_id() & 31); }
-__device__ __forceinline__ int tile_col(int j, int g) { return wave_n() * 64 + 32 * j + 8 * g + 4 * (lane_id() >> 5); }
+
+__device__ __forceinline__ float half_of(uint32_t w, int t) {
+  return float(__builtin_bit_cast(_Float16, uint16_t(t ? w >> 16 : w)));
+}
+
+// A 32 x 32 sub-tile of a matrix of blocks as the accumulators hold it: w[g]
+// the lane's four values of run g (the inverse of put_subtile's swap).
+__device__ __forceinline__ void get_subtile(const _Float16* __restrict__ src, int rows, int row0, int col0,
+                                            u32x2 (&w)[4]) {
+  const int at = in_block(lane_id() & 31, lane_id() >> 5);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(src + block_at(rows, row0 / 32, col0 / 16 + p) + at);
+    const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+    w[2 * p] = u32x2{a[0], b[0]};
+    w[2 * p + 1] = u32x2{a[1], b[1]};
+  }
+}
 
 // ------------------------------------------------------------------ images
 //
@@ -578,10 +617,6 @@ __device__ __forceinline__ bool sym_active(int bi, int bj, int mp) {
   return rb * 128 < mp && cb <= rb;
 }
 
-struct NoPass {
-  __device__ __forceinline__ void operator()(int, const _Float16*) const {}
-};
-
 // The blocks of a symmetric result, fp16, times f, and their mirror images.
 // diag (or NULL): what the rounding of the diagonal lost.
 __device__ __forceinline__ void store_symmetric(const Acc& acc, float f, _Float16* __restrict__ out, int rows, int bi,
@@ -635,56 +670,50 @@ __global__ __launch_bounds__(kThreads) void ortho_gram_kernel(const _Float16* __
   sym_tile(t, &bi, &bj);
   const _Float16* Xe = X + e * d.mp * d.np;
   const bool active = sym_active(bi, bj, d.mp);
+  const Operand P = operand_k(Xe, d.mp, d.np, bi * kTM), Q = operand_k(Xe, d.mp, d.np, bj * kTN);
+  const int nk = d.np / kBK;
   Acc acc;
-  NoPass pass;
-  if (!product<false>(operand_k(Xe, d.mp, d.np, bi * kTM), operand_k(Xe, d.mp, d.np, bj * kTN), d.np / kBK, active, acc,
-                      pass))
+  first_slabs(P, Q, nk);
+  if (!active) {
+    slabs<false, false>(P, Q, nk, acc);
     return;
+  }
+  zero(acc);
+  slabs<false, true>(P, Q, nk, acc);
   const float s = scale ? scale[e] : 1.f / kXScale;
   store_symmetric(acc, s * s, A + e * d.mp * d.mp, d.mp, bi, bj, nullptr);
 }
 
-// While the slab passes whose k are the columns of this wave's sub-tiles j, the
-// P rows hold the tile of A itself: acc += ratio A.
-struct AddTile {
-  int kt0;      // slab of the wave's sub-tile j = 0
-  float ratio;
-  Acc& acc;
-  __device__ __forceinline__ void operator()(int kt, const _Float16* lds) const {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (kt == kt0 + j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + ((g >> 1) * 8 + wave_m() * 4 + i) * kBlock +
-                                                           in_block(lane_id() & 31, g & 1) + 4 * (lane_id() >> 5));
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] = fmaf(float(v[t]), ratio, acc.c[i][j][4 * g + t]);
-            __builtin_amdgcn_sched_barrier(0);  // few reads at a time: registers
-          }
-      }
-  }
-};
-
-// B = b A + c A A = f (A A + ratio A) in fp16 (or, c negligible, f ratio A),
-// and what the rounding of its diagonal lost.
-template <bool MMA>
+// B = b A + c A A = f (A A + ratio A) in fp16 (or, c negligible, f ratio A: no
+// products), and what the rounding of its diagonal lost. The accumulators
+// start from ratio A.
 __global__ __launch_bounds__(kThreads) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d, int tiles,
-                                                              float f, float ratio, _Float16* __restrict__ B,
-                                                              float* __restrict__ diag) {
+                                                                bool products, float f, float ratio,
+                                                                _Float16* __restrict__ B, float* __restrict__ diag) {
   int64_t e;
   int t, bi, bj;
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
   sym_tile(t, &bi, &bj);
   const _Float16* Ae = A + e * d.mp * d.mp;
   const bool active = sym_active(bi, bj, d.mp);
+  const Operand P = operand_k(Ae, d.mp, d.mp, bi * kTM), Q = operand_k(Ae, d.mp, d.mp, bj * kTN);
+  const int nk = products ? d.mp / kBK : 0;
   Acc acc;
-  AddTile pass{(bj * kTN + wave_n() * 64) / kBK, ratio, acc};
-  if (!product<false, MMA>(operand_k(Ae, d.mp, d.mp, bi * kTM), operand_k(Ae, d.mp, d.mp, bj * kTN), d.mp / kBK, active,
-                           acc, pass))
+  if (products) first_slabs(P, Q, nk);
+  if (!active) {
+    slabs<false, false>(P, Q, nk, acc);
     return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x2 w[4];
+      get_subtile(Ae, d.mp, bi * kTM + wave_m() * 128 + 32 * i, bj * kTN + wave_n() * 64 + 32 * j, w);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc.c[i][j][q] = ratio * half_of(w[q >> 2][(q >> 1) & 1], q & 1);
+    }
+  slabs<false, true>(P, Q, nk, acc);
   store_symmetric(acc, f, B + e * d.mp * d.mp, d.mp, bi, bj, diag + e * d.mp);
 }
 
@@ -697,34 +726,7 @@ struct OrthoOut {
   float keep, step;  // W keep - step U
 };
 
-// While the slab passes whose k are the rows of this wave's sub-tiles i, the Q
-// rows hold the tile of X itself: acc += (a + diag) X.
-struct AddLinear {
-  int kt0;          // slab of the wave's sub-tile i = 0
-  const float* lin;  // a + diag of the lane's row in sub-tile i
-  Acc& acc;
-  __device__ __forceinline__ void operator()(int kt, const _Float16* lds) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (kt == kt0 + i) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f16x4 v = *reinterpret_cast<const f16x4*>(lds + kSlabP + (wave_n() * 4 + 2 * j + (g >> 1)) * kBlock +
-                                                           in_block(lane_id() & 31, g & 1) + 4 * (lane_id() >> 5));
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] = fmaf(float(v[t]), lin[i], acc.c[i][j][4 * g + t]);
-          }
-      }
-  }
-};
-
 __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
-__device__ __forceinline__ float half_of(uint32_t w, int t) {
-  return float(__builtin_bit_cast(_Float16, uint16_t(t ? w >> 16 : w)));
-}
-
 // Eight consecutive elements of the result at element `at` of matrix storage:
 // v holds bf16 values (U) or fp16 values (the step of W). Only `count` of
 // them exist; rows of whole 16-byte pieces (vec) go at once.
@@ -780,16 +782,34 @@ __device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, cons
   }
 }
 
-// X' = (a + diag) X + B X; the last step writes the result instead. U leaves
-// as bf16; the step of the weights goes through LDS as fp16 (2^-12 of the
+// The slab whose k are the rows of sub-tile row i holds, as Q, the sub-tiles of X
+// itself: acc += lin X.
+__device__ __forceinline__ void add_linear(const _Float16* lds, int i, float lin, Acc& acc) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f16x4 v = *reinterpret_cast<const f16x4*>(lds + kSlabP + (wave_n() * 4 + 2 * j + (g >> 1)) * kBlock +
+                                                     in_block(lane_id() & 31, g & 1) + 4 * (lane_id() >> 5));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] = fmaf(float(v[t]), lin, acc.c[i][j][4 * g + t]);
+    }
+}
+
+// X' = (a + diag) X + B X. The four slabs whose k are this wave's rows are a turn
+// of their own, in which X's fp16 part is taken for the linear term as it
+// passes (read again from memory it cost the update as much as it is long).
+// FIRST: X is X0, whose value is scale[e] times what is stored (and whose
+// remainder may be zero: Xl NULL). LAST: the result is written instead of X'. U leaves as
+// bf16; the step of the weights goes through LDS as fp16 (2^-12 of the
 // update, an eighth of what the products' roundings leave).
-template <bool LAST>
+template <bool FIRST, bool LAST>
 __global__ __launch_bounds__(kThreads) void ortho_update_kernel(const _Float16* __restrict__ X,
-                                                              const uint8_t* __restrict__ Xl, float lo_inv,
-                                                              const _Float16* __restrict__ B,
-                                                              const float* __restrict__ diag, OrthoDims d, int tiles,
-                                                              float ca, const float* __restrict__ scale,
-                                                              OrthoOut out) {
+                                                                const uint8_t* __restrict__ Xl,
+                                                                const _Float16* __restrict__ B,
+                                                                const float* __restrict__ diag, OrthoDims d, int tiles,
+                                                                float ca, const float* __restrict__ scale,
+                                                                OrthoOut out) {
   int64_t e;
   int t;
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
@@ -798,55 +818,65 @@ __global__ __launch_bounds__(kThreads) void ortho_update_kernel(const _Float16* 
   const bool active = bi * kTM + wave_m() * 128 < d.mp && bj * kTN + wave_n() * 64 < d.np;
   const int64_t xo = e * d.mp * d.np;
   const int lane = lane_id();
+  const int64_t ltile = e * tiles + t;
+  const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
+  const Operand P = operand_k(B + e * d.mp * d.mp, d.mp, d.mp, bi * kTM), Q = operand_mn(X + xo, d.mp, d.np, bj * kTN);
+  const int nk = d.mp / kBK;
   float lin[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) lin[i] = active ? ca + diag[e * d.mp + bi * kTM + tile_row(i)] : 0.f;
-  // the remainders, read ahead of the products
-  const int64_t ltile = e * tiles + t;
   u32x4 lo[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     lo[q] = u32x4{0u, 0u, 0u, 0u};
-    if (Xl && active) lo[q] = *reinterpret_cast<const u32x4*>(Xl + lo_offset(ltile, wave_id(), q, lane));
+    if (active && (!FIRST || Xl)) lo[q] = *reinterpret_cast<const u32x4*>(Xl + lo_offset(ltile, wave_id(), q, lane));
   }
   Acc acc;
-  AddLinear pass{(bi * kTM + wave_m() * 128) / kBK, lin, acc};
-  if (!product<true>(operand_k(B + e * d.mp * d.mp, d.mp, d.mp, bi * kTM), operand_mn(X + xo, d.mp, d.np, bj * kTN),
-                     d.mp / kBK, active, acc, pass))
+  first_slabs(P, Q, nk);
+  if (!active) {
+    slabs<true, false>(P, Q, nk, acc);
     return;
-  const float s = scale ? scale[e] : 1.f / kXScale;  // takes a stored iterate to its value
-  const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
-  const float sz = s * kXScale;
+  }
+  zero(acc);
+  const int own = row0 / kBK;
+  turns<true, true>(P, Q, 0, own, nk, acc);
+  slab_step<0, true, true>(P, Q, own, nk, acc);
+  add_linear(g_s0, 0, lin[0], acc);
+  slab_step<1, true, true>(P, Q, own + 1, nk, acc);
+  add_linear(g_s1, 1, lin[1], acc);
+  slab_step<2, true, true>(P, Q, own + 2, nk, acc);
+  add_linear(g_s2, 2, lin[2], acc);
+  slab_step<3, true, true>(P, Q, own + 3, nk, acc);
+  add_linear(g_s3, 3, lin[3], acc);
+  turns<true, true>(P, Q, own + 4, nk, nk, acc);
+  slabs_end();
+  const float s = FIRST ? scale[e] : 1.f / kXScale;  // takes a stored iterate to its value
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii) {
       const int i = 2 * h + ii;
-      const float f = lin[i] * lo_inv;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         u32x4 nlo;
         u32x2 w[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          float y[4];
-          // no remainder: lo is zero, and so is what it adds
           const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[2 * i + j][g]), false);
           const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[2 * i + j][g]), true);
-          y[0] = fmaf(f, a[0], acc.c[i][j][4 * g]);
-          y[1] = fmaf(f, a[1], acc.c[i][j][4 * g + 1]);
-          y[2] = fmaf(f, b[0], acc.c[i][j][4 * g + 2]);
-          y[3] = fmaf(f, b[1], acc.c[i][j][4 * g + 3]);
-          if (!LAST) {
-            float r[4];
+          float y[4] = {a[0], a[1], b[0], b[1]};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) y[q] *= sz;
+          for (int q = 0; q < 4; ++q) y[q] = fmaf(y[q], lin[i], acc.c[i][j][4 * g + q]);
+          if constexpr (!LAST) {
+            if constexpr (FIRST) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) y[q] *= s * kXScale;
+            }
             w[g] = u32x2{pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              r[q] = __builtin_amdgcn_fmed3f((y[q] - half_of(w[g][q >> 1], q & 1)) * kLoScale, -448.f, 448.f);
-            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
-            nlo[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], v, true));
+            for (int q = 0; q < 4; ++q) y[q] -= half_of(w[g][q >> 1], q & 1);
+            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+            nlo[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], v, true));
           } else if (out.U) {
             w[g] = u32x2{pack_bf16x2(y[0] * s, y[1] * s), pack_bf16x2(y[2] * s, y[3] * s)};
           } else {
@@ -912,7 +942,7 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   size_t o = 0;
   // The products read up to 128 rows past a matrix (as zeros: the buffer
   // resource ends with it); B is followed by X, each X by its remainders.
-  p.part = o;  o = up256(o + size_t(p.group) * kNormParts * 8);
+  p.part = o;  o = up256(o + size_t(p.group) * kNormParts * sizeof(NormPart));
   p.scale = o; o = up256(o + size_t(p.group) * 4);
   p.diag = o;  o = up256(o + size_t(p.group) * d.mp * 4);
   p.A = o;     o = up256(o + size_t(p.group) * q * 2);
@@ -936,7 +966,7 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
   auto f16 = [&](size_t o) { return reinterpret_cast<_Float16*>(base + o); };
   auto u8 = [&](size_t o) { return reinterpret_cast<uint8_t*>(base + o); };
   auto f32 = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
-  double* part = reinterpret_cast<double*>(base + p.part);
+  NormPart* part = reinterpret_cast<NormPart*>(base + p.part);
   const int64_t count = int64_t(a.R) * a.C;
   const size_t gsize = a.grad_f32 ? 4 : 2;
   for (int64_t e0 = 0; e0 < a.E; e0 += p.group) {
@@ -970,30 +1000,27 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
       }
       {
         TimedLaunch tl(timer, "ortho_square", st);
-        hipLaunchKernelGGL(square ? ortho_square_kernel<true> : ortho_square_kernel<false>,
-                           dim3(grid_of(d.E * st_tiles)), dim3(kThreads), 0, st, f16(p.A), d, st_tiles, f, ratio, f16(p.B),
-                           f32(p.diag));
+        hipLaunchKernelGGL(ortho_square_kernel, dim3(grid_of(d.E * st_tiles)), dim3(kThreads), 0, st, f16(p.A), d,
+                           st_tiles, square, f, ratio, f16(p.B), f32(p.diag));
       }
-      const bool lo = k > 0 || lo0;
-      const uint8_t* xl = lo ? u8(p.Xl[cur]) : nullptr;
-      const float lo_inv = 1.f / (k == 0 ? kLoScale0 : kLoScale);
-      const dim3 grid(grid_of(d.E * up_tiles));
+      const uint8_t* xl = k > 0 || lo0 ? u8(p.Xl[cur]) : nullptr;
+      const bool last = k + 1 == a.steps;
       OrthoOut out{};
-      TimedLaunch tl(timer, "ortho_update", st);
-      if (k + 1 < a.steps) {
+      if (!last) {
         out.X = f16(p.X[1 - cur]);
         out.Xl = u8(p.Xl[1 - cur]);
-        hipLaunchKernelGGL(ortho_update_kernel<false>, grid, dim3(kThreads), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
-                           f32(p.diag), d, up_tiles, a.a, scale, out);
       } else {
         out.U = t.U ? t.U + e0 * count : nullptr;
         out.W = t.W ? t.W + e0 * count : nullptr;
         out.master = t.master ? t.master + e0 * count : nullptr;
         out.keep = t.keep;
         out.step = t.step;
-        hipLaunchKernelGGL(ortho_update_kernel<true>, grid, dim3(kThreads), 0, st, f16(p.X[cur]), xl, lo_inv, f16(p.B),
-                           f32(p.diag), d, up_tiles, a.a, scale, out);
       }
+      TimedLaunch tl(timer, last ? "ortho_update_last" : "ortho_update", st);
+      const auto kernel = k == 0 ? (last ? ortho_update_kernel<true, true> : ortho_update_kernel<true, false>)
+                                 : (last ? ortho_update_kernel<false, true> : ortho_update_kernel<false, false>);
+      hipLaunchKernelGGL(kernel, dim3(grid_of(d.E * up_tiles)), dim3(kThreads), 0, st, f16(p.X[cur]), xl, f16(p.B),
+                         f32(p.diag), d, up_tiles, a.a, scale, out);
     }
   }
   return hipGetLastError();

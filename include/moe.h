@@ -430,8 +430,8 @@ moe_status moe_bwd(const moe_shape* s, const void* dy, const void* x, const int3
  * (about 15 significant bits) for the linear term, the products take its
  * fp16 part, A and B = b A + c A^2 in fp16 with fp32 accumulation, and the
  * rounding of B's diagonal is made good in fp32; norms are summed in 64
- * bits. Iterates must stay below 63 in magnitude (they stay below 1.3 with
- * the usual coefficients). A matrix of zeros gives zeros; a matrix with a
+ * bits. Elements of the iterates must stay below 2 in magnitude (with the usual
+ * coefficients they stay below 1.3); past it the matrix's result is NaN. A matrix of zeros gives zeros; a matrix with a
  * NaN or an infinity gives NaN throughout, and leaves the others as they are.
  *   grad_dtype   MOE_DT_BF16 or MOE_DT_F32: the type of G
  *   num_cus      as in moe_shape
