@@ -44,16 +44,11 @@ constexpr int kLoadTile = 64;
 constexpr float kXScale = 32768.f;
 constexpr int kX0Exp = 14;
 
-// output tile of the products
-constexpr int kTM = 256;
-constexpr int kTN = 256;
-constexpr int kThreads = 512;  // 8 waves of 128 x 64, 2 x 4
-
-// The remainders are kept in the order in which the update's lanes hold a tile:
-// [tile][wave][sub-tile][lane][16 bytes], so they are read and written 16
-// bytes a lane.
-__device__ __forceinline__ int64_t lo_offset(int64_t tile, int wave, int sub, int lane) {
-  return (((tile * 8 + wave) * 8 + sub) * 64 + lane) * 16;
+// The remainders are kept in the order in which the update's lanes hold 64 x 64
+// elements: [64 columns][64 rows][2 x 2 sub-tiles][lane][16 bytes], so they are
+// read and written 16 bytes a lane. r0, c0: multiples of 64.
+__device__ __forceinline__ int64_t lo_offset(int rows, int r0, int c0, int sub, int lane) {
+  return (((int64_t(c0 / 64) * (rows / 64) + r0 / 64) * 4 + sub) * 64 + lane) * 16;
 }
 
 // X, A and B live in the workspace in blocks of 32 rows x 16 columns (1 KiB), the
@@ -294,73 +289,98 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d
       const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
       v[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true));
     }
-    const int nrow = (d.mp + kTM - 1) / kTM, ncol = (d.np + kTN - 1) / kTN;
-    const int64_t t = int64_t(c0 / kTN) * nrow + r0 / kTM;
-    const int wave = 4 * ((r0 / 128) & 1) + ((c0 / 64) & 3);
-    const int i = 2 * ((r0 / 64) & 1) + (sub >> 1);
-    *reinterpret_cast<u32x4*>(Xl + lo_offset(int64_t(e) * nrow * ncol + t, wave, 2 * i + (sub & 1), lane)) = v;
+    *reinterpret_cast<u32x4*>(Xl + int64_t(e) * d.mp * d.np + lo_offset(d.mp, r0, c0, sub, lane)) = v;
   }
 }
 
 // ------------------------------------------------------------------ products
 //
-// Every product is C = P Q^T (or P Q) in tiles of 256 x 256, 8 waves of
-// 128 x 64 in a 2 x 4 grid (two a SIMD), v_mfma_f32_32x32x16_f16 with fp32
-// accumulators. The k-slabs of 32 go straight into LDS (buffer_load ... lds),
-// four stages of 32 KiB: while a slab is multiplied, the next two are on their
-// way and the loads of a third are issued. What bounds the loop is moving the
-// slabs into LDS (20 TB/s from L2 over the chip with no products at all), so
-// the tile is as large as the registers allow: 256 x 128 tiles, two workgroups
-// a CU, move half as much again per product and their epilogues did not
-// overlap the other workgroup's products.
-//   * k-major slab (P, and Q of the symmetric products): 8 blocks of 32
-//     entities for each 16 k, fragments with one ds_read_b128.
-//   * mn-major slab (Q of the update): 16 blocks of 32 k-rows x 16 columns,
-//     read with the LDS transpose read ds_read_b64_tr_b16 (four consecutive k
-//     of one entity a lane).
+// Every product is C = P Q^T (or P Q), v_mfma_f32_32x32x16_f16 with fp32
+// accumulators, in tiles of one of two shapes:
+//   Big    256 x 256, 8 waves of 128 x 64 in a 2 x 4 grid (two a SIMD), one
+//          workgroup a CU. What bounds its loop is moving the slabs into LDS
+//          (20 TB/s from L2 over the chip with no products at all), so the
+//          tile is as large as the registers allow: 256 x 128 tiles, two
+//          workgroups a CU, move half as much again per product, and their
+//          epilogues did not run under the other workgroup's products.
+//   Small  128 x 128, 4 waves of 64 x 64, two workgroups a CU, for stacks with
+//          too few big tiles to go round.
+// The k-slabs of 32 go straight into LDS (buffer_load ... lds), four stages:
+// while a slab is multiplied, the next two are on their way and the loads of a
+// third are issued.
+//   * k-major slab (P, and Q of the symmetric products): for each 16 k the
+//     blocks of the tile's rows, fragments with one ds_read_b128.
+//   * mn-major slab (Q of the update): blocks of 32 k-rows x 16 columns, read
+//     with the LDS transpose read ds_read_b64_tr_b16 (four consecutive k of
+//     one entity a lane).
 // The MFMA's A operand is the Q fragment, so a lane holds one row m and four
 // runs of four consecutive columns n of each 32 x 32 sub-tile.
 // The stages are separate LDS objects, named at compile time, so that the
 // compiler can tell a slab's reads from the loads in flight.
 
 constexpr int kBK = 32;
-constexpr int kSlabP = kTM * kBK;              // halves of the P part of a stage
-constexpr int kStage = (kTM + kTN) * kBK;      // halves of a stage
-__shared__ __attribute__((aligned(1024))) _Float16 g_s0[kStage];
-__shared__ __attribute__((aligned(1024))) _Float16 g_s1[kStage];
-__shared__ __attribute__((aligned(1024))) _Float16 g_s2[kStage];
-__shared__ __attribute__((aligned(1024))) _Float16 g_s3[kStage];
-template <int S>
-__device__ __forceinline__ _Float16* stage() {
-  return S == 0 ? g_s0 : S == 1 ? g_s1 : S == 2 ? g_s2 : g_s3;
-}
+
+// TI: 32-row sub-tiles of a wave (2 sub-tiles wide); WN: waves side by side.
+template <int TI_, int WN_>
+struct TileShape {
+  static constexpr int TI = TI_, WN = WN_;
+  static constexpr int kWaves = 2 * WN;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kRows = 64 * TI, kCols = 64 * WN;
+  static constexpr int kSlabP = kRows * kBK;             // halves of the P part of a stage
+  static constexpr int kStage = (kRows + kCols) * kBK;   // halves of a stage
+  // each operand's slab is 2 kWaves blocks: two loads a wave
+  static_assert(2 * TI == kWaves && 2 * WN == kWaves, "a wave per row block of either operand");
+
+  static __device__ __forceinline__ int wave_m();
+  static __device__ __forceinline__ int wave_n();
+  template <int S>
+  static __device__ __forceinline__ _Float16* stage() {
+    __shared__ __attribute__((aligned(1024))) _Float16 buf[kStage];
+    return buf;
+  }
+  // a wave's 8 KiB for the images of its results, in the stages once they are free
+  static __device__ __forceinline__ uint16_t* image();
+};
+using Big = TileShape<4, 4>;
+using Small = TileShape<2, 2>;
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef short v8i16 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 
-struct Acc {
-  f32x16 c[4][2];
-};
-__device__ __forceinline__ void zero(Acc& acc) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc.c[i][j][r] = 0.f;
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)); }
+template <int TI_, int WN_>
+__device__ __forceinline__ int TileShape<TI_, WN_>::wave_m() { return wave_id() / WN; }
+template <int TI_, int WN_>
+__device__ __forceinline__ int TileShape<TI_, WN_>::wave_n() { return wave_id() % WN; }
+template <int TI_, int WN_>
+__device__ __forceinline__ uint16_t* TileShape<TI_, WN_>::image() {
+  constexpr int kPerStage = kStage / 4096;
+  static_assert(kPerStage * 2 == kWaves, "two stages hold the images");
+  const int w = wave_id();
+  return reinterpret_cast<uint16_t*>(w < kPerStage ? stage<0>() : stage<1>()) + (w % kPerStage) * 4096;
 }
 
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)); }
-__device__ __forceinline__ int wave_m() { return wave_id() >> 2; }
-__device__ __forceinline__ int wave_n() { return wave_id() & 3; }
+template <class T>
+struct Acc {
+  f32x16 c[T::TI][2];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < T::TI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) c[i][j][r] = 0.f;
+  }
+};
 
-// One operand of a product: load i (0, 1) of wave w moves block 8 i + w of a
-// slab's 16. Reads past the matrix give zeros.
+// One operand of a product: load i (0, 1) of wave w moves block kWaves i + w of
+// a slab. Reads past the matrix give zeros.
 struct Operand {
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t blk;    // byte offset of block w of slab 0
-  uint32_t next;   // bytes from block w to block 8 + w
+  uint32_t next;   // bytes from block w to block kWaves + w
   uint32_t slab;   // bytes from one slab to the next
 };
 
@@ -368,8 +388,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const _Float16* base, 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(base), 0, int(uint32_t(halves * 2)), 0x00020000);
 }
 
-// Rows [e0, e0 + 256) of a matrix, k along its columns: block j is row block
-// j % 8 of column block j / 8.
+// Rows from e0 on, k along the columns: block j is row block j % kWaves of
+// column block j / kWaves.
 __device__ __forceinline__ Operand operand_k(const _Float16* base, int rows, int cols, int e0) {
   Operand o;
   o.rsrc = rsrc_of(base, int64_t(rows) * cols);
@@ -378,35 +398,40 @@ __device__ __forceinline__ Operand operand_k(const _Float16* base, int rows, int
   o.slab = uint32_t(rows / 32) * 2u * kBlock * 2u;
   return o;
 }
-// Columns [e0, e0 + 256) of a matrix, k along its rows: block j is column block j.
+// Columns from e0 on, k along the rows: block j is column block j.
+template <class T>
 __device__ __forceinline__ Operand operand_mn(const _Float16* base, int rows, int cols, int e0) {
   Operand o;
   o.rsrc = rsrc_of(base, int64_t(rows) * cols);
   o.blk = uint32_t(block_at(rows, 0, e0 / 16 + wave_id())) * 2u;
-  o.next = uint32_t(rows / 32) * 8u * kBlock * 2u;
+  o.next = uint32_t(rows / 32) * T::kWaves * kBlock * 2u;
   o.slab = kBlock * 2;
   return o;
 }
 
+template <class T>
 __device__ __forceinline__ void load_slab(const Operand& o, int kt, _Float16* lds) {
   const int w = wave_id();
   const uint32_t off = uint32_t(lane_id()) * 16u;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(o.rsrc,
-                                             (__attribute__((address_space(3))) void*)(lds + (8 * i + w) * kBlock), 16,
-                                             off, int(o.blk + kt * o.slab + i * o.next), 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        o.rsrc, (__attribute__((address_space(3))) void*)(lds + (T::kWaves * i + w) * kBlock), 16, off,
+        int(o.blk + kt * o.slab + i * o.next), 0, 0);
 }
 // Slab kt of both operands; past the last one, the last one again.
+template <class T>
 __device__ __forceinline__ void load_stage(const Operand& P, const Operand& Q, int kt, int nk, _Float16* lds) {
   kt = kt < nk ? kt : nk - 1;
-  load_slab(P, kt, lds);
-  load_slab(Q, kt, lds + kSlabP);
+  load_slab<T>(P, kt, lds);
+  load_slab<T>(Q, kt, lds + T::kSlabP);
 }
 
 // 32 entities x 16 k of a k-major slab, from entity ent0 and k = 16 kk on.
+template <class T>
 __device__ __forceinline__ f16x8 frag_k(const _Float16* lds, int ent0, int kk) {
-  return *reinterpret_cast<const f16x8*>(lds + (kk * 8 + (ent0 >> 5)) * kBlock + in_block(lane_id() & 31, lane_id() >> 5));
+  return *reinterpret_cast<const f16x8*>(lds + (kk * T::kWaves + (ent0 >> 5)) * kBlock +
+                                         in_block(lane_id() & 31, lane_id() >> 5));
 }
 // The same of an mn-major slab: in each 16-lane group the transpose read gives
 // lane p element p % 4 of the 8-byte pieces that lanes 4 j + p / 4 address. The
@@ -424,20 +449,22 @@ __device__ __forceinline__ f16x8 frag_mn(const _Float16* lds, int ent0, int kk) 
   return __builtin_bit_cast(f16x8, v8i16(__builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7)));
 }
 
-template <bool Q_MN>
-__device__ __forceinline__ void mma_slab(const _Float16* lds, Acc& acc) {
+template <class T, bool Q_MN>
+__device__ __forceinline__ void mma_slab(const _Float16* lds, Acc<T>& acc) {
   __builtin_amdgcn_iglp_opt(0);
-  const int pm = wave_m() * 128, qn = wave_n() * 64;
+  const int pm = T::wave_m() * 32 * T::TI, qn = T::wave_n() * 64;
 #pragma unroll
   for (int kk = 0; kk < kBK / 16; ++kk) {
-    f16x8 pf[4], qf[2];
+    f16x8 pf[T::TI], qf[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      qf[j] = Q_MN ? frag_mn(lds + kSlabP, qn + 32 * j, kk) : frag_k(lds + kSlabP, qn + 32 * j, kk);
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (Q_MN) qf[j] = frag_mn(lds + T::kSlabP, qn + 32 * j, kk);
+      else qf[j] = frag_k<T>(lds + T::kSlabP, qn + 32 * j, kk);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pf[i] = frag_k(lds, pm + 32 * i, kk);
+    for (int i = 0; i < T::TI; ++i) pf[i] = frag_k<T>(lds, pm + 32 * i, kk);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < T::TI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         acc.c[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[j], pf[i], acc.c[i][j], 0, 0, 0);
@@ -451,57 +478,55 @@ constexpr int wait_imm(int vm) { return 0x0070 | (vm & 15) | ((vm >> 4) << 14); 
 // Slab kt out of stage S, while slabs kt + 1 and kt + 2 are on their way and the
 // loads of slab kt + 3 go to the stage that slab kt - 1 has left. ACTIVE
 // false: the wave only moves data.
-template <int S, bool Q_MN, bool ACTIVE>
-__device__ __forceinline__ void slab_step(const Operand& P, const Operand& Q, int kt, int nk, Acc& acc) {
-  __builtin_amdgcn_s_waitcnt(wait_imm(8));
+template <class T, int S, bool Q_MN, bool ACTIVE>
+__device__ __forceinline__ void slab_step(const Operand& P, const Operand& Q, int kt, int nk, Acc<T>& acc) {
+  __builtin_amdgcn_s_waitcnt(wait_imm(8));  // four loads a slab
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  load_stage(P, Q, kt + 3, nk, stage<(S + 3) % 4>());
-  if constexpr (ACTIVE) mma_slab<Q_MN>(stage<S>(), acc);
+  load_stage<T>(P, Q, kt + 3, nk, T::template stage<(S + 3) % 4>());
+  if constexpr (ACTIVE) mma_slab<T, Q_MN>(T::template stage<S>(), acc);
 }
 
-// The loads of the first three slabs; between them and slabs() a kernel reads
-// what its accumulators start from.
+// The loads of the first three slabs.
+template <class T>
 __device__ __forceinline__ void first_slabs(const Operand& P, const Operand& Q, int nk) {
-  load_stage(P, Q, 0, nk, g_s0);
-  load_stage(P, Q, 1, nk, g_s1);
-  load_stage(P, Q, 2, nk, g_s2);
+  load_stage<T>(P, Q, 0, nk, T::template stage<0>());
+  load_stage<T>(P, Q, 1, nk, T::template stage<1>());
+  load_stage<T>(P, Q, 2, nk, T::template stage<2>());
 }
 
 // The k loop, four slabs a turn (nk is a multiple of four: matrices are padded
 // to 128): one body and no branch in it (more exits, or work on the
 // accumulators under a condition, made the compiler copy them), so that it
 // also counts the loads and waits for a slab's own only.
-template <bool Q_MN, bool ACTIVE>
-__device__ __forceinline__ void turns(const Operand& P, const Operand& Q, int from, int to, int nk, Acc& acc) {
+template <class T, bool Q_MN, bool ACTIVE>
+__device__ __forceinline__ void turns(const Operand& P, const Operand& Q, int from, int to, int nk, Acc<T>& acc) {
   for (int kt = from; kt < to; kt += 4) {
-    slab_step<0, Q_MN, ACTIVE>(P, Q, kt, nk, acc);
-    slab_step<1, Q_MN, ACTIVE>(P, Q, kt + 1, nk, acc);
-    slab_step<2, Q_MN, ACTIVE>(P, Q, kt + 2, nk, acc);
-    slab_step<3, Q_MN, ACTIVE>(P, Q, kt + 3, nk, acc);
+    slab_step<T, 0, Q_MN, ACTIVE>(P, Q, kt, nk, acc);
+    slab_step<T, 1, Q_MN, ACTIVE>(P, Q, kt + 1, nk, acc);
+    slab_step<T, 2, Q_MN, ACTIVE>(P, Q, kt + 2, nk, acc);
+    slab_step<T, 3, Q_MN, ACTIVE>(P, Q, kt + 3, nk, acc);
   }
 }
 __device__ __forceinline__ void slabs_end() {
   __builtin_amdgcn_s_waitcnt(wait_imm(0));
   __syncthreads();  // the stages are free for the epilogue's images
 }
-template <bool Q_MN, bool ACTIVE>
-__device__ __forceinline__ void slabs(const Operand& P, const Operand& Q, int nk, Acc& acc) {
-  turns<Q_MN, ACTIVE>(P, Q, 0, nk, nk, acc);
+template <class T, bool Q_MN, bool ACTIVE>
+__device__ __forceinline__ void slabs(const Operand& P, const Operand& Q, int nk, Acc<T>& acc) {
+  turns<T, Q_MN, ACTIVE>(P, Q, 0, nk, nk, acc);
   slabs_end();
 }
-
-// Row and first of 4 columns, inside the tile, of registers 4g .. 4g+3 of
-// sub-tile (i, j).
-__device__ __forceinline__ int tile_row(int i) { return wave_m() * 128 + 32 * i + (lane_id() & 31); }
 
 __device__ __forceinline__ float half_of(uint32_t w, int t) {
   return float(__builtin_bit_cast(_Float16, uint16_t(t ? w >> 16 : w)));
 }
 
 // A 32 x 32 sub-tile of a matrix of blocks as the accumulators hold it: w[g]
-// the lane's four values of run g (the inverse of put_subtile's swap).
+// the lane's four values of run g (row lane % 32, columns 8 g + 4 (lane / 32) ..
+// + 3). The swap of the upper half of one register with the lower half of
+// another turns whole 16-byte chunks into runs, and back in put_subtile.
 __device__ __forceinline__ void get_subtile(const _Float16* __restrict__ src, int rows, int row0, int col0,
                                             u32x2 (&w)[4]) {
   const int at = in_block(lane_id() & 31, lane_id() >> 5);
@@ -514,18 +539,25 @@ __device__ __forceinline__ void get_subtile(const _Float16* __restrict__ src, in
     w[2 * p + 1] = u32x2{a[1], b[1]};
   }
 }
+__device__ __forceinline__ void put_subtile(const u32x2 (&w)[4], _Float16* __restrict__ out, int rows, int row0,
+                                            int col0) {
+  const int at = in_block(lane_id() & 31, lane_id() >> 5);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[2 * p][0], w[2 * p + 1][0], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[2 * p][1], w[2 * p + 1][1], false, false);
+    *reinterpret_cast<u32x4*>(out + block_at(rows, row0 / 32, col0 / 16 + p) + at) = u32x4{a[0], b[0], a[1], b[1]};
+  }
+}
 
 // ------------------------------------------------------------------ images
 //
-// A wave writes its results through LDS, 64 rows x 64 columns of 16-bit values
-// at a time (8 KiB of its own: no barrier): 16-byte chunk c of row r at
-// c ^ ((r / 2) % 8). Rows come out as 16-byte pieces, columns (the mirrored
-// half of a symmetric product, a tall matrix) through the transpose read.
+// What has to leave in another order than the registers' (the mirrored half of
+// a symmetric product, the caller's row-major result) goes through LDS, 64
+// rows x 64 columns of 16-bit values of a wave at a time (8 KiB of its own: no
+// barrier): 16-byte chunk c of row r at c ^ ((r / 2) % 8). Rows come out as
+// 16-byte pieces, columns through the transpose read.
 
-__device__ __forceinline__ uint16_t* image() {
-  const int w = wave_id();
-  return reinterpret_cast<uint16_t*>(w < 4 ? g_s0 : g_s1) + (w & 3) * 4096;
-}
 // four values of row r (0 .. 63), columns 4 q .. 4 q + 3
 __device__ __forceinline__ void image_put(uint16_t* im, int r, int q, uint32_t lo, uint32_t hi) {
   u32x2 v = {lo, hi};
@@ -536,8 +568,8 @@ __device__ __forceinline__ u32x4 image_row(const uint16_t* im, int r, int c) {
   return *reinterpret_cast<const u32x4*>(im + r * 64 + ((c ^ ((r >> 1) & 7)) << 3));
 }
 // Every lane: eight values of one column, rows r0 .. r0 + 7, for the 16
-// columns from n0 on (column n0 + lane % 16; r0 may differ from one 16-lane
-// group to another).
+// columns from n0 on (column n0 + lane % 16; r0 and n0 may differ from one
+// 16-lane group to another).
 __device__ __forceinline__ u32x4 image_col(const uint16_t* im, int r0, int n0) {
   const int p = lane_id() & 15;
   const int r = r0 + (p >> 2), n = n0 + 4 * (p & 3);
@@ -559,20 +591,6 @@ __device__ __forceinline__ void put_blocks_mirrored(const uint16_t* im, _Float16
     const u32x4 v = image_col(im, 8 * q, 16 * (n >> 4));
     *reinterpret_cast<u32x4*>(out + block_at(rows, col0 / 32 + (n >> 5), row0 / 16 + (q >> 1)) +
                               in_block(n & 31, q & 1)) = v;
-  }
-}
-// A 32 x 32 sub-tile (rows row0 .., columns col0 ..) straight from the MFMA's
-// registers: w[g] holds the lane's row lane % 32, columns 8 g + 4 (lane / 32) ..
-// + 3. The swap of the upper half of one run with the lower half of the next
-// gives every lane a whole 16-byte chunk.
-__device__ __forceinline__ void put_subtile(const u32x2 (&w)[4], _Float16* __restrict__ out, int rows, int row0,
-                                            int col0) {
-  const int at = in_block(lane_id() & 31, lane_id() >> 5);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const auto a = __builtin_amdgcn_permlane32_swap(w[2 * p][0], w[2 * p + 1][0], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(w[2 * p][1], w[2 * p + 1][1], false, false);
-    *reinterpret_cast<u32x4*>(out + block_at(rows, row0 / 32, col0 / 16 + p) + at) = u32x4{a[0], b[0], a[1], b[1]};
   }
 }
 // LDS writes of the wave are visible to its own reads
@@ -598,10 +616,10 @@ __device__ __forceinline__ bool take_tile(int64_t total, int tiles, int64_t* e, 
 }
 unsigned grid_of(int64_t total) { return unsigned((total + 7) / 8 * 8); }
 
-// The tiles of a symmetric product: 256 x 256 on and below the diagonal; of a
+// The tiles of a symmetric product: those on and below the diagonal; of a
 // tile, the 128 x 128 blocks on and below it.
-int sym_tiles(int mp) {
-  const int h = (mp + kTM - 1) / kTM;
+int sym_tiles(int mp, int rows) {
+  const int h = (mp + rows - 1) / rows;
   return h * (h + 1) / 2;
 }
 __device__ __forceinline__ void sym_tile(int t, int* bi, int* bj) {
@@ -611,22 +629,25 @@ __device__ __forceinline__ void sym_tile(int t, int* bi, int* bj) {
   *bi = b;
   *bj = t - b * (b + 1) / 2;
 }
-// Whether this wave's 128 x 64 are part of it.
-__device__ __forceinline__ bool sym_active(int bi, int bj, int mp) {
-  const int rb = 2 * bi + wave_m(), cb = 2 * bj + (wave_n() >> 1);
-  return rb * 128 < mp && cb <= rb;
-}
+
+// A wave's part of tile (bi, bj).
+template <class T>
+struct WavePart {
+  int row0, col0;
+  __device__ __forceinline__ WavePart(int bi, int bj)
+      : row0(bi * T::kRows + T::wave_m() * 32 * T::TI), col0(bj * T::kCols + T::wave_n() * 64) {}
+};
 
 // The blocks of a symmetric result, fp16, times f, and their mirror images.
 // diag (or NULL): what the rounding of the diagonal lost.
-__device__ __forceinline__ void store_symmetric(const Acc& acc, float f, _Float16* __restrict__ out, int rows, int bi,
-                                                int bj, float* __restrict__ diag) {
-  uint16_t* im = image();
-  const bool mirror = 2 * bi + wave_m() != 2 * bj + (wave_n() >> 1);  // blocks of 128
-  const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
+template <class T>
+__device__ __forceinline__ void store_symmetric(const Acc<T>& acc, float f, _Float16* __restrict__ out, int rows,
+                                                WavePart<T> at, float* __restrict__ diag) {
+  uint16_t* im = T::image();
+  const bool mirror = at.row0 / 128 != at.col0 / 128;
   const int lane = lane_id();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < T::TI / 2; ++h) {
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii) {
       const int i = 2 * h + ii;
@@ -639,82 +660,85 @@ __device__ __forceinline__ void store_symmetric(const Acc& acc, float f, _Float1
           w[g] = u32x2{pack_f16(c[4 * g] * f, c[4 * g + 1] * f), pack_f16(c[4 * g + 2] * f, c[4 * g + 3] * f)};
           if (mirror) image_put(im, 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), w[g][0], w[g][1]);
         }
-        put_subtile(w, out, rows, row0 + 32 * i, col0 + 32 * j);
-        if (diag && !mirror && row0 + 32 * i == col0 + 32 * j) {
+        put_subtile(w, out, rows, at.row0 + 32 * i, at.col0 + 32 * j);
+        if (diag && at.row0 + 32 * i == at.col0 + 32 * j) {
           // register q of the lane is row lane % 32, column 8 (q / 4) + 4 (lane / 32) + q % 4
           const int n = lane & 31;
 #pragma unroll
           for (int q = 0; q < 16; ++q)
             if (n == 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) {
               const float x = c[q] * f;
-              diag[row0 + 32 * i + n] = x - float(static_cast<_Float16>(x));
+              diag[at.row0 + 32 * i + n] = x - float(static_cast<_Float16>(x));
             }
         }
       }
     }
     if (mirror) {
       image_sync();
-      put_blocks_mirrored(im, out, rows, row0 + 64 * h, col0);
+      put_blocks_mirrored(im, out, rows, at.row0 + 64 * h, at.col0);
       image_sync();
     }
   }
 }
 
 // A = X X^T times the square of the iterate's scale.
-__global__ __launch_bounds__(kThreads) void ortho_gram_kernel(const _Float16* __restrict__ X, OrthoDims d, int tiles,
-                                                            const float* __restrict__ scale,
-                                                            _Float16* __restrict__ A) {
+template <class T>
+__global__ __launch_bounds__(T::kThreads, 2) void ortho_gram_kernel(const _Float16* __restrict__ X, OrthoDims d,
+                                                                    int tiles, const float* __restrict__ scale,
+                                                                    _Float16* __restrict__ A) {
   int64_t e;
   int t, bi, bj;
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
   sym_tile(t, &bi, &bj);
   const _Float16* Xe = X + e * d.mp * d.np;
-  const bool active = sym_active(bi, bj, d.mp);
-  const Operand P = operand_k(Xe, d.mp, d.np, bi * kTM), Q = operand_k(Xe, d.mp, d.np, bj * kTN);
+  const WavePart<T> at(bi, bj);
+  const Operand P = operand_k(Xe, d.mp, d.np, bi * T::kRows), Q = operand_k(Xe, d.mp, d.np, bj * T::kCols);
   const int nk = d.np / kBK;
-  Acc acc;
-  first_slabs(P, Q, nk);
-  if (!active) {
-    slabs<false, false>(P, Q, nk, acc);
+  Acc<T> acc;
+  first_slabs<T>(P, Q, nk);
+  if (at.row0 >= d.mp || at.col0 / 128 > at.row0 / 128) {
+    slabs<T, false, false>(P, Q, nk, acc);
     return;
   }
-  zero(acc);
-  slabs<false, true>(P, Q, nk, acc);
+  acc.zero();
+  slabs<T, false, true>(P, Q, nk, acc);
   const float s = scale ? scale[e] : 1.f / kXScale;
-  store_symmetric(acc, s * s, A + e * d.mp * d.mp, d.mp, bi, bj, nullptr);
+  store_symmetric<T>(acc, s * s, A + e * d.mp * d.mp, d.mp, at, nullptr);
 }
 
 // B = b A + c A A = f (A A + ratio A) in fp16 (or, c negligible, f ratio A: no
 // products), and what the rounding of its diagonal lost. The accumulators
 // start from ratio A.
-__global__ __launch_bounds__(kThreads) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d, int tiles,
-                                                                bool products, float f, float ratio,
-                                                                _Float16* __restrict__ B, float* __restrict__ diag) {
+template <class T>
+__global__ __launch_bounds__(T::kThreads, 2) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d,
+                                                                      int tiles, bool products, float f, float ratio,
+                                                                      _Float16* __restrict__ B,
+                                                                      float* __restrict__ diag) {
   int64_t e;
   int t, bi, bj;
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
   sym_tile(t, &bi, &bj);
   const _Float16* Ae = A + e * d.mp * d.mp;
-  const bool active = sym_active(bi, bj, d.mp);
-  const Operand P = operand_k(Ae, d.mp, d.mp, bi * kTM), Q = operand_k(Ae, d.mp, d.mp, bj * kTN);
+  const WavePart<T> at(bi, bj);
+  const Operand P = operand_k(Ae, d.mp, d.mp, bi * T::kRows), Q = operand_k(Ae, d.mp, d.mp, bj * T::kCols);
   const int nk = products ? d.mp / kBK : 0;
-  Acc acc;
-  if (products) first_slabs(P, Q, nk);
-  if (!active) {
-    slabs<false, false>(P, Q, nk, acc);
+  Acc<T> acc;
+  if (products) first_slabs<T>(P, Q, nk);
+  if (at.row0 >= d.mp || at.col0 / 128 > at.row0 / 128) {
+    slabs<T, false, false>(P, Q, nk, acc);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < T::TI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       u32x2 w[4];
-      get_subtile(Ae, d.mp, bi * kTM + wave_m() * 128 + 32 * i, bj * kTN + wave_n() * 64 + 32 * j, w);
+      get_subtile(Ae, d.mp, at.row0 + 32 * i, at.col0 + 32 * j, w);
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc.c[i][j][q] = ratio * half_of(w[q >> 2][(q >> 1) & 1], q & 1);
     }
-  slabs<false, true>(P, Q, nk, acc);
-  store_symmetric(acc, f, B + e * d.mp * d.mp, d.mp, bi, bj, diag + e * d.mp);
+  slabs<T, false, true>(P, Q, nk, acc);
+  store_symmetric<T>(acc, f, B + e * d.mp * d.mp, d.mp, at, diag + e * d.mp);
 }
 
 struct OrthoOut {
@@ -727,6 +751,7 @@ struct OrthoOut {
 };
 
 __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
+
 // Eight consecutive elements of the result at element `at` of matrix storage:
 // v holds bf16 values (U) or fp16 values (the step of W). Only `count` of
 // them exist; rows of whole 16-byte pieces (vec) go at once.
@@ -784,75 +809,82 @@ __device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, cons
 
 // The slab whose k are the rows of sub-tile row i holds, as Q, the sub-tiles of X
 // itself: acc += lin X.
-__device__ __forceinline__ void add_linear(const _Float16* lds, int i, float lin, Acc& acc) {
+template <class T>
+__device__ __forceinline__ void add_linear(const _Float16* lds, int i, float lin, Acc<T>& acc) {
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const f16x4 v = *reinterpret_cast<const f16x4*>(lds + kSlabP + (wave_n() * 4 + 2 * j + (g >> 1)) * kBlock +
-                                                     in_block(lane_id() & 31, g & 1) + 4 * (lane_id() >> 5));
+      const f16x4 v =
+          *reinterpret_cast<const f16x4*>(lds + T::kSlabP + (T::wave_n() * 4 + 2 * j + (g >> 1)) * kBlock +
+                                         in_block(lane_id() & 31, g & 1) + 4 * (lane_id() >> 5));
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc.c[i][j][4 * g + t] = fmaf(float(v[t]), lin, acc.c[i][j][4 * g + t]);
     }
 }
+// The turn of the tile's own rows (a big tile's wave has a turn of its own; the
+// two waves of a small tile share one).
+template <class T, int S>
+__device__ __forceinline__ void own_step(const Operand& P, const Operand& Q, int own, int nk, const float (&lin)[T::TI],
+                                         Acc<T>& acc) {
+  slab_step<T, S, true, true>(P, Q, own + S, nk, acc);
+  if (T::TI == 4 || T::wave_m() == S / 2) add_linear<T>(T::template stage<S>(), S % T::TI, lin[S % T::TI], acc);
+}
 
-// X' = (a + diag) X + B X. The four slabs whose k are this wave's rows are a turn
-// of their own, in which X's fp16 part is taken for the linear term as it
-// passes (read again from memory it cost the update as much as it is long).
-// FIRST: X is X0, whose value is scale[e] times what is stored (and whose
-// remainder may be zero: Xl NULL). LAST: the result is written instead of X'. U leaves as
-// bf16; the step of the weights goes through LDS as fp16 (2^-12 of the
-// update, an eighth of what the products' roundings leave).
-template <bool FIRST, bool LAST>
-__global__ __launch_bounds__(kThreads) void ortho_update_kernel(const _Float16* __restrict__ X,
-                                                                const uint8_t* __restrict__ Xl,
-                                                                const _Float16* __restrict__ B,
-                                                                const float* __restrict__ diag, OrthoDims d, int tiles,
-                                                                float ca, const float* __restrict__ scale,
-                                                                OrthoOut out) {
+// X' = (a + diag) X + B X. In the turn whose k are the tile's rows, X's fp16
+// part is taken for the linear term as it passes (read again from memory, it
+// took the update 13 % longer). FIRST: X is X0, whose value is scale[e] times
+// what is stored (and whose remainder may be zero: Xl NULL). LAST: the result
+// is written instead of X'. U leaves as bf16; the step of the weights goes
+// through LDS as fp16 (2^-12 of the update, an eighth of what the products'
+// roundings leave).
+template <class T, bool FIRST, bool LAST>
+__global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Float16* __restrict__ X,
+                                                                      const uint8_t* __restrict__ Xl,
+                                                                      const _Float16* __restrict__ B,
+                                                                      const float* __restrict__ diag, OrthoDims d,
+                                                                      int tiles, float ca,
+                                                                      const float* __restrict__ scale, OrthoOut out) {
   int64_t e;
   int t;
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
-  const int nrow = (d.mp + kTM - 1) / kTM;
+  const int nrow = (d.mp + T::kRows - 1) / T::kRows;
   const int bi = t % nrow, bj = t / nrow;  // the row tiles of a column panel follow each other
-  const bool active = bi * kTM + wave_m() * 128 < d.mp && bj * kTN + wave_n() * 64 < d.np;
+  const WavePart<T> at(bi, bj);
+  const bool active = at.row0 < d.mp && at.col0 < d.np;
   const int64_t xo = e * d.mp * d.np;
   const int lane = lane_id();
-  const int64_t ltile = e * tiles + t;
-  const int row0 = bi * kTM + wave_m() * 128, col0 = bj * kTN + wave_n() * 64;
-  const Operand P = operand_k(B + e * d.mp * d.mp, d.mp, d.mp, bi * kTM), Q = operand_mn(X + xo, d.mp, d.np, bj * kTN);
+  const Operand P = operand_k(B + e * d.mp * d.mp, d.mp, d.mp, bi * T::kRows);
+  const Operand Q = operand_mn<T>(X + xo, d.mp, d.np, bj * T::kCols);
   const int nk = d.mp / kBK;
-  float lin[4];
+  float lin[T::TI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) lin[i] = active ? ca + diag[e * d.mp + bi * kTM + tile_row(i)] : 0.f;
-  u32x4 lo[8];
+  for (int i = 0; i < T::TI; ++i) lin[i] = active ? ca + diag[e * d.mp + at.row0 + 32 * i + (lane & 31)] : 0.f;
+  u32x4 lo[2 * T::TI];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < 2 * T::TI; ++q) {
     lo[q] = u32x4{0u, 0u, 0u, 0u};
-    if (active && (!FIRST || Xl)) lo[q] = *reinterpret_cast<const u32x4*>(Xl + lo_offset(ltile, wave_id(), q, lane));
+    if (active && (!FIRST || Xl))
+      lo[q] = *reinterpret_cast<const u32x4*>(Xl + xo + lo_offset(d.mp, at.row0 + 64 * (q >> 2), at.col0, q & 3, lane));
   }
-  Acc acc;
-  first_slabs(P, Q, nk);
+  Acc<T> acc;
+  first_slabs<T>(P, Q, nk);
   if (!active) {
-    slabs<true, false>(P, Q, nk, acc);
+    slabs<T, true, false>(P, Q, nk, acc);
     return;
   }
-  zero(acc);
-  const int own = row0 / kBK;
-  turns<true, true>(P, Q, 0, own, nk, acc);
-  slab_step<0, true, true>(P, Q, own, nk, acc);
-  add_linear(g_s0, 0, lin[0], acc);
-  slab_step<1, true, true>(P, Q, own + 1, nk, acc);
-  add_linear(g_s1, 1, lin[1], acc);
-  slab_step<2, true, true>(P, Q, own + 2, nk, acc);
-  add_linear(g_s2, 2, lin[2], acc);
-  slab_step<3, true, true>(P, Q, own + 3, nk, acc);
-  add_linear(g_s3, 3, lin[3], acc);
-  turns<true, true>(P, Q, own + 4, nk, nk, acc);
+  acc.zero();
+  const int own = (T::TI == 4 ? at.row0 : bi * T::kRows) / kBK;
+  turns<T, true, true>(P, Q, 0, own, nk, acc);
+  own_step<T, 0>(P, Q, own, nk, lin, acc);
+  own_step<T, 1>(P, Q, own, nk, lin, acc);
+  own_step<T, 2>(P, Q, own, nk, lin, acc);
+  own_step<T, 3>(P, Q, own, nk, lin, acc);
+  turns<T, true, true>(P, Q, own + 4, nk, nk, acc);
   slabs_end();
   const float s = FIRST ? scale[e] : 1.f / kXScale;  // takes a stored iterate to its value
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < T::TI / 2; ++h) {
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii) {
       const int i = 2 * h + ii;
@@ -884,26 +916,28 @@ __global__ __launch_bounds__(kThreads) void ortho_update_kernel(const _Float16* 
           }
         }
         if constexpr (!LAST) {
-          put_subtile(w, out.X + xo, d.mp, row0 + 32 * i, col0 + 32 * j);
-          *reinterpret_cast<u32x4*>(out.Xl + lo_offset(ltile, wave_id(), 2 * i + j, lane)) = nlo;
+          put_subtile(w, out.X + xo, d.mp, at.row0 + 32 * i, at.col0 + 32 * j);
+          *reinterpret_cast<u32x4*>(out.Xl + xo + lo_offset(d.mp, at.row0 + 64 * h, at.col0, 2 * ii + j, lane)) = nlo;
         } else {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            image_put(image(), 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), w[g][0], w[g][1]);
+            image_put(T::image(), 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), w[g][0], w[g][1]);
         }
       }
     }
     if constexpr (LAST) {
-      const uint16_t* im = image();
+      const uint16_t* im = T::image();
       image_sync();
       for (int q = 0; q < 8; ++q) {
         if (!d.tall) {
-          const int r = row0 + 64 * h + 8 * q + (lane >> 3), c = col0 + 8 * (lane & 7);
+          const int r = at.row0 + 64 * h + 8 * q + (lane >> 3), c = at.col0 + 8 * (lane & 7);
           const u32x4 v = image_row(im, 8 * q + (lane >> 3), lane & 7);
           if (r < d.m && c < d.n) put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c, (d.C & 7) == 0);
         } else {
-          const int r = row0 + 64 * h + 8 * q, c = col0 + lane;
-          const u32x4 v = image_col(im, 8 * q, 16 * (lane >> 4));
+          // 16 columns of X (rows of the result) x four pieces of 8 rows: 64 bytes a row
+          const int r0 = 32 * (q & 1) + 8 * (lane >> 4), n0 = 16 * (q >> 1);
+          const int r = at.row0 + 64 * h + r0, c = at.col0 + n0 + (lane & 15);
+          const u32x4 v = image_col(im, r0, n0);
           if (r < d.m && c < d.n) put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r, (d.C & 7) == 0);
         }
       }
@@ -913,6 +947,13 @@ __global__ __launch_bounds__(kThreads) void ortho_update_kernel(const _Float16* 
 }
 
 // ------------------------------------------------------------------ plan
+
+// Big tiles of a product from which they are used: two rounds of the 256 CUs.
+// Gram / square / update in us, big against small tiles: 768 / 768 / 3072 big
+// tiles (128 matrices 768 x 2048) 183 : 217, 100 : 103, 411 : 462; 336 / 336 /
+// 768 (16 of 1536 x 2048) 111 : 108, 93 : 81, 171 : 197; 60 / 60 / 96 (6 of
+// 777 x 1000) 26 : 14, 26 : 14, 29 : 21.
+constexpr int64_t kBigTiles = 512;
 
 struct OrthoPlan {
   OrthoDims d;
@@ -933,7 +974,6 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   d.mp = (d.m + 127) / 128 * 128;
   d.np = (d.n + 127) / 128 * 128;
   const int64_t x = int64_t(d.mp) * d.np, q = int64_t(d.mp) * d.mp;
-  const int64_t xl = int64_t((d.mp + kTM - 1) / kTM * kTM) * ((d.np + kTN - 1) / kTN * kTN);  // whole tiles
   // at most about 4 GiB of state
   const int64_t bytes = 6 * x + 4 * q;
   int64_t g = (int64_t(4) << 30) / bytes;
@@ -949,11 +989,84 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   p.B = o;     o = up256(o + size_t(p.group) * q * 2);
   for (int i = 0; i < 2; ++i) {
     p.X[i] = o;  o = up256(o + size_t(p.group) * x * 2);
-    p.Xl[i] = o; o = up256(o + size_t(p.group) * xl);
+    p.Xl[i] = o; o = up256(o + size_t(p.group) * x);
   }
   p.total = o;
   return p;
 }
+
+// The steps of one group.
+struct OrthoSteps {
+  const OrthoArgs& a;
+  const OrthoTarget& t;
+  const OrthoPlan& p;
+  OrthoDims d;
+  char* base;
+  int64_t count, e0;
+  bool lo0;
+  hipStream_t st;
+  KernelTimer* timer;
+
+  void go() const {
+    // f (A A + ratio A); a c below 2^-20 of b adds nothing that fp16 holds
+    const bool square = std::fabs(a.c) > 1e-6f * std::fabs(a.b);
+    const float f = square ? a.c : 1.f, ratio = square ? a.b / a.c : a.b;
+    const bool big_sym = d.E * sym_tiles(d.mp, Big::kRows) >= kBigTiles;
+    const bool big_upd = d.E * update_tiles<Big>() >= kBigTiles;
+    for (int k = 0; k < a.steps; ++k) {
+      if (big_sym) symmetric<Big>(k, square, f, ratio); else symmetric<Small>(k, square, f, ratio);
+      if (big_upd) update<Big>(k); else update<Small>(k);
+    }
+  }
+
+ private:
+  template <class U>
+  U* at(size_t o) const {
+    return reinterpret_cast<U*>(base + o);
+  }
+  const float* scale(int k) const { return k == 0 ? at<float>(p.scale) : nullptr; }
+  template <class T>
+  int64_t update_tiles() const {
+    return int64_t((d.mp + T::kRows - 1) / T::kRows) * ((d.np + T::kCols - 1) / T::kCols);
+  }
+
+  template <class T>
+  void symmetric(int k, bool square, float f, float ratio) const {
+    const int tiles = sym_tiles(d.mp, T::kRows);
+    const dim3 grid(grid_of(d.E * tiles)), block(T::kThreads);
+    {
+      TimedLaunch tl(timer, "ortho_gram", st);
+      hipLaunchKernelGGL(ortho_gram_kernel<T>, grid, block, 0, st, at<_Float16>(p.X[k & 1]), d, tiles, scale(k),
+                         at<_Float16>(p.A));
+    }
+    TimedLaunch tl(timer, "ortho_square", st);
+    hipLaunchKernelGGL(ortho_square_kernel<T>, grid, block, 0, st, at<_Float16>(p.A), d, tiles, square, f, ratio,
+                       at<_Float16>(p.B), at<float>(p.diag));
+  }
+
+  template <class T>
+  void update(int k) const {
+    const int tiles = int(update_tiles<T>()), cur = k & 1;
+    const uint8_t* xl = k > 0 || lo0 ? at<uint8_t>(p.Xl[cur]) : nullptr;
+    const bool last = k + 1 == a.steps;
+    OrthoOut out{};
+    if (!last) {
+      out.X = at<_Float16>(p.X[1 - cur]);
+      out.Xl = at<uint8_t>(p.Xl[1 - cur]);
+    } else {
+      out.U = t.U ? t.U + e0 * count : nullptr;
+      out.W = t.W ? t.W + e0 * count : nullptr;
+      out.master = t.master ? t.master + e0 * count : nullptr;
+      out.keep = t.keep;
+      out.step = t.step;
+    }
+    TimedLaunch tl(timer, last ? "ortho_update_last" : "ortho_update", st);
+    const auto kernel = k == 0 ? (last ? ortho_update_kernel<T, true, true> : ortho_update_kernel<T, true, false>)
+                               : (last ? ortho_update_kernel<T, false, true> : ortho_update_kernel<T, false, false>);
+    hipLaunchKernelGGL(kernel, dim3(grid_of(d.E * tiles)), dim3(T::kThreads), 0, st, at<_Float16>(p.X[cur]), xl,
+                       at<_Float16>(p.B), at<float>(p.diag), d, tiles, a.a, scale(k), out);
+  }
+};
 
 }  // namespace
 
@@ -985,43 +1098,7 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
       hipLaunchKernelGGL(ortho_load_kernel, dim3(d.np / kLoadTile, d.mp / kLoadTile, ge), dim3(256), 0, st, in, d, part,
                          a.eps, f16(p.X[0]), lo0 ? u8(p.Xl[0]) : nullptr, f32(p.scale));
     }
-    const int st_tiles = sym_tiles(d.mp);
-    const int up_tiles = (d.mp + kTM - 1) / kTM * ((d.np + kTN - 1) / kTN);
-    // B = f (A A + ratio A); a c below 2^-20 of b adds nothing that fp16 holds
-    const bool square = std::fabs(a.c) > 1e-6f * std::fabs(a.b);
-    const float f = square ? a.c : 1.f, ratio = square ? a.b / a.c : a.b;
-    for (int k = 0; k < a.steps; ++k) {
-      const int cur = k & 1;
-      const float* scale = k == 0 ? f32(p.scale) : nullptr;
-      {
-        TimedLaunch tl(timer, "ortho_gram", st);
-        hipLaunchKernelGGL(ortho_gram_kernel, dim3(grid_of(d.E * st_tiles)), dim3(kThreads), 0, st, f16(p.X[cur]), d,
-                           st_tiles, scale, f16(p.A));
-      }
-      {
-        TimedLaunch tl(timer, "ortho_square", st);
-        hipLaunchKernelGGL(ortho_square_kernel, dim3(grid_of(d.E * st_tiles)), dim3(kThreads), 0, st, f16(p.A), d,
-                           st_tiles, square, f, ratio, f16(p.B), f32(p.diag));
-      }
-      const uint8_t* xl = k > 0 || lo0 ? u8(p.Xl[cur]) : nullptr;
-      const bool last = k + 1 == a.steps;
-      OrthoOut out{};
-      if (!last) {
-        out.X = f16(p.X[1 - cur]);
-        out.Xl = u8(p.Xl[1 - cur]);
-      } else {
-        out.U = t.U ? t.U + e0 * count : nullptr;
-        out.W = t.W ? t.W + e0 * count : nullptr;
-        out.master = t.master ? t.master + e0 * count : nullptr;
-        out.keep = t.keep;
-        out.step = t.step;
-      }
-      TimedLaunch tl(timer, last ? "ortho_update_last" : "ortho_update", st);
-      const auto kernel = k == 0 ? (last ? ortho_update_kernel<true, true> : ortho_update_kernel<true, false>)
-                                 : (last ? ortho_update_kernel<false, true> : ortho_update_kernel<false, false>);
-      hipLaunchKernelGGL(kernel, dim3(grid_of(d.E * up_tiles)), dim3(kThreads), 0, st, f16(p.X[cur]), xl, f16(p.B),
-                         f32(p.diag), d, up_tiles, a.a, scale, out);
-    }
+    OrthoSteps{a, t, p, d, base, count, e0, lo0, st, timer}.go();
   }
   return hipGetLastError();
 }

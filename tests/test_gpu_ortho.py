@@ -136,6 +136,55 @@ def test_past_32_bits(B):
     assert torch.equal(U[0], few[0]) and torch.equal(U[E - 3], few[0]) and torch.equal(U[E // 2], few[0])
 
 
+BIG = [
+    # (E, R, C, dtype): enough matrices for the large tiles, sides that end inside one
+    (200, 300, 500, "bf16"),
+    (200, 500, 300, "f32"),
+    (180, 130, 700, "bf16"),
+    (520, 128, 256, "bf16"),
+    (130, 640, 385, "bf16"),
+]
+
+
+@pytest.mark.parametrize("E,R,C,dtype", BIG)
+def test_large_stacks_match_oracle(B, E, R, C, dtype):
+    """A stack that runs in large tiles: matrices from its ends and its middle."""
+    print(f"case ortho stack E={E} R={R} C={C} {dtype}", flush=True)
+    few = _grad(4, R, C, dtype, 11, rank=min(R, C) // 2)
+    G = few[torch.arange(E, device=DEV) % 3].contiguous()
+    G[E // 2 + 1] = few[3]
+    G[E - 1] = few[3]
+    U = B.orthogonalize(B.OrthoBuffers.allocate(B.make_ortho_shape(E, R, C, grad=dtype)), G)
+    want = oo.orthogonalize(_f64(few))
+    assert _off(_f64(U[:3]), want[:3]) <= TOL
+    assert _off(_f64(U[E - 1:]), want[3:]) <= TOL
+    same = torch.arange(E, device=DEV) % 3
+    same[E // 2 + 1] = same[E - 1] = 3
+    ref = torch.cat([U[:3], U[E - 1:]])
+    assert torch.equal(U, ref[same])
+
+
+@pytest.mark.parametrize("master", [False, True])
+def test_large_stack_of_weights(B, master):
+    E, R, C = 200, 500, 301
+    few = _grad(2, R, C, "bf16", 5, rank=200)
+    G = few[torch.arange(E, device=DEV) % 2].contiguous()
+    g = torch.Generator().manual_seed(1)
+    mast = (0.05 * torch.randn((1, R, C), generator=g)).to(DEV).expand(E, R, C).contiguous()
+    W = mast.to(torch.bfloat16)
+    mom = torch.zeros_like(mast)
+    want_m, want = oo.muon_step(_f64(few), np.zeros((2, R, C)), _f64(mast[:2] if master else W[:2]), 0.02, 0.9, 0.1, 2.0,
+                                True)
+    before = _f64(mast[:2] if master else W[:2]) * (1 - 0.02 * 0.1)
+    B.muon_step(B.OrthoBuffers.allocate(B.make_ortho_shape(E, R, C)), G, mom, W, lr=0.02, momentum_coef=0.9,
+                weight_decay=0.1, scale=2.0, nesterov=True, master=mast if master else None)
+    for k in (0, E - 2):
+        got = _f64((mast if master else W)[k:k + 2])
+        tol = (2.0 ** -22 if master else 2.0 ** -8) * np.linalg.norm(want) + TOL * np.linalg.norm(want - before)
+        assert np.linalg.norm(got - want) <= tol
+        assert _off(_f64(mom[k:k + 2]), want_m) <= 2.0 ** -22
+
+
 MUON = [
     # (E, R, C, dtype, nesterov, master)
     (2, 100, 60, "bf16", True, False),
