@@ -24,115 +24,13 @@
 // bf16 products 1.3e-2 on full ones.
 #include <cmath>
 
-#include "device_common.h"
-#include "kernels.h"
+#include "ortho_device.h"
 
 namespace moe {
 
+using namespace ortho;
+
 namespace {
-
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kNormThreads = 256;
-constexpr int kNormParts = 64;      // partial sums (and maxima) per matrix
-constexpr int kLoadTile = 64;
-// An iterate is stored times 2^15 (iterates stay below 2, fp16 ends at 65504),
-// X0 times the power of two that takes its largest element to [2^14, 2^15):
-// then the remainders need no scale of their own to lie in E4M3's range
-// (16 at most), and elements 2^-20 of the largest still have theirs.
-constexpr float kXScale = 32768.f;
-constexpr int kX0Exp = 14;
-
-// The remainders are kept in the order in which the update's lanes hold 64 x 64
-// elements: [64 columns][64 rows][2 x 2 sub-tiles][lane][16 bytes], so they are
-// read and written 16 bytes a lane. r0, c0: multiples of 64.
-__device__ __forceinline__ int64_t lo_offset(int rows, int r0, int c0, int sub, int lane) {
-  return (((int64_t(c0 / 64) * (rows / 64) + r0 / 64) * 4 + sub) * 64 + lane) * 16;
-}
-
-// X, A and B live in the workspace in blocks of 32 rows x 16 columns (1 KiB), the
-// row blocks of a column block one after the other. A block is an MFMA fragment
-// in the order of its lanes: 16-byte chunk h (columns 8 h .. 8 h + 7) of row r
-// at slot 32 h + (r ^ 4 h). So a load of a wave moves a block into LDS as it
-// lies, a fragment with k along the rows is one linear LDS read, a store of a
-// 32 x 16 result is one linear 1 KiB, and the transpose read (two chunks of
-// four rows) finds its four rows of both chunks in different banks (the xor).
-// Row-major matrices (64-byte pieces of 16 rows a load) cost 13 to 25 % of the
-// products' time.
-constexpr int kBlock = 512;  // halves
-__device__ __forceinline__ int64_t block_at(int rows, int rb, int cb) { return (int64_t(cb) * (rows / 32) + rb) * kBlock; }
-// element (r, 8 h ..) inside a block
-__device__ __forceinline__ int in_block(int r, int h) { return (32 * h + (r ^ (4 * h))) * 8; }
-
-struct OrthoDims {
-  int64_t E;   // matrices of the group
-  int R, C;    // as given
-  int m, n;    // smaller, larger side
-  int mp, np;  // padded
-  bool tall;   // R > C: X = G^T
-};
-
-// ------------------------------------------------------------------ input
-
-__device__ __forceinline__ float grad_at(const void* g, bool f32, int64_t i) {
-  return f32 ? static_cast<const float*>(g)[i]
-             : __uint_as_float(uint32_t(static_cast<const uint16_t*>(g)[i]) << 16);
-}
-
-// What is orthogonalised.
-struct OrthoIn {
-  const void* grad;
-  bool f32;
-  float* mom;  // NULL: the gradient itself
-  float mu;
-  bool nesterov;
-};
-
-// Eight neighbouring gradient values (16-byte aligned).
-__device__ __forceinline__ void grad8(const OrthoIn& in, int64_t i, float (&x)[8]) {
-  if (in.f32) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(in.grad) + i);
-    const f32x4 a = p[0], b = p[1];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      x[t] = a[t];
-      x[4 + t] = b[t];
-    }
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(in.grad) + i);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      x[2 * t] = bf16_lo(a[t]);
-      x[2 * t + 1] = bf16_hi(a[t]);
-    }
-  }
-}
-
-// One element of what is orthogonalised, the momentum being up to date.
-__device__ __forceinline__ float input_at(const OrthoIn& in, int64_t i) {
-  if (!in.mom) return grad_at(in.grad, in.f32, i);
-  return in.nesterov ? grad_at(in.grad, in.f32, i) + in.mu * in.mom[i] : in.mom[i];
-}
-__device__ __forceinline__ void input8(const OrthoIn& in, int64_t i, float (&x)[8]) {
-  if (!in.mom || in.nesterov) grad8(in, i, x);
-  if (in.mom) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(in.mom + i);
-    const f32x4 a = p[0], b = p[1];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const float m = t < 4 ? a[t & 3] : b[t & 3];
-      x[t] = in.nesterov ? x[t] + in.mu * m : m;
-    }
-  }
-}
-
-// What the norm pass leaves of a part of a matrix.
-struct NormPart {
-  double sum;  // of squares
-  float amax;  // largest magnitude
-  float pad;
-};
 
 // Partial sums of squares and maxima, after the momentum step if there is one.
 // HBM-bound: 16-byte accesses where a matrix is a whole number of them.
@@ -200,25 +98,11 @@ __global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(OrthoIn in, in
   }
 }
 
-// The exponent p of X0 = G 2^p, and s = 1 / ((|G| + eps) 2^p), in every lane.
-static_assert(kNormParts == 64, "a lane per partial sum");
-__device__ __forceinline__ void matrix_scale(const NormPart* __restrict__ part, float eps, int* p, float* s) {
-  double q = part[lane_id()].sum;
-  float m = part[lane_id()].amax;
-  for (int o = 32; o > 0; o >>= 1) {
-    q += __shfl_xor(q, o);
-    m = fmaxf(m, __shfl_xor(m, o));
-  }
-  const double norm = sqrt(q);
-  const bool finite = norm < 1e300;
-  *p = finite && m > 0.f ? kX0Exp - ilogbf(m) : 0;
-  *s = !finite ? NAN : norm == 0.0 ? 0.f : float(ldexp(1.0 / (norm + double(eps)), -*p));
-}
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {  // v_cvt_pk_f16_f32, nearest even
-  const f32x2 v = {a, b};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+// The remainders are kept in the order in which the update's lanes hold 64 x 64
+// elements: [64 columns][64 rows][2 x 2 sub-tiles][lane][16 bytes], so they are
+// read and written 16 bytes a lane. r0, c0: multiples of 64.
+__device__ __forceinline__ int64_t lo_offset(int rows, int r0, int c0, int sub, int lane) {
+  return (((int64_t(c0 / 64) * (rows / 64) + r0 / 64) * 4 + sub) * 64 + lane) * 16;
 }
 
 // X0 and its remainder, 64 x 64 elements a workgroup, through LDS (transposed
@@ -345,11 +229,6 @@ struct TileShape {
 using Big = TileShape<4, 4>;
 using Small = TileShape<2, 2>;
 
-typedef short v4i16 __attribute__((ext_vector_type(4)));
-typedef short v8i16 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)); }
 template <int TI_, int WN_>
 __device__ __forceinline__ int TileShape<TI_, WN_>::wave_m() { return wave_id() / WN; }
 template <int TI_, int WN_>
@@ -519,67 +398,6 @@ __device__ __forceinline__ void slabs(const Operand& P, const Operand& Q, int nk
   slabs_end();
 }
 
-__device__ __forceinline__ float half_of(uint32_t w, int t) {
-  return float(__builtin_bit_cast(_Float16, uint16_t(t ? w >> 16 : w)));
-}
-
-// A 32 x 32 sub-tile of a matrix of blocks as the accumulators hold it: w[g]
-// the lane's four values of run g (row lane % 32, columns 8 g + 4 (lane / 32) ..
-// + 3). The swap of the upper half of one register with the lower half of
-// another turns whole 16-byte chunks into runs, and back in put_subtile.
-__device__ __forceinline__ void get_subtile(const _Float16* __restrict__ src, int rows, int row0, int col0,
-                                            u32x2 (&w)[4]) {
-  const int at = in_block(lane_id() & 31, lane_id() >> 5);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(src + block_at(rows, row0 / 32, col0 / 16 + p) + at);
-    const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
-    w[2 * p] = u32x2{a[0], b[0]};
-    w[2 * p + 1] = u32x2{a[1], b[1]};
-  }
-}
-__device__ __forceinline__ void put_subtile(const u32x2 (&w)[4], _Float16* __restrict__ out, int rows, int row0,
-                                            int col0) {
-  const int at = in_block(lane_id() & 31, lane_id() >> 5);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const auto a = __builtin_amdgcn_permlane32_swap(w[2 * p][0], w[2 * p + 1][0], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(w[2 * p][1], w[2 * p + 1][1], false, false);
-    *reinterpret_cast<u32x4*>(out + block_at(rows, row0 / 32, col0 / 16 + p) + at) = u32x4{a[0], b[0], a[1], b[1]};
-  }
-}
-
-// ------------------------------------------------------------------ images
-//
-// What has to leave in another order than the registers' (the mirrored half of
-// a symmetric product, the caller's row-major result) goes through LDS, 64
-// rows x 64 columns of 16-bit values of a wave at a time (8 KiB of its own: no
-// barrier): 16-byte chunk c of row r at c ^ ((r / 2) % 8). Rows come out as
-// 16-byte pieces, columns through the transpose read.
-
-// four values of row r (0 .. 63), columns 4 q .. 4 q + 3
-__device__ __forceinline__ void image_put(uint16_t* im, int r, int q, uint32_t lo, uint32_t hi) {
-  u32x2 v = {lo, hi};
-  *reinterpret_cast<u32x2*>(im + r * 64 + (((q >> 1) ^ ((r >> 1) & 7)) << 3) + (q & 1) * 4) = v;
-}
-// eight values of row r, columns 8 c .. 8 c + 7
-__device__ __forceinline__ u32x4 image_row(const uint16_t* im, int r, int c) {
-  return *reinterpret_cast<const u32x4*>(im + r * 64 + ((c ^ ((r >> 1) & 7)) << 3));
-}
-// Every lane: eight values of one column, rows r0 .. r0 + 7, for the 16
-// columns from n0 on (column n0 + lane % 16; r0 and n0 may differ from one
-// 16-lane group to another).
-__device__ __forceinline__ u32x4 image_col(const uint16_t* im, int r0, int n0) {
-  const int p = lane_id() & 15;
-  const int r = r0 + (p >> 2), n = n0 + 4 * (p & 3);
-  // rows r and r + 4 differ in the chunk's position
-  const uint16_t* a = im + r * 64 + (((n >> 3) ^ ((r >> 1) & 7)) << 3) + (n & 7);
-  const uint16_t* b = im + (r + 4) * 64 + (((n >> 3) ^ (((r + 4) >> 1) & 7)) << 3) + (n & 7);
-  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a));
-  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(b));
-  return __builtin_bit_cast(u32x4, v8i16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
-}
 // The image's 64 x 64 values transposed into a matrix of blocks: image column n
 // is row col0 + n, image row r column row0 + r. Lane n takes column n, 8 image
 // rows (a chunk) at a time.
@@ -593,13 +411,6 @@ __device__ __forceinline__ void put_blocks_mirrored(const uint16_t* im, _Float16
                               in_block(n & 31, q & 1)) = v;
   }
 }
-// LDS writes of the wave are visible to its own reads
-__device__ __forceinline__ void image_sync() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  asm volatile("" ::: "memory");
-}
-
 // ------------------------------------------------------------------ tiles
 //
 // Workgroups of one launch are dealt to the eight XCDs in turn (blockIdx % 8);
@@ -741,72 +552,6 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_square_kernel(const _Flo
   store_symmetric<T>(acc, f, B + e * d.mp * d.mp, d.mp, at, diag + e * d.mp);
 }
 
-struct OrthoOut {
-  _Float16* X;      // next iterate (NULL in the last step)
-  uint8_t* Xl;      // its remainder
-  uint16_t* U;      // last step: the result, or
-  uint16_t* W;      // the weights it updates (with master: their fp32 form)
-  float* master;
-  float keep, step;  // W keep - step U
-};
-
-__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
-
-// Eight consecutive elements of the result at element `at` of matrix storage:
-// v holds bf16 values (U) or fp16 values (the step of W). Only `count` of
-// them exist; rows of whole 16-byte pieces (vec) go at once.
-__device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, const u32x4& v, int count, bool vec) {
-  if (out.U) {
-    if (vec) {
-      *reinterpret_cast<u32x4*>(out.U + at) = v;
-    } else {
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-        if (t < count) out.U[at + t] = uint16_t(v[t >> 1] >> (16 * (t & 1)));
-    }
-    return;
-  }
-  float w[8];
-  if (vec) {
-    if (out.master) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(out.master + at);
-      const f32x4 b = *reinterpret_cast<const f32x4*>(out.master + at + 4);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        w[t] = a[t];
-        w[4 + t] = b[t];
-      }
-    } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(out.W + at);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        w[2 * t] = bf16_lo(a[t]);
-        w[2 * t + 1] = bf16_hi(a[t]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < 8; ++t) w[t] = t < count ? (out.master ? out.master[at + t] : bf16_at(out.W + at + t)) : 0.f;
-  }
-#pragma unroll
-  for (int t = 0; t < 8; ++t) w[t] = out.keep * w[t] - out.step * half_of(v[t >> 1], t & 1);
-  if (vec) {
-    if (out.master) {
-      *reinterpret_cast<f32x4*>(out.master + at) = f32x4{w[0], w[1], w[2], w[3]};
-      *reinterpret_cast<f32x4*>(out.master + at + 4) = f32x4{w[4], w[5], w[6], w[7]};
-    }
-    *reinterpret_cast<u32x4*>(out.W + at) = u32x4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
-                                                  pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
-  } else {
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if (t < count) {
-        if (out.master) out.master[at + t] = w[t];
-        out.W[at + t] = uint16_t(pack_bf16x2(w[t], 0.f));
-      }
-  }
-}
-
 // The slab whose k are the rows of sub-tile row i holds, as Q, the sub-tiles of X
 // itself: acc += lin X.
 template <class T>
@@ -926,21 +671,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Flo
       }
     }
     if constexpr (LAST) {
-      const uint16_t* im = T::image();
       image_sync();
-      for (int q = 0; q < 8; ++q) {
-        if (!d.tall) {
-          const int r = at.row0 + 64 * h + 8 * q + (lane >> 3), c = at.col0 + 8 * (lane & 7);
-          const u32x4 v = image_row(im, 8 * q + (lane >> 3), lane & 7);
-          if (r < d.m && c < d.n) put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c, (d.C & 7) == 0);
-        } else {
-          // 16 columns of X (rows of the result) x four pieces of 8 rows: 64 bytes a row
-          const int r0 = 32 * (q & 1) + 8 * (lane >> 4), n0 = 16 * (q >> 1);
-          const int r = at.row0 + 64 * h + r0, c = at.col0 + n0 + (lane & 15);
-          const u32x4 v = image_col(im, r0, n0);
-          if (r < d.m && c < d.n) put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r, (d.C & 7) == 0);
-        }
-      }
+      put_image(out, T::image(), d, e, at.row0 + 64 * h, at.col0);
       image_sync();
     }
   }
@@ -959,12 +691,15 @@ struct OrthoPlan {
   OrthoDims d;
   int64_t group;                            // matrices at a time
   size_t part, scale, X[2], Xl[2], A, B, diag, total;  // workspace offsets
+  size_t small;                             // of the small matrices' path
 };
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+constexpr int64_t kSmallGroup = 1024;
+
 OrthoPlan ortho_plan(const OrthoArgs& a) {
-  OrthoPlan p;
+  OrthoPlan p{};
   OrthoDims& d = p.d;
   d.R = a.R;
   d.C = a.C;
@@ -973,6 +708,13 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   d.n = d.tall ? a.R : a.C;
   d.mp = (d.m + 127) / 128 * 128;
   d.np = (d.n + 127) / 128 * 128;
+  if (small_fits(a)) {
+    p.group = a.E < 1 ? 1 : a.E > kSmallGroup ? kSmallGroup : a.E;
+    p.part = 0;
+    p.small = up256(size_t(p.group) * kNormParts * sizeof(NormPart));
+    p.total = p.small + small_plan(a, p.group).total;
+    return p;
+  }
   const int64_t x = int64_t(d.mp) * d.np, q = int64_t(d.mp) * d.mp;
   // at most about 4 GiB of state
   const int64_t bytes = 6 * x + 4 * q;
@@ -993,6 +735,17 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   }
   p.total = o;
   return p;
+}
+
+// The caller's result from element `first` on.
+OrthoOut target_of(const OrthoTarget& t, int64_t first) {
+  OrthoOut out{};
+  out.U = t.U ? t.U + first : nullptr;
+  out.W = t.W ? t.W + first : nullptr;
+  out.master = t.master ? t.master + first : nullptr;
+  out.keep = t.keep;
+  out.step = t.step;
+  return out;
 }
 
 // The steps of one group.
@@ -1054,11 +807,7 @@ struct OrthoSteps {
       out.X = at<_Float16>(p.X[1 - cur]);
       out.Xl = at<uint8_t>(p.Xl[1 - cur]);
     } else {
-      out.U = t.U ? t.U + e0 * count : nullptr;
-      out.W = t.W ? t.W + e0 * count : nullptr;
-      out.master = t.master ? t.master + e0 * count : nullptr;
-      out.keep = t.keep;
-      out.step = t.step;
+      out = target_of(t, e0 * count);
     }
     TimedLaunch tl(timer, last ? "ortho_update_last" : "ortho_update", st);
     const auto kernel = k == 0 ? (last ? ortho_update_kernel<T, true, true> : ortho_update_kernel<T, true, false>)
@@ -1091,6 +840,11 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
     {
       TimedLaunch tl(timer, "ortho_norm", st);
       hipLaunchKernelGGL(ortho_norm_kernel, dim3(kNormParts, ge), dim3(kNormThreads), 0, st, in, count, part);
+    }
+    if (small_fits(a)) {
+      const hipError_t e = launch_small(a, in, d, part, target_of(t, e0 * count), base + p.small, st, timer);
+      if (e != hipSuccess) return e;
+      continue;
     }
     const bool lo0 = a.grad_f32 || in.mom;  // a bf16 G is exact in fp16
     {
