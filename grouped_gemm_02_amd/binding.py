@@ -69,7 +69,7 @@ class moe_ortho_shape(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int64), ("R", ctypes.c_int64), ("C", ctypes.c_int64),
                 ("steps", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
                 ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float),
-                ("num_cus", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("reserved", ctypes.c_int32)]
 
 
 class moe_muon_params(ctypes.Structure):
@@ -376,12 +376,12 @@ def moe_route_bwd(shape, logits, topk_idx, topk_w, d_topk_w, renorm, d_logits, s
                                int(bool(renorm)), _ptr(d_logits), _stream(stream)), "moe_route_bwd")
 
 
-def make_ortho_shape(E, R, C, steps=5, grad="bf16", coeffs=NS_COEFFS, eps=1e-7, num_cus=0) -> moe_ortho_shape:
+def make_ortho_shape(E, R, C, steps=5, grad="bf16", coeffs=NS_COEFFS, eps=1e-7) -> moe_ortho_shape:
     """E matrices [R, C]; grad: "bf16" or "f32", the type of what is orthogonalised."""
     a, b, c = coeffs
     g = MOE_DT[grad] if isinstance(grad, str) else int(grad)
     return moe_ortho_shape(int(E), int(R), int(C), int(steps), g, float(a), float(b), float(c), float(eps),
-                           int(num_cus), 0)
+                           0)
 
 
 def moe_balance_scratch_bytes(shape: moe_shape, S: int) -> int:

@@ -10,7 +10,10 @@
 //   ortho_gram    A = X X^T
 //   ortho_square  B = b A + c A A (A is symmetric, so A A = A A^T)
 //   ortho_update  X' = a X + B X
-// The last update writes U, or updates the weights, instead of X'.
+// The last update writes U, or updates the weights, instead of X'. Wide matrices
+// take the first two steps as one (ortho_pairs): with P = a + B, the second step's
+// X X^T is P A P, and X'' = P2 P X = (a^2 + D) X, all but the last product m x m.
+// Matrices of at most 128 rows have a path of their own (ortho_small.hip).
 //
 // Numbers. Singular values far below the norm are multiplied by a (3.44) at
 // every step, 480-fold in five, and so is whatever a step rounds away in
@@ -19,8 +22,9 @@
 // small exactly in those directions, take the fp16 part. B's diagonal is near
 // b + c for converged rows and would carry the largest rounding: what its
 // rounding lost is kept in fp32 and added with the linear term. Measured
-// against 64 bits after the bf16 output rounding (1.7e-3 by itself): 1.8e-3
-// to 2.3e-3 on inputs of every rank; fp16 alone is 2.6e-2 off on low ranks,
+// against 64 bits after the bf16 output rounding (1.7e-3 by itself): 1.6e-3
+// to 2.4e-3 on bf16 inputs of every rank (fp32 inputs, which X0 rounds: 3.9e-3 on
+// rank one, 2.1e-3 on full rank); fp16 alone is 2.6e-2 off on low ranks,
 // bf16 products 1.3e-2 on full ones.
 #include <cmath>
 
@@ -105,6 +109,19 @@ __device__ __forceinline__ int64_t lo_offset(int rows, int r0, int c0, int sub, 
   return (((int64_t(c0 / 64) * (rows / 64) + r0 / 64) * 4 + sub) * 64 + lane) * 16;
 }
 
+// Four remainders in E4M3, times 16 (the conversions scale as they go): at most
+// 256, of an element near 65504, and off by 2^-4 of themselves, or by 2^-14 where
+// they are below 2^-10. Unscaled, the large elements' remainders would be as
+// good, and those below 2^-9 lost: 3.0e-3 instead of 1.8e-3 on a matrix of rank one.
+constexpr float kLoStep = 0.0625f;
+__device__ __forceinline__ uint32_t pack_lo(const float (&r)[4]) {
+  typedef short v2i16 __attribute__((ext_vector_type(2)));
+  v2i16 v = {0, 0};
+  v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, r[0], r[1], kLoStep, false);
+  v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, r[2], r[3], kLoStep, true);
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // X0 and its remainder, 64 x 64 elements a workgroup, through LDS (transposed
 // when G is tall). HBM-bound.
 __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d, const NormPart* __restrict__ part,
@@ -170,8 +187,7 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d
         const float x = tile[r][32 * (sub & 1) + 8 * g + 4 * (lane >> 5) + t];
         q[t] = x - float(static_cast<_Float16>(x));
       }
-      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-      v[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true));
+      v[g] = pack_lo(q);
     }
     *reinterpret_cast<u32x4*>(Xl + int64_t(e) * d.mp * d.np + lo_offset(d.mp, r0, c0, sub, lane)) = v;
   }
@@ -517,39 +533,62 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_gram_kernel(const _Float
   store_symmetric<T>(acc, s * s, A + e * d.mp * d.mp, d.mp, at, nullptr);
 }
 
-// B = b A + c A A = f (A A + ratio A) in fp16 (or, c negligible, f ratio A: no
-// products), and what the rounding of its diagonal lost. The accumulators
-// start from ratio A.
+// A product of m x m matrices that are polynomials of X X^T, so symmetric and
+// commuting: out = f (P Q^T + (r1 + d1) M1 + r2 M2) in fp16, d1 a diagonal (or
+// NULL), M2 NULL if there is none; on the diagonal also re (e1 + e2) (or NULL).
+// The accumulators start from the terms besides the product.
+struct SymProduct {
+  const _Float16 *P, *Q, *M1, *M2;
+  float r1, r2, f, re;
+  const float *d1, *e1, *e2;
+  bool product;    // false: without P Q^T
+  _Float16* out;
+  float* diag;     // what the rounding of out's diagonal lost (or NULL)
+};
+
 template <class T>
-__global__ __launch_bounds__(T::kThreads, 2) void ortho_square_kernel(const _Float16* __restrict__ A, OrthoDims d,
-                                                                      int tiles, bool products, float f, float ratio,
-                                                                      _Float16* __restrict__ B,
-                                                                      float* __restrict__ diag) {
+__global__ __launch_bounds__(T::kThreads, 2) void ortho_product_kernel(SymProduct a, OrthoDims d, int tiles) {
   int64_t e;
   int t, bi, bj;
   if (!take_tile(d.E * tiles, tiles, &e, &t)) return;
   sym_tile(t, &bi, &bj);
-  const _Float16* Ae = A + e * d.mp * d.mp;
+  const int64_t mo = e * d.mp * d.mp, vo = e * d.mp;
   const WavePart<T> at(bi, bj);
-  const Operand P = operand_k(Ae, d.mp, d.mp, bi * T::kRows), Q = operand_k(Ae, d.mp, d.mp, bj * T::kCols);
-  const int nk = products ? d.mp / kBK : 0;
+  const Operand P = operand_k(a.P + mo, d.mp, d.mp, bi * T::kRows), Q = operand_k(a.Q + mo, d.mp, d.mp, bj * T::kCols);
+  const int nk = a.product ? d.mp / kBK : 0;
   Acc<T> acc;
-  if (products) first_slabs<T>(P, Q, nk);
+  if (a.product) first_slabs<T>(P, Q, nk);
   if (at.row0 >= d.mp || at.col0 / 128 > at.row0 / 128) {
     slabs<T, false, false>(P, Q, nk, acc);
     return;
   }
+  const int lane = lane_id();
 #pragma unroll
-  for (int i = 0; i < T::TI; ++i)
+  for (int i = 0; i < T::TI; ++i) {
+    const int row = at.row0 + 32 * i + (lane & 31);
+    const float r1 = a.r1 + (a.d1 ? a.d1[vo + row] : 0.f);
+    const float on = a.e1 ? a.re * (a.e1[vo + row] + a.e2[vo + row]) : 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       u32x2 w[4];
-      get_subtile(Ae, d.mp, at.row0 + 32 * i, at.col0 + 32 * j, w);
+      get_subtile(a.M1 + mo, d.mp, at.row0 + 32 * i, at.col0 + 32 * j, w);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc.c[i][j][q] = ratio * half_of(w[q >> 2][(q >> 1) & 1], q & 1);
+      for (int q = 0; q < 16; ++q) acc.c[i][j][q] = r1 * half_of(w[q >> 2][(q >> 1) & 1], q & 1);
+      if (a.M2) {
+        get_subtile(a.M2 + mo, d.mp, at.row0 + 32 * i, at.col0 + 32 * j, w);
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          acc.c[i][j][q] = fmaf(a.r2, half_of(w[q >> 2][(q >> 1) & 1], q & 1), acc.c[i][j][q]);
+      }
+      if (a.e1 && at.row0 + 32 * i == at.col0 + 32 * j) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if ((lane & 31) == 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) acc.c[i][j][q] += on;
+      }
     }
+  }
   slabs<T, false, true>(P, Q, nk, acc);
-  store_symmetric<T>(acc, f, B + e * d.mp * d.mp, d.mp, at, diag + e * d.mp);
+  store_symmetric<T>(acc, a.f, a.out + mo, d.mp, at, a.diag ? a.diag + vo : nullptr);
 }
 
 // The slab whose k are the rows of sub-tile row i holds, as Q, the sub-tiles of X
@@ -639,8 +678,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Flo
         u32x2 w[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[2 * i + j][g]), false);
-          const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo[2 * i + j][g]), true);
+          const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo[2 * i + j][g], kLoStep, false);
+          const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo[2 * i + j][g], kLoStep, true);
           float y[4] = {a[0], a[1], b[0], b[1]};
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] = fmaf(y[q], lin[i], acc.c[i][j][4 * g + q]);
@@ -652,8 +691,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Flo
             w[g] = u32x2{pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
 #pragma unroll
             for (int q = 0; q < 4; ++q) y[q] -= half_of(w[g][q >> 1], q & 1);
-            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-            nlo[g] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], v, true));
+            nlo[g] = pack_lo(y);
           } else if (out.U) {
             w[g] = u32x2{pack_bf16x2(y[0] * s, y[1] * s), pack_bf16x2(y[2] * s, y[3] * s)};
           } else {
@@ -690,7 +728,7 @@ constexpr int64_t kBigTiles = 512;
 struct OrthoPlan {
   OrthoDims d;
   int64_t group;                            // matrices at a time
-  size_t part, scale, X[2], Xl[2], A, B, diag, total;  // workspace offsets
+  size_t part, scale, X[2], Xl[2], M[3], diag, total;  // workspace offsets
   size_t small;                             // of the small matrices' path
 };
 
@@ -717,24 +755,35 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   }
   const int64_t x = int64_t(d.mp) * d.np, q = int64_t(d.mp) * d.mp;
   // at most about 4 GiB of state
-  const int64_t bytes = 6 * x + 4 * q;
+  const int64_t bytes = 6 * x + 6 * q;
   int64_t g = (int64_t(4) << 30) / bytes;
   g = g < 1 ? 1 : (g > 4096 ? 4096 : g);
   p.group = a.E < g ? (a.E > 0 ? a.E : 1) : g;
   size_t o = 0;
   // The products read up to 128 rows past a matrix (as zeros: the buffer
-  // resource ends with it); B is followed by X, each X by its remainders.
+  // resource ends with it); the m x m matrices are followed by X, each X by its
+  // remainders.
   p.part = o;  o = up256(o + size_t(p.group) * kNormParts * sizeof(NormPart));
   p.scale = o; o = up256(o + size_t(p.group) * 4);
-  p.diag = o;  o = up256(o + size_t(p.group) * d.mp * 4);
-  p.A = o;     o = up256(o + size_t(p.group) * q * 2);
-  p.B = o;     o = up256(o + size_t(p.group) * q * 2);
+  p.diag = o;  o = up256(o + size_t(p.group) * d.mp * 4 * 3);
+  for (int i = 0; i < 3; ++i) {
+    p.M[i] = o; o = up256(o + size_t(p.group) * q * 2);
+  }
   for (int i = 0; i < 2; ++i) {
     p.X[i] = o;  o = up256(o + size_t(p.group) * x * 2);
     p.Xl[i] = o; o = up256(o + size_t(p.group) * x);
   }
   p.total = o;
   return p;
+}
+
+// Whether the first two steps run as one update: it saves a pass over X (X X^T and
+// the update, 1.5 m^2 n multiply-adds) for three more m x m products (1.5 m^3).
+// Measured, apart and as one: n / m = 2.67 (48 x 768 x 2048) 3.70 and 3.47 ms, n / m
+// = 2.67 (8 x 1536 x 4096 of 96) 44.3 and 40.4 ms in all, n / m = 1.33 1.99 and 1.99
+// ms, n / m = 1.29 283 and 303 us. fp16's range limits a^2.
+bool ortho_pairs(const OrthoArgs& a, const OrthoDims& d) {
+  return a.steps >= 2 && std::fabs(a.a) <= 16.f && 2 * int64_t(d.n) >= 3 * int64_t(d.m);
 }
 
 // The caller's result from element `first` on.
@@ -761,15 +810,7 @@ struct OrthoSteps {
   KernelTimer* timer;
 
   void go() const {
-    // f (A A + ratio A); a c below 2^-20 of b adds nothing that fp16 holds
-    const bool square = std::fabs(a.c) > 1e-6f * std::fabs(a.b);
-    const float f = square ? a.c : 1.f, ratio = square ? a.b / a.c : a.b;
-    const bool big_sym = d.E * sym_tiles(d.mp, Big::kRows) >= kBigTiles;
-    const bool big_upd = d.E * update_tiles<Big>() >= kBigTiles;
-    for (int k = 0; k < a.steps; ++k) {
-      if (big_sym) symmetric<Big>(k, square, f, ratio); else symmetric<Small>(k, square, f, ratio);
-      if (big_upd) update<Big>(k); else update<Small>(k);
-    }
+    if (d.E * sym_tiles(d.mp, Big::kRows) >= kBigTiles) steps<Big>(); else steps<Small>();
   }
 
  private:
@@ -777,31 +818,71 @@ struct OrthoSteps {
   U* at(size_t o) const {
     return reinterpret_cast<U*>(base + o);
   }
-  const float* scale(int k) const { return k == 0 ? at<float>(p.scale) : nullptr; }
+  _Float16* M(int i) const { return at<_Float16>(p.M[i]); }
+  float* diag(int i) const { return at<float>(p.diag) + int64_t(i) * p.group * d.mp; }
   template <class T>
   int64_t update_tiles() const {
     return int64_t((d.mp + T::kRows - 1) / T::kRows) * ((d.np + T::kCols - 1) / T::kCols);
   }
 
+  // T: tile shape of the symmetric products
   template <class T>
-  void symmetric(int k, bool square, float f, float ratio) const {
-    const int tiles = sym_tiles(d.mp, T::kRows);
-    const dim3 grid(grid_of(d.E * tiles)), block(T::kThreads);
-    {
-      TimedLaunch tl(timer, "ortho_gram", st);
-      hipLaunchKernelGGL(ortho_gram_kernel<T>, grid, block, 0, st, at<_Float16>(p.X[k & 1]), d, tiles, scale(k),
-                         at<_Float16>(p.A));
+  void steps() const {
+    int done = 0, updates = 0;
+    if (ortho_pairs(a, d)) {
+      // the first two steps as one update: with P = a + B, B = b A + c A A,
+      // A2 = P A P is the second step's X X^T and X2 = P2 P X = (a^2 + D) X
+      gram<T>(0, M(0));
+      square<T>(M(0), M(1), diag(0));
+      product<T>("ortho_square", SymProduct{M(1), M(0), M(0), nullptr, a.a, 0.f, 1.f, 0.f, diag(0), nullptr, nullptr, true,
+                                            M(2), nullptr});   // P A
+      product<T>("ortho_square", SymProduct{M(1), M(2), M(2), nullptr, a.a, 0.f, 1.f, 0.f, diag(0), nullptr, nullptr, true,
+                                            M(0), nullptr});   // A2
+      square<T>(M(0), M(2), diag(1));
+      product<T>("ortho_square", SymProduct{M(2), M(1), M(1), M(2), a.a, a.a, 1.f, a.a, nullptr, diag(0), diag(1), true,
+                                            M(0), diag(2)});   // D
+      done = 2;
+      update(updates++, M(0), a.a * a.a, diag(2), done == a.steps);
     }
-    TimedLaunch tl(timer, "ortho_square", st);
-    hipLaunchKernelGGL(ortho_square_kernel<T>, grid, block, 0, st, at<_Float16>(p.A), d, tiles, square, f, ratio,
-                       at<_Float16>(p.B), at<float>(p.diag));
+    for (; done < a.steps; ++updates) {
+      gram<T>(updates, M(0));
+      square<T>(M(0), M(1), diag(0));
+      ++done;
+      update(updates, M(1), a.a, diag(0), done == a.steps);
+    }
   }
 
   template <class T>
-  void update(int k) const {
-    const int tiles = int(update_tiles<T>()), cur = k & 1;
-    const uint8_t* xl = k > 0 || lo0 ? at<uint8_t>(p.Xl[cur]) : nullptr;
-    const bool last = k + 1 == a.steps;
+  void gram(int updates, _Float16* out) const {
+    const int tiles = sym_tiles(d.mp, T::kRows);
+    TimedLaunch tl(timer, "ortho_gram", st);
+    hipLaunchKernelGGL(ortho_gram_kernel<T>, dim3(grid_of(d.E * tiles)), dim3(T::kThreads), 0, st,
+                       at<_Float16>(p.X[updates & 1]), d, tiles, updates == 0 ? at<float>(p.scale) : nullptr, out);
+  }
+  template <class T>
+  void product(const char* name, const SymProduct& q) const {
+    const int tiles = sym_tiles(d.mp, T::kRows);
+    TimedLaunch tl(timer, name, st);
+    hipLaunchKernelGGL(ortho_product_kernel<T>, dim3(grid_of(d.E * tiles)), dim3(T::kThreads), 0, st, q, d, tiles);
+  }
+  // B = b A + c A A as c (A A + b / c A); a c below 2^-20 of b adds nothing that fp16 holds
+  template <class T>
+  void square(const _Float16* A, _Float16* B, float* dg) const {
+    const bool whole = std::fabs(a.c) > 1e-6f * std::fabs(a.b);
+    product<T>("ortho_square", SymProduct{A, A, A, nullptr, whole ? a.b / a.c : a.b, 0.f, whole ? a.c : 1.f, 0.f, nullptr,
+                                          nullptr, nullptr, whole, B, dg});
+  }
+
+  // X <- (lin + dg) X + B X
+  void update(int updates, const _Float16* B, float lin, const float* dg, bool last) const {
+    if (d.E * update_tiles<Big>() >= kBigTiles) update_in<Big>(updates, B, lin, dg, last);
+    else update_in<Small>(updates, B, lin, dg, last);
+  }
+  template <class T>
+  void update_in(int updates, const _Float16* B, float lin, const float* dg, bool last) const {
+    const int tiles = int(update_tiles<T>()), cur = updates & 1;
+    const bool first = updates == 0;
+    const uint8_t* xl = !first || lo0 ? at<uint8_t>(p.Xl[cur]) : nullptr;
     OrthoOut out{};
     if (!last) {
       out.X = at<_Float16>(p.X[1 - cur]);
@@ -810,10 +891,10 @@ struct OrthoSteps {
       out = target_of(t, e0 * count);
     }
     TimedLaunch tl(timer, last ? "ortho_update_last" : "ortho_update", st);
-    const auto kernel = k == 0 ? (last ? ortho_update_kernel<T, true, true> : ortho_update_kernel<T, true, false>)
-                               : (last ? ortho_update_kernel<T, false, true> : ortho_update_kernel<T, false, false>);
-    hipLaunchKernelGGL(kernel, dim3(grid_of(d.E * tiles)), dim3(T::kThreads), 0, st, at<_Float16>(p.X[cur]), xl,
-                       at<_Float16>(p.B), at<float>(p.diag), d, tiles, a.a, scale(k), out);
+    const auto kernel = first ? (last ? ortho_update_kernel<T, true, true> : ortho_update_kernel<T, true, false>)
+                              : (last ? ortho_update_kernel<T, false, true> : ortho_update_kernel<T, false, false>);
+    hipLaunchKernelGGL(kernel, dim3(grid_of(d.E * tiles)), dim3(T::kThreads), 0, st, at<_Float16>(p.X[cur]), xl, B, dg,
+                       d, tiles, lin, first ? at<float>(p.scale) : nullptr, out);
   }
 };
 

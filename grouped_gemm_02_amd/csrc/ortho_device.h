@@ -15,10 +15,10 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 constexpr int kNormThreads = 256;
 constexpr int kNormParts = 64;      // partial sums (and maxima) per matrix
 constexpr int kLoadTile = 64;
-// An iterate is stored times 2^15 (iterates stay below 2, fp16 ends at 65504),
-// X0 times the power of two that takes its largest element to [2^14, 2^15):
-// then the remainders need no scale of their own to lie in E4M3's range
-// (16 at most), and elements 2^-20 of the largest still have theirs.
+// An iterate is stored times 2^15 (its elements stay below 2, fp16 ends at
+// 65504), X0 times the power of two that takes its largest element to [2^14,
+// 2^15): what the rounding to fp16 leaves is 16 at most, and lies well inside
+// E4M3's range for elements down to 2^-20 of the largest.
 constexpr float kXScale = 32768.f;
 constexpr int kX0Exp = 14;
 

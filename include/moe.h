@@ -430,11 +430,16 @@ moe_status moe_bwd(const moe_shape* s, const void* dy, const void* x, const int3
  * (about 15 significant bits) for the linear term, the products take its
  * fp16 part, A and B = b A + c A^2 in fp16 with fp32 accumulation, and the
  * rounding of B's diagonal is made good in fp32; norms are summed in 64
- * bits. Elements of the iterates must stay below 2 in magnitude (with the usual
- * coefficients they stay below 1.3); past it the matrix's result is NaN. A matrix of zeros gives zeros; a matrix with a
- * NaN or an infinity gives NaN throughout, and leaves the others as they are.
+ * bits. When the larger side is 1.5 times the smaller or more, the first two
+ * steps are one update by a polynomial of A; matrices whose smaller side is at
+ * most 128 take every step on A (pairs of fp16, 22 bits) and meet G once more at
+ * the end. Against 64 bits the result is off by 1.6e-3 to 2.4e-3 of its norm
+ * (the bf16 of U alone is 1.7e-3), and by up to 4e-3 where an fp32 G has rank
+ * one. Elements of the iterates must stay below 2 in magnitude (with the usual
+ * coefficients they stay below 1.3); past it the matrix's result is NaN. A matrix
+ * of zeros gives zeros; a matrix with a NaN or an infinity gives NaN throughout,
+ * and leaves the others as they are. Results are deterministic.
  *   grad_dtype   MOE_DT_BF16 or MOE_DT_F32: the type of G
- *   num_cus      as in moe_shape
  * Limits: 0 <= E, 1 <= R, C <= 16384, E R C < 2^40, 1 <= steps <= 32, a, b,
  * c finite, eps >= 0 and finite, reserved 0. */
 typedef enum moe_dtype { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 } moe_dtype;
@@ -444,8 +449,7 @@ typedef struct moe_ortho_shape {
   int32_t steps;
   int32_t grad_dtype; /* moe_dtype */
   float a, b, c, eps;
-  int32_t num_cus;
-  int32_t reserved;
+  int32_t reserved; /* 0 */
 } moe_ortho_shape;
 
 /* Bytes of the scratch of moe_orthogonalize and moe_muon_step. It holds the
@@ -454,8 +458,8 @@ moe_status moe_ortho_workspace_size(const moe_ortho_shape* s, size_t* ws_bytes);
 
 /* U bf16 [E, R, C] (written) = the orthogonalised G [E, R, C] (grad_dtype).
  * U may be the very buffer of a bf16 G, but not overlap it otherwise. The
- * caller owns every buffer; ws 16-byte aligned; enqueued on `stream`. Results
- * do not depend on num_cus. Calls that share `ws` must not overlap. */
+ * caller owns every buffer; ws 16-byte aligned; enqueued on `stream`. Calls
+ * that share `ws` must not overlap. */
 moe_status moe_orthogonalize(const moe_ortho_shape* s, const void* G, void* U, void* ws, size_t ws_bytes,
                              void* stream);
 

@@ -69,7 +69,7 @@ def test_balance_bwd_refusals(B):
 BAD_ORTHO = [(dict(E=-1), 2), (dict(R=0), 2), (dict(C=0), 2), (dict(R=16385), 2), (dict(C=16385), 2),
              (dict(E=1 << 20, R=1024, C=1024), 2), (dict(steps=0), 2), (dict(steps=33), 2),
              (dict(grad=2), 4), (dict(coeffs=(math.nan, 0, 0)), 2), (dict(coeffs=(1, math.inf, 0)), 2),
-             (dict(eps=-1.0), 2), (dict(eps=math.inf), 2), (dict(num_cus=-1), 2)]
+             (dict(eps=-1.0), 2), (dict(eps=math.inf), 2)]
 
 
 @pytest.mark.parametrize("kw,status", BAD_ORTHO)

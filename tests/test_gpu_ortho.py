@@ -66,6 +66,12 @@ CASES = [
     (2, 384, 200, "bf16", None, 2, oo.COEFFS),
     (2, 200, 384, "f32", None, 6, oo.COEFFS),
     (2, 150, 150, "bf16", None, 8, (1.5, -0.5, 0.0)),
+    (2, 256, 256, "bf16", 1, 5, oo.COEFFS),
+    (2, 256, 768, "bf16", 1, 5, oo.COEFFS),
+    (1, 777, 400, "f32", 1, 5, oo.COEFFS),
+    (1, 200, 299, "bf16", None, 2, oo.COEFFS),
+    (1, 200, 300, "bf16", None, 2, oo.COEFFS),
+    (1, 200, 300, "f32", 20, 3, (2.0, -1.5, 0.5)),
 ]
 
 
