@@ -1,0 +1,215 @@
+"""The training operators in a run, as a step uses them: router and layer
+forward, balance losses, layer backward, router and balance backward,
+optimizer steps on the expert weights. Each is compared with its float64 oracle
+on the values that reached it; a captured step and a step on another stream
+repeat the eager one bit by bit (every kernel adds in a fixed order)."""
+import numpy as np
+import pytest
+import torch
+
+from grouped_gemm_02_amd import inputs
+from oracle import moe_balance as ob
+from oracle import moe_oracle as mo
+from oracle import moe_ortho as oo
+from oracle import moe_router as rt
+from tests.helpers import TOL_BF16, max_rel_err
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TOL_F32 = 1e-5     # as derived in test_gpu_balance.py
+TOL_ORTHO = 6e-3   # as derived in test_gpu_ortho.py
+LR, MU, WD = 1.0, 0.9, 0.1
+D_LOSS = (0.01, 0.001)
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from grouped_gemm_02_amd import binding
+    binding.lib()
+    return binding
+
+
+class Step:
+    """One layer's training step on buffers of its own. The last tokens lie
+    behind the last sequence; `mask` takes some more out of the losses."""
+
+    def __init__(self, B, T=160, H=256, I=128, E=8, k=2, S=3, seed=5):
+        self.B, self.renorm = B, True
+        self.s = B.make_shape(T, H, I, E, k)
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        n = lambda *sz: torch.randn(sz, generator=g, device=DEV)  # noqa: E731
+        self.x, self.dy = n(T, H).bfloat16(), n(T, H).bfloat16()
+        self.logits = inputs.make_router_logits(T, E, seed, DEV, skew=0.6)
+        self.off = torch.tensor([0, T // 4, T // 4, T - 9], dtype=torch.int32, device=DEV)
+        self.mask = (torch.rand((T,), generator=g, device=DEV) > 0.2).to(torch.uint8)
+        self.W13, self.W2 = (0.02 * n(E, 2 * I, H)).bfloat16(), (0.02 * n(E, H, I)).bfloat16()
+        self.master = self.W2.float()
+        self.m13, self.m2 = 0.1 * n(E, 2 * I, H), 0.1 * n(E, H, I)
+        self.idx = torch.full((T, k), -1, dtype=torch.int32, device=DEV)
+        self.w = torch.full((T, k), -1.0, device=DEV)
+        self.y = torch.empty_like(self.x)
+        self.grads = (torch.empty_like(self.x), torch.empty_like(self.w), torch.empty_like(self.W13),
+                      torch.empty_like(self.W2))
+        self.d_logits = torch.empty_like(self.logits)
+        self.d_loss = torch.tensor(D_LOSS, device=DEV)
+        self.layer = B.LayerBuffers.allocate(self.s)
+        self.bal = B.BalanceBuffers.allocate(self.s, S)
+        self.o13 = B.OrthoBuffers.allocate(B.make_ortho_shape(2 * E, I, H))   # gate and up apart
+        self.o2 = B.OrthoBuffers.allocate(B.make_ortho_shape(E, H, I))
+        for t in (self.layer.fwd_ws, self.layer.saved, self.layer.bwd_ws, self.bal.ws, self.o13.ws, self.o2.ws):
+            t.fill_(0xFF)
+
+    def losses(self):
+        B = self.B
+        B.forward_logits(self.layer, self.x, self.logits, self.renorm, self.idx, self.w, self.W13, self.W2, self.y)
+        B.balance(self.bal, self.logits, self.idx, self.off, self.mask)
+
+    def gradients(self):
+        B = self.B
+        B.backward(self.layer, self.dy, self.x, self.idx, self.w, self.W13, self.W2, self.grads)
+        B.balance_bwd(self.bal, self.logits, self.idx, self.w, self.grads[1], self.renorm, self.d_loss, self.off,
+                      self.mask, d_logits=self.d_logits)
+
+    def weights(self):
+        kw = dict(lr=LR, momentum_coef=MU, weight_decay=WD, scale=0.2)
+        self.B.muon_step(self.o13, self.grads[2], self.m13, self.W13, **kw)
+        self.B.muon_step(self.o2, self.grads[3], self.m2, self.W2, master=self.master, nesterov=False, **kw)
+
+    def run(self):
+        self.losses()
+        self.gradients()
+        self.weights()
+
+    def results(self):
+        return [t.clone() for t in (self.idx, self.w, self.y, self.bal.loss, self.bal.counts, self.bal.seq_counts,
+                                    self.bal.seq_probs, *self.grads, self.d_logits, self.m13, self.m2, self.W13,
+                                    self.W2, self.master)]
+
+    def state(self):
+        return [t.clone() for t in (self.x, self.dy, self.logits, self.m13, self.m2, self.W13, self.W2, self.master)]
+
+    def restore(self, state):
+        for t, v in zip((self.x, self.dy, self.logits, self.m13, self.m2, self.W13, self.W2, self.master), state):
+            t.copy_(v)
+
+
+def _np(t):
+    return t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+def test_step_matches_oracles(B):
+    print("case train step", flush=True)
+    s = Step(B)
+    z, x, dy, off, mask = (_np(t) for t in (s.logits, s.x, s.dy, s.off, s.mask))
+    W13, W2, m13, m2 = (_np(t) for t in (s.W13, s.W2, s.m13, s.m2))
+    s.run()
+    torch.cuda.synchronize()
+    idx, w = _np(s.idx), _np(s.w)
+    ridx, rw = rt.route(z, idx.shape[1], s.renorm)
+    np.testing.assert_array_equal(idx, ridx)
+    assert max_rel_err(w, rw) < TOL_F32
+    assert max_rel_err(_np(s.y), mo.forward(x, idx, w, W13, W2)) < TOL_BF16
+    ref = ob.balance(z, idx, off, mask)
+    np.testing.assert_array_equal(_np(s.bal.counts), ref["counts"])
+    assert max_rel_err(_np(s.bal.loss), ref["loss"]) < TOL_F32
+    dx, dw, dW13, dW2 = (_np(t) for t in s.grads)
+    want = mo.backward(dy, x, idx, w, W13, W2)
+    for got, ref in zip((dx, dw, dW13, dW2), want):
+        assert max_rel_err(got, ref) < TOL_BF16
+    dz = ob.balance_backward(z, idx, w, dw, s.renorm, D_LOSS, off, mask)
+    assert max_rel_err(_np(s.d_logits), dz) < TOL_F32
+    E, I2, H = W13.shape
+    kw = dict(lr=LR, mu=MU, weight_decay=WD, scale=0.2)
+    halves = lambda a: a.reshape(2 * E, I2 // 2, H)  # noqa: E731
+    for got, gw, gm, grad, m, old, nesterov in (
+            (_np(s.W13), 2.0 ** -8, _np(s.m13), halves(dW13), halves(m13), halves(W13), True),
+            (_np(s.master), 2.0 ** -21, _np(s.m2), dW2, m2, W2, False)):
+        em, eW = oo.muon_step(grad, m, old, nesterov=nesterov, **kw)
+        assert max_rel_err(gm.reshape(em.shape), em) < 2.0 ** -22   # a product and a sum in fp32
+        d = got.reshape(eW.shape) - eW
+        moved = np.linalg.norm(eW - old * (1 - LR * WD), axis=(1, 2))
+        # the orthogonalised update, and the rounding of the weights themselves
+        assert np.all(np.linalg.norm(d, axis=(1, 2)) <= TOL_ORTHO * moved + gw * np.linalg.norm(eW, axis=(1, 2)))
+        assert np.all(moved > 0.1 * np.linalg.norm(old, axis=(1, 2)))
+    assert torch.equal(s.W2, s.master.bfloat16())
+
+
+def _same(a, b):
+    for i, (u, v) in enumerate(zip(a, b)):
+        assert torch.equal(u, v), i
+
+
+def test_captured_step_repeats_the_eager_one(B):
+    """Two graphs (losses and gradients; weights) replayed on new inputs, with
+    eager steps of the same and of another shape between, which use the same
+    workspaces."""
+    print("case captured train step", flush=True)
+    s, other = Step(B), Step(B, T=33, H=512, I=256, E=4, S=3, seed=6)
+    start = s.state()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        s.run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        s.losses()
+        s.gradients()
+    with torch.cuda.graph(second):
+        s.weights()
+    for r in range(4):
+        state = [t.roll(r, 0) for t in start]
+        s.restore(state)
+        first.replay()
+        second.replay()
+        torch.cuda.synchronize()
+        got = s.results()
+        other.run()
+        s.restore(state)
+        s.run()
+        torch.cuda.synchronize()
+        _same(got, s.results())
+
+
+def test_step_on_another_stream_and_again(B):
+    print("case train step, streams", flush=True)
+    s = Step(B)
+    start = s.state()
+    s.run()
+    torch.cuda.synchronize()
+    want = s.results()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        s.restore(start)
+        for t in (s.d_logits, *s.grads):
+            t.fill_(3.0)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            s.run()
+        torch.cuda.current_stream().wait_stream(side)
+        _same(s.results(), want)
+
+
+def test_two_steps_at_once(B):
+    """Steps with buffers of their own on two streams do not disturb each other."""
+    print("case two train steps at once", flush=True)
+    a, b = Step(B), Step(B, T=200, H=512, I=256, E=16, k=4, S=3, seed=8)
+    starts = a.state(), b.state()
+    wants = []
+    for s in (a, b):
+        s.run()
+        torch.cuda.synchronize()
+        wants.append(s.results())
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for s, start in zip((a, b), starts):
+        s.restore(start)
+    torch.cuda.synchronize()
+    for s, stream in zip((a, b), streams):
+        with torch.cuda.stream(stream):
+            s.run()
+    torch.cuda.synchronize()
+    for s, want in zip((a, b), wants):
+        _same(s.results(), want)
