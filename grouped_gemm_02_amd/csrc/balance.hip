@@ -15,7 +15,9 @@
 //                    Each piece gets its sums of p and lse^2, its counts
 //                    (integer atomics in LDS) and its live tokens.
 //   balance_seq      a workgroup per sequence and 32 experts adds its pieces.
-//   balance_finish   adds the sequences.
+//   balance_finish   adds the sequences. (The last workgroup of balance_seq doing
+//                    it, behind device-wide fences: 3 us more on 16,384 x 128, 9
+//                    on 131,072 x 256.)
 #include "device_common.h"
 #include "kernels.h"
 
@@ -28,7 +30,10 @@ constexpr int kBalRows = 4;  // 16-byte loads of logits a lane has in flight
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
-// T * E up to which one workgroup does the whole forward
+// T * E up to which one workgroup does the whole forward of one sequence. In us,
+// against the three launches: 64 x 8 9.5 : 14.1, 512 x 64 9.9 : 14.2, 2048 x 16
+// 11.3 : 14.6, 4096 x 16 15.1 : 14.5, 1024 x 128 24 : 14. (A workgroup that takes
+// several sequences in turn: 7 us each.)
 constexpr int64_t kSmallWork = 32768;
 
 int balance_chunk_tokens(int64_t T) {
@@ -255,7 +260,6 @@ __device__ __forceinline__ double block_sum(double v, double* sm) {
 }
 
 constexpr int kSeqExperts = 32;
-constexpr int kSmallSeqs = 16;
 
 // 32 experts x 32 pieces at a time.
 __global__ __launch_bounds__(1024) void balance_seq_kernel(int64_t T, int E, const int32_t* __restrict__ off,
@@ -366,12 +370,11 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(int E, int k, int 
   }
 }
 
-// The whole forward in one workgroup, for batches whose three launches would
-// cost more than their work (see launch_balance).
+// The whole forward of one sequence in one workgroup.
 template <int LPT, int V>
 __global__ __launch_bounds__(1024) void balance_small_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t T, int E, int k,
-    const int32_t* __restrict__ off, int S, const uint8_t* __restrict__ mask, float* __restrict__ loss,
+    const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, float* __restrict__ loss,
     int32_t* __restrict__ counts, int32_t* __restrict__ seq_counts, float* __restrict__ seq_probs,
     float* __restrict__ seq_scale) {
   constexpr int kGroups = 1024 / LPT;
@@ -380,48 +383,32 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(
   __shared__ float sz[kGroups];
   __shared__ int32_t sn[kGroups];
   __shared__ double sm[16];
-  __shared__ int32_t live_of[kSmallSeqs];
   const int tid = threadIdx.x;
-  double term = 0.0, z = 0.0, n = 0.0, used = 0.0;
-  int32_t total = 0;  // expert tid's count over the sequences (E <= 1024)
-  for (int q = 0; q < S; ++q) {
-    const int64_t lo = off ? max(int64_t(0), int64_t(off[q])) : 0;
-    const int64_t hi = off ? min(T, int64_t(off[q + 1])) : T;
-    if (tid < E) sc[tid] = 0;
-    __syncthreads();
-    sum_tokens<LPT, V, kGroups>(logits, idx, lo, hi, E, k, mask, sp, sc, sz, sn);
-    __syncthreads();
-    const double zq = block_sum(tid < kGroups ? double(sz[tid]) : 0.0, sm);
-    const double nq = block_sum(tid < kGroups ? double(sn[tid]) : 0.0, sm);
-    double P = 0.0;
-    int32_t c = 0;
-    if (tid < E) {
-#pragma unroll 8
-      for (int g = 0; g < kGroups; ++g) P += sp[g * 4 * LPT * V + tid];
-      c = sc[tid];
-      seq_counts[int64_t(q) * E + tid] = c;
-      seq_probs[int64_t(q) * E + tid] = nq > 0.0 ? float(P / nq) : 0.f;
-      total += c;
-    }
-    const double t = block_sum(double(c) * P, sm);
-    if (nq > 0.0) {
-      term += t * double(E) / (double(k) * nq * nq);
-      used += 1.0;
-    }
-    z += zq;
-    n += nq;
-    if (tid == 0) live_of[q] = int32_t(nq);
-  }
-  if (tid < E) counts[tid] = total;
+  const int64_t lo = off ? max(int64_t(0), int64_t(off[0])) : 0;
+  const int64_t hi = off ? min(T, int64_t(off[1])) : T;
+  if (tid < E) sc[tid] = 0;  // E <= 1024
   __syncthreads();
-  if (tid < S) {
-    const double nq = live_of[tid];
-    seq_scale[tid] = nq > 0.0 ? float(double(E) / (used * double(k) * nq * nq)) : 0.f;
+  sum_tokens<LPT, V, kGroups>(logits, idx, lo, hi, E, k, mask, sp, sc, sz, sn);
+  __syncthreads();
+  const double z = block_sum(tid < kGroups ? double(sz[tid]) : 0.0, sm);
+  const double n = block_sum(tid < kGroups ? double(sn[tid]) : 0.0, sm);
+  double P = 0.0;
+  int32_t c = 0;
+  if (tid < E) {
+#pragma unroll 8
+    for (int g = 0; g < kGroups; ++g) P += sp[g * 4 * LPT * V + tid];
+    c = sc[tid];
+    counts[tid] = c;
+    seq_counts[tid] = c;
+    seq_probs[tid] = n > 0.0 ? float(P / n) : 0.f;
   }
+  const double t = block_sum(double(c) * P, sm);
   if (tid == 0) {
-    loss[0] = used > 0.0 ? float(term / used) : 0.f;
-    loss[1] = n > 0.0 ? float(z / n) : 0.f;
-    seq_scale[S] = n > 0.0 ? float(1.0 / n) : 0.f;
+    const bool any = n > 0.0;
+    loss[0] = any ? float(t * double(E) / (double(k) * n * n)) : 0.f;
+    loss[1] = any ? float(z / n) : 0.f;
+    seq_scale[0] = any ? float(double(E) / (double(k) * n * n)) : 0.f;
+    seq_scale[1] = any ? float(1.0 / n) : 0.f;
   }
 }
 
@@ -623,7 +610,7 @@ struct SmallLaunch {
   template <int LPT, int V>
   void operator()() const {
     hipLaunchKernelGGL((balance_small_kernel<LPT, V>), dim3(1), dim3(1024), 0, st, a.logits, a.idx, a.T, a.E, a.k, a.off,
-                       int(a.S), a.mask, loss, counts, seq_counts, seq_probs, seq_scale);
+                       a.mask, loss, counts, seq_counts, seq_probs, seq_scale);
   }
 };
 
@@ -650,7 +637,7 @@ size_t balance_scratch_bytes(int64_t T, int E, int64_t S) { return balance_ws(T,
 
 hipError_t launch_balance(const BalanceArgs& a, float* loss, int32_t* counts, int32_t* seq_counts, float* seq_probs,
                           float* seq_scale, void* ws, hipStream_t st, KernelTimer* timer) {
-  if (a.S <= kSmallSeqs && a.T * a.E <= kSmallWork) {
+  if (a.S == 1 && a.T * a.E <= kSmallWork) {
     TimedLaunch tl(timer, "balance_small", st);
     with_layout(a.E, SmallLaunch{a, loss, counts, seq_counts, seq_probs, seq_scale, st});
     return hipGetLastError();

@@ -72,6 +72,9 @@ CASES = [
     (130, 1024, 8, 2, 0, 0.1, 100, False),
     (200, 24, 3, 200, 0, 0.0, 0, True),       # as many sequences as tokens
     (40000, 33, 2, 3, 5, 0.1, 0, True),       # chunks of 64 tokens
+    (5000, 40, 3, 2500, 7, 0.1, 0, True),     # more sequences than threads
+    (64, 1024, 3, 1, 9, 0.5, 0, True),
+    (32, 1000, 3, 1, 0, 0.1, 7, False),       # one workgroup, all its threads' experts
 ]
 
 
