@@ -514,12 +514,14 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
       float sum, lse;
       row_softmax<LPT, V>(v[u], sum, lse);
       const float inv = inverse_of(sum);
-      // G: what is weighted by p; H: the renormalised weights' gradient, added as it is
+      // G: what is weighted by p; H: the renormalised weights' gradient, added as it
+      // is. A row outside the losses may hold anything: without G there, p is 0.
+      const bool need = live || (dw && !renorm);
       f32x4 G[V], H[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[u][i] *= inv;
         H[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        v[u][i] = need ? v[u][i] * inv : H[i];
         G[i] = live ? bal[i] : H[i];
         if (dw) {
           const f32x4 x = *reinterpret_cast<const f32x4*>(row + u * kRow + 4 * (l + LPT * i));

@@ -337,7 +337,8 @@ moe_status moe_balance(const moe_shape* s, const float* logits, const int32_t* t
  * q (0 for any other token) and G = d_topk_w placed on the selected experts:
  *   d_logits[t] = p (B - <p, B>) + 2 d_loss[1] seq_scale[S] lse p  [live]
  *               + the gradient moe_route_bwd gives (with renorm as there)
- * The mask and the sequences bear on the first two terms only. A row with
+ * The mask and the sequences bear on the first two terms only; a token they
+ * leave out takes nothing from its logits there, NaN or not. A row with
  * nothing but -inf gets 0 from them. topk_idx, topk_w and d_topk_w are read
  * only when d_topk_w is given (topk_idx and topk_w may be NULL otherwise);
  * an expert named twice by one token takes the sum of both slots. The other

@@ -173,6 +173,32 @@ def test_nonfinite_and_dead_rows(B):
     assert torch.isnan(buf.seq_probs[2]).any().item() and torch.isfinite(buf.seq_probs[0]).all().item()
 
 
+def test_gradient_of_dead_rows_with_nonfinite_logits(B):
+    """Rows outside the losses take nothing from their logits: their gradient is
+    0, or that of the renormalised weights, whatever the logits hold."""
+    T, E, k = 70, 40, 3
+    z, idx, _, _ = _inputs(T, E, k, 1, 0, 0.0, 0, 4)
+    off = torch.tensor([5, 30, 30, 60], dtype=torch.int32, device=DEV)
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+    mask[10] = 0
+    s = B.make_shape(T, 256, 128, E, k)
+    w = torch.empty((T, k), device=DEV)
+    B.moe_route(s, z, True, idx, w)
+    clean = z.clone()
+    z[10], z[3, 5], z[65], z[62] = math.nan, math.nan, math.inf, -math.inf
+    dead = [10, 3, 65, 62]
+    buf = B.BalanceBuffers.allocate(s, 3)
+    B.balance(buf, z, idx, off, mask)
+    dl = torch.tensor([1.0, 0.1], device=DEV)
+    dw = torch.randn((T, k), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    for d in (None, dw):
+        dz = _np(B.balance_bwd(buf, z, idx, w, d, True, dl, off, mask))
+        want = ob.balance_backward(_np(clean), _np(idx), _np(w), _np(d), True, _np(dl).astype(np.float64), _np(off),
+                                   _np(mask))
+        assert max_rel_err(dz, want) <= TOL
+        assert d is not None or not dz[dead].any()
+
+
 def test_nothing_live_and_no_tokens(B):
     E, k = 24, 2
     z, idx, _, _ = _inputs(50, E, k, 1, 0, 0.0, 0, 6)
