@@ -115,6 +115,22 @@ def test_zero_nan_and_extreme_matrices(B):
     assert _off(_f64(B.orthogonalize(B.OrthoBuffers.allocate(s), G[:1])), oo.orthogonalize(_f64(G[:1]), eps=s.eps)) <= TOL
 
 
+@pytest.mark.parametrize("R,C", [(40, 70), (150, 290)])   # either path
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_magnitudes_at_the_ends_of_the_types(B, R, C, dtype):
+    """Largest elements near the type's largest, near its smallest normal and
+    among its subnormals (eps 0); a norm far below eps."""
+    print(f"case ortho magnitudes R={R} C={C} {dtype}", flush=True)
+    G = _grad(4, R, C, "f32", 4)
+    G = G / G.abs().amax(dim=(1, 2), keepdim=True)
+    G = (G.double() * torch.tensor([3.3e38, 2e-38, 2e-39, 1e-10], device=DEV, dtype=torch.float64).view(4, 1, 1))
+    G = G.float().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for eps, rows in ((0.0, slice(0, 3)), (1e-7, slice(3, 4))):
+        s = B.make_ortho_shape(G[rows].shape[0], R, C, grad=dtype, eps=eps)
+        U = B.orthogonalize(B.OrthoBuffers.allocate(s), G[rows].clone())
+        assert _off(_f64(U), oo.orthogonalize(_f64(G[rows]), eps=s.eps)) <= TOL
+
+
 def test_matrices_do_not_depend_on_their_stack(B):
     """A matrix gives the same bits alone, in a stack, in place, and again."""
     for E, R, C in ((6, 200, 300), (5, 64, 100), (5, 300, 200)):
