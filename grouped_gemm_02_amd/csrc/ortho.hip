@@ -37,7 +37,8 @@ using namespace ortho;
 namespace {
 
 // Partial sums of squares and maxima, after the momentum step if there is one.
-// HBM-bound: 16-byte accesses where a matrix is a whole number of them.
+// HBM-bound: 16-byte accesses where a matrix is a whole number of them (128 of
+// 768 x 2048 in bf16: 403 MB in 87 us, 4.6 TB/s).
 __global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(OrthoIn in, int64_t count,
                                                                   NormPart* __restrict__ part) {
   __shared__ double sm[kNormThreads / 64];
@@ -123,7 +124,8 @@ __device__ __forceinline__ uint32_t pack_lo(const float (&r)[4]) {
 }
 
 // X0 and its remainder, 64 x 64 elements a workgroup, through LDS (transposed
-// when G is tall). HBM-bound.
+// when G is tall). HBM-bound (the same stack: 136 us for 805 MB, some of what it
+// reads still in the last-level cache from ortho_norm).
 __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d, const NormPart* __restrict__ part,
                                                          float eps, _Float16* __restrict__ X,
                                                          uint8_t* __restrict__ Xl, float* __restrict__ scale) {
@@ -508,7 +510,9 @@ __device__ __forceinline__ void store_symmetric(const Acc<T>& acc, float f, _Flo
   }
 }
 
-// A = X X^T times the square of the iterate's scale.
+// A = X X^T times the square of the iterate's scale. MFMA-bound: 128 of 768 x 2048
+// in 180 us, 1.15 PFLOP/s of the six tiles of nine that it computes (a square
+// library product of 8192 reaches 1.21).
 template <class T>
 __global__ __launch_bounds__(T::kThreads, 2) void ortho_gram_kernel(const _Float16* __restrict__ X, OrthoDims d,
                                                                     int tiles, const float* __restrict__ scale,
@@ -536,7 +540,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_gram_kernel(const _Float
 // A product of m x m matrices that are polynomials of X X^T, so symmetric and
 // commuting: out = f (P Q^T + (r1 + d1) M1 + r2 M2) in fp16, d1 a diagonal (or
 // NULL), M2 NULL if there is none; on the diagonal also re (e1 + e2) (or NULL).
-// The accumulators start from the terms besides the product.
+// The accumulators start from the terms besides the product. 128 of 768 x 768 in
+// 111 us: 0.70 PFLOP/s of the six tiles of nine, 300 to 450 MB to and from HBM,
+// and an epilogue (the mirrored store) for every 24 slabs.
 struct SymProduct {
   const _Float16 *P, *Q, *M1, *M2;
   float r1, r2, f, re;
@@ -621,7 +627,10 @@ __device__ __forceinline__ void own_step(const Operand& P, const Operand& Q, int
 // what is stored (and whose remainder may be zero: Xl NULL). LAST: the result
 // is written instead of X'. U leaves as bf16; the step of the weights goes
 // through LDS as fp16 (2^-12 of the update, an eighth of what the products'
-// roundings leave).
+// roundings leave). 128 of 768 x 2048 in 403 us: 0.77 PFLOP/s and 1.2 GB, 3.0
+// TB/s. The MFMAs alone would take 255, the bytes 246; a tile's first loads and
+// last stores do not run under its products (the wait counter holds loads and
+// stores in one order, so a next tile's loads would wait for the stores too).
 template <class T, bool FIRST, bool LAST>
 __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Float16* __restrict__ X,
                                                                       const uint8_t* __restrict__ Xl,
@@ -720,9 +729,11 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Flo
 
 // Big tiles of a product from which they are used: two rounds of the 256 CUs.
 // Gram / square / update in us, big against small tiles: 768 / 768 / 3072 big
-// tiles (128 matrices 768 x 2048) 183 : 217, 100 : 103, 411 : 462; 336 / 336 /
-// 768 (16 of 1536 x 2048) 111 : 108, 93 : 81, 171 : 197; 60 / 60 / 96 (6 of
-// 777 x 1000) 26 : 14, 26 : 14, 29 : 21.
+// tiles (128 matrices 768 x 2048) 180 : 215, 111 : 116, 403 : 458; 336 / 336 /
+// 768 (16 of 1536 x 2048) 105 : 108, 91 : 81, 179 : 197; 60 / 60 / 96 (6 of
+// 777 x 1000) 26 : 15, 28 : 15, 29 : 21. Eight stages instead of four for small
+// tiles of one workgroup a CU changed nothing: the turns of a lone workgroup are
+// as long as its LDS reads and MFMAs one after the other.
 constexpr int64_t kBigTiles = 512;
 
 struct OrthoPlan {
@@ -754,7 +765,9 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
     return p;
   }
   const int64_t x = int64_t(d.mp) * d.np, q = int64_t(d.mp) * d.mp;
-  // at most about 4 GiB of state
+  // At most about 4 GiB of state (256 matrices 1536 x 4096: 1 GiB 44.6 ms, 2 GiB
+  // 42.9, 4 GiB 40.3, 8 GiB 40.0, 16 GiB 39.7: the last round of tiles of each
+  // launch). As many matrices as fit, the rest last; groups of equal size 41.0.
   const int64_t bytes = 6 * x + 6 * q;
   int64_t g = (int64_t(4) << 30) / bytes;
   g = g < 1 ? 1 : (g > 4096 ? 4096 : g);
@@ -779,8 +792,8 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
 
 // Whether the first two steps run as one update: it saves a pass over X (X X^T and
 // the update, 1.5 m^2 n multiply-adds) for three more m x m products (1.5 m^3).
-// Measured, apart and as one: n / m = 2.67 (48 x 768 x 2048) 3.70 and 3.47 ms, n / m
-// = 2.67 (8 x 1536 x 4096 of 96) 44.3 and 40.4 ms in all, n / m = 1.33 1.99 and 1.99
+// Measured, apart and as one: n / m = 2.67 (128 of 768 x 2048) 3.70 and 3.47 ms, n / m
+// = 2.67 (256 of 1536 x 4096) 44.3 and 40.4 ms, n / m = 1.33 1.99 and 1.99
 // ms, n / m = 1.29 283 and 303 us. fp16's range limits a^2.
 bool ortho_pairs(const OrthoArgs& a, const OrthoDims& d) {
   return a.steps >= 2 && std::fabs(a.a) <= 16.f && 2 * int64_t(d.n) >= 3 * int64_t(d.m);
