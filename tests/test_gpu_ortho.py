@@ -167,6 +167,7 @@ BIG = [
     (200, 500, 300, "f32"),
     (180, 130, 700, "bf16"),
     (520, 128, 256, "bf16"),
+    (1100, 24, 33, "f32"),     # more than a group of small matrices
     (130, 640, 385, "bf16"),
 ]
 
