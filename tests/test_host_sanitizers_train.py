@@ -9,9 +9,11 @@ import subprocess
 import pytest
 
 from tests.helpers import ROOT
-from tests.test_host_sanitizers import HIPCC, SAN
 
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 pytestmark = pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
+SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+       "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer"]
 
 
 def test_train_host_code_is_clean_under_asan_and_ubsan(tmp_path):
