@@ -171,20 +171,24 @@ def _want(t, name: str, dtype, numel: int | None = None, optional: bool = False)
         raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, expected a GPU tensor")
 
 
-def _here(*wanted) -> None:
+def _here(stream, *wanted) -> list:
     """_want for each (tensor, name, dtype, numel), and the tensor must be on the
-    current device, whose stream the call is enqueued on."""
-    dev = None
+    current device, whose stream the call is enqueued on. Returns their
+    addresses and the stream's handle."""
+    dev, at = -1, []
     for t, name, dtype, numel in wanted:
         if not isinstance(t, torch.Tensor):
+            at.append(t)
             continue
-        if t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
-            if dev is None:
-                dev = torch.cuda.current_device()
-            if t.get_device() == dev:
-                continue
-            raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{dev}")
+        if dev < 0 and t.is_cuda:
+            dev = torch.cuda.current_device()
+        if t.get_device() == dev >= 0 and t.dtype is dtype and t.numel() >= numel and t.is_contiguous():
+            at.append(t.data_ptr())
+            continue
         _want(t, name, dtype, numel)
+        raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{dev}")
+    at.append(torch._C._cuda_getCurrentRawStream(dev) if stream is None and dev >= 0 else _stream(stream))
+    return at
 
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
@@ -391,37 +395,25 @@ def moe_balance_scratch_bytes(shape: moe_shape, S: int) -> int:
 def moe_balance(shape, logits, topk_idx, seq_offsets, S, mask, loss, counts, seq_counts, seq_probs, seq_scale, ws,
                 stream=None) -> None:
     T, E, k, S = shape.T, shape.E, shape.k, int(S)
-    _here((logits, "logits", _F32, T * E),
-          (topk_idx, "topk_idx", _I32, T * k),
-          (seq_offsets, "seq_offsets", _I32, S + 1),
-          (mask, "mask", _U8, T),
-          (loss, "loss", _F32, 2),
-          (counts, "counts", _I32, E),
-          (seq_counts, "seq_counts", _I32, S * E),
-          (seq_probs, "seq_probs", _F32, S * E),
-          (seq_scale, "seq_scale", _F32, S + 1),
-          (ws, "ws", _U8, 0))
-    _check(lib().moe_balance(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), S, _ptr(mask),
-                             _ptr(loss), _ptr(counts), _ptr(seq_counts), _ptr(seq_probs), _ptr(seq_scale), _ptr(ws),
-                             ws.numel() * ws.element_size(), _stream(stream)), "moe_balance")
+    z, idx, off, m, l, c, sc, sp, ss, w, st = _here(
+        stream, (logits, "logits", _F32, T * E), (topk_idx, "topk_idx", _I32, T * k),
+        (seq_offsets, "seq_offsets", _I32, S + 1), (mask, "mask", _U8, T), (loss, "loss", _F32, 2),
+        (counts, "counts", _I32, E), (seq_counts, "seq_counts", _I32, S * E), (seq_probs, "seq_probs", _F32, S * E),
+        (seq_scale, "seq_scale", _F32, S + 1), (ws, "ws", _U8, 0))
+    _check(lib().moe_balance(ctypes.byref(shape), z, idx, off, S, m, l, c, sc, sp, ss, w, ws.numel(), st),
+           "moe_balance")
 
 
 def moe_balance_bwd(shape, logits, topk_idx, topk_w, d_topk_w, renorm, seq_offsets, S, mask, seq_counts, seq_scale,
                     d_loss, d_logits, stream=None) -> None:
     T, E, k, S = shape.T, shape.E, shape.k, int(S)
-    _here((logits, "logits", _F32, T * E),
-          (topk_idx, "topk_idx", _I32, T * k),
-          (topk_w, "topk_w", _F32, T * k),
-          (d_topk_w, "d_topk_w", _F32, T * k),
-          (seq_offsets, "seq_offsets", _I32, S + 1),
-          (mask, "mask", _U8, T),
-          (seq_counts, "seq_counts", _I32, S * E),
-          (seq_scale, "seq_scale", _F32, S + 1),
-          (d_loss, "d_loss", _F32, 2),
-          (d_logits, "d_logits", _F32, T * E))
-    _check(lib().moe_balance_bwd(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w),
-                                 int(bool(renorm)), _ptr(seq_offsets), S, _ptr(mask), _ptr(seq_counts),
-                                 _ptr(seq_scale), _ptr(d_loss), _ptr(d_logits), _stream(stream)), "moe_balance_bwd")
+    z, idx, w, dw, off, m, sc, ss, dl, dz, st = _here(
+        stream, (logits, "logits", _F32, T * E), (topk_idx, "topk_idx", _I32, T * k), (topk_w, "topk_w", _F32, T * k),
+        (d_topk_w, "d_topk_w", _F32, T * k), (seq_offsets, "seq_offsets", _I32, S + 1), (mask, "mask", _U8, T),
+        (seq_counts, "seq_counts", _I32, S * E), (seq_scale, "seq_scale", _F32, S + 1), (d_loss, "d_loss", _F32, 2),
+        (d_logits, "d_logits", _F32, T * E))
+    _check(lib().moe_balance_bwd(ctypes.byref(shape), z, idx, w, dw, 1 if renorm else 0, off, S, m, sc, ss, dl, dz, st),
+           "moe_balance_bwd")
 
 
 def moe_ortho_workspace_size(shape: moe_ortho_shape) -> int:
@@ -432,22 +424,17 @@ def moe_ortho_workspace_size(shape: moe_ortho_shape) -> int:
 
 def moe_orthogonalize(shape, G, U, ws, stream=None) -> None:
     n = shape.E * shape.R * shape.C
-    _here((G, "G", _BF16 if shape.grad_dtype == 0 else _F32, n),
-          (U, "U", _BF16, n),
-          (ws, "ws", _U8, 0))
-    _check(lib().moe_orthogonalize(ctypes.byref(shape), _ptr(G), _ptr(U), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _stream(stream)), "moe_orthogonalize")
+    g, u, w, st = _here(stream, (G, "G", _BF16 if shape.grad_dtype == 0 else _F32, n), (U, "U", _BF16, n),
+                        (ws, "ws", _U8, 0))
+    _check(lib().moe_orthogonalize(ctypes.byref(shape), g, u, w, ws.numel(), st), "moe_orthogonalize")
 
 
 def moe_muon_step(shape, params, grad, momentum, W, master, ws, stream=None) -> None:
     n = shape.E * shape.R * shape.C
-    _here((grad, "grad", _BF16 if shape.grad_dtype == 0 else _F32, n),
-          (momentum, "momentum", _F32, n),
-          (W, "W", _BF16, n),
-          (master, "master", _F32, n),
-          (ws, "ws", _U8, 0))
-    _check(lib().moe_muon_step(ctypes.byref(shape), ctypes.byref(params), _ptr(grad), _ptr(momentum), _ptr(W),
-                               _ptr(master), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+    g, m, w, ms, sp, st = _here(stream, (grad, "grad", _BF16 if shape.grad_dtype == 0 else _F32, n),
+                                (momentum, "momentum", _F32, n), (W, "W", _BF16, n), (master, "master", _F32, n),
+                                (ws, "ws", _U8, 0))
+    _check(lib().moe_muon_step(ctypes.byref(shape), ctypes.byref(params), g, m, w, ms, sp, ws.numel(), st),
            "moe_muon_step")
 
 
@@ -568,7 +555,7 @@ def balance_bwd(buf: BalanceBuffers, logits, topk_idx, topk_w, d_topk_w, renorm,
     """d_logits of the balance losses and, with d_topk_w, of the routing
     weights; seq_counts and seq_scale default to what balance left in `buf`."""
     if d_logits is None:
-        d_logits = torch.empty((buf.shape.T, buf.shape.E), dtype=_F32, device=buf.loss.device)
+        d_logits = buf.loss.new_empty((buf.shape.T, buf.shape.E))
     moe_balance_bwd(buf.shape, logits, topk_idx, topk_w, d_topk_w, renorm, seq_offsets, buf.S, mask,
                     buf.seq_counts if seq_counts is None else seq_counts,
                     buf.seq_scale if seq_scale is None else seq_scale, d_loss, d_logits, stream)

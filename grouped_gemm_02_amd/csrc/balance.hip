@@ -32,10 +32,10 @@ constexpr int kBalRows = 4;  // 16-byte loads of logits a lane has in flight
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
 // T * E up to which one workgroup does the whole forward of one sequence. In us,
-// against the three launches: 64 x 8 9.5 : 14.1, 512 x 64 9.9 : 14.2, 2048 x 16
-// 11.3 : 14.6, 4096 x 16 15.1 : 14.5, 1024 x 128 24 : 14. (A workgroup that takes
-// several sequences in turn: 7 us each.)
-constexpr int64_t kSmallWork = 32768;
+// against the three launches: 64 x 8 8.1 : 14.3, 4096 x 16 11.2 : 14.3, 512 x 128
+// 12.9 : 14.5, 256 x 256 13.8 : 16.2, 8192 x 16 18.8 : 14.7, 1024 x 128 22.2 : 14.6.
+// (A workgroup that takes several sequences in turn: 4 to 7 us each.)
+constexpr int64_t kSmallWork = 65536;
 
 int balance_chunk_tokens(int64_t T) {
   // 32 tokens a workgroup until 1024 workgroups are reached, then more
@@ -92,6 +92,19 @@ __device__ __forceinline__ float group_sum(float v) {
   return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
 }
 
+// The sums over the groups of LPT lanes of a wave, lane by lane (rotations in
+// rows of 16 lanes, then the swaps), in every group.
+template <int LPT>
+__device__ __forceinline__ float wave_groups_sum(float v) {
+  if constexpr (LPT <= 8)
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 15, 15, true));
+  if constexpr (LPT <= 4)
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 15, 15, true));
+  if constexpr (LPT <= 16) v = butterfly<32>(v, [](float a, float b) { return a + b; });
+  if constexpr (LPT <= 32) v = butterfly<64>(v, [](float a, float b) { return a + b; });
+  return v;
+}
+
 // The softmax of one row, in powers of two on the transcendental unit: v
 // becomes 2^(v log2(e) - c) with c = max log2(e) (c's rounding cancels between
 // v and sum, the product's is inside the fma), sum its sum, lse the log-sum-
@@ -139,8 +152,8 @@ struct BalancePieces {
 };
 
 // Sums over the tokens [lo, hi), by a workgroup of kGroups groups of LPT lanes:
-// on return (after a barrier by the caller) sp[group][e] holds the sums of p,
-// sc[e] the counts, sz and sn each group's sum of lse^2 and live tokens.
+// on return (after a barrier by the caller) sp[wave][e] holds the sums of p,
+// sc[e] the counts, sz and sn each wave's sum of lse^2 and live tokens.
 template <int LPT, int V, int kGroups>
 __device__ __forceinline__ void sum_tokens(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                                            int64_t lo, int64_t hi, int E, int k, const uint8_t* __restrict__ mask,
@@ -154,24 +167,28 @@ __device__ __forceinline__ void sum_tokens(const float* __restrict__ logits, con
   int32_t n = 0;
   // the trip count is the same for a whole wave: the butterflies stay converged
   for (int64_t b = lo; b < hi; b += kGroups * U) {
+    // no load waits for another: rows and ids are read whatever the mask says
     f32x4 v[U][V];
     bool live[U];
+    int e[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t tt = b + u * kGroups + grp;
-      live[u] = tt < hi && (!mask || mask[tt] != 0);
-      const int64_t tr = live[u] ? tt : lo;
+      const int64_t tr = tt < hi ? tt : lo;
+      live[u] = tt < hi && (!mask || mask[tr] != 0);
+      e[u] = l < k ? idx[tr * k + l] : -1;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[u][i] = load4(logits + tr * E, 4 * (l + LPT * i), E);
     }
     for (int j0 = 0; j0 < k; j0 += LPT) {
-      int e[U];
+      if (j0 > 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          e[u] = live[u] && j0 + l < k ? idx[(b + u * kGroups + grp) * k + j0 + l] : -1;
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        e[u] = live[u] && j0 + l < k ? idx[(b + u * kGroups + grp) * k + j0 + l] : -1;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (e[u] >= 0 && e[u] < E) atomicAdd(&sc[e[u]], 1);
+        if (live[u] && e[u] >= 0 && e[u] < E) atomicAdd(&sc[e[u]], 1);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -188,11 +205,20 @@ __device__ __forceinline__ void sum_tokens(const float* __restrict__ logits, con
       }
     }
   }
+  z = wave_groups_sum<LPT>(z);
+  const float nf = wave_groups_sum<LPT>(float(n));  // exact: below 2^24 tokens a workgroup
 #pragma unroll
-  for (int i = 0; i < V; ++i) *reinterpret_cast<f32x4*>(sp + grp * 4 * LPT * V + 4 * (l + LPT * i)) = acc[i];
-  if (l == 0) {
-    sz[grp] = z;
-    sn[grp] = n;
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = wave_groups_sum<LPT>(acc[i][j]);
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) < LPT) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) *reinterpret_cast<f32x4*>(sp + wave * 4 * LPT * V + 4 * (l + LPT * i)) = acc[i];
+  }
+  if ((threadIdx.x & 63) == 0) {
+    sz[wave] = z;
+    sn[wave] = int32_t(nf);
   }
 }
 
@@ -200,11 +226,11 @@ template <int LPT, int V>
 __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t T, int E, int k,
     const int32_t* __restrict__ off, int S, const uint8_t* __restrict__ mask, int chunk, BalancePieces out) {
-  constexpr int kGroups = kBalThreads / LPT;
-  __shared__ __attribute__((aligned(16))) float sp[kGroups * 4 * LPT * V];
+  constexpr int kGroups = kBalThreads / LPT, kWaves = kBalThreads / 64;
+  __shared__ __attribute__((aligned(16))) float sp[kWaves * 4 * LPT * V];
   __shared__ int32_t sc[4 * LPT * V];
-  __shared__ float sz[kGroups];
-  __shared__ int32_t sn[kGroups];
+  __shared__ float sz[kWaves];
+  __shared__ int32_t sn[kWaves];
   const int tid = threadIdx.x;
   const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(T, t0 + chunk);
   int q = off ? seq_of(off, S, t0) : 0;
@@ -221,20 +247,21 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
     const int64_t piece = int64_t(blockIdx.x) + q;
     for (int e = tid; e < E; e += kBalThreads) {
       float s = 0.f;
-#pragma unroll 8
-      for (int g = 0; g < kGroups; ++g) s += sp[g * 4 * LPT * V + e];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) s += sp[w * 4 * LPT * V + e];
       out.p[piece * E + e] = s;
       out.c[piece * E + e] = sc[e];
     }
-    if (tid < 64) {  // kGroups <= 64
-      float s = tid < kGroups ? sz[tid] : 0.f;
-      int32_t m = tid < kGroups ? sn[tid] : 0;
-      s = group_sum<64>(s);
-      for (int o = 32; o > 0; o >>= 1) m += __shfl_xor(m, o);
-      if (tid == 0) {
-        out.z[piece] = s;
-        out.n[piece] = m;
+    if (tid == 0) {
+      float s = 0.f;
+      int32_t m = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        s += sz[w];
+        m += sn[w];
       }
+      out.z[piece] = s;
+      out.n[piece] = m;
     }
     __syncthreads();
   }
@@ -247,27 +274,36 @@ struct BalanceSeq {
   int32_t* n;    // [S] live tokens
 };
 
-// Sum over the workgroup's 1024 threads, in every thread.
-__device__ __forceinline__ double block_sum(double v, double* sm) {
+// Sums over the workgroup's 1024 threads, in every thread.
+template <int N>
+__device__ __forceinline__ void block_sum(double (&v)[N], double (&sm)[N][16]) {
   const int tid = threadIdx.x;
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if ((tid & 63) == 0) sm[tid >> 6] = v;
-  __syncthreads();
-  double r = 0.0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r += sm[i];
+  for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o);
+  if ((tid & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sm[i][tid >> 6] = v[i];
+  }
   __syncthreads();
-  return r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = 0.0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v[i] += sm[i][w];
+  }
 }
 
 constexpr int kSeqExperts = 32;
 
-// 32 experts x 32 pieces at a time.
+// 32 experts x 32 pieces at a time, kSeqBatch of them in flight.
+constexpr int kSeqBatch = 8;
 __global__ __launch_bounds__(1024) void balance_seq_kernel(int64_t T, int E, const int32_t* __restrict__ off,
                                                            int chunk, BalancePieces in,
                                                            int32_t* __restrict__ seq_counts,
                                                            float* __restrict__ seq_probs, BalanceSeq out) {
-  __shared__ double sm[16];
+  __shared__ double sm[2][16];
   __shared__ double sP[32][kSeqExperts + 1];
   __shared__ int32_t sC[32][kSeqExperts + 1];
   const int q = blockIdx.x, tid = threadIdx.x;
@@ -276,24 +312,33 @@ __global__ __launch_bounds__(1024) void balance_seq_kernel(int64_t T, int E, con
   const int64_t p0 = lo / chunk + q, p1 = hi > lo ? (hi - 1) / chunk + q + 1 : p0;
   const int e = blockIdx.y * kSeqExperts + (tid & 31);
   const int pl = tid >> 5;
+  double zn[2] = {0.0, 0.0};
+  for (int64_t p = p0 + tid; p < p1; p += 1024) {
+    zn[0] += in.z[p];
+    zn[1] += in.n[p];
+  }
   double P = 0.0;
   int32_t c = 0;
-  if (e < E) {
-#pragma unroll 4
-    for (int64_t p = p0 + pl; p < p1; p += 32) {
-      P += in.p[p * E + e];
-      c += in.c[p * E + e];
+  for (int64_t p = p0 + pl; p < p1; p += 32 * kSeqBatch) {
+    float x[kSeqBatch];
+    int32_t y[kSeqBatch];
+#pragma unroll
+    for (int u = 0; u < kSeqBatch; ++u) {
+      const int64_t at = (p + 32 * u < p1 ? p + 32 * u : p) * E + (e < E ? e : 0);
+      x[u] = in.p[at];
+      y[u] = in.c[at];
     }
+#pragma unroll
+    for (int u = 0; u < kSeqBatch; ++u)
+      if (e < E && p + 32 * u < p1) {
+        P += x[u];
+        c += y[u];
+      }
   }
   sP[pl][tid & 31] = P;
   sC[pl][tid & 31] = c;
-  double z = 0.0, n = 0.0;
-  for (int64_t p = p0 + tid; p < p1; p += 1024) {
-    z += in.z[p];
-    n += in.n[p];
-  }
-  z = block_sum(z, sm);
-  n = block_sum(n, sm);
+  block_sum(zn, sm);
+  const double z = zn[0], n = zn[1];
   double term = 0.0;
   if (tid < kSeqExperts) {
     P = 0.0;
@@ -324,7 +369,7 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(int E, int k, int 
                                                               const int32_t* __restrict__ seq_counts,
                                                               float* __restrict__ loss, int32_t* __restrict__ counts,
                                                               float* __restrict__ seq_scale) {
-  __shared__ double sm[16];
+  __shared__ double sm[4][16];
   __shared__ int32_t sC[16][64];
   const int tid = threadIdx.x;
   if (blockIdx.x > 0) {
@@ -344,22 +389,21 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(int E, int k, int 
     }
     return;
   }
-  double term = 0.0, z = 0.0, n = 0.0, used = 0.0;
+  double v[4] = {0.0, 0.0, 0.0, 0.0};  // the balance terms, lse^2, live tokens, sequences with any
   for (int q = tid; q < S; q += 1024) {
     const double nq = in.n[q];
-    z += in.z[q];
-    n += nq;
+    double t = 0.0;
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) t += in.term[int64_t(q) * blocks + b];
+    v[1] += in.z[q];
+    v[2] += nq;
     if (nq > 0.0) {
-      double t = 0.0;
-      for (int b = 0; b < blocks; ++b) t += in.term[int64_t(q) * blocks + b];
-      term += t * double(E) / (double(k) * nq * nq);
-      used += 1.0;
+      v[0] += t * double(E) / (double(k) * nq * nq);
+      v[3] += 1.0;
     }
   }
-  term = block_sum(term, sm);
-  z = block_sum(z, sm);
-  n = block_sum(n, sm);
-  used = block_sum(used, sm);
+  block_sum(v, sm);
+  const double term = v[0], z = v[1], n = v[2], used = v[3];
   for (int q = tid; q < S; q += 1024) {
     const double nq = in.n[q];
     seq_scale[q] = nq > 0.0 ? float(double(E) / (used * double(k) * nq * nq)) : 0.f;
@@ -379,11 +423,11 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(
     int32_t* __restrict__ counts, int32_t* __restrict__ seq_counts, float* __restrict__ seq_probs,
     float* __restrict__ seq_scale) {
   constexpr int kGroups = 1024 / LPT;
-  __shared__ __attribute__((aligned(16))) float sp[kGroups * 4 * LPT * V];
+  __shared__ __attribute__((aligned(16))) float sp[16 * 4 * LPT * V];
   __shared__ int32_t sc[4 * LPT * V];
-  __shared__ float sz[kGroups];
-  __shared__ int32_t sn[kGroups];
-  __shared__ double sm[16];
+  __shared__ float sz[16];
+  __shared__ int32_t sn[16];
+  __shared__ double sm[1][16];
   const int tid = threadIdx.x;
   const int64_t lo = off ? max(int64_t(0), int64_t(off[0])) : 0;
   const int64_t hi = off ? min(T, int64_t(off[1])) : T;
@@ -391,22 +435,26 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(
   __syncthreads();
   sum_tokens<LPT, V, kGroups>(logits, idx, lo, hi, E, k, mask, sp, sc, sz, sn);
   __syncthreads();
-  const double z = block_sum(tid < kGroups ? double(sz[tid]) : 0.0, sm);
-  const double n = block_sum(tid < kGroups ? double(sn[tid]) : 0.0, sm);
-  double P = 0.0;
+  double z = 0.0, n = 0.0, P = 0.0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    z += double(sz[w]);
+    n += double(sn[w]);
+  }
   int32_t c = 0;
   if (tid < E) {
-#pragma unroll 8
-    for (int g = 0; g < kGroups; ++g) P += sp[g * 4 * LPT * V + tid];
+#pragma unroll
+    for (int w = 0; w < 16; ++w) P += sp[w * 4 * LPT * V + tid];
     c = sc[tid];
     counts[tid] = c;
     seq_counts[tid] = c;
     seq_probs[tid] = n > 0.0 ? float(P / n) : 0.f;
   }
-  const double t = block_sum(double(c) * P, sm);
+  double t[1] = {double(c) * P};
+  block_sum(t, sm);
   if (tid == 0) {
     const bool any = n > 0.0;
-    loss[0] = any ? float(t * double(E) / (double(k) * n * n)) : 0.f;
+    loss[0] = any ? float(t[0] * double(E) / (double(k) * n * n)) : 0.f;
     loss[1] = any ? float(z / n) : 0.f;
     seq_scale[0] = any ? float(double(E) / (double(k) * n * n)) : 0.f;
     seq_scale[1] = any ? float(1.0 / n) : 0.f;

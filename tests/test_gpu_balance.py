@@ -74,6 +74,8 @@ CASES = [
     (40000, 33, 2, 3, 5, 0.1, 0, True),       # chunks of 64 tokens
     (5000, 40, 3, 2500, 7, 0.1, 0, True),     # more sequences than threads
     (64, 1024, 3, 1, 9, 0.5, 0, True),
+    (1024, 64, 4, 1, 13, 0.1, 0, True),       # the most that one workgroup does
+    (1025, 64, 4, 1, 13, 0.1, 0, True),
     (32, 1000, 3, 1, 0, 0.1, 7, False),       # one workgroup, all its threads' experts
 ]
 
