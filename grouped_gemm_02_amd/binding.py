@@ -175,19 +175,17 @@ def _here(stream, *wanted) -> list:
     """_want for each (tensor, name, dtype, numel), and the tensor must be on the
     current device, whose stream the call is enqueued on. Returns their
     addresses and the stream's handle."""
-    dev, at = -1, []
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None  # without it there is no GPU tensor
+    at = []
     for t, name, dtype, numel in wanted:
-        if not isinstance(t, torch.Tensor):
+        if t is None or type(t) is int:
             at.append(t)
-            continue
-        if dev < 0 and t.is_cuda:
-            dev = torch.cuda.current_device()
-        if t.get_device() == dev >= 0 and t.dtype is dtype and t.numel() >= numel and t.is_contiguous():
+        elif t.get_device() == dev and t.dtype is dtype and t.numel() >= numel and t.is_contiguous():
             at.append(t.data_ptr())
-            continue
-        _want(t, name, dtype, numel)
-        raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{dev}")
-    at.append(torch._C._cuda_getCurrentRawStream(dev) if stream is None and dev >= 0 else _stream(stream))
+        else:
+            _want(t, name, dtype, numel)
+            raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{dev}")
+    at.append(_stream(stream) if dev is None or stream is not None else torch._C._cuda_getCurrentRawStream(dev))
     return at
 
 

@@ -728,10 +728,10 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Flo
 // ------------------------------------------------------------------ plan
 
 // Big tiles of a product from which they are used: two rounds of the 256 CUs.
-// Gram / square / update in us, big against small tiles: 768 / 768 / 3072 big
-// tiles (128 matrices 768 x 2048) 180 : 215, 111 : 116, 403 : 458; 336 / 336 /
-// 768 (16 of 1536 x 2048) 105 : 108, 91 : 81, 179 : 197; 60 / 60 / 96 (6 of
-// 777 x 1000) 26 : 15, 28 : 15, 29 : 21. Eight stages instead of four for small
+// Gram / square / update in us, big against small tiles: 128 matrices 768 x 2048
+// (6, 6 and 24 big tiles each) 180 : 215, 111 : 116, 403 : 458; 16 of 1536 x 2048
+// (21, 21, 48) 105 : 108, 91 : 81, 179 : 197; 6 of 777 x 1000 (10, 10, 16)
+// 26 : 15, 28 : 15, 29 : 21. Eight stages instead of four for small
 // tiles of one workgroup a CU changed nothing: the turns of a lone workgroup are
 // as long as its LDS reads and MFMAs one after the other.
 constexpr int64_t kBigTiles = 512;
