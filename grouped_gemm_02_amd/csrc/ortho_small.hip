@@ -345,12 +345,35 @@ int row_blocks(const OrthoArgs& a) { return ((a.R < a.C ? a.R : a.C) + 31) / 32;
 
 }  // namespace
 
-// P = a + b x + c x^2 must not leave [-a, a] for x in [0, 2] (squared singular
-// values of the iterates), and a^steps must leave Q the bits it needs.
+namespace {
+
+// The largest |s (a + b s^2 + c s^4)| for s in [0, r], or r if that is larger.
+double grown(const OrthoArgs& a, double r) {
+  double most = r;
+  auto at = [&](double x) { most = std::fmax(most, std::fabs(std::sqrt(x) * (a.a + x * (a.b + x * a.c)))); };
+  at(r * r);
+  const double p = 3.0 * a.b, q = 5.0 * a.c, disc = p * p - 4.0 * q * a.a;  // a + 3 b x + 5 c x^2 = 0
+  if (q == 0.0) {
+    if (p != 0.0 && -a.a / p > 0.0 && -a.a / p < r * r) at(-a.a / p);
+  } else if (disc >= 0.0) {
+    for (double x : {(-p - std::sqrt(disc)) / (2.0 * q), (-p + std::sqrt(disc)) / (2.0 * q)})
+      if (x > 0.0 && x < r * r) at(x);
+  }
+  return most;
+}
+
+}  // namespace
+
+// The squared singular values of the iterates must stay in [0, 2] (they start in
+// [0, 1]), P = a + b x + c x^2 in [-a, a] there, and a^steps must leave Q the bits it
+// needs.
 bool small_fits(const OrthoArgs& a) {
   if ((a.R < a.C ? a.R : a.C) > kSmallSide) return false;
   if (!(a.a > 0.f && a.a <= 30.f && a.b <= 0.f && a.c >= 0.f) || std::pow(double(a.a), a.steps) > 1000.0) return false;
   if (2.f * a.c > -a.b) return false;                                  // P(2) <= a, so P <= a on [0, 2]
+  double r = 1.0;
+  for (int i = 1; i < a.steps && r * r <= 2.0; ++i) r = grown(a, r);
+  if (!(r * r <= 2.0)) return false;
   const float low = a.c > 0.f && -a.b < 4.f * a.c ? a.a - a.b * a.b / (4.f * a.c)  // the vertex lies in [0, 2]
                                                   : a.a + 2.f * a.b + 4.f * a.c;
   return low >= -a.a;

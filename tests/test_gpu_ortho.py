@@ -131,6 +131,20 @@ def test_magnitudes_at_the_ends_of_the_types(B, R, C, dtype):
         assert _off(_f64(U), oo.orthogonalize(_f64(G[rows]), eps=s.eps)) <= TOL
 
 
+@pytest.mark.parametrize("coeffs,steps", [((17.0, 0.0, 0.0), 2), ((2.0, -0.3, 0.0), 4), ((2.5, -2.0, 0.5), 5)])
+def test_polynomials_that_let_small_matrices_grow(B, coeffs, steps):
+    """Singular values well past 1, elements below 2."""
+    print(f"case ortho polynomial {coeffs} {steps}", flush=True)
+    G = torch.zeros((2, 96, 128), device=DEV)
+    G[0, 5] = 1.0
+    G[1] = torch.randn((96, 128), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    G = G.bfloat16()
+    s = B.make_ortho_shape(2, 96, 128, steps=steps, coeffs=coeffs)
+    U = B.orthogonalize(B.OrthoBuffers.allocate(s), G)
+    want = oo.orthogonalize(_f64(G), steps, tuple(float(np.float32(c)) for c in coeffs))
+    assert np.isfinite(want).all() and _off(_f64(U), want) <= TOL
+
+
 def test_matrices_do_not_depend_on_their_stack(B):
     """A matrix gives the same bits alone, in a stack, in place, and again."""
     for E, R, C in ((6, 200, 300), (5, 64, 100), (5, 300, 200)):
