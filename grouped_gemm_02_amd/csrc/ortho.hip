@@ -7,7 +7,8 @@
 //   ortho_norm    (momentum step and) the sum of squares, in 64 bits
 //   ortho_load    X0 = G times a power of two, as fp16 value + E4M3 remainder
 //   then per step
-//   ortho_gram    A = X X^T
+//   ortho_gram    A = X X^T (few tiles over a long axis: in parts, ortho_gram_part
+//                 and ortho_gram_join)
 //   ortho_square  B = b A + c A A (A is symmetric, so A A = A A^T)
 //   ortho_update  X' = a X + B X
 // The last update writes U, or updates the weights, instead of X'. Wide matrices
@@ -37,52 +38,49 @@ using namespace ortho;
 namespace {
 
 // Partial sums of squares and maxima, after the momentum step if there is one.
-// HBM-bound: 16-byte accesses where a matrix is a whole number of them (128 of
-// 768 x 2048 in bf16: 403 MB in 87 us, 4.6 TB/s).
+// HBM-bound (128 of 768 x 2048 in bf16: 403 MB in 87 us, 4.6 TB/s).
 __global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(OrthoIn in, int64_t count,
                                                                   NormPart* __restrict__ part) {
   __shared__ double sm[kNormThreads / 64];
   __shared__ float mx[kNormThreads / 64];
   const int64_t base = int64_t(blockIdx.y) * count;
   const int64_t first = int64_t(blockIdx.x) * kNormThreads + threadIdx.x;
-  constexpr int64_t kStep = int64_t(kNormParts) * kNormThreads;
+  const int64_t step = int64_t(gridDim.x) * kNormThreads;
   double s = 0.0;
   float m = 0.f;  // fmaxf drops a NaN; the sum keeps it
-  if ((count & 7) == 0) {
 #pragma unroll 2
-    for (int64_t i = first * 8; i < count; i += kStep * 8) {
-      float x[8];
-      grad8(in, base + i, x);
-      if (in.mom) {
-        f32x4* p = reinterpret_cast<f32x4*>(in.mom + base + i);
-        f32x4 a = p[0], b = p[1];
+  for (int64_t i = first * 8; i + 8 <= count; i += step * 8) {
+    float x[8];
+    grad8(in, base + i, x);
+    if (in.mom) {
+      f32x4u* p = reinterpret_cast<f32x4u*>(in.mom + base + i);
+      f32x4 a = p[0], b = p[1];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          a[t] = in.mu * a[t] + x[t];
-          b[t] = in.mu * b[t] + x[4 + t];
-          x[t] = in.nesterov ? x[t] + in.mu * a[t] : a[t];
-          x[4 + t] = in.nesterov ? x[4 + t] + in.mu * b[t] : b[t];
-        }
-        p[0] = a;
-        p[1] = b;
+      for (int t = 0; t < 4; ++t) {
+        a[t] = in.mu * a[t] + x[t];
+        b[t] = in.mu * b[t] + x[4 + t];
+        x[t] = in.nesterov ? x[t] + in.mu * a[t] : a[t];
+        x[4 + t] = in.nesterov ? x[4 + t] + in.mu * b[t] : b[t];
       }
+      p[0] = a;
+      p[1] = b;
+    }
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        s += double(x[t]) * double(x[t]);
-        m = fmaxf(m, fabsf(x[t]));
-      }
+    for (int t = 0; t < 8; ++t) {
+      s += double(x[t]) * double(x[t]);
+      m = fmaxf(m, fabsf(x[t]));
     }
-  } else {
-    for (int64_t i = first; i < count; i += kStep) {
-      float x = grad_at(in.grad, in.f32, base + i);
-      if (in.mom) {
-        const float v = in.mu * in.mom[base + i] + x;
-        in.mom[base + i] = v;
-        x = in.nesterov ? x + in.mu * v : v;
-      }
-      s += double(x) * double(x);
-      m = fmaxf(m, fabsf(x));
+  }
+  if (first < (count & 7)) {  // what is left of a matrix past its last eight
+    const int64_t i = (count & ~int64_t(7)) + first;
+    float x = grad_at(in.grad, in.f32, base + i);
+    if (in.mom) {
+      const float v = in.mu * in.mom[base + i] + x;
+      in.mom[base + i] = v;
+      x = in.nesterov ? x + in.mu * v : v;
     }
+    s += double(x) * double(x);
+    m = fmaxf(m, fabsf(x));
   }
   for (int o = 32; o > 0; o >>= 1) {
     s += __shfl_xor(s, o);
@@ -99,7 +97,7 @@ __global__ __launch_bounds__(kNormThreads) void ortho_norm_kernel(OrthoIn in, in
       s += sm[i];
       m = fmaxf(m, mx[i]);
     }
-    part[int64_t(blockIdx.y) * kNormParts + blockIdx.x] = NormPart{s, m, 0.f};
+    part[int64_t(blockIdx.y) * gridDim.x + blockIdx.x] = NormPart{s, m, 0.f};
   }
 }
 
@@ -133,35 +131,24 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoIn in, OrthoDims d
   const int e = blockIdx.z, r0 = blockIdx.y * kLoadTile, c0 = blockIdx.x * kLoadTile;
   int p;
   float s;
-  matrix_scale(part + int64_t(e) * kNormParts, eps, &p, &s);
+  matrix_scale(part + int64_t(e) * d.parts, d.parts, eps, &p, &s);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) scale[e] = s;
   // a, b: row and column of G inside the tile
   const int g0 = d.tall ? c0 : r0, h0 = d.tall ? r0 : c0;
-  if ((d.C & 7) == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int a = 32 * i + int(threadIdx.x >> 3), b = int(threadIdx.x & 7) * 8;
-      float x[8];
+  for (int i = 0; i < 2; ++i) {
+    const int a = 32 * i + int(threadIdx.x >> 3), b = int(threadIdx.x & 7) * 8;
+    float x[8];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) x[t] = 0.f;
-      if (g0 + a < d.R && h0 + b < d.C) {
-        input8(in, (int64_t(e) * d.R + g0 + a) * d.C + h0 + b, x);
+    for (int t = 0; t < 8; ++t) x[t] = 0.f;
+    const int left = g0 + a < d.R ? d.C - (h0 + b) : 0;
+    if (left > 0) {
+      input_row(in, (int64_t(e) * d.R + g0 + a) * d.C + h0 + b, left, x);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) x[t] = s == s ? ldexpf(x[t], p) : NAN;
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t) tile[d.tall ? b + t : a][d.tall ? a : b + t] = x[t];
+      for (int t = 0; t < 8; ++t) x[t] = s == s ? ldexpf(x[t], p) : NAN;
     }
-  } else {
-    for (int i = threadIdx.x; i < kLoadTile * kLoadTile; i += 256) {
-      const int a = i / kLoadTile, b = i % kLoadTile;
-      float x = 0.f;
-      if (g0 + a < d.R && h0 + b < d.C) {
-        x = input_at(in, (int64_t(e) * d.R + g0 + a) * d.C + h0 + b);
-        x = s == s ? ldexpf(x, p) : NAN;
-      }
-      tile[d.tall ? b : a][d.tall ? a : b] = x;
-    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) tile[d.tall ? b + t : a][d.tall ? a : b + t] = x[t];
   }
   __syncthreads();
 #pragma unroll
@@ -537,6 +524,88 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_gram_kernel(const _Float
   store_symmetric<T>(acc, s * s, A + e * d.mp * d.mp, d.mp, at, nullptr);
 }
 
+// The same of few tiles over a long axis: each part of the k loop is a workgroup of
+// its own, [matrix][tile][part][wave][2 x 2 sub-tiles][4][lane][4] in fp32.
+__global__ __launch_bounds__(Small::kThreads, 2) void ortho_gram_part_kernel(const _Float16* __restrict__ X, OrthoDims d,
+                                                                             int tiles, int parts, int part_slabs,
+                                                                             float* __restrict__ sums) {
+  using T = Small;
+  int64_t e;
+  int t, bi, bj;
+  if (!take_tile(d.E * tiles * parts, tiles * parts, &e, &t)) return;
+  const int part = t / tiles;  // the tiles of a part follow each other: they share its columns
+  t %= tiles;
+  sym_tile(t, &bi, &bj);
+  const _Float16* Xe = X + e * d.mp * d.np;
+  Operand P = operand_k(Xe, d.mp, d.np, bi * T::kRows), Q = operand_k(Xe, d.mp, d.np, bj * T::kCols);
+  P.blk += uint32_t(part * part_slabs) * P.slab;
+  Q.blk += uint32_t(part * part_slabs) * Q.slab;
+  const int nk = min(part_slabs, d.np / kBK - part * part_slabs);
+  Acc<T> acc;
+  first_slabs<T>(P, Q, nk);
+  acc.zero();
+  slabs<T, false, true>(P, Q, nk, acc);
+  float* out = sums + (((e * tiles + t) * parts + part) * T::kWaves + wave_id()) * 4096;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(out + (((2 * i + j) * 4 + g) * 64 + lane_id()) * 4) =
+            f32x4{acc.c[i][j][4 * g], acc.c[i][j][4 * g + 1], acc.c[i][j][4 * g + 2], acc.c[i][j][4 * g + 3]};
+}
+
+// Adds the parts, in their order: a wave for each 32 x 32 sub-tile.
+constexpr int kJoinWaves = 4;
+__global__ __launch_bounds__(64 * kJoinWaves) void ortho_gram_join_kernel(const float* __restrict__ sums, OrthoDims d,
+                                                                          int tiles, int parts,
+                                                                          const float* __restrict__ scale,
+                                                                          _Float16* __restrict__ A) {
+  using T = Small;
+  constexpr int kRow = 40;  // halves: 16-byte chunks of the mirror image's rows
+  __shared__ __attribute__((aligned(16))) _Float16 mirror[kJoinWaves][32 * kRow];
+  const int64_t id = int64_t(blockIdx.x) * kJoinWaves + wave_id();
+  const int sub = int(id & 15), lane = lane_id();
+  const int64_t tile = id >> 4, e = tile / tiles;  // 16 sub-tiles a tile: the grid is exact
+  int bi, bj;
+  sym_tile(int(tile % tiles), &bi, &bj);
+  const int wave = sub >> 2, i = (sub >> 1) & 1, j = sub & 1;
+  const float* src = sums + (tile * parts * T::kWaves + wave) * 4096 + (sub & 3) * 1024 + lane * 4;
+  f32x4 c[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) c[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) c[g] += *reinterpret_cast<const f32x4*>(src + int64_t(p) * T::kWaves * 4096 + g * 256);
+  const float s = scale ? scale[e] : 1.f / kXScale;
+  const float f = s * s;
+  const int row0 = bi * T::kRows + (wave / T::WN) * 64 + 32 * i, col0 = bj * T::kCols + (wave % T::WN) * 64 + 32 * j;
+  _Float16* out = A + e * d.mp * d.mp;
+  _Float16* im = mirror[wave_id()];
+  u32x2 w[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    w[g] = u32x2{pack_f16(c[g][0] * f, c[g][1] * f), pack_f16(c[g][2] * f, c[g][3] * f)};
+    // row lane % 32, columns 8 g + 4 (lane / 32) + 0 .. 3
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      im[(8 * g + 4 * (lane >> 5) + q) * kRow + (lane & 31)] =
+          __builtin_bit_cast(_Float16, uint16_t(w[g][q >> 1] >> (16 * (q & 1))));
+  }
+  put_subtile(w, out, d.mp, row0, col0);
+  if (bi == bj) return;
+  image_sync();
+  // the mirrored sub-tile: rows col0 + n, 16-byte chunks of eight columns
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int n = lane & 31, chunk = 2 * q + (lane >> 5);
+    *reinterpret_cast<u32x4*>(out + block_at(d.mp, col0 / 32, row0 / 16 + (chunk >> 1)) + in_block(n, chunk & 1)) =
+        *reinterpret_cast<const u32x4*>(im + n * kRow + 8 * chunk);
+  }
+}
+
 // A product of m x m matrices that are polynomials of X X^T, so symmetric and
 // commuting: out = f (P Q^T + (r1 + d1) M1 + r2 M2) in fp16, d1 a diagonal (or
 // NULL), M2 NULL if there is none; on the diagonal also re (e1 + e2) (or NULL).
@@ -739,13 +808,39 @@ constexpr int64_t kBigTiles = 512;
 struct OrthoPlan {
   OrthoDims d;
   int64_t group;                            // matrices at a time
-  size_t part, scale, X[2], Xl[2], M[3], diag, total;  // workspace offsets
+  size_t part, scale, X[2], Xl[2], M[3], diag, sums, total;  // workspace offsets
+  int gram_parts, gram_part_slabs;          // of the k loop of X X^T
   size_t small;                             // of the small matrices' path
 };
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 constexpr int64_t kSmallGroup = 1024;
+
+// Elements of a matrix from which its norm is 256 partial sums instead of 64: one of
+// 1024 x 4096 in 7.5 us instead of 16.4; for 128 of 768 x 2048 ortho_norm would gain 5
+// us of 87 and ortho_load, which adds them, lose as much.
+constexpr int64_t kManyElements = 1 << 21;
+
+// Parts of the k loop of X X^T: enough for two workgroups a CU, of 512 columns at
+// least, where the tiles leave most CUs without work. In us a call, whole and in
+// parts: 1 of 256 x 16384 533 : 176, 3 of 300 x 4000 238 : 170, 1 of 1024 x 4096 (36
+// tiles) 302 : 248, 10 of 256 x 2048 (30) 174 : 153, 20 of 200 x 1500 (60) 181 : 176;
+// 2 of 1024 x 2048 (72) 241 : 245, 30 of 256 x 2048 (90) 234 : 263; 512 x 1024 152 : 150.
+// (A matrix of a stack whose products are split may differ in its last bits
+// from itself in a larger stack.)
+constexpr int64_t kSplitTiles = 64;
+constexpr int kSplitSlabs = 16, kSplitFrom = 48;
+void gram_split(const OrthoArgs& a, OrthoPlan* p) {
+  const int nk = p->d.np / kBK;
+  const int64_t tiles = a.E * sym_tiles(p->d.mp, Small::kRows);
+  p->gram_parts = 1;
+  p->gram_part_slabs = nk;
+  if (a.E > p->group || a.E < 1 || tiles > kSplitTiles || nk < kSplitFrom) return;
+  const int most = int(512 / tiles) < nk / kSplitSlabs ? int(512 / tiles) : nk / kSplitSlabs;
+  p->gram_part_slabs = ((nk + most - 1) / most + 3) / 4 * 4;  // turns of four slabs
+  p->gram_parts = (nk + p->gram_part_slabs - 1) / p->gram_part_slabs;
+}
 
 OrthoPlan ortho_plan(const OrthoArgs& a) {
   OrthoPlan p{};
@@ -757,10 +852,11 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   d.n = d.tall ? a.R : a.C;
   d.mp = (d.m + 127) / 128 * 128;
   d.np = (d.n + 127) / 128 * 128;
+  d.parts = int64_t(d.R) * d.C >= kManyElements ? 256 : 64;
   if (small_fits(a)) {
     p.group = a.E < 1 ? 1 : a.E > kSmallGroup ? kSmallGroup : a.E;
     p.part = 0;
-    p.small = up256(size_t(p.group) * kNormParts * sizeof(NormPart));
+    p.small = up256(size_t(p.group) * d.parts * sizeof(NormPart));
     p.total = p.small + small_plan(a, p.group).total;
     return p;
   }
@@ -776,7 +872,7 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   // The products read up to 128 rows past a matrix (as zeros: the buffer
   // resource ends with it); the m x m matrices are followed by X, each X by its
   // remainders.
-  p.part = o;  o = up256(o + size_t(p.group) * kNormParts * sizeof(NormPart));
+  p.part = o;  o = up256(o + size_t(p.group) * d.parts * sizeof(NormPart));
   p.scale = o; o = up256(o + size_t(p.group) * 4);
   p.diag = o;  o = up256(o + size_t(p.group) * d.mp * 4 * 3);
   for (int i = 0; i < 3; ++i) {
@@ -786,6 +882,9 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
     p.X[i] = o;  o = up256(o + size_t(p.group) * x * 2);
     p.Xl[i] = o; o = up256(o + size_t(p.group) * x);
   }
+  gram_split(a, &p);
+  p.sums = o;
+  if (p.gram_parts > 1) o = up256(o + size_t(p.group) * sym_tiles(d.mp, Small::kRows) * p.gram_parts * Small::kRows * Small::kCols * 4);
   p.total = o;
   return p;
 }
@@ -868,6 +967,19 @@ struct OrthoSteps {
   template <class T>
   void gram(int updates, _Float16* out) const {
     const int tiles = sym_tiles(d.mp, T::kRows);
+    if constexpr (T::kRows == Small::kRows) {
+      if (p.gram_parts > 1) {
+        {
+          TimedLaunch tl(timer, "ortho_gram_part", st);
+          hipLaunchKernelGGL(ortho_gram_part_kernel, dim3(grid_of(d.E * tiles * p.gram_parts)), dim3(T::kThreads), 0, st,
+                             at<_Float16>(p.X[updates & 1]), d, tiles, p.gram_parts, p.gram_part_slabs, at<float>(p.sums));
+        }
+        TimedLaunch tl(timer, "ortho_gram_join", st);
+        hipLaunchKernelGGL(ortho_gram_join_kernel, dim3(unsigned(d.E * tiles * 16 / kJoinWaves)), dim3(64 * kJoinWaves), 0,
+                           st, at<float>(p.sums), d, tiles, p.gram_parts, updates == 0 ? at<float>(p.scale) : nullptr, out);
+        return;
+      }
+    }
     TimedLaunch tl(timer, "ortho_gram", st);
     hipLaunchKernelGGL(ortho_gram_kernel<T>, dim3(grid_of(d.E * tiles)), dim3(T::kThreads), 0, st,
                        at<_Float16>(p.X[updates & 1]), d, tiles, updates == 0 ? at<float>(p.scale) : nullptr, out);
@@ -933,7 +1045,7 @@ hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipS
                      t.momentum ? t.momentum + e0 * count : nullptr, t.mu, t.nesterov};
     {
       TimedLaunch tl(timer, "ortho_norm", st);
-      hipLaunchKernelGGL(ortho_norm_kernel, dim3(kNormParts, ge), dim3(kNormThreads), 0, st, in, count, part);
+      hipLaunchKernelGGL(ortho_norm_kernel, dim3(unsigned(d.parts), ge), dim3(kNormThreads), 0, st, in, count, part);
     }
     if (small_fits(a)) {
       const hipError_t e = launch_small(a, in, d, part, target_of(t, e0 * count), base + p.small, st, timer);

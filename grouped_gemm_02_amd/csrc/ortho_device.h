@@ -13,7 +13,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kNormThreads = 256;
-constexpr int kNormParts = 64;      // partial sums (and maxima) per matrix
+// Vectors at any address of their elements: the caller's rows begin anywhere.
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
 constexpr int kLoadTile = 64;
 // An iterate is stored times 2^15 (its elements stay below 2, fp16 ends at
 // 65504), X0 times the power of two that takes its largest element to [2^14,
@@ -28,6 +31,7 @@ struct OrthoDims {
   int m, n;    // smaller, larger side
   int mp, np;  // padded
   bool tall;   // R > C: X = G^T
+  int parts;   // partial sums of the norm: 64 or 256
 };
 
 // X, A and B live in the workspace in blocks of 32 rows x 16 columns (1 KiB), the
@@ -60,10 +64,10 @@ struct OrthoIn {
   bool nesterov;
 };
 
-// Eight neighbouring gradient values (16-byte aligned).
+// Eight neighbouring gradient values.
 __device__ __forceinline__ void grad8(const OrthoIn& in, int64_t i, float (&x)[8]) {
   if (in.f32) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(in.grad) + i);
+    const f32x4u* p = reinterpret_cast<const f32x4u*>(static_cast<const float*>(in.grad) + i);
     const f32x4 a = p[0], b = p[1];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -71,7 +75,7 @@ __device__ __forceinline__ void grad8(const OrthoIn& in, int64_t i, float (&x)[8
       x[4 + t] = b[t];
     }
   } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(in.grad) + i);
+    const u32x4 a = *reinterpret_cast<const u32x4u*>(static_cast<const uint16_t*>(in.grad) + i);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       x[2 * t] = bf16_lo(a[t]);
@@ -88,13 +92,24 @@ __device__ __forceinline__ float input_at(const OrthoIn& in, int64_t i) {
 __device__ __forceinline__ void input8(const OrthoIn& in, int64_t i, float (&x)[8]) {
   if (!in.mom || in.nesterov) grad8(in, i, x);
   if (in.mom) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(in.mom + i);
+    const f32x4u* p = reinterpret_cast<const f32x4u*>(in.mom + i);
     const f32x4 a = p[0], b = p[1];
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       const float m = t < 4 ? a[t & 3] : b[t & 3];
       x[t] = in.nesterov ? x[t] + in.mu * m : m;
     }
+  }
+}
+
+// The same of a row's end: `left` of them exist, the others are not touched.
+__device__ __forceinline__ void input_row(const OrthoIn& in, int64_t i, int left, float (&x)[8]) {
+  if (left >= 8) {
+    input8(in, i, x);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (t < left) x[t] = input_at(in, i + t);
   }
 }
 
@@ -106,10 +121,19 @@ struct NormPart {
 };
 
 // The exponent p of X0 = G 2^p, and s = 1 / ((|G| + eps) 2^p), in every lane.
-static_assert(kNormParts == 64, "a lane per partial sum");
-__device__ __forceinline__ void matrix_scale(const NormPart* __restrict__ part, float eps, int* p, float* s) {
+__device__ __forceinline__ void matrix_scale(const NormPart* __restrict__ part, int parts, float eps, int* p, float* s) {
   double q = part[lane_id()].sum;
   float m = part[lane_id()].amax;
+  if (parts > 64) {
+    NormPart n[3];  // 256 parts, read at once
+#pragma unroll
+    for (int i = 0; i < 3; ++i) n[i] = part[64 * (i + 1) + lane_id()];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      q += n[i].sum;
+      m = fmaxf(m, n[i].amax);
+    }
+  }
   for (int o = 32; o > 0; o >>= 1) {
     q += __shfl_xor(q, o);
     m = fmaxf(m, __shfl_xor(m, o));
@@ -214,11 +238,12 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_f
 
 // Eight consecutive elements of the result at element `at` of matrix storage:
 // v holds bf16 values (U) or fp16 values (the step of W). Only `count` of
-// them exist; rows of whole 16-byte pieces (vec) go at once.
-__device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, const u32x4& v, int count, bool vec) {
+// them exist; eight go at once.
+__device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, const u32x4& v, int count) {
+  const bool vec = count >= 8;
   if (out.U) {
     if (vec) {
-      *reinterpret_cast<u32x4*>(out.U + at) = v;
+      *reinterpret_cast<u32x4u*>(out.U + at) = v;
     } else {
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -229,15 +254,15 @@ __device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, cons
   float w[8];
   if (vec) {
     if (out.master) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(out.master + at);
-      const f32x4 b = *reinterpret_cast<const f32x4*>(out.master + at + 4);
+      const f32x4 a = *reinterpret_cast<const f32x4u*>(out.master + at);
+      const f32x4 b = *reinterpret_cast<const f32x4u*>(out.master + at + 4);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         w[t] = a[t];
         w[4 + t] = b[t];
       }
     } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(out.W + at);
+      const u32x4 a = *reinterpret_cast<const u32x4u*>(out.W + at);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         w[2 * t] = bf16_lo(a[t]);
@@ -252,10 +277,10 @@ __device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, cons
   for (int t = 0; t < 8; ++t) w[t] = out.keep * w[t] - out.step * half_of(v[t >> 1], t & 1);
   if (vec) {
     if (out.master) {
-      *reinterpret_cast<f32x4*>(out.master + at) = f32x4{w[0], w[1], w[2], w[3]};
-      *reinterpret_cast<f32x4*>(out.master + at + 4) = f32x4{w[4], w[5], w[6], w[7]};
+      *reinterpret_cast<f32x4u*>(out.master + at) = f32x4{w[0], w[1], w[2], w[3]};
+      *reinterpret_cast<f32x4u*>(out.master + at + 4) = f32x4{w[4], w[5], w[6], w[7]};
     }
-    *reinterpret_cast<u32x4*>(out.W + at) = u32x4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
+    *reinterpret_cast<u32x4u*>(out.W + at) = u32x4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
                                                   pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
   } else {
 #pragma unroll
@@ -276,13 +301,13 @@ __device__ __forceinline__ void put_image(const OrthoOut& out, const uint16_t* i
     if (!d.tall) {
       const int r = row0 + 8 * q + (lane >> 3), c = col0 + 8 * (lane & 7);
       const u32x4 v = image_row(im, 8 * q + (lane >> 3), lane & 7);
-      if (r < d.m && c < d.n) put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c, (d.C & 7) == 0);
+      if (r < d.m && c < d.n) put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c);
     } else {
       // 16 columns of X (rows of the result) x four pieces of 8 rows: 64 bytes a row
       const int r0 = 32 * (q & 1) + 8 * (lane >> 4), n0 = 16 * (q >> 1);
       const int r = row0 + r0, c = col0 + n0 + (lane & 15);
       const u32x4 v = image_col(im, r0, n0);
-      if (r < d.m && c < d.n) put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r, (d.C & 7) == 0);
+      if (r < d.m && c < d.n) put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r);
     }
   }
 }

@@ -107,13 +107,7 @@ __device__ __forceinline__ void load_columns(const OrthoIn& in, const OrthoDims&
     const int gr = d.tall ? c0 + c : r, gc = d.tall ? r : c0 + c;
     if (gr < d.R && gc < d.C) {
       const int64_t at = (e * d.R + gr) * d.C + gc;
-      if ((d.C & 7) == 0) {
-        input8(in, at, x);
-      } else {
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (gc + t < d.C) x[t] = input_at(in, at + t);
-      }
+      input_row(in, at, d.C - gc, x);
 #pragma unroll
       for (int t = 0; t < 8; ++t) x[t] = finite ? ldexpf(x[t], p) : NAN;
     }
@@ -153,7 +147,7 @@ __global__ __launch_bounds__(64 * kWaves<NB>) void ortho_small_gram_kernel(Ortho
   const int64_t e = blockIdx.y;
   int p;
   float s;
-  matrix_scale(part + e * kNormParts, eps, &p, &s);
+  matrix_scale(part + e * d.parts, d.parts, eps, &p, &s);
   const bool finite = s == s;
   f32x16 acc;
 #pragma unroll
@@ -187,14 +181,14 @@ __global__ __launch_bounds__(64 * kWaves<NB>) void ortho_small_gram_kernel(Ortho
 // holds P.
 template <int NB>
 __global__ __launch_bounds__(64 * kWaves<NB>) void ortho_small_steps_kernel(const float* __restrict__ gram, int parts,
-                                                                     const NormPart* __restrict__ norm, float eps,
+                                                                     const NormPart* __restrict__ norm, int norms, float eps,
                                                                      int steps, float ca, float cb, float cc,
                                                                      _Float16* __restrict__ Qout) {
   __shared__ __attribute__((aligned(16))) Pairs<NB> M1, M2;
   const int64_t e = blockIdx.x;
   int p;
   float s;
-  matrix_scale(norm + e * kNormParts, eps, &p, &s);
+  matrix_scale(norm + e * norms, norms, eps, &p, &s);
   f32x16 H, Q, P;
 #pragma unroll
   for (int r = 0; r < 16; ++r) H[r] = Q[r] = P[r] = 0.f;
@@ -265,7 +259,7 @@ __global__ __launch_bounds__((NB + 1) / 2 * 64) void ortho_small_apply_kernel(Or
   const int c0 = blockIdx.x * kSub;
   int p;
   float s;
-  matrix_scale(part + e * kNormParts, eps, &p, &s);
+  matrix_scale(part + e * d.parts, d.parts, eps, &p, &s);
   load_columns<NB, false, LO, kApply * 64>(in, d, e, c0, p, s == s, hi, lo);
   __syncthreads();
   constexpr int kHalves = Pairs<NB>::kBlocks * kBlock;
@@ -331,7 +325,7 @@ hipError_t run(const OrthoArgs& a, const OrthoIn& in, const OrthoDims& d, const 
   }
   {
     TimedLaunch tl(timer, "ortho_small_steps", st);
-    hipLaunchKernelGGL(ortho_small_steps_kernel<NB>, dim3(E), dim3(64 * kWaves<NB>), 0, st, gram, p.parts, part, a.eps, a.steps,
+    hipLaunchKernelGGL(ortho_small_steps_kernel<NB>, dim3(E), dim3(64 * kWaves<NB>), 0, st, gram, p.parts, part, d.parts, a.eps, a.steps,
                        a.a, a.b, a.c, q);
   }
   TimedLaunch tl(timer, "ortho_small_apply", st);

@@ -71,6 +71,9 @@ CASES = [
     (1, 777, 400, "f32", 1, 5, oo.COEFFS),
     (1, 200, 299, "bf16", None, 2, oo.COEFFS),
     (1, 16384, 130, "bf16", None, 5, oo.COEFFS),
+    (2, 334, 3542, "bf16", None, 5, oo.COEFFS),       # X X^T in parts, the last one shorter
+    (1, 1030, 140, "f32", None, 5, oo.COEFFS),        # two parts
+    (3, 400, 1300, "bf16", 1, 5, oo.COEFFS),
     (1, 40, 16384, "f32", None, 5, oo.COEFFS),
     (2, 200, 384, "bf16", None, 3, (1.5, -0.5, 0.0)),
     (1, 200, 300, "bf16", None, 2, oo.COEFFS),
