@@ -37,11 +37,15 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 // (A workgroup that takes several sequences in turn: 4 to 7 us each.)
 constexpr int64_t kSmallWork = 65536;
 
-int balance_chunk_tokens(int64_t T) {
-  // 32 tokens a workgroup until 1024 workgroups are reached, then more
-  int64_t c = (T + 1023) / 1024;
-  c = (c + 31) / 32 * 32;
-  return int(c < 32 ? 32 : c);
+// Chunks of four experts a lane has of a row.
+constexpr int lane_chunks(int E) { return E <= 256 ? 1 : E <= 512 ? 2 : 4; }
+
+int balance_chunk_tokens(int64_t T, int E) {
+  // two rounds of loads a workgroup until 1024 workgroups are reached, then more (32
+  // tokens for any E: 3000 x 805 20.1 us instead of 16.8, 30 x 805 20.5 instead of 15.0)
+  const int base = 32 / lane_chunks(E);
+  const int64_t c = ((T + 1023) / 1024 + base - 1) / base * base;
+  return int(c < base ? base : c);
 }
 
 // Four logits of a row from expert e0 on; experts past E are -inf.
@@ -464,11 +468,13 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(
 // Rows a group of the backward has in flight, and the tokens of a workgroup.
 // 131,072 x 256: two rows and 32 tokens 71 us, four rows 83, two rows and 64
 // tokens 85, four rows and 128 tokens 113 (fewer registers and more
-// workgroups: more loads in flight); 16,384 x 128: 16 tokens 9.6 us, 32 10.6.
+// workgroups: more loads in flight); 16,384 x 128: 16 tokens 9.6 us, 32 10.6; below
+// 4096 tokens as many workgroups as CUs: 30 x 805 8.4 us, with 16 tokens 12.9, 3000 x
+// 805 10.7 and 12.1.
 constexpr int bwd_rows(int V) { return V == 1 ? 2 : 1; }
 int bwd_chunk(int64_t T, int groups, int V) {
-  const int base = T >= 65536 ? 32 : 16, batch = groups * bwd_rows(V);
-  return base > batch ? base : batch;
+  const int base = T >= 65536 ? 32 : T >= 16 * 256 ? 16 : int((T + 255) / 256), batch = groups * bwd_rows(V);
+  return base > batch ? (base + batch - 1) / batch * batch : batch;
 }
 
 // One pass over the logits. HBM-bound for long batches (reads and writes a
@@ -625,7 +631,7 @@ struct BalanceWs {
 int seq_blocks(int E) { return (E + kSeqExperts - 1) / kSeqExperts; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 BalanceWs balance_ws(int64_t T, int E, int64_t S) {
-  const int chunk = balance_chunk_tokens(T);
+  const int chunk = balance_chunk_tokens(T, E);
   const size_t pieces = size_t((T + chunk - 1) / chunk + S);
   BalanceWs L;
   size_t o = 0;
@@ -700,7 +706,7 @@ hipError_t launch_balance(const BalanceArgs& a, float* loss, int32_t* counts, in
                          reinterpret_cast<float*>(base + L.z), reinterpret_cast<int32_t*>(base + L.n)};
   const BalanceSeq sq{reinterpret_cast<double*>(base + L.term), reinterpret_cast<double*>(base + L.qz),
                       reinterpret_cast<int32_t*>(base + L.qn)};
-  const int chunk = balance_chunk_tokens(a.T);
+  const int chunk = balance_chunk_tokens(a.T, a.E);
   if (a.T > 0) {
     TimedLaunch tl(timer, "balance_partial", st);
     with_layout(a.E, PartialLaunch{a, pc, chunk, dim3(unsigned((a.T + chunk - 1) / chunk)), st});
