@@ -460,7 +460,7 @@ moe_status moe_ortho_workspace_size(const moe_ortho_shape* s, size_t* ws_bytes);
 
 /* U bf16 [E, R, C] (written) = the orthogonalised G [E, R, C] (grad_dtype).
  * U may be the very buffer of a bf16 G, but not overlap it otherwise. The
- * caller owns every buffer; ws 16-byte aligned; enqueued on `stream`. Calls
+ * caller owns every buffer, each 16-byte aligned; enqueued on `stream`. Calls
  * that share `ws` must not overlap. */
 moe_status moe_orthogonalize(const moe_ortho_shape* s, const void* G, void* U, void* ws, size_t ws_bytes,
                              void* stream);

@@ -174,6 +174,33 @@ def test_captured_step_repeats_the_eager_one(B):
         _same(got, s.results())
 
 
+@pytest.mark.parametrize("E,R,C", [(2, 96, 70), (3, 200, 310), (1, 150, 1700)])   # each path
+def test_two_graphs_share_a_workspace(B, E, R, C):
+    """Two captured calls on one workspace, replayed in turn and between eager
+    calls on it, with inputs that change."""
+    print(f"case two graphs, one workspace {E} {R} {C}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    buf = B.OrthoBuffers.allocate(B.make_ortho_shape(E, R, C))
+    buf.ws.fill_(0xFF)
+    G = [torch.randn((E, R, C), generator=g, device=DEV).bfloat16() for _ in range(2)]
+    U = [torch.empty_like(t) for t in G]
+    B.orthogonalize(buf, G[0], U[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for t, u in zip(G, U):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            B.orthogonalize(buf, t, u)
+    for r in range(3):
+        for t in G:
+            t.copy_(t.roll(1, 2))
+        for k in (0, 1, 0):
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        for t, u in zip(G, U):
+            assert torch.equal(u, B.orthogonalize(buf, t))
+
+
 def test_step_on_another_stream_and_again(B):
     print("case train step, streams", flush=True)
     s = Step(B)
