@@ -260,10 +260,21 @@ __global__ __launch_bounds__((NB + 1) / 2 * 64) void ortho_small_apply_kernel(Or
   int p;
   float s;
   matrix_scale(part + e * d.parts, d.parts, eps, &p, &s);
-  load_columns<NB, false, LO, kApply * 64>(in, d, e, c0, p, s == s, hi, lo);
-  __syncthreads();
+  // Q's rows of the wave on their way while the columns are laid out
   constexpr int kHalves = Pairs<NB>::kBlocks * kBlock;
   const _Float16* Qh = Qm + e * 2 * kHalves;
+  f16x8 qh[2][2 * NB], ql[2][2 * NB];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int rb = min(2 * wave_id() + i, NB - 1);  // an odd last row block is done twice, stored once
+#pragma unroll
+    for (int kk = 0; kk < 2 * NB; ++kk) {
+      qh[i][kk] = fragment(Qh, NB, rb, kk);
+      ql[i][kk] = fragment(Qh + kHalves, NB, rb, kk);
+    }
+  }
+  load_columns<NB, false, LO, kApply * 64>(in, d, e, c0, p, s == s, hi, lo);
+  __syncthreads();
   f32x16 acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -281,13 +292,11 @@ __global__ __launch_bounds__((NB + 1) / 2 * 64) void ortho_small_apply_kernel(Or
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int rb = min(2 * wave_id() + i, NB - 1);  // an odd last row block is done twice, stored once
-      const f16x8 qh = fragment(Qh, NB, rb, kk), ql = fragment(Qh + kHalves, NB, rb, kk);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (LO) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl[j], qh, acc[i][j], 0, 0, 0);
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[j], ql, acc[i][j], 0, 0, 0);
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[j], qh, acc[i][j], 0, 0, 0);
+        if (LO) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl[j], qh[i][kk], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[j], ql[i][kk], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[j], qh[i][kk], acc[i][j], 0, 0, 0);
       }
     }
   }
