@@ -177,12 +177,24 @@ __global__ __launch_bounds__(64 * kWaves<NB>) void ortho_small_gram_kernel(Ortho
         f32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
 }
 
-// The steps on H and Q. M1 holds H, then T = P H, Q and the next H in turn; M2
-// holds P.
+// P = a + b H + c H^2, of which P holds H^2.
+template <int NB>
+__device__ __forceinline__ void polynomial(const f32x16& H, float ca, float cb, float cc, f32x16& P) {
+  const bool diag = wave_id() / NB == wave_id() % NB;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const bool one = diag && (lane_id() & 31) == 8 * (q >> 2) + 4 * (lane_id() >> 5) + (q & 3);
+    P[q] = (one ? ca : 0.f) + cb * H[q] + cc * P[q];
+  }
+}
+
+// The steps on H and Q. Up to 96 x 96 every matrix has its place in LDS, and T = P H
+// and P Q run side by side: three barriers a step. At 128 x 128 two fit: M1 holds
+// H, then T, Q and the next H in turn, M2 holds P.
 template <int NB>
 __global__ __launch_bounds__(64 * kWaves<NB>) void ortho_small_steps_kernel(const float* __restrict__ gram, int parts,
-                                                                     const NormPart* __restrict__ norm, int norms, float eps,
-                                                                     int steps, float ca, float cb, float cc,
+                                                                     const NormPart* __restrict__ norm, int norms,
+                                                                     float eps, int steps, float ca, float cb, float cc,
                                                                      _Float16* __restrict__ Qout) {
   __shared__ __attribute__((aligned(16))) Pairs<NB> M1, M2;
   const int64_t e = blockIdx.x;
@@ -193,7 +205,8 @@ __global__ __launch_bounds__(64 * kWaves<NB>) void ortho_small_steps_kernel(cons
 #pragma unroll
   for (int r = 0; r < 16; ++r) H[r] = Q[r] = P[r] = 0.f;
   const bool mine = has_tile<NB>();
-  for (int c = 0; mine && c < parts; ++c) {
+#pragma unroll 4
+  for (int c = 0; c < (mine ? parts : 0); ++c) {
     const float* src = gram + (e * parts + c) * (NB * NB * 1024) + wave_id() * 1024;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -207,36 +220,51 @@ __global__ __launch_bounds__(64 * kWaves<NB>) void ortho_small_steps_kernel(cons
   store_pairs<NB>(H, kHScale, M1.hi, M1.lo);
   __syncthreads();
   constexpr float kHH = 1.f / (kHScale * kHScale), kHQ = 1.f / (kHScale * kQScale);
-  const bool diag = wave_id() / NB == wave_id() % NB;
-  for (int k = 0; k < steps; ++k) {
-    const bool last = k + 1 == steps;
-    multiply<NB>(M1, M1, kHH, P);  // H^2
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const bool one = diag && (lane_id() & 31) == 8 * (q >> 2) + 4 * (lane_id() >> 5) + (q & 3);
-      P[q] = (one ? ca : 0.f) + cb * H[q] + cc * P[q];
-    }
-    store_pairs<NB>(P, kHScale, M2.hi, M2.lo);
-    __syncthreads();
-    if (!last) {
-      multiply<NB>(M2, M1, kHH, H);  // T = P H
+  if constexpr (NB <= 3) {
+    __shared__ __attribute__((aligned(16))) Pairs<NB> MT, MQ;
+    for (int k = 0; k < steps; ++k) {
+      const bool last = k + 1 == steps;
+      multiply<NB>(M1, M1, kHH, P);
+      polynomial<NB>(H, ca, cb, cc, P);
+      store_pairs<NB>(P, kHScale, M2.hi, M2.lo);
       __syncthreads();
+      if (!last) multiply<NB>(M2, M1, kHH, H);  // T = P H
+      if (k == 0) Q = P; else multiply<NB>(M2, MQ, kHQ, Q);
+      if (last) break;
+      store_pairs<NB>(H, kHScale, MT.hi, MT.lo);
+      __syncthreads();
+      multiply<NB>(M2, MT, kHH, H);  // P T^T
       store_pairs<NB>(H, kHScale, M1.hi, M1.lo);
-      __syncthreads();
-      multiply<NB>(M2, M1, kHH, H);  // P T^T
-    }
-    __syncthreads();
-    if (k == 0) {
-      Q = P;
-    } else {
-      store_pairs<NB>(Q, kQScale, M1.hi, M1.lo);
-      __syncthreads();
-      multiply<NB>(M2, M1, kHQ, Q);  // P Q
+      store_pairs<NB>(Q, kQScale, MQ.hi, MQ.lo);
       __syncthreads();
     }
-    if (!last) {
-      store_pairs<NB>(H, kHScale, M1.hi, M1.lo);
+  } else {
+    for (int k = 0; k < steps; ++k) {
+      const bool last = k + 1 == steps;
+      multiply<NB>(M1, M1, kHH, P);  // H^2
+      polynomial<NB>(H, ca, cb, cc, P);
+      store_pairs<NB>(P, kHScale, M2.hi, M2.lo);
       __syncthreads();
+      if (!last) {
+        multiply<NB>(M2, M1, kHH, H);  // T = P H
+        __syncthreads();
+        store_pairs<NB>(H, kHScale, M1.hi, M1.lo);
+        __syncthreads();
+        multiply<NB>(M2, M1, kHH, H);  // P T^T
+      }
+      __syncthreads();
+      if (k == 0) {
+        Q = P;
+      } else {
+        store_pairs<NB>(Q, kQScale, M1.hi, M1.lo);
+        __syncthreads();
+        multiply<NB>(M2, M1, kHQ, Q);  // P Q
+        __syncthreads();
+      }
+      if (!last) {
+        store_pairs<NB>(H, kHScale, M1.hi, M1.lo);
+        __syncthreads();
+      }
     }
   }
   constexpr int kHalves = Pairs<NB>::kBlocks * kBlock;
