@@ -9,8 +9,8 @@
 //   ortho_small_apply  the result Q X0, to U or the weights
 // Bound by its launches and, past m = 64, by the LDS reads of the m x m products.
 // In us, against three launches per step of the tiled path: 16 x 16 alone 21 :
-// 72, 16 of 64 x 64 31 : 79, 64 of 128 x 128 71 : 85, 2 of 128 x 4096 75 : 115,
-// 64 of 96 x 4000 121 : 353, 1000 of 128 x 256 447 : 651.
+// 72, 16 of 64 x 64 31 : 79, 64 of 128 x 128 69 : 85, 2 of 128 x 4096 72 : 115,
+// 64 of 96 x 4000 116 : 353, 1000 of 128 x 256 450 : 651.
 //
 // Numbers. Q X0 cancels: Q is a^steps (485) on the directions of small singular
 // values and near 1 / sigma on the others, and they only separate through Q's
