@@ -110,10 +110,12 @@ __device__ __forceinline__ float wave_groups_sum(float v) {
 }
 
 // The softmax of one row, in powers of two on the transcendental unit: v
-// becomes 2^(v log2(e) - c) with c = max log2(e) (c's rounding cancels between
-// v and sum, the product's is inside the fma), sum its sum, lse the log-sum-
-// exp. fmaxf drops a NaN, so a NaN reaches the sum through the power. A row of
-// -inf alone gives v = 0 and sum = 0 (and lse = -inf).
+// becomes 2^((v - max) log2(e)), sum its sum, lse the log-sum-exp. The maximum is
+// taken off first: finite logits of any magnitude leave differences in [-inf, 0]
+// and a sum of 1 at least (scaled first, the maximum's own rounding grows with it
+// and is past the exponent's range from 2^31 on). fmaxf drops a NaN, so a NaN
+// reaches the sum through the power. A row of -inf alone gives v = 0 and sum = 0
+// (and lse = -inf).
 template <int LPT, int V>
 __device__ __forceinline__ void row_softmax(f32x4 (&v)[V], float& sum, float& lse) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -123,17 +125,17 @@ __device__ __forceinline__ void row_softmax(f32x4 (&v)[V], float& sum, float& ls
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i][j]);
   m = group_max<LPT>(m);
-  const float c = m == -INFINITY ? 0.f : m * kLog2e;
+  if (m == -INFINITY) m = 0.f;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[i][j] = __builtin_amdgcn_exp2f(fmaf(v[i][j], kLog2e, -c));
+      v[i][j] = __builtin_amdgcn_exp2f((v[i][j] - m) * kLog2e);
       s += v[i][j];
     }
   sum = group_sum<LPT>(s);
-  lse = (c + __builtin_amdgcn_logf(sum)) * kLn2;
+  lse = fmaf(__builtin_amdgcn_logf(sum), kLn2, m);
 }
 // 1 / sum; 0 for a row of -inf alone, NaN stays
 __device__ __forceinline__ float inverse_of(float sum) { return sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum); }
