@@ -153,23 +153,24 @@ __device__ __forceinline__ int seq_of(const int32_t* __restrict__ off, int S, in
 struct BalancePieces {
   float* p;        // [pieces][E]
   int32_t* c;      // [pieces][E]
-  float* z;        // [pieces]
+  double* z;       // [pieces]
   int32_t* n;      // [pieces]
 };
 
 // Sums over the tokens [lo, hi), by a workgroup of kGroups groups of LPT lanes:
 // on return (after a barrier by the caller) sp[wave][e] holds the sums of p,
-// sc[e] the counts, sz and sn each wave's sum of lse^2 and live tokens.
+// sc[e] the counts, sz and sn each wave's sum of lse^2 and live tokens. The squares
+// are 64-bit: a finite lse's may leave fp32 where their mean does not.
 template <int LPT, int V, int kGroups>
 __device__ __forceinline__ void sum_tokens(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                                            int64_t lo, int64_t hi, int E, int k, const uint8_t* __restrict__ mask,
-                                           float* sp, int32_t* sc, float* sz, int32_t* sn) {
+                                           float* sp, int32_t* sc, double* sz, int32_t* sn) {
   constexpr int U = kBalRows / V;
   const int grp = threadIdx.x / LPT, l = threadIdx.x % LPT;
   f32x4 acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float z = 0.f;
+  double z = 0.0;
   int32_t n = 0;
   // the trip count is the same for a whole wave: the butterflies stay converged
   for (int64_t b = lo; b < hi; b += kGroups * U) {
@@ -206,12 +207,13 @@ __device__ __forceinline__ void sum_tokens(const float* __restrict__ logits, con
         for (int i = 0; i < V; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][j] += v[u][i][j] * inv;
-        z += sum == 0.f ? 0.f : lse * lse;
+        z += sum == 0.f ? 0.0 : double(lse) * double(lse);
         ++n;
       }
     }
   }
-  z = wave_groups_sum<LPT>(z);
+#pragma unroll
+  for (int o = LPT; o < 64; o *= 2) z += __shfl_xor(z, o);
   const float nf = wave_groups_sum<LPT>(float(n));  // exact: below 2^24 tokens a workgroup
 #pragma unroll
   for (int i = 0; i < V; ++i)
@@ -235,7 +237,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
   constexpr int kGroups = kBalThreads / LPT, kWaves = kBalThreads / 64;
   __shared__ __attribute__((aligned(16))) float sp[kWaves * 4 * LPT * V];
   __shared__ int32_t sc[4 * LPT * V];
-  __shared__ float sz[kWaves];
+  __shared__ double sz[kWaves];
   __shared__ int32_t sn[kWaves];
   const int tid = threadIdx.x;
   const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(T, t0 + chunk);
@@ -259,7 +261,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
       out.c[piece * E + e] = sc[e];
     }
     if (tid == 0) {
-      float s = 0.f;
+      double s = 0.0;
       int32_t m = 0;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
@@ -433,7 +435,7 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(
   constexpr int kGroups = 1024 / LPT;
   __shared__ __attribute__((aligned(16))) float sp[16 * 4 * LPT * V];
   __shared__ int32_t sc[4 * LPT * V];
-  __shared__ float sz[16];
+  __shared__ double sz[16];
   __shared__ int32_t sn[16];
   __shared__ double sm[1][16];
   const int tid = threadIdx.x;
@@ -446,7 +448,7 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(
   double z = 0.0, n = 0.0, P = 0.0;
 #pragma unroll
   for (int w = 0; w < 16; ++w) {
-    z += double(sz[w]);
+    z += sz[w];
     n += double(sn[w]);
   }
   int32_t c = 0;
@@ -641,7 +643,7 @@ BalanceWs balance_ws(int64_t T, int E, int64_t S) {
   size_t o = 0;
   L.p = o;    o = up256(o + pieces * size_t(E) * 4);
   L.c = o;    o = up256(o + pieces * size_t(E) * 4);
-  L.z = o;    o = up256(o + pieces * 4);
+  L.z = o;    o = up256(o + pieces * 8);
   L.n = o;    o = up256(o + pieces * 4);
   L.term = o; o = up256(o + size_t(S) * seq_blocks(E) * 8);
   L.qz = o;   o = up256(o + size_t(S) * 8);
@@ -707,7 +709,7 @@ hipError_t launch_balance(const BalanceArgs& a, float* loss, int32_t* counts, in
   const BalanceWs L = balance_ws(a.T, a.E, a.S);
   char* base = static_cast<char*>(ws);
   const BalancePieces pc{reinterpret_cast<float*>(base + L.p), reinterpret_cast<int32_t*>(base + L.c),
-                         reinterpret_cast<float*>(base + L.z), reinterpret_cast<int32_t*>(base + L.n)};
+                         reinterpret_cast<double*>(base + L.z), reinterpret_cast<int32_t*>(base + L.n)};
   const BalanceSeq sq{reinterpret_cast<double*>(base + L.term), reinterpret_cast<double*>(base + L.qz),
                       reinterpret_cast<int32_t*>(base + L.qn)};
   const int chunk = balance_chunk_tokens(a.T, a.E);

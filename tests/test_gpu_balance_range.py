@@ -107,3 +107,18 @@ def test_gradient_of_large_finite_rows(B, T, E, k, S, v, renorm):
     B.moe_route_bwd(s, z, idx, w, dw, renorm, dz)
     alone = B.balance_bwd(buf, z, idx, w, dw, renorm, zero, off, mask, counts, scale)
     assert ((alone - dz).abs() <= TOL * dw.abs().sum(1, keepdim=True)).all().item()
+
+
+@pytest.mark.parametrize("T,E,k,S", SHAPES)
+@pytest.mark.parametrize("v", [2e19, -1e20, 3e20])
+def test_squares_past_fp32_whose_mean_is_not(B, T, E, k, S, v):
+    """lse^2 of one row leaves fp32, the mean over the tokens does not."""
+    print(f"case balance lse^2 T={T} E={E} S={S} v={v:g}", flush=True)
+    z, idx, off, mask = _batch(T, E, k, S, 1e10)
+    z[7] = v / 4 if T < 1000 else v
+    buf = B.BalanceBuffers.allocate(B.make_shape(T, 256, 128, E, k), S)
+    B.balance(buf, z, idx, off, mask)
+    torch.cuda.synchronize()
+    want = ob.balance(_np(z), _np(idx), _np(off), _np(mask))["loss"][1]
+    got = buf.loss[1].item()
+    assert got == math.inf if want > FMAX else abs(got - want) <= TOL * want
