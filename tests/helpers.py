@@ -31,3 +31,16 @@ def header_symbols() -> list[str]:
     src = open(os.path.join(ROOT, "include", "moe.h")).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     return sorted(set(re.findall(r"\b(moe_[a-z_0-9]+)\s*\(", src)))
+
+
+def max_matrix_err(got, ref) -> float:
+    """Largest Frobenius error of a matrix of a stack, relative to the matrix
+    (0 when both are all-zero). inf where `got` has a NaN or an infinity that
+    `ref` has not: a comparison with a bound cannot pass on one."""
+    out = 0.0
+    for a, b in zip(np.asarray(got, dtype=np.float64), np.asarray(ref, dtype=np.float64)):
+        assert a.shape == b.shape, (a.shape, b.shape)
+        n, d = np.linalg.norm(b), np.linalg.norm(a - b)
+        err = (0.0 if d == 0.0 else np.inf) if n == 0.0 else d / n
+        out = max(out, err if np.isfinite(a).all() and np.isfinite(err) else np.inf)
+    return float(out)
