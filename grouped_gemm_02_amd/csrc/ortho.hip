@@ -1025,7 +1025,19 @@ struct OrthoSteps {
 
 }  // namespace
 
-size_t ortho_workspace_bytes(const OrthoArgs& a) { return ortho_plan(a).total; }
+// What any stack of up to a.E such matrices needs: the parts' sums of a smaller one
+// may be more than a larger one, without parts, has besides.
+size_t ortho_workspace_bytes(const OrthoArgs& a) {
+  const OrthoPlan p = ortho_plan(a);
+  size_t most = p.total;
+  if (small_fits(a) || p.d.np / kBK < kSplitFrom) return most;
+  OrthoArgs fewer = a;
+  for (fewer.E = 1; fewer.E < a.E && fewer.E * sym_tiles(p.d.mp, Small::kRows) <= kSplitTiles; ++fewer.E) {
+    const size_t n = ortho_plan(fewer).total;
+    if (n > most) most = n;
+  }
+  return most;
+}
 
 hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipStream_t st, KernelTimer* timer) {
   if (a.E <= 0) return hipSuccess;

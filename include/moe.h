@@ -456,7 +456,8 @@ typedef struct moe_ortho_shape {
 } moe_ortho_shape;
 
 /* Bytes of the scratch of moe_orthogonalize and moe_muon_step. It holds the
- * state of a group of matrices at a time, not of all E. Pure host function. */
+ * state of a group of matrices at a time, not of all E, and serves every E up to
+ * this one. Pure host function. */
 moe_status moe_ortho_workspace_size(const moe_ortho_shape* s, size_t* ws_bytes);
 
 /* U bf16 [E, R, C] (written) = the orthogonalised G [E, R, C] (grad_dtype).
