@@ -319,7 +319,8 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
  *                              for a sequence with none)
  *   seq_scale   fp32  [S+1]    written (for the backward): per sequence
  *                              E / (S' k n_q^2), 0 when n_q = 0; last 1 / N
- *   ws          moe_balance_scratch_bytes(s, S) bytes, 16-byte aligned
+ *   ws          moe_balance_scratch_bytes(s, S) bytes, 16-byte aligned; serves
+ *               fewer tokens and sequences of the same E too
  * Uses s->T, E, k (check as moe_workspace_size); 1 <= S <= 2^20, S * E < 2^28.
  * Sums run in a fixed order: results are reproducible bit for bit. With
  * T == 0 every output is written as 0 (logits and topk_idx may be NULL).
