@@ -31,14 +31,24 @@ constexpr int kBalRows = 4;  // 16-byte loads of logits a lane has in flight
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
-// T * E up to which one workgroup does the whole forward of one sequence. In us,
-// against the three launches: 64 x 8 8.1 : 14.3, 4096 x 16 11.2 : 14.3, 512 x 128
-// 12.9 : 14.5, 256 x 256 13.8 : 16.2, 8192 x 16 18.8 : 14.7, 1024 x 128 22.2 : 14.6.
-// (A workgroup that takes several sequences in turn: 4 to 7 us each.)
+// Tokens times row_cost up to which one workgroup does the whole forward of one
+// sequence. In us (replayed), against the three launches: 2048 x 8 8.0 : 11.7, 4096 x 1
+// 12.1 : 11.6, 4096 x 16 11.5 : 11.5, 1024 x 40 13.3 : 12.2, 256 x 130 15.4 : 14.0, 128 x 300
+// 11.0 : 12.8, 64 x 1024 8.9 : 12.1, 80 x 805 10.4 : 12.6, 100 x 600 13.0 : 12.7; past it 8192 x 8
+// 21.4 : 12.8, 32768 x 2 71.7 : 19.2, 1500 x 40 18.4 : 12.2, 400 x 160 23.1 : 14.2. (A workgroup
+// that takes several sequences in turn: 4 to 7 us each.)
 constexpr int64_t kSmallWork = 65536;
 
 // Chunks of four experts a lane has of a row.
 constexpr int lane_chunks(int E) { return E <= 256 ? 1 : E <= 512 ? 2 : 4; }
+// Experts that a row costs the lanes of its layout: 4 LPT of with_layout, and those
+// it has in the layout of four chunks, whose last ones are mostly past the row.
+constexpr int row_cost(int E) {
+  if (E > 512) return E;
+  int w = 16;
+  while (w < E) w *= 2;
+  return w;
+}
 
 // Two rounds of loads a workgroup until kBalChunks workgroups are reached, then more (32
 // tokens for any E: 3000 x 805 20.1 us instead of 16.8, 30 x 805 20.5 instead of 15.0).
@@ -704,7 +714,7 @@ size_t balance_scratch_bytes(int64_t T, int E, int64_t S) { return balance_ws(T,
 
 hipError_t launch_balance(const BalanceArgs& a, float* loss, int32_t* counts, int32_t* seq_counts, float* seq_probs,
                           float* seq_scale, void* ws, hipStream_t st, KernelTimer* timer) {
-  if (a.S == 1 && a.T * a.E <= kSmallWork) {
+  if (a.S == 1 && a.T * row_cost(a.E) <= kSmallWork) {
     TimedLaunch tl(timer, "balance_small", st);
     with_layout(a.E, SmallLaunch{a, loss, counts, seq_counts, seq_probs, seq_scale, st});
     return hipGetLastError();
