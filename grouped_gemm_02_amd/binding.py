@@ -201,6 +201,24 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _result(stream, sizes, dtype, device) -> torch.Tensor:
+    """A result for a call on `stream`: memory of that stream, whose earlier work
+    alone may still touch it, kept until what the current stream has queued by
+    the time it is freed is done as well."""
+    device = torch.device(device)
+    if stream is None or device.type != "cuda":
+        return torch.empty(sizes, dtype=dtype, device=device)
+    here, handle = torch.cuda.current_stream(device), _stream(stream)
+    if handle == here.cuda_stream:
+        return torch.empty(sizes, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(sizes, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def make_shape(T, H, I, E, k, precision="bf16", num_cus=0, wgrad="bf16") -> moe_shape:
     """wgrad: "bf16" (default) or "fp8" (sets MOE_FLAG_FP8_WGRAD)."""
     p = PRECISIONS[precision] if isinstance(precision, str) else int(precision)
@@ -491,7 +509,7 @@ def forward(buf: LayerBuffers, x, topk_idx, topk_w, W13, W2, y=None, training=Tr
     """Forward; for FP8 precisions buf.wq must hold quantize_weights of W13, W2."""
     s = buf.shape
     if y is None:
-        y = torch.empty((s.T, s.H), dtype=torch.bfloat16, device=x.device)
+        y = _result(stream, (s.T, s.H), _BF16, x.device)
     moe_fwd(s, x, topk_idx, topk_w, W13, W2, buf.wq, y, buf.saved if training else None, buf.fwd_ws, stream)
     return y
 
@@ -501,7 +519,7 @@ def forward_logits(buf: LayerBuffers, x, logits, renorm, topk_idx, topk_w, W13, 
     """Forward with the router fused in: writes topk_idx and topk_w."""
     s = buf.shape
     if y is None:
-        y = torch.empty((s.T, s.H), dtype=torch.bfloat16, device=x.device)
+        y = _result(stream, (s.T, s.H), _BF16, x.device)
     moe_fwd_logits(s, x, logits, renorm, topk_idx, topk_w, W13, W2, buf.wq, y, buf.saved if training else None,
                    buf.fwd_ws, stream)
     return y
@@ -511,10 +529,8 @@ def backward(buf: LayerBuffers, dy, x, topk_idx, topk_w, W13, W2, grads=None, st
     s = buf.shape
     if grads is None:
         dev = dy.device
-        grads = (torch.empty((s.T, s.H), dtype=torch.bfloat16, device=dev),
-                 torch.empty((s.T, s.k), dtype=torch.float32, device=dev),
-                 torch.empty((s.E, 2 * s.I, s.H), dtype=torch.bfloat16, device=dev),
-                 torch.empty((s.E, s.H, s.I), dtype=torch.bfloat16, device=dev))
+        grads = (_result(stream, (s.T, s.H), _BF16, dev), _result(stream, (s.T, s.k), _F32, dev),
+                 _result(stream, (s.E, 2 * s.I, s.H), _BF16, dev), _result(stream, (s.E, s.H, s.I), _BF16, dev))
     dx, dw, dW13, dW2 = grads
     moe_bwd(s, dy, x, topk_idx, topk_w, W13, W2, buf.wq, buf.saved, dx, dw, dW13, dW2, buf.bwd_ws, stream)
     return grads
@@ -553,7 +569,7 @@ def balance_bwd(buf: BalanceBuffers, logits, topk_idx, topk_w, d_topk_w, renorm,
     """d_logits of the balance losses and, with d_topk_w, of the routing
     weights; seq_counts and seq_scale default to what balance left in `buf`."""
     if d_logits is None:
-        d_logits = buf.loss.new_empty((buf.shape.T, buf.shape.E))
+        d_logits = _result(stream, (buf.shape.T, buf.shape.E), _F32, buf.loss.device)
     moe_balance_bwd(buf.shape, logits, topk_idx, topk_w, d_topk_w, renorm, seq_offsets, buf.S, mask,
                     buf.seq_counts if seq_counts is None else seq_counts,
                     buf.seq_scale if seq_scale is None else seq_scale, d_loss, d_logits, stream)
@@ -575,7 +591,7 @@ def orthogonalize(buf: OrthoBuffers, G, U=None, stream=None):
     """The orthogonalised G (bf16); U may be a bf16 G itself."""
     s = buf.shape
     if U is None:
-        U = torch.empty((s.E, s.R, s.C), dtype=_BF16, device=G.device)
+        U = _result(stream, (s.E, s.R, s.C), _BF16, G.device)
     moe_orthogonalize(s, G, U, buf.ws, stream)
     return U
 
