@@ -270,7 +270,7 @@ moe_status check_ortho(const moe_ortho_shape* s) {
   if (!s) return MOE_ERR_NULL;
   if (s->grad_dtype != MOE_DT_BF16 && s->grad_dtype != MOE_DT_F32) return MOE_ERR_PRECISION;
   if (s->E < 0 || s->R < 1 || s->C < 1 || s->R > 16384 || s->C > 16384) return MOE_ERR_SHAPE;
-  if (s->E >= (int64_t(1) << 40) / (s->R * s->C)) return MOE_ERR_SHAPE;
+  if (s->E > ((int64_t(1) << 40) - 1) / (s->R * s->C)) return MOE_ERR_SHAPE;  // E R C < 2^40
   if (s->steps < 1 || s->steps > 32 || s->reserved != 0) return MOE_ERR_SHAPE;
   if (!std::isfinite(s->a) || !std::isfinite(s->b) || !std::isfinite(s->c)) return MOE_ERR_SHAPE;
   if (!std::isfinite(s->eps) || s->eps < 0.f) return MOE_ERR_SHAPE;
