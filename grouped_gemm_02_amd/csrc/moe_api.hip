@@ -781,6 +781,7 @@ moe_status moe_muon_step(const moe_ortho_shape* s, const moe_muon_params* p, con
   if (!std::isfinite(p->lr) || !std::isfinite(p->mu) || p->mu < 0.f || p->mu >= 1.f || !std::isfinite(p->weight_decay) ||
       !std::isfinite(p->scale) || p->reserved != 0)
     return MOE_ERR_SHAPE;
+  if (!std::isfinite(p->lr * p->scale) || !std::isfinite(p->lr * p->weight_decay)) return MOE_ERR_SHAPE;
   if (s->E == 0) return MOE_OK;
   if (!grad || !momentum || !W || !ws) return MOE_ERR_NULL;
   if (!aligned16(grad) || !aligned16(momentum) || !aligned16(W) || !aligned16(master) || !aligned16(ws))

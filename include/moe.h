@@ -477,7 +477,8 @@ moe_status moe_orthogonalize(const moe_ortho_shape* s, const void* G, void* U, v
  *   master   fp32 [E, R, C] or NULL: when given, the update is taken on it
  *            and W becomes its bf16 rounding (W is not read)
  * The parameters are host values, read at the call (a captured call replays
- * them). lr, mu (0 <= mu < 1), weight_decay and scale finite. */
+ * them). lr, mu (0 <= mu < 1), weight_decay, scale, lr scale and lr weight_decay
+ * finite in fp32. */
 typedef struct moe_muon_params {
   float lr, mu, weight_decay, scale;
   int32_t nesterov;
