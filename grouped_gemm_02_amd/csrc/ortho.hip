@@ -228,8 +228,10 @@ struct TileShape {
     __shared__ __attribute__((aligned(1024))) _Float16 buf[kStage];
     return buf;
   }
-  // a wave's 8 KiB for the images of its results, in the stages once they are free
+  // a wave's 8 KiB for an image of its results, and for a second one, in the stages
+  // once they are free
   static __device__ __forceinline__ uint16_t* image();
+  static __device__ __forceinline__ uint16_t* image2();
 };
 using Big = TileShape<4, 4>;
 using Small = TileShape<2, 2>;
@@ -244,6 +246,12 @@ __device__ __forceinline__ uint16_t* TileShape<TI_, WN_>::image() {
   static_assert(kPerStage * 2 == kWaves, "two stages hold the images");
   const int w = wave_id();
   return reinterpret_cast<uint16_t*>(w < kPerStage ? stage<0>() : stage<1>()) + (w % kPerStage) * 4096;
+}
+template <int TI_, int WN_>
+__device__ __forceinline__ uint16_t* TileShape<TI_, WN_>::image2() {
+  constexpr int kPerStage = kStage / 4096;
+  const int w = wave_id();
+  return reinterpret_cast<uint16_t*>(w < kPerStage ? stage<2>() : stage<3>()) + (w % kPerStage) * 4096;
 }
 
 template <class T>
@@ -695,11 +703,12 @@ __device__ __forceinline__ void own_step(const Operand& P, const Operand& Q, int
 // took the update 13 % longer). FIRST: X is X0, whose value is scale[e] times
 // what is stored (and whose remainder may be zero: Xl NULL). LAST: the result
 // is written instead of X'. U leaves as bf16; the step of the weights goes
-// through LDS as fp16 (2^-12 of the update, an eighth of what the products'
-// roundings leave). 128 of 768 x 2048 in 403 us: 0.77 PFLOP/s and 1.2 GB, 3.0
-// TB/s. The MFMAs alone would take 255, the bytes 246; a tile's first loads and
-// last stores do not run under its products (the wait counter holds loads and
-// stores in one order, so a next tile's loads would wait for the stores too).
+// through LDS as pairs of bf16, to 2^-17 of each element at any magnitude (fp16's
+// range ends where |G| is small against eps, or the polynomial is steep; 256 of
+// 768 x 2048 in 8.25 ms, with fp16 8.19). 128 of 768 x 2048 in 403 us: 0.77 PFLOP/s
+// and 1.2 GB, 3.0 TB/s. The MFMAs alone would take 255, the bytes 246; a tile's first
+// loads and last stores do not run under its products (the wait counter holds loads
+// and stores in one order, so a next tile's loads would wait for the stores too).
 template <class T, bool FIRST, bool LAST>
 __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Float16* __restrict__ X,
                                                                       const uint8_t* __restrict__ Xl,
@@ -773,7 +782,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Flo
           } else if (out.U) {
             w[g] = u32x2{pack_bf16x2(y[0] * s, y[1] * s), pack_bf16x2(y[2] * s, y[3] * s)};
           } else {
-            w[g] = u32x2{pack_f16(y[0] * s, y[1] * s), pack_f16(y[2] * s, y[3] * s)};
+            const u32x2 a = pair_bf16x2(y[0] * s, y[1] * s), b = pair_bf16x2(y[2] * s, y[3] * s);
+            w[g] = u32x2{a[0], b[0]};
+            image_put(T::image2(), 32 * ii + (lane & 31), 8 * j + 2 * g + (lane >> 5), a[1], b[1]);
           }
         }
         if constexpr (!LAST) {
@@ -788,7 +799,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void ortho_update_kernel(const _Flo
     }
     if constexpr (LAST) {
       image_sync();
-      put_image(out, T::image(), d, e, at.row0 + 64 * h, at.col0);
+      put_image(out, T::image(), T::image2(), d, e, at.row0 + 64 * h, at.col0);
       image_sync();
     }
   }

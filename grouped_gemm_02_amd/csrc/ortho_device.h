@@ -236,10 +236,16 @@ struct OrthoOut {
 
 __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
 
+// Two values as pairs of bf16 (16 bits and fp32's range): upper and lower halves.
+__device__ __forceinline__ u32x2 pair_bf16x2(float a, float b) {
+  const uint32_t hi = pack_bf16x2(a, b);
+  return u32x2{hi, pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi))};
+}
+
 // Eight consecutive elements of the result at element `at` of matrix storage:
-// v holds bf16 values (U) or fp16 values (the step of W). Only `count` of
-// them exist; eight go at once.
-__device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, const u32x4& v, int count) {
+// v holds bf16 values of U; for the step of W, v and l hold its pairs. Only `count`
+// of them exist; eight go at once.
+__device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, const u32x4& v, const u32x4& l, int count) {
   const bool vec = count >= 8;
   if (out.U) {
     if (vec) {
@@ -274,7 +280,10 @@ __device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, cons
     for (int t = 0; t < 8; ++t) w[t] = t < count ? (out.master ? out.master[at + t] : bf16_at(out.W + at + t)) : 0.f;
   }
 #pragma unroll
-  for (int t = 0; t < 8; ++t) w[t] = out.keep * w[t] - out.step * half_of(v[t >> 1], t & 1);
+  for (int t = 0; t < 8; ++t) {
+    const float u = t & 1 ? bf16_hi(v[t >> 1]) + bf16_hi(l[t >> 1]) : bf16_lo(v[t >> 1]) + bf16_lo(l[t >> 1]);
+    w[t] = out.keep * w[t] - out.step * u;
+  }
   if (vec) {
     if (out.master) {
       *reinterpret_cast<f32x4u*>(out.master + at) = f32x4{w[0], w[1], w[2], w[3]};
@@ -293,21 +302,25 @@ __device__ __forceinline__ void put_result(const OrthoOut& out, int64_t at, cons
 }
 
 // The 64 x 64 values of a wave's image (rows row0 .., columns col0 .. of X) to the
-// caller's matrix e.
-__device__ __forceinline__ void put_image(const OrthoOut& out, const uint16_t* im, const OrthoDims& d, int64_t e,
-                                          int row0, int col0) {
+// caller's matrix e. iml: the image of the pairs' lower halves, for the step of W.
+__device__ __forceinline__ void put_image(const OrthoOut& out, const uint16_t* im, const uint16_t* iml,
+                                          const OrthoDims& d, int64_t e, int row0, int col0) {
   const int lane = lane_id();
   for (int q = 0; q < 8; ++q) {
     if (!d.tall) {
       const int r = row0 + 8 * q + (lane >> 3), c = col0 + 8 * (lane & 7);
       const u32x4 v = image_row(im, 8 * q + (lane >> 3), lane & 7);
-      if (r < d.m && c < d.n) put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, d.n - c);
+      u32x4 l = {0u, 0u, 0u, 0u};
+      if (!out.U) l = image_row(iml, 8 * q + (lane >> 3), lane & 7);
+      if (r < d.m && c < d.n) put_result(out, (e * d.R + r) * int64_t(d.C) + c, v, l, d.n - c);
     } else {
       // 16 columns of X (rows of the result) x four pieces of 8 rows: 64 bytes a row
       const int r0 = 32 * (q & 1) + 8 * (lane >> 4), n0 = 16 * (q >> 1);
       const int r = row0 + r0, c = col0 + n0 + (lane & 15);
       const u32x4 v = image_col(im, r0, n0);
-      if (r < d.m && c < d.n) put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, d.m - r);
+      u32x4 l = {0u, 0u, 0u, 0u};
+      if (!out.U) l = image_col(iml, r0, n0);
+      if (r < d.m && c < d.n) put_result(out, (e * d.R + c) * int64_t(d.C) + r, v, l, d.m - r);
     }
   }
 }

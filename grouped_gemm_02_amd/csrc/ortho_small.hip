@@ -282,9 +282,11 @@ __global__ __launch_bounds__((NB + 1) / 2 * 64) void ortho_small_apply_kernel(Or
                                                                               const _Float16* __restrict__ Qm,
                                                                               OrthoOut out) {
   constexpr int kApply = (NB + 1) / 2;  // waves
-  __shared__ __attribute__((aligned(16))) _Float16 hi[4 * NB * kBlock];
-  __shared__ __attribute__((aligned(16))) _Float16 lo[LO ? 4 * NB * kBlock : 8];
+  constexpr int kCols = 4 * NB * kBlock;
+  __shared__ __attribute__((aligned(16))) _Float16 cols[(LO ? 2 : 1) * kCols];
   __shared__ __attribute__((aligned(16))) uint16_t images[kApply][4096];
+  static_assert(2 * kCols >= kApply * 4096, "the second images take the columns' place");
+  _Float16 *const hi = cols, *const lo = cols + (LO ? kCols : 0);
   const int64_t e = blockIdx.y;
   const int c0 = blockIdx.x * kSub;
   int p;
@@ -332,7 +334,14 @@ __global__ __launch_bounds__((NB + 1) / 2 * 64) void ortho_small_apply_kernel(Or
   }
   const float f = s * (1.f / kQScale);
   uint16_t* im = images[wave_id()];
+  uint16_t* im2 = im;
   const int lane = lane_id();
+  if constexpr (LO) {  // a step of weights is never without its momentum
+    if (!out.U) {
+      im2 = reinterpret_cast<uint16_t*>(cols) + wave_id() * 4096;
+      __syncthreads();  // the columns are read
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -341,12 +350,14 @@ __global__ __launch_bounds__((NB + 1) / 2 * 64) void ortho_small_apply_kernel(Or
       for (int g = 0; g < 4; ++g) {
         const f32x16& c = acc[i][j];
         const float y0 = c[4 * g] * f, y1 = c[4 * g + 1] * f, y2 = c[4 * g + 2] * f, y3 = c[4 * g + 3] * f;
-        // the step of the weights as fp16, as in the tiled path
-        image_put(im, 32 * i + (lane & 31), 8 * j + 2 * g + (lane >> 5),
-                  out.U ? pack_bf16x2(y0, y1) : pack_f16(y0, y1), out.U ? pack_bf16x2(y2, y3) : pack_f16(y2, y3));
+        // the step of the weights as pairs of bf16, as in the tiled path
+        const u32x2 a = pair_bf16x2(y0, y1), b = pair_bf16x2(y2, y3);
+        const int row = 32 * i + (lane & 31), piece = 8 * j + 2 * g + (lane >> 5);
+        image_put(im, row, piece, a[0], b[0]);
+        if (LO && !out.U) image_put(im2, row, piece, a[1], b[1]);
       }
   image_sync();
-  put_image(out, im, d, e, 64 * wave_id(), c0);
+  put_image(out, im, im2, d, e, 64 * wave_id(), c0);
 }
 
 template <int NB>

@@ -476,6 +476,9 @@ moe_status moe_orthogonalize(const moe_ortho_shape* s, const void* G, void* U, v
  *   W        bf16 [E, R, C]
  *   master   fp32 [E, R, C] or NULL: when given, the update is taken on it
  *            and W becomes its bf16 rounding (W is not read)
+ * The update is added in fp32, to 2^-17 of each of its elements (it is not rounded
+ * to bf16 as U is): full-rank updates of a master are off by 1.1e-3 to 1.3e-3 of their
+ * norm, by 1e-5 where the smaller side is at most 128, by up to 3.5e-3 at rank one.
  * The parameters are host values, read at the call (a captured call replays
  * them). lr, mu (0 <= mu < 1), weight_decay, scale, lr scale and lr weight_decay
  * finite in fp32. */
