@@ -268,7 +268,7 @@ struct Acc {
 };
 
 // One operand of a product: load i (0, 1) of wave w moves block kWaves i + w of
-// a slab. Reads past the matrix give zeros.
+// a slab. What lies past the matrix's rows or columns goes to waves without results.
 struct Operand {
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t blk;    // byte offset of block w of slab 0
@@ -880,9 +880,11 @@ OrthoPlan ortho_plan(const OrthoArgs& a) {
   g = g < 1 ? 1 : (g > 4096 ? 4096 : g);
   p.group = a.E < g ? (a.E > 0 ? a.E : 1) : g;
   size_t o = 0;
-  // The products read up to 128 rows past a matrix (as zeros: the buffer
-  // resource ends with it); the m x m matrices are followed by X, each X by its
-  // remainders.
+  // A big tile's operands reach up to 128 rows or columns past a matrix: row blocks
+  // past mp are those of the next column block, and past the last block lies what
+  // follows in the workspace (each m x m matrix is followed by X, each X by its
+  // remainders) or, where the buffer resource ends, zeros. None of it reaches a
+  // result: the waves whose rows and columns those are only move data.
   p.part = o;  o = up256(o + size_t(p.group) * d.parts * sizeof(NormPart));
   p.scale = o; o = up256(o + size_t(p.group) * 4);
   p.diag = o;  o = up256(o + size_t(p.group) * d.mp * 4 * 3);
