@@ -185,18 +185,23 @@ def _here(stream, *wanted) -> list:
         else:
             _want(t, name, dtype, numel)
             raise MoEError(MOE_ERR_SHAPE, f"{name} is on {t.device}, the current device is cuda:{dev}")
-    at.append(_stream(stream) if dev is None or stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    at.append(_stream(stream) if dev is None or stream is not None else _current_handle(dev))
     return at
 
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
 
+# The handle of a device's current stream: torch's own short cut, which builds no
+# Stream object, where this torch has it.
+_current_handle = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         if torch.cuda.is_available():
-            # the current stream's handle without building a Stream object
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+            return _current_handle(torch.cuda.current_device())
         return None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
