@@ -438,8 +438,8 @@ moe_status moe_bwd(const moe_shape* s, const void* dy, const void* x, const int3
  * the end. Against 64 bits the result is off by 1.6e-3 to 2.4e-3 of its norm
  * (the bf16 of U alone is 1.7e-3), and by up to 4e-3 where an fp32 G has rank
  * one. Elements of the iterates must stay below 2 in magnitude (with the usual
- * coefficients they stay below 1.3); past it the matrix's result is NaN. They are
- * resolved to 2^-39, so digits go where |G| is below eps by 10^5 or more, or where
+ * coefficients they stay below 1.3), those of b A + c A^2 below 65504; past either
+ * the matrix's result is not finite. Iterates are resolved to 2^-39, so digits go where |G| is below eps by 10^5 or more, or where
  * the polynomial shrinks X as far (a < 1 over many steps). A matrix
  * of zeros gives zeros; a matrix with a NaN or an infinity gives NaN throughout,
  * and leaves the others as they are. Results are deterministic.
