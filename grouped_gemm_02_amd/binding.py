@@ -77,6 +77,35 @@ class moe_muon_params(ctypes.Structure):
                 ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
+MOE_STATES = {"f32": 0, "8bit": 1}
+STATE_BLOCK = 128  # elements that share a scale where moments are held in 8 bits
+
+
+class moe_gate_params(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("groups_kept", ctypes.c_int32), ("group_top", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class moe_linear_shape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_int64)]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "master", "m", "v", "m_scale", "v_scale")] + \
+               [("n", ctypes.c_int64), ("lr_mul", ctypes.c_float), ("decay_mul", ctypes.c_float)]
+
+
+class moe_adamw_params(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32), ("step", ctypes.c_int64),
+                ("reserved", ctypes.c_int64)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -110,6 +139,16 @@ _SIGS = {
     "moe_orthogonalize": (ctypes.c_int, [ctypes.POINTER(moe_ortho_shape), _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_muon_step": (ctypes.c_int, [ctypes.POINTER(moe_ortho_shape), ctypes.POINTER(moe_muon_params), _P, _P, _P, _P,
                                      _P, ctypes.c_size_t, _P]),
+    "moe_gate": (ctypes.c_int, [ctypes.POINTER(moe_shape), ctypes.POINTER(moe_gate_params), _P, _P, _P, _P, _P, _P]),
+    "moe_gate_bwd": (ctypes.c_int, [ctypes.POINTER(moe_shape), ctypes.POINTER(moe_gate_params), _P, _P, _P,
+                                    ctypes.c_int32, _P, _P]),
+    "moe_linear_workspace_size": (ctypes.c_int, [ctypes.POINTER(moe_linear_shape), ctypes.POINTER(ctypes.c_size_t),
+                                                 ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_linear": (ctypes.c_int, [ctypes.POINTER(moe_linear_shape), _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_linear_bwd": (ctypes.c_int, [ctypes.POINTER(moe_linear_shape), _P, _P, _P, _P, _P, _P, _P, _P,
+                                      ctypes.c_size_t, _P]),
+    "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(moe_adamw_params), ctypes.POINTER(moe_adamw_tensor),
+                                      ctypes.c_int64, _P, _P, _P]),
     "moe_read_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_set_kernel_timing": (ctypes.c_int, [ctypes.c_int]),
@@ -459,6 +498,72 @@ def moe_muon_step(shape, params, grad, momentum, W, master, ws, stream=None) -> 
            "moe_muon_step")
 
 
+def make_gate_params(score="softmax", renorm=True, groups=1, groups_kept=None, group_top=1, scale=1.0) -> moe_gate_params:
+    """score: "softmax" or "sigmoid"; groups_kept defaults to all groups."""
+    sc = MOE_SCORES[score] if isinstance(score, str) else int(score)
+    return moe_gate_params(sc, int(bool(renorm)), int(groups), int(groups if groups_kept is None else groups_kept),
+                           int(group_top), float(scale), 0)
+
+
+def moe_gate(shape, params, logits, bias, mask, topk_idx, topk_w, stream=None) -> None:
+    T, E, k = shape.T, shape.E, shape.k
+    z, b, m, i, w, st = _here(stream, (logits, "logits", _F32, T * E), (bias, "bias", _F32, E), (mask, "mask", _U8, T),
+                              (topk_idx, "topk_idx", _I32, T * k), (topk_w, "topk_w", _F32, T * k))
+    _check(lib().moe_gate(ctypes.byref(shape), ctypes.byref(params), z, b, m, i, w, st), "moe_gate")
+
+
+def moe_gate_bwd(shape, params, logits, topk_idx, d_topk_w, accumulate, d_logits, stream=None) -> None:
+    T, E, k = shape.T, shape.E, shape.k
+    z, i, w, d, st = _here(stream, (logits, "logits", _F32, T * E), (topk_idx, "topk_idx", _I32, T * k),
+                           (d_topk_w, "d_topk_w", _F32, T * k), (d_logits, "d_logits", _F32, T * E))
+    _check(lib().moe_gate_bwd(ctypes.byref(shape), ctypes.byref(params), z, i, w, 1 if accumulate else 0, d, st),
+           "moe_gate_bwd")
+
+
+def make_linear_shape(M, N, K, act="none", out="bf16") -> moe_linear_shape:
+    """act: one of MOE_ACTS ("swiglu": W has 2 N rows); out: "bf16" or "f32", the type of Y, residual and dY."""
+    a = MOE_ACTS[act] if isinstance(act, str) else int(act)
+    o = MOE_DT[out] if isinstance(out, str) else int(out)
+    return moe_linear_shape(int(M), int(N), int(K), a, o, 0)
+
+
+def linear_rows(shape: moe_linear_shape) -> int:
+    """N': the rows of W, the columns of P."""
+    return 2 * shape.N if shape.act == MOE_ACTS["swiglu"] else shape.N
+
+
+def moe_linear_workspace_size(shape: moe_linear_shape):
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().moe_linear_workspace_size(ctypes.byref(shape), ctypes.byref(f), ctypes.byref(b)),
+           "moe_linear_workspace_size")
+    return f.value, b.value
+
+
+def moe_linear(shape, X, W, bias, residual, Y, pre, ws, stream=None) -> None:
+    M, N, K, R = shape.M, shape.N, shape.K, linear_rows(shape)
+    out = _BF16 if shape.out_dtype == 0 else _F32
+    x, w, b, r, y, p, s, st = _here(stream, (X, "X", _BF16, M * K), (W, "W", _BF16, R * K), (bias, "bias", _F32, R),
+                                    (residual, "residual", out, M * N), (Y, "Y", out, M * N), (pre, "pre", _BF16, M * R),
+                                    (ws, "ws", _U8, 0))
+    _check(lib().moe_linear(ctypes.byref(shape), x, w, b, r, y, p, s, 0 if ws is None else ws.numel(), st), "moe_linear")
+
+
+def moe_linear_bwd(shape, dY, X, W, pre, dX, dW, dbias, ws, stream=None) -> None:
+    M, N, K, R = shape.M, shape.N, shape.K, linear_rows(shape)
+    out = _BF16 if shape.out_dtype == 0 else _F32
+    dy, x, w, p, dx, dw, db, s, st = _here(
+        stream, (dY, "dY", out, M * N), (X, "X", _BF16, M * K), (W, "W", _BF16, R * K), (pre, "pre", _BF16, M * R),
+        (dX, "dX", _BF16, M * K), (dW, "dW", _BF16, R * K), (dbias, "dbias", _F32, R), (ws, "ws", _U8, 0))
+    _check(lib().moe_linear_bwd(ctypes.byref(shape), dy, x, w, p, dx, dw, db, s, 0 if ws is None else ws.numel(), st),
+           "moe_linear_bwd")
+
+
+def moe_adamw_step(params, tensors, count, grad_scale=None, hyper=None, stream=None) -> None:
+    """tensors: a ctypes array of moe_adamw_tensor (see AdamWBuffers)."""
+    g, h, st = _here(stream, (grad_scale, "grad_scale", _F32, 1), (hyper, "hyper", _F32, 4))
+    _check(lib().moe_adamw_step(ctypes.byref(params), tensors, int(count), g, h, st), "moe_adamw_step")
+
+
 def moe_read_status(ws, stream=None) -> int:
     out = ctypes.c_int32()
     _check(lib().moe_read_status(_ptr(ws), ctypes.byref(out), _stream(stream)), "moe_read_status")
@@ -606,3 +711,173 @@ def muon_step(buf: OrthoBuffers, grad, momentum, W, *, lr, momentum_coef=0.95, w
     """One optimizer step on the weights W in place (see moe_muon_step)."""
     p = moe_muon_params(float(lr), float(momentum_coef), float(weight_decay), float(scale), int(bool(nesterov)), 0)
     moe_muon_step(buf.shape, p, grad, momentum, W, master, buf.ws, stream)
+
+
+def gate(shape: moe_shape, params: moe_gate_params, logits, bias=None, mask=None, topk_idx=None, topk_w=None,
+         stream=None):
+    """(topk_idx, topk_w) of the experts chosen for each token (see moe_gate)."""
+    if topk_idx is None:
+        topk_idx = _result(stream, (shape.T, shape.k), _I32, logits.device)
+    if topk_w is None:
+        topk_w = _result(stream, (shape.T, shape.k), _F32, logits.device)
+    moe_gate(shape, params, logits, bias, mask, topk_idx, topk_w, stream)
+    return topk_idx, topk_w
+
+
+def gate_bwd(shape: moe_shape, params: moe_gate_params, logits, topk_idx, d_topk_w, d_logits=None, accumulate=False,
+             stream=None):
+    """d_logits of the chosen weights' gradient; accumulate adds to the d_logits given."""
+    if d_logits is None:
+        if accumulate:
+            raise MoEError(MOE_ERR_SHAPE, "accumulate needs a d_logits to add to")
+        d_logits = _result(stream, (shape.T, shape.E), _F32, logits.device)
+    moe_gate_bwd(shape, params, logits, topk_idx, d_topk_w, accumulate, d_logits, stream)
+    return d_logits
+
+
+@dataclasses.dataclass
+class LinearBuffers:
+    """Scratch of linear and linear_bwd for one shape; serves fewer rows too."""
+    shape: moe_linear_shape
+    fwd_ws: torch.Tensor
+    bwd_ws: torch.Tensor | None
+
+    @classmethod
+    def allocate(cls, shape: moe_linear_shape, device="cuda", training=True) -> "LinearBuffers":
+        f, b = moe_linear_workspace_size(shape)
+        mk = lambda n: torch.empty(max(n, 256), dtype=_U8, device=device)  # noqa: E731
+        return cls(shape, mk(f), mk(b) if training else None)
+
+    def _of(self, X) -> moe_linear_shape:
+        s = self.shape
+        if X.shape[0] == s.M:
+            return s
+        if X.shape[0] > s.M:
+            raise MoEError(MOE_ERR_SHAPE, f"X has {X.shape[0]} rows, the buffers are for {s.M}")
+        return moe_linear_shape(X.shape[0], s.N, s.K, s.act, s.out_dtype, 0)
+
+
+def linear(buf: LinearBuffers, X, W, bias=None, residual=None, Y=None, pre=None, stream=None):
+    """act(X W^T + bias) + residual for the rows X has (see moe_linear)."""
+    s = buf._of(X)
+    if Y is None:
+        Y = _result(stream, (s.M, s.N), _BF16 if s.out_dtype == 0 else _F32, X.device)
+    moe_linear(s, X, W, bias, residual, Y, pre, buf.fwd_ws, stream)
+    return Y
+
+
+def linear_bwd(buf: LinearBuffers, dY, X, W, pre=None, bias=False, dX=None, dW=None, dbias=None, need_dX=True,
+               need_dW=True, stream=None):
+    """(dX, dW, dbias) of linear; dbias is None unless `bias` (or a dbias) is
+    given, dX and dW are None where they are not needed."""
+    s, dev = buf._of(dY), dY.device
+    R = linear_rows(s)
+    if dX is None and need_dX:
+        dX = _result(stream, (s.M, s.K), _BF16, dev)
+    if dW is None and need_dW:
+        dW = _result(stream, (R, s.K), _BF16, dev)
+    if dbias is None and bias:
+        dbias = _result(stream, (R,), _F32, dev)
+    moe_linear_bwd(s, dY, X, W, pre, dX, dW, dbias, buf.bwd_ws, stream)
+    return dX, dW, dbias
+
+
+class AdamWBuffers:
+    """The tensors of an AdamW step with their moments: lists of the parameters
+    (bf16 or fp32, one type for all), m and v (fp32 of the parameter's size, or
+    uint8 codes with a scale byte per 128 elements), optionally fp32 masters of bf16
+    parameters (an entry may be None) and multipliers of the learning rate and the
+    weight decay per tensor. It holds the tensors, so that they outlive it."""
+
+    def __init__(self, params, m, v, m_scale=None, v_scale=None, master=None, lr_mul=None, decay_mul=None):
+        n = len(params)
+        none = [None] * n
+        self.params, self.m, self.v = list(params), list(m), list(v)
+        self.m_scale, self.v_scale = list(m_scale or none), list(v_scale or none)
+        self.master = list(master or none)
+        self.state = "f32" if m_scale is None else "8bit"
+        self.lr_mul, self.decay_mul = list(lr_mul or [1.0] * n), list(decay_mul or [1.0] * n)
+        for name in ("m", "v", "m_scale", "v_scale", "master", "lr_mul", "decay_mul"):
+            if len(getattr(self, name)) != n:
+                raise MoEError(MOE_ERR_SHAPE, f"{n} parameters and {len(getattr(self, name))} of {name}")
+        if (m_scale is None) != (v_scale is None):
+            raise MoEError(MOE_ERR_SHAPE, "m_scale and v_scale go together")
+        self.dtype = self.params[0].dtype if n else _F32
+        if self.dtype not in (_BF16, _F32):
+            raise MoEError(MOE_ERR_SHAPE, f"parameters are {self.dtype}, expected bf16 or fp32")
+        mt = _F32 if self.state == "f32" else _U8
+        self.device = self.params[0].device if n else None
+        for i, p in enumerate(self.params):
+            k = p.numel()
+            b = -(-k // STATE_BLOCK)
+            for t, name, dt, size in ((p, "param", self.dtype, k), (self.m[i], "m", mt, k), (self.v[i], "v", mt, k),
+                                      (self.m_scale[i], "m_scale", _U8, b), (self.v_scale[i], "v_scale", _U8, b),
+                                      (self.master[i], "master", _F32, k)):
+                if t is None and name in ("master", "m_scale", "v_scale"):
+                    continue
+                _want(t, f"{name}[{i}]", dt, size)
+                if t.device != self.device:
+                    raise MoEError(MOE_ERR_SHAPE, f"{name}[{i}] is on {t.device}, param[0] on {self.device}")
+        self._refuse_overlap()
+        self._table = (moe_adamw_tensor * max(n, 1))()
+        for i in range(n):
+            e = self._table[i]
+            e.n, e.lr_mul, e.decay_mul = self.params[i].numel(), float(self.lr_mul[i]), float(self.decay_mul[i])
+
+    def _refuse_overlap(self, grads=()) -> None:
+        """No buffer that a step writes may share memory with another of its buffers."""
+        spans = []
+        for name in ("params", "m", "v", "m_scale", "v_scale", "master"):
+            spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
+                      for t in getattr(self, name) if t is not None and t.numel()]
+        spans.sort()
+        for a, b in zip(spans, spans[1:]):
+            if b[0] < a[1]:
+                raise MoEError(MOE_ERR_SHAPE, f"buffers of {a[2]} and {b[2]} overlap")
+
+    @classmethod
+    def allocate(cls, params, state="f32", master=False, lr_mul=None, decay_mul=None) -> "AdamWBuffers":
+        """Moments of zero (and fp32 copies of bf16 parameters as masters) beside the parameters."""
+        params = list(params)
+        if state not in MOE_STATES:
+            raise MoEError(MOE_ERR_SHAPE, f"state is {state!r}, expected one of {sorted(MOE_STATES)}")
+        mk = lambda p, n, dt: torch.zeros(n, dtype=dt, device=p.device)  # noqa: E731
+        dt = _F32 if state == "f32" else _U8
+        m, v = ([mk(p, p.numel(), dt) for p in params] for _ in range(2))
+        sc = [None, None]
+        if state == "8bit":
+            sc = [[mk(p, -(-p.numel() // STATE_BLOCK), _U8) for p in params] for _ in range(2)]
+        ms = [p.detach().float().clone().view(-1) for p in params] if master else None
+        return cls(params, m, v, sc[0], sc[1], ms, lr_mul, decay_mul)
+
+
+def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1,
+               grad_scale=None, hyper=None, stream=None) -> None:
+    """One AdamW step on the parameters in place (see moe_adamw_step). grads: one tensor
+    per parameter, bf16 or fp32, one type for all; None passes a parameter over."""
+    n = len(buf.params)
+    if len(grads) != n:
+        raise MoEError(MOE_ERR_SHAPE, f"{n} parameters and {len(grads)} gradients")
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    if n and buf.device.type == "cuda" and buf.device.index != dev:
+        raise MoEError(MOE_ERR_SHAPE, f"the parameters are on {buf.device}, the current device is cuda:{dev}")
+    gt = next((g.dtype for g in grads if g is not None), _F32)
+    if gt not in (_BF16, _F32):
+        raise MoEError(MOE_ERR_SHAPE, f"gradients are {gt}, expected bf16 or fp32")
+    table = buf._table
+    for i, g in enumerate(grads):
+        e, p = table[i], buf.params[i]
+        if g is None:
+            e.n = 0
+            continue
+        k = p.numel()
+        if g.get_device() != dev or g.dtype is not gt or g.numel() != k or not g.is_contiguous():
+            _want(g, f"grads[{i}]", gt, k)
+            raise MoEError(MOE_ERR_SHAPE, f"grads[{i}] holds {g.numel()} elements on {g.device}, needs {k} on cuda:{dev}")
+        e.n, e.param, e.grad = k, p.data_ptr(), g.data_ptr()
+        e.m, e.v = buf.m[i].data_ptr(), buf.v[i].data_ptr()
+        e.m_scale, e.v_scale, e.master = _ptr(buf.m_scale[i]), _ptr(buf.v_scale[i]), _ptr(buf.master[i])
+    p = moe_adamw_params(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
+                         MOE_DT["bf16"] if buf.dtype is _BF16 else MOE_DT["f32"],
+                         MOE_DT["bf16"] if gt is _BF16 else MOE_DT["f32"], MOE_STATES[buf.state], int(step), 0)
+    moe_adamw_step(p, table, n, grad_scale, hyper, stream)

@@ -197,4 +197,59 @@ struct OrthoTarget {
 size_t ortho_workspace_bytes(const OrthoArgs& a);
 hipError_t launch_ortho(const OrthoArgs& a, const OrthoTarget& t, void* ws, hipStream_t st, KernelTimer* timer);
 
+// ---------------------------------------------------------------- gate
+struct GateArgs {
+  const float* logits;
+  const float* bias;    // nullptr: the choice goes by the logits
+  const uint8_t* mask;  // nullptr: every token counts
+  int64_t T;
+  int E, k;
+  bool sigmoid, renorm;
+  int groups, groups_kept, group_top;
+  float scale;
+};
+hipError_t launch_gate(const GateArgs& a, int32_t* idx, float* w, hipStream_t st, KernelTimer* timer);
+// a.bias, a.mask and the groups are not read
+hipError_t launch_gate_bwd(const GateArgs& a, const int32_t* idx, const float* dw, int accumulate, float* dz,
+                           hipStream_t st, KernelTimer* timer);
+
+// ---------------------------------------------------------------- dense products
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActSwiglu = 4;
+struct LinearArgs {
+  int64_t M, N, K;
+  int act;
+  bool out_f32;
+};
+size_t linear_workspace_bytes(const LinearArgs& a, bool bwd);
+hipError_t launch_linear(const LinearArgs& a, const uint16_t* X, const uint16_t* W, const float* bias,
+                         const void* residual, void* Y, uint16_t* pre, void* ws, hipStream_t st, KernelTimer* timer);
+hipError_t launch_linear_bwd(const LinearArgs& a, const void* dY, const uint16_t* X, const uint16_t* W,
+                             const uint16_t* pre, uint16_t* dX, uint16_t* dW, float* dbias, void* ws, hipStream_t st,
+                             KernelTimer* timer);
+
+// ---------------------------------------------------------------- AdamW
+struct AdamwHyper {
+  float lr, beta1, beta2, alpha1, alpha2, eps, weight_decay;  // alpha = 1 - beta, rounded once
+  float bias1, root2;  // 1 - beta1^t, 1 / sqrt(1 - beta2^t)
+};
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t n;
+  float lr_mul, decay_mul;
+};
+struct AdamwArgs {
+  AdamwHyper h;
+  bool param_bf16, grad_bf16, eight;
+  const float* grad_scale;  // device, or nullptr
+  const float* hyper;       // device, or nullptr
+};
+hipError_t launch_adamw(const AdamwArgs& a, const AdamwTensor* tensors, int64_t count, hipStream_t st,
+                        KernelTimer* timer);
+
 }  // namespace moe

@@ -1,0 +1,816 @@
+// Dense products with bias, activation and residual, and their gradients
+// (include/moe.h: moe_linear, moe_linear_bwd): the router's logits and a shared
+// expert beside the routed ones (the pages' layer is the routed experts alone).
+//
+// Every product is C[m][n] = sum_k P[m][k] Q[n][k]:
+//   forward  P = X, Q = W                    both with k along their rows (k-major)
+//   dX       P = dP, Q = W^T                 W has one memory row per k (mn-major)
+//   dW       P = dP^T, Q = X^T               both mn-major, k the token
+// Tiles of BM x BN, slabs of 64 k staged in LDS in two stages by loads that go there
+// directly (buffer_load ... lds): while one slab is multiplied the next one is on its
+// way. Waves take 32 x 32 sub-tiles with v_mfma_f32_32x32x16_bf16, Q's fragment as the A
+// operand, so that a lane holds one row m and runs of four columns n.
+//   k-major operand in LDS: rows of 64 k, 16-byte chunk c of row r at slot c ^ (r / 2) % 8:
+//     fragment reads (16 rows, one chunk) then touch 16 different bank groups.
+//   mn-major operand: k-rows of the tile's entities, chunk c of k-row k at slot
+//     c ^ 4 (k % 4) (64 entities: c ^ 4 ((k / 2) % 2)); a fragment comes from two
+//     transpose reads (ds_read_b64_tr_b16), whose 16 (row, chunk) pairs lie in
+//     different bank groups.
+// Rows and columns past the matrix are read from a valid row or as zeros and not
+// stored; k past the end is zero in both operands. Rows that are no multiple of 16 bytes
+// are first copied to rows that are.
+#include <algorithm>
+
+#include "device_common.h"
+#include "kernels.h"
+
+namespace moe {
+namespace lin {
+
+constexpr int BK = 64;
+constexpr uint32_t kPast = 0x80000000u;  // an offset beyond any extent: reads as zero
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef short v8i16 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, int(uint32_t(bytes)), 0x00020000);
+}
+
+// 16 bytes a lane from the resource's offset off + at (zeros past its end) into 1 KiB of LDS
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint16_t* lds, uint32_t off, int at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(lds), 16, off, at, 0, 0);
+}
+__device__ __forceinline__ void load_lds(const void* base, int64_t bytes, uint16_t* lds, uint32_t off) {
+  load_lds(rsrc(base, bytes), lds, off, 0);
+}
+
+// ------------------------------------------------------------------ what a result goes through
+
+// P's columns c .. c+7 of row r on their way out. For SwiGLU u holds the up part.
+struct Out {
+  const float* bias;
+  const void* residual;
+  void* Y;
+  uint16_t* pre;
+  int64_t M;
+  int N;      // columns of Y
+  int act;    // kAct*
+  bool f32;   // type of Y and residual
+};
+
+__device__ __forceinline__ float sigmoid(float x) { return sigmoidf_fast(x); }
+// sigmoid(2 sqrt(2 / pi) (x + 0.044715 x^3)): GELU's factor in its tanh form
+__device__ __forceinline__ float gelu_gate(float x) { return sigmoid(1.5957691216057308f * (x + 0.044715f * x * x * x)); }
+
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], int cols) {
+  if (cols >= 8) {
+    *reinterpret_cast<u32x4u*>(p) =
+        u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < cols) p[i] = uint16_t(pack_bf16x2(v[i], 0.f));
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], int cols) {
+  if (cols >= 8) {
+    f32x4u* q = reinterpret_cast<f32x4u*>(p);
+    q[0] = f32x4{v[0], v[1], v[2], v[3]};
+    q[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < cols) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8], int cols) {
+  if (cols >= 8) {
+    const u32x4 a = *reinterpret_cast<const u32x4u*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(a[i]);
+      v[2 * i + 1] = bf16_hi(a[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < cols ? __uint_as_float(uint32_t(p[i]) << 16) : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8], int cols) {
+  if (cols >= 8) {
+    const f32x4u* q = reinterpret_cast<const f32x4u*>(p);
+    const f32x4 a = q[0], b = q[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < cols ? p[i] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void finish8(const Out& o, int64_t r, int c, float (&v)[8], float (&u)[8]) {
+  const int cols = o.N - c;
+  float b[8];
+  if (o.bias) {
+    load8(o.bias + c, b, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+  }
+  if (o.act == kActSwiglu) {
+    if (o.bias) {
+      load8(o.bias + o.N + c, b, cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] += b[i];
+    }
+    if (o.pre) {
+      store8(o.pre + r * (2 * int64_t(o.N)) + c, v, cols);
+      store8(o.pre + r * (2 * int64_t(o.N)) + o.N + c, u, cols);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
+  } else {
+    if (o.pre) store8(o.pre + r * int64_t(o.N) + c, v, cols);
+    if (o.act == kActRelu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] > 0.f || v[i] != v[i] ? v[i] : 0.f;
+    } else if (o.act == kActSilu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= sigmoid(v[i]);
+    } else if (o.act == kActGelu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= gelu_gate(v[i]);
+    }
+  }
+  const int64_t at = r * int64_t(o.N) + c;
+  if (o.residual) {
+    if (o.f32) load8(static_cast<const float*>(o.residual) + at, b, cols);
+    else load8(static_cast<const uint16_t*>(o.residual) + at, b, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+  }
+  if (o.f32) store8(static_cast<float*>(o.Y) + at, v, cols);
+  else store8(static_cast<uint16_t*>(o.Y) + at, v, cols);
+}
+
+// ------------------------------------------------------------------ operands
+
+struct Operand {
+  const uint16_t* data;
+  int64_t ld;    // elements from row to row, a multiple of 8
+  int64_t ents;  // entities (rows m of P, n of Q)
+  bool pair;     // SwiGLU's W: entities are read as 32 gate rows, 32 up rows, ...
+};
+
+// Matrix row (k-major) of tile entity q of a paired operand with ents = 2 N rows:
+// 32 gate rows and their 32 up rows take turns.
+__device__ __forceinline__ int64_t paired_row(int64_t q0, int q, int64_t N) {
+  const int64_t o = (q0 >> 1) + (q >> 6) * 32 + (q & 31);
+  return (q >> 5 & 1) * N + (o < N ? o : N - 1);
+}
+
+// k-major: thread t's load i fills LDS slot t + THREADS i (row = slot / 8).
+template <int ROWS, int THREADS>
+struct KMajor {
+  static constexpr int kPer = ROWS * 8 / THREADS;
+  __amdgpu_buffer_rsrc_t data;
+  uint32_t off[kPer];
+  int chunk;  // of every row this thread loads
+  int K;      // a multiple of 8
+  __device__ __forceinline__ void init(const Operand& op, int64_t e0, int64_t, int Kp) {
+    const int r0 = threadIdx.x >> 3;
+    chunk = int(threadIdx.x & 7) ^ (r0 >> 1 & 7);
+    K = Kp;
+    const int64_t left = op.ents - e0;
+    const int64_t first = op.pair ? 0 : e0;
+    data = rsrc(op.data + first * op.ld, op.pair ? op.ents * op.ld * 2 : (left < ROWS ? left : ROWS) * op.ld * 2);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int q = r0 + THREADS / 8 * i;
+      const int64_t row = op.pair ? paired_row(e0, q, op.ents >> 1) : (q < left ? q : left - 1);
+      off[i] = uint32_t(row * op.ld * 2) + 16u * chunk;
+    }
+  }
+  __device__ __forceinline__ void load(int kt, uint16_t* lds) const {
+    const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const uint32_t past = kt * BK + 8 * chunk < K ? 0u : kPast;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      load_lds(data, lds + (64 * w + THREADS * i) * 8, off[i] | past, kt * 2 * BK);
+  }
+};
+
+// mn-major: slab kt is memory rows 64 kt ..; its buffer resource ends with the last k.
+template <int COLS, int THREADS>
+struct MNMajor {
+  static constexpr int kPer = COLS * 8 / THREADS;
+  static constexpr int kRow = COLS / 8;  // chunks of a k-row
+  const uint16_t* base;
+  int64_t ld, kend, e0;
+  uint32_t off[kPer];
+  __device__ __forceinline__ void init(const Operand& op, int64_t e, int64_t kred, int) {
+    base = op.data;
+    ld = op.ld;
+    kend = kred;
+    e0 = e;
+    const int64_t left = op.ents - e;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int q = int(threadIdx.x) + THREADS * i;
+      const int k = q / kRow, c = (q % kRow) ^ (COLS >= 128 ? 4 * (k & 3) : 4 * (k >> 1 & 1));
+      off[i] = uint32_t((k * ld + 8 * c) * 2) | (8 * c < left ? 0u : kPast);
+    }
+  }
+  __device__ __forceinline__ void load(int kt, uint16_t* lds) const {
+    const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int64_t k0 = int64_t(kt) * BK;
+    const int64_t rows = kend - k0 < BK ? kend - k0 : BK;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      load_lds(base + k0 * ld + e0, (rows * ld - e0) * 2, lds + (64 * w + THREADS * i) * 8, off[i]);
+  }
+};
+
+template <bool MN, int ENTS, int THREADS>
+struct LoaderOf { using type = KMajor<ENTS, THREADS>; };
+template <int ENTS, int THREADS>
+struct LoaderOf<true, ENTS, THREADS> { using type = MNMajor<ENTS, THREADS>; };
+
+// slot of chunk c of k-row k of an mn-major slab `ents` wide
+__device__ __forceinline__ int mn_swz(int ents, int k) { return ents >= 128 ? 4 * (k & 3) : 4 * (k >> 1 & 1); }
+
+// 32 entities x 16 k: lane holds entity lane % 32, k = 16 kk + 8 (lane / 32) + 0..7.
+__device__ __forceinline__ bf16x8 frag_k(const uint16_t* lds, int ent0, int kk) {
+  const int lane = lane_id();
+  const int e = ent0 + (lane & 31), c = 2 * kk + (lane >> 5);
+  return *reinterpret_cast<const bf16x8*>(lds + e * BK + ((c ^ (e >> 1 & 7)) << 3));
+}
+// The same of an mn-major slab. In each 16-lane group lane p addresses k-row k0 + p / 4
+// at entities n0 + 4 (p % 4) and receives four consecutive k of entity n0 + p; rows k and
+// k + 4 have the same swizzle.
+__device__ __forceinline__ bf16x8 frag_mn(const uint16_t* lds, int ents, int ent0, int kk) {
+  const int lane = lane_id();
+  const int g = lane >> 4, p = lane & 15;
+  const int n = ent0 + 16 * (g & 1) + 4 * (p & 3);
+  const int k0 = 8 * (g >> 1) + (p >> 2);
+  int off = k0 * ents + (((n >> 3) ^ mn_swz(ents, k0)) << 3) + (n & 7);
+  asm("" : "+v"(off));  // one offset for all of a sub-tile's reads
+  const uint16_t* a = lds + off + kk * 16 * ents;
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(a + 4 * ents));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <bool MN, int ENTS>
+__device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int ent0, int kk) {
+  if constexpr (MN) return frag_mn(lds, ENTS, ent0, kk);
+  return frag_k(lds, ent0, kk);
+}
+
+// ------------------------------------------------------------------ the tile kernel
+
+struct Problem {
+  Operand P, Q;
+  int64_t kred;     // k that exist
+  int Kp;           // kred rounded up to 8 (k-major operands)
+  int mt, nt;       // tiles
+  int splits;       // parts of the k axis; more than one: sums go to `partial`
+  int slabs;        // slabs of a part
+  float* partial;   // fp32 [splits][M][ldp]
+  int64_t ldp;
+  Out out;
+};
+
+// Block b's tile: the eight XCDs (b % 8) take contiguous ranges of tiles, and a range
+// walks groups of eight row tiles column by column, so that tiles that run at once in
+// an XCD share rows of both operands in its L2.
+__device__ __forceinline__ void tile_of(const Problem& p, uint32_t b, uint32_t total, int* m, int* n, int* s) {
+  const uint32_t q = total / 8, r = total % 8, x = b % 8;
+  uint32_t t = x * q + (x < r ? x : r) + b / 8;
+  const uint32_t per = uint32_t(p.mt) * uint32_t(p.nt);
+  *s = int(t / per);
+  t %= per;
+  const uint32_t group = t / (8u * uint32_t(p.nt));
+  const uint32_t rows = min(8u, uint32_t(p.mt) - 8u * group);
+  t -= group * 8u * uint32_t(p.nt);
+  *m = int(8u * group + t % rows);
+  *n = int(t / rows);
+}
+
+template <int BM, int BN, int WM, int WN, bool P_MN, bool Q_MN>
+__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const Problem p) {
+  constexpr int kThreads = 64 * WM * WN;
+  constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+  constexpr int kStage = (BM + BN) * BK;
+  // two LDS objects, so that the compiler can tell reads of one stage from loads in
+  // flight into the other
+  __shared__ __attribute__((aligned(16))) uint16_t s0[kStage];
+  __shared__ __attribute__((aligned(16))) uint16_t s1[kStage];
+  int mi, ni, si;
+  tile_of(p, blockIdx.x, gridDim.x, &mi, &ni, &si);
+  const int64_t m0 = int64_t(mi) * BM, n0 = int64_t(ni) * BN;
+  const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN, lane = lane_id();
+  typename LoaderOf<P_MN, BM, kThreads>::type lp;
+  typename LoaderOf<Q_MN, BN, kThreads>::type lq;
+  lp.init(p.P, m0, p.kred, p.Kp);
+  lq.init(p.Q, n0, p.kred, p.Kp);
+  const int all = int((p.kred + BK - 1) / BK);
+  const int k0 = si * p.slabs, nk = min(p.slabs, all - k0);
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  auto fetch = [&](int kt, uint16_t* s) {
+    lp.load(kt, s);
+    lq.load(kt, s + BM * BK);
+  };
+  auto slab = [&](int kt, const uint16_t* cur, uint16_t* nxt) {
+    if (kt + 1 < nk) fetch(k0 + kt + 1, nxt);
+    __builtin_amdgcn_iglp_opt(0);
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk) {
+      bf16x8 pf[TM], qf[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) qf[j] = frag<Q_MN, BN>(cur + BM * BK, wn * WTN + 32 * j, kk);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) pf[i] = frag<P_MN, BM>(cur, wm * WTM + 32 * i, kk);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma_32x32x16(qf[j], pf[i], acc[i][j]);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the next slab is there
+    __syncthreads();
+  };
+  if (nk > 0) {
+    fetch(k0, s0);
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    int kt = 0;
+    for (; kt + 1 < nk; kt += 2) {
+      slab(kt, s0, s1);
+      slab(kt + 1, s1, s0);
+    }
+    if (kt < nk) slab(kt, s0, s1);
+  }
+  // The accumulators go through LDS in fp32, HC columns at a time (rows [0, BM / 2) in
+  // the first stage), 16-byte chunk c of row m at slot c ^ m; then a thread takes eight
+  // columns of a row, so that stores and the loads of the epilogue are contiguous.
+  constexpr int kParts = BM * BN * 4 > 4 * kStage ? 2 : 1;
+  constexpr int HC = BN / kParts;
+  constexpr int kSlots = HC / 4;
+  static_assert(BM * HC * 4 <= 4 * kStage && WTN <= HC, "the tile's part fits both stages");
+  auto row = [&](int m) { return reinterpret_cast<float*>(m < BM / 2 ? s0 : s1) + (m % (BM / 2)) * HC; };
+  for (int h = 0; h < kParts; ++h) {
+    if (kParts == 1 || wn / (WN / kParts) == h) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int m = wm * WTM + 32 * i + (lane & 31);
+        float* dst = row(m);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int c = (wn * WTN + 32 * j + 8 * g + 4 * (lane >> 5) - h * HC) / 4;
+            const f32x16& a = acc[i][j];
+            *reinterpret_cast<f32x4*>(dst + ((c ^ (m & (kSlots - 1))) << 2)) =
+                f32x4{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
+          }
+      }
+    }
+    __syncthreads();
+    auto get = [&](int m, int c, float (&v)[8]) {
+      const float* src = row(m);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(src + (((c / 4 + q) ^ (m & (kSlots - 1))) << 2));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * q + i] = a[i];
+      }
+    };
+    const int rows = int(min(int64_t(BM), p.P.ents - m0));
+    if (p.splits > 1) {
+      constexpr int kPerRow = HC / 8;
+      for (int q = threadIdx.x; q < rows * kPerRow; q += kThreads) {
+        const int m = q / kPerRow, c = 8 * (q % kPerRow);
+        const int64_t col = n0 + h * HC + c;
+        if (col >= p.ldp) continue;
+        float v[8];
+        get(m, c, v);
+        float* dst = p.partial + (int64_t(si) * p.P.ents + m0 + m) * p.ldp + col;
+        *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      }
+    } else if (p.Q.pair) {
+      constexpr int kPerRow = HC / 16;
+      for (int q = threadIdx.x; q < rows * kPerRow; q += kThreads) {
+        const int m = q / kPerRow, o = 8 * (q % kPerRow), c = (o >> 5) * 64 + (o & 31);
+        const int col = int(n0 / 2) + h * (HC / 2) + o;
+        if (col >= p.out.N) continue;
+        float v[8], u[8];
+        get(m, c, v);
+        get(m, c + 32, u);
+        finish8(p.out, m0 + m, col, v, u);
+      }
+    } else {
+      constexpr int kPerRow = HC / 8;
+      for (int q = threadIdx.x; q < rows * kPerRow; q += kThreads) {
+        const int m = q / kPerRow, c = 8 * (q % kPerRow);
+        const int col = int(n0) + h * HC + c;
+        if (col >= p.out.N) continue;
+        float v[8], u[8];
+        get(m, c, v);
+        finish8(p.out, m0 + m, col, v, u);
+      }
+    }
+    if (kParts > 1) __syncthreads();
+  }
+}
+
+// The parts of a split product added in their order, and on through the epilogue. A
+// paired product's columns stand in the order its tiles have them.
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, int splits, int64_t ldp, bool pair,
+                                                   Out o) {
+  const int per = (o.N + 7) / 8;
+  const int64_t total = o.M * per;
+  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < total; q += int64_t(gridDim.x) * 256) {
+    const int64_t m = q / per;
+    const int c = int(q % per) * 8;
+    const int col = pair ? (c >> 5) * 64 + (c & 31) : c;
+    float v[8], u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+    const float* src = partial + m * ldp + col;
+    for (int s = 0; s < splits; ++s, src += o.M * ldp) {
+      float a[8];
+      load8(src, a, 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += a[i];
+      if (pair) {
+        load8(src + 32, a, 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] += a[i];
+      }
+    }
+    finish8(o, m, c, v, u);
+  }
+}
+
+// ------------------------------------------------------------------ passes around the products
+
+// rows [R, C] -> [R, ld], the columns past C zero
+__global__ __launch_bounds__(256) void pad_kernel(const uint16_t* __restrict__ in, int64_t R, int C, int64_t ld,
+                                                  uint16_t* __restrict__ out) {
+  const int per = int(ld / 8);
+  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < R * per; q += int64_t(gridDim.x) * 256) {
+    const int64_t r = q / per;
+    const int c = int(q % per) * 8;
+    const uint16_t* src = in + r * C + c;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (c + 8 <= C) {
+      v = *reinterpret_cast<const u32x4u*>(src);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < C) v[i / 2] |= uint32_t(src[i]) << (16 * (i & 1));
+    }
+    *reinterpret_cast<u32x4*>(out + r * ld + c) = v;
+  }
+}
+
+struct DpArgs {
+  const void* dY;
+  const uint16_t* pre;
+  int64_t M;
+  int N;       // columns of dY
+  int act;
+  bool f32;    // type of dY
+  uint16_t* dP;  // [M, ld], columns past N' zero, or NULL
+  int64_t ld;
+  float* sums;  // [blocks][cols] column sums of dP, or NULL
+  int cols;     // N'
+  int rows;     // rows of a block
+};
+
+// dP = dY act'(P), and its column sums. A workgroup takes `rows` rows of 8 x 32 = 256
+// columns; thread t the columns 8 (t % 32) of rows t / 32, + 8, ...
+__global__ __launch_bounds__(256) void dp_kernel(const DpArgs a) {
+  __shared__ float red[8][256];
+  const int tr = threadIdx.x >> 5, tc = threadIdx.x & 31;
+  const int c = int(blockIdx.y) * 256 + 8 * tc;
+  const int64_t r0 = int64_t(blockIdx.x) * a.rows;
+  const bool pair = a.act == kActSwiglu;
+  const int cols = a.N - c;
+  float sv[8], su[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sv[i] = su[i] = 0.f;
+  if (cols > 0) {
+    for (int64_t r = r0 + tr; r < min(a.M, r0 + a.rows); r += 8) {
+      float d[8], g[8], u[8], o[8], up[8];
+      if (a.f32) load8(static_cast<const float*>(a.dY) + r * a.N + c, d, cols);
+      else load8(static_cast<const uint16_t*>(a.dY) + r * a.N + c, d, cols);
+      if (a.act != kActNone) load8(a.pre + r * a.cols + c, g, cols);
+      if (pair) load8(a.pre + r * a.cols + a.N + c, u, cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        up[i] = 0.f;
+        o[i] = d[i];
+        if (a.act == kActRelu) {
+          o[i] = g[i] > 0.f ? d[i] : (g[i] != g[i] ? g[i] : 0.f);
+        } else if (a.act == kActGelu) {
+          const float s = gelu_gate(g[i]);
+          o[i] = d[i] * (s + g[i] * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * g[i] * g[i]));
+        } else if (a.act == kActSilu || pair) {
+          const float s = sigmoid(g[i]);
+          const float slope = s * (1.f + g[i] * (1.f - s));
+          o[i] = pair ? d[i] * u[i] * slope : d[i] * slope;
+          if (pair) up[i] = d[i] * g[i] * s;
+        }
+        sv[i] += o[i];
+        su[i] += up[i];
+      }
+      if (a.dP) {
+        // a row's last chunk takes the zeros behind it along (up's, for a pair)
+        uint16_t* dst = a.dP + r * a.ld + c;
+        if (!pair) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = i < cols ? o[i] : 0.f;
+          store8(dst, o, 8);
+        } else {
+          store8(dst, o, cols);
+          store8(dst + a.N, up, cols);
+          if (cols <= 8)
+            for (int64_t z = 2 * int64_t(a.N); z < a.ld; ++z) a.dP[r * a.ld + z] = 0;
+        }
+      }
+    }
+  }
+  if (!a.sums) return;
+  for (int part = 0; part < (pair ? 2 : 1); ++part) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[tr][8 * tc + i] = part ? su[i] : sv[i];
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
+    const int col = int(blockIdx.y) * 256 + int(threadIdx.x);
+    if (col < a.N) a.sums[int64_t(blockIdx.x) * a.cols + part * a.N + col] = s;
+  }
+}
+
+// dbias from the blocks' sums; no blocks: zeros
+__global__ __launch_bounds__(256) void bias_kernel(const float* __restrict__ sums, int blocks, int cols,
+                                                   float* __restrict__ out) {
+  __shared__ float red[4][64];
+  const int lane = lane_id(), w = threadIdx.x >> 6;
+  const int c = int(blockIdx.x) * 64 + lane;
+  float s = 0.f;
+  if (c < cols)
+    for (int b = w; b < blocks; b += 4) s += sums[int64_t(b) * cols + c];
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < cols) out[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t* __restrict__ p, int64_t n) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) p[i] = 0;
+}
+
+// ------------------------------------------------------------------ plans
+
+// How a product M x N over kred is cut.
+struct Plan {
+  int tile;    // 256, 128 or 64
+  int splits;  // parts of the k axis
+};
+
+constexpr int kMaxSplits = 16;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+Plan plan_of(int64_t M, int64_t N, int64_t kred) {
+  const int64_t slabs = ceil_div(kred, BK);
+  Plan best{64, 1};
+  double least = 1e300;
+  for (int tile : {256, 128, 64}) {
+    const int64_t tiles = ceil_div(M, tile) * ceil_div(N, tile);
+    if (tile < 256 && tiles > (1 << 20)) continue;  // a grid has less than 2^32 threads
+    const int64_t slots = tile == 256 ? 256 : tile == 128 ? 512 : 1024;  // workgroups that run at once
+    for (int64_t s = 1; s <= kMaxSplits && s <= slabs; s *= 2) {
+      if (s > 1 && tiles * s > 2 * slots) break;
+      const double rounds = double(ceil_div(tiles * s, slots));
+      // per slab and tile, with the slots full: 256 x 256 in 1.6 us, and so on
+      const double slab = tile == 256 ? 1.6 : tile == 128 ? 1.1 : 0.75;
+      const double join = s > 1 ? 4.0 + 2.0 * double(s) * double(M) * double(N) * 4e-6 / 4.0 : 0.0;
+      const double t = rounds * (double(ceil_div(slabs, s)) * slab + 4.0) + join;
+      if (t < least) {
+        least = t;
+        best = Plan{tile, int(s)};
+      }
+    }
+  }
+  return best;
+}
+
+int64_t pad8(int64_t n) { return (n + 7) & ~int64_t(7); }
+
+template <int T, int W>
+hipError_t launch_tiles(const Problem& p, bool pmn, bool qmn, hipStream_t st) {
+  const dim3 grid(unsigned(int64_t(p.mt) * p.nt * p.splits)), block(64 * W * (T == 256 ? 4 : W));
+  constexpr int WN = T == 256 ? 4 : W;
+  if (!pmn && !qmn) hipLaunchKernelGGL((tile_kernel<T, T, W, WN, false, false>), grid, block, 0, st, p);
+  else if (!pmn) hipLaunchKernelGGL((tile_kernel<T, T, W, WN, false, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((tile_kernel<T, T, W, WN, true, true>), grid, block, 0, st, p);
+  return hipGetLastError();
+}
+
+// What the parts of a split product M x N may take at most: kMaxSplits of them, and
+// twice as many tiles as run at once. Grows with M, so a scratch serves smaller M.
+size_t partial_bytes(int64_t M, int64_t N) {
+  const size_t all = size_t(kMaxSplits) * size_t(M) * size_t(ceil_div(N, 64) * 64) * 4;
+  return std::min(all, size_t(2 * 256) * 256 * 256 * 4);
+}
+
+hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64_t kred, const Out& out, float* partial,
+                   hipStream_t st, KernelTimer* timer, const char* name) {
+  const Plan pl = plan_of(P.ents, Q.ents, kred);
+  Problem p;
+  p.P = P;
+  p.Q = Q;
+  p.kred = kred;
+  p.Kp = int(pad8(kred));
+  p.mt = int(ceil_div(P.ents, pl.tile));
+  // a pair's columns come in groups of 64 with 32 of each part
+  const int64_t ncols = Q.pair ? ceil_div(Q.ents / 2, 32) * 64 : Q.ents;
+  p.nt = int(ceil_div(ncols, pl.tile));
+  const int64_t slabs = ceil_div(kred, BK);
+  p.slabs = int(ceil_div(slabs, pl.splits));
+  p.splits = int(ceil_div(slabs, p.slabs));
+  p.partial = partial;
+  p.ldp = ceil_div(ncols, 64) * 64;
+  p.out = out;
+  hipError_t e;
+  {
+    TimedLaunch tl(timer, name, st);
+    e = pl.tile == 256 ? launch_tiles<256, 2>(p, pmn, qmn, st)
+        : pl.tile == 128 ? launch_tiles<128, 2>(p, pmn, qmn, st) : launch_tiles<64, 2>(p, pmn, qmn, st);
+  }
+  if (e != hipSuccess || p.splits == 1) return e;
+  TimedLaunch tl(timer, "linear_join", st);
+  const int64_t blocks = ceil_div(out.M * ceil_div(out.N, 8), 256);
+  hipLaunchKernelGGL(join_kernel, dim3(unsigned(std::min<int64_t>(blocks, 4096))), dim3(256), 0, st, partial, p.splits,
+                     p.ldp, Q.pair, out);
+  return hipGetLastError();
+}
+
+hipError_t pad(const uint16_t* in, int64_t R, int64_t C, uint16_t* out, hipStream_t st, KernelTimer* timer) {
+  TimedLaunch tl(timer, "linear_pad", st);
+  const int64_t blocks = ceil_div(R * (pad8(C) / 8), 256);
+  hipLaunchKernelGGL(pad_kernel, dim3(unsigned(std::min<int64_t>(blocks, 8192))), dim3(256), 0, st, in, R, int(C),
+                     pad8(C), out);
+  return hipGetLastError();
+}
+
+constexpr size_t kAlign = 256;
+size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+constexpr int64_t kDpRows = 64, kDpBlocks = 256;
+// rows of a block of dp_kernel: no more than kDpBlocks blocks
+int64_t dp_rows(int64_t M) { return std::max<int64_t>(kDpRows, ceil_div(M, kDpBlocks)); }
+
+struct Layout {
+  size_t x, w, dp, sums, partial, total;
+};
+
+Layout layout(const LinearArgs& a, bool bwd) {
+  const int64_t R = a.act == kActSwiglu ? 2 * a.N : a.N;
+  Layout L{};
+  size_t o = 0;
+  const bool odd = a.K % 8 != 0;
+  L.x = o; o += odd ? up(size_t(a.M) * pad8(a.K) * 2) : 0;
+  L.w = o; o += odd ? up(size_t(R) * pad8(a.K) * 2) : 0;
+  if (!bwd) {
+    L.partial = o;
+    o += up(partial_bytes(a.M, R));
+  } else {
+    L.dp = o; o += up(size_t(a.M) * pad8(R) * 2);
+    L.sums = o; o += up(size_t(std::min<int64_t>(ceil_div(a.M, kDpRows), kDpBlocks)) * R * 4);
+    L.partial = o;
+    o += up(std::max(partial_bytes(a.M, a.K), partial_bytes(R, a.K)));
+  }
+  L.total = o;
+  return L;
+}
+
+}  // namespace lin
+
+size_t linear_workspace_bytes(const LinearArgs& a, bool bwd) { return lin::layout(a, bwd).total; }
+
+hipError_t launch_linear(const LinearArgs& a, const uint16_t* X, const uint16_t* W, const float* bias,
+                         const void* residual, void* Y, uint16_t* pre, void* ws, hipStream_t st, KernelTimer* timer) {
+  using namespace lin;
+  if (a.M <= 0) return hipSuccess;
+  const Layout L = layout(a, false);
+  char* base = static_cast<char*>(ws);
+  const int64_t R = a.act == kActSwiglu ? 2 * a.N : a.N;
+  if (a.K % 8 != 0) {
+    uint16_t* xp = reinterpret_cast<uint16_t*>(base + L.x);
+    uint16_t* wp = reinterpret_cast<uint16_t*>(base + L.w);
+    hipError_t e = pad(X, a.M, a.K, xp, st, timer);
+    if (e == hipSuccess) e = pad(W, R, a.K, wp, st, timer);
+    if (e != hipSuccess) return e;
+    X = xp;
+    W = wp;
+  }
+  const Out out{bias, residual, Y, pre, a.M, int(a.N), a.act, a.out_f32};
+  return product(Operand{X, pad8(a.K), a.M, false}, false, Operand{W, pad8(a.K), R, a.act == kActSwiglu}, false, a.K, out,
+                 reinterpret_cast<float*>(base + L.partial), st, timer, "linear");
+}
+
+hipError_t launch_linear_bwd(const LinearArgs& a, const void* dY, const uint16_t* X, const uint16_t* W,
+                             const uint16_t* pre, uint16_t* dX, uint16_t* dW, float* dbias, void* ws, hipStream_t st,
+                             KernelTimer* timer) {
+  using namespace lin;
+  const int64_t R = a.act == kActSwiglu ? 2 * a.N : a.N;
+  hipError_t e = hipSuccess;
+  if (a.M <= 0) {
+    if (dW) {
+      TimedLaunch tl(timer, "linear_zero", st);
+      hipLaunchKernelGGL(zero_kernel, dim3(unsigned(std::min<int64_t>(ceil_div(R * a.K, 256), 8192))), dim3(256), 0, st,
+                         dW, R * a.K);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess && dbias) {
+      TimedLaunch tl(timer, "linear_dbias", st);
+      hipLaunchKernelGGL(bias_kernel, dim3(unsigned(ceil_div(R, 64))), dim3(256), 0, st, nullptr, 0, int(R), dbias);
+      e = hipGetLastError();
+    }
+    return e;
+  }
+  const Layout L = layout(a, true);
+  char* base = static_cast<char*>(ws);
+  const bool as_is = a.act == kActNone && !a.out_f32 && R % 8 == 0;  // dY is dP already
+  const uint16_t* dP = static_cast<const uint16_t*>(dY);
+  const bool products = dX || dW;
+  if (dbias || (products && !as_is)) {
+    DpArgs d;
+    d.dY = dY;
+    d.pre = pre;
+    d.M = a.M;
+    d.N = int(a.N);
+    d.act = a.act;
+    d.f32 = a.out_f32;
+    d.dP = products && !as_is ? reinterpret_cast<uint16_t*>(base + L.dp) : nullptr;
+    d.ld = pad8(R);
+    d.sums = dbias ? reinterpret_cast<float*>(base + L.sums) : nullptr;
+    d.cols = int(R);
+    d.rows = int(dp_rows(a.M));
+    const int blocks = int(ceil_div(a.M, d.rows));
+    {
+      TimedLaunch tl(timer, "linear_dp", st);
+      hipLaunchKernelGGL(dp_kernel, dim3(unsigned(blocks), unsigned(ceil_div(a.N, 256))), dim3(256), 0, st, d);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (dbias) {
+      TimedLaunch tl(timer, "linear_dbias", st);
+      hipLaunchKernelGGL(bias_kernel, dim3(unsigned(ceil_div(R, 64))), dim3(256), 0, st, d.sums, blocks, int(R), dbias);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (d.dP) dP = d.dP;
+  }
+  const int64_t ldr = pad8(R), ldk = pad8(a.K);
+  float* partial = reinterpret_cast<float*>(base + L.partial);
+  if (dX) {
+    if (a.K % 8 != 0) {
+      uint16_t* wp = reinterpret_cast<uint16_t*>(base + L.w);
+      if ((e = pad(W, R, a.K, wp, st, timer)) != hipSuccess) return e;
+      W = wp;
+    }
+    const Out out{nullptr, nullptr, dX, nullptr, a.M, int(a.K), kActNone, false};
+    e = product(Operand{dP, ldr, a.M, false}, false, Operand{W, ldk, a.K, false}, true, R, out, partial, st, timer,
+                "linear_dx");
+    if (e != hipSuccess) return e;
+  }
+  if (dW) {
+    if (a.K % 8 != 0) {
+      uint16_t* xp = reinterpret_cast<uint16_t*>(base + L.x);
+      if ((e = pad(X, a.M, a.K, xp, st, timer)) != hipSuccess) return e;
+      X = xp;
+    }
+    const Out out{nullptr, nullptr, dW, nullptr, R, int(a.K), kActNone, false};
+    e = product(Operand{dP, ldr, R, false}, true, Operand{X, ldk, a.K, false}, true, a.M, out, partial, st, timer,
+                "linear_dw");
+  }
+  return e;
+}
+
+}  // namespace moe

@@ -281,6 +281,48 @@ OrthoArgs ortho_args(const moe_ortho_shape& s) {
   return OrthoArgs{s.E, int(s.R), int(s.C), s.steps, s.grad_dtype == MOE_DT_F32, s.a, s.b, s.c, s.eps};
 }
 
+// ------------------------------------------------------------ gate, dense products, AdamW
+
+moe_status check_gate(const moe_shape& s, const moe_gate_params* p) {
+  if (!p) return MOE_ERR_NULL;
+  if (p->score != MOE_SCORE_SOFTMAX && p->score != MOE_SCORE_SIGMOID) return MOE_ERR_PRECISION;
+  if (p->groups < 1 || p->groups > 64 || s.E % p->groups != 0) return MOE_ERR_SHAPE;
+  if (p->groups_kept < 1 || p->groups_kept > p->groups || p->group_top < 1 || p->group_top > 2) return MOE_ERR_SHAPE;
+  if (s.k > p->groups_kept * (s.E / p->groups)) return MOE_ERR_SHAPE;
+  if (!std::isfinite(p->scale) || p->reserved != 0) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+GateArgs gate_args(const moe_shape& s, const moe_gate_params& p, const float* logits, const float* bias,
+                   const uint8_t* mask) {
+  return GateArgs{logits, bias, mask, s.T, int(s.E), int(s.k), p.score == MOE_SCORE_SIGMOID, p.renorm != 0,
+                  p.groups, p.groups_kept, p.group_top, p.scale};
+}
+
+int64_t linear_rows(const moe_linear_shape& s) { return s.act == MOE_ACT_SWIGLU ? 2 * s.N : s.N; }
+
+moe_status check_linear(const moe_linear_shape* s) {
+  if (!s) return MOE_ERR_NULL;
+  if (s->act < MOE_ACT_NONE || s->act > MOE_ACT_SWIGLU) return MOE_ERR_PRECISION;
+  if (s->out_dtype != MOE_DT_BF16 && s->out_dtype != MOE_DT_F32) return MOE_ERR_PRECISION;
+  const int64_t side = int64_t(1) << 20, area = int64_t(1) << 36;
+  if (s->M < 0 || s->M > (int64_t(1) << 24) || s->N < 1 || s->K < 1 || s->N > side || s->K > side) return MOE_ERR_SHAPE;
+  const int64_t R = linear_rows(*s);
+  if (R > side || s->M * s->K >= area || s->M * R >= area) return MOE_ERR_SHAPE;
+  // 32-bit byte offsets into W
+  if (R * ((s->K + 7) / 8 * 8) > (int64_t(1) << 30) || s->reserved != 0) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+LinearArgs linear_args(const moe_linear_shape& s) {
+  static_assert(MOE_ACT_NONE == kActNone && MOE_ACT_RELU == kActRelu && MOE_ACT_SILU == kActSilu &&
+                    MOE_ACT_GELU == kActGelu && MOE_ACT_SWIGLU == kActSwiglu,
+                "the kernels know the activations by the same numbers");
+  return LinearArgs{s.M, s.N, s.K, s.act, s.out_dtype == MOE_DT_F32};
+}
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
 int effective_cus(const moe_shape& s, int dev_cus) {
   return (s.num_cus > 0 && s.num_cus < dev_cus) ? s.num_cus : dev_cus;
 }
@@ -801,6 +843,140 @@ moe_status moe_muon_step(const moe_ortho_shape* s, const moe_muon_params* p, con
   t.step = p->lr * p->scale;
   std::lock_guard<std::mutex> lk(g_timer_mu);
   return launch_status(launch_ortho(a, t, ws, static_cast<hipStream_t>(stream), timer()));
+}
+
+moe_status moe_gate(const moe_shape* s, const moe_gate_params* p, const float* logits, const float* bias,
+                    const uint8_t* mask, int32_t* topk_idx, float* topk_w, void* stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_gate(*s, p)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_w) return MOE_ERR_NULL;
+  if (!aligned4(logits) || !aligned4(bias) || !aligned4(topk_idx) || !aligned4(topk_w)) return MOE_ERR_ALIGN;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_gate(gate_args(*s, *p, logits, bias, mask), topk_idx, topk_w,
+                                   static_cast<hipStream_t>(stream), timer()));
+}
+
+moe_status moe_gate_bwd(const moe_shape* s, const moe_gate_params* p, const float* logits, const int32_t* topk_idx,
+                        const float* d_topk_w, int32_t accumulate, float* d_logits, void* stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_gate(*s, p)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !d_topk_w || !d_logits) return MOE_ERR_NULL;
+  if (!aligned4(logits) || !aligned4(topk_idx) || !aligned4(d_topk_w) || !aligned4(d_logits)) return MOE_ERR_ALIGN;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_gate_bwd(gate_args(*s, *p, logits, nullptr, nullptr), topk_idx, d_topk_w, accumulate != 0,
+                                       d_logits, static_cast<hipStream_t>(stream), timer()));
+}
+
+moe_status moe_linear_workspace_size(const moe_linear_shape* s, size_t* fwd_ws, size_t* bwd_ws) {
+  const moe_status st = check_linear(s);
+  if (st != MOE_OK) return st;
+  if (fwd_ws) *fwd_ws = linear_workspace_bytes(linear_args(*s), false);
+  if (bwd_ws) *bwd_ws = linear_workspace_bytes(linear_args(*s), true);
+  return MOE_OK;
+}
+
+moe_status moe_linear(const moe_linear_shape* s, const void* X, const void* W, const float* bias, const void* residual,
+                      void* Y, void* pre, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_linear(s);
+  if (st != MOE_OK) return st;
+  if (s->M == 0) return MOE_OK;
+  const LinearArgs a = linear_args(*s);
+  const size_t need = linear_workspace_bytes(a, false);
+  if (!X || !W || !Y || (need > 0 && !ws)) return MOE_ERR_NULL;
+  for (const void* p : {X, W, static_cast<const void*>(bias), residual, static_cast<const void*>(Y),
+                        static_cast<const void*>(pre), static_cast<const void*>(ws)})
+    if (!aligned16(p)) return MOE_ERR_ALIGN;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_linear(a, static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), bias, residual,
+                                     Y, static_cast<uint16_t*>(pre), ws, static_cast<hipStream_t>(stream), timer()));
+}
+
+moe_status moe_linear_bwd(const moe_linear_shape* s, const void* dY, const void* X, const void* W, const void* pre,
+                          void* dX, void* dW, float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_linear(s);
+  if (st != MOE_OK) return st;
+  if (!dX && !dW && !dbias) return MOE_OK;
+  const LinearArgs a = linear_args(*s);
+  const size_t need = linear_workspace_bytes(a, true);
+  if (s->M > 0) {
+    if (!dY || (dW && !X) || (dX && !W) || (s->act != MOE_ACT_NONE && !pre) || (need > 0 && !ws)) return MOE_ERR_NULL;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  }
+  for (const void* p : {dY, X, W, pre, static_cast<const void*>(dX), static_cast<const void*>(dW),
+                        static_cast<const void*>(dbias), static_cast<const void*>(ws)})
+    if (!aligned16(p)) return MOE_ERR_ALIGN;
+  int cus = 0;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_linear_bwd(a, dY, static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W),
+                                         static_cast<const uint16_t*>(pre), static_cast<uint16_t*>(dX),
+                                         static_cast<uint16_t*>(dW), dbias, ws, static_cast<hipStream_t>(stream),
+                                         timer()));
+}
+
+moe_status moe_adamw_step(const moe_adamw_params* p, const moe_adamw_tensor* tensors, int64_t count,
+                          const float* grad_scale, const float* hyper, void* stream) {
+  if (!p) return MOE_ERR_NULL;
+  if ((p->param_dtype != MOE_DT_BF16 && p->param_dtype != MOE_DT_F32) ||
+      (p->grad_dtype != MOE_DT_BF16 && p->grad_dtype != MOE_DT_F32) ||
+      (p->state != MOE_STATE_F32 && p->state != MOE_STATE_8BIT))
+    return MOE_ERR_PRECISION;
+  const double most = 3.4028234e38;  // of fp32, and false for NaN
+  if (!(std::fabs(p->lr) <= most) || !(p->eps >= 0.0 && p->eps <= most) || !(std::fabs(p->weight_decay) <= most) ||
+      !(std::fabs(p->lr * p->weight_decay) <= most))
+    return MOE_ERR_SHAPE;
+  const double below = 1.0 - 0x1p-24;  // what rounds to 1 in fp32 is no average
+  if (!(p->beta1 >= 0.0 && p->beta1 < below && p->beta2 >= 0.0 && p->beta2 < below)) return MOE_ERR_SHAPE;
+  if (p->step < 1 || p->reserved != 0 || count < 0) return MOE_ERR_SHAPE;
+  if (count == 0) return MOE_OK;
+  if (!tensors) return MOE_ERR_NULL;
+  if (!aligned4(grad_scale) || !aligned4(hyper)) return MOE_ERR_ALIGN;
+  if (hyper && grad_scale) return MOE_ERR_SHAPE;
+  AdamwArgs a;
+  a.param_bf16 = p->param_dtype == MOE_DT_BF16;
+  a.grad_bf16 = p->grad_dtype == MOE_DT_BF16;
+  a.eight = p->state == MOE_STATE_8BIT;
+  for (int64_t i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n >= (int64_t(1) << 40) || !std::isfinite(t.lr_mul) || !std::isfinite(t.decay_mul)) return MOE_ERR_SHAPE;
+    if (t.master && !a.param_bf16) return MOE_ERR_SHAPE;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v || a.eight != (t.m_scale != nullptr) || a.eight != (t.v_scale != nullptr))
+      return MOE_ERR_NULL;
+    if (!aligned_to(t.param, a.param_bf16 ? 2 : 4) || !aligned_to(t.grad, a.grad_bf16 ? 2 : 4) || !aligned4(t.master) ||
+        !aligned_to(t.m, a.eight ? 1 : 4) || !aligned_to(t.v, a.eight ? 1 : 4))
+      return MOE_ERR_ALIGN;
+  }
+  const double t = double(p->step);
+  a.h.lr = float(p->lr);
+  a.h.beta1 = float(p->beta1);
+  a.h.beta2 = float(p->beta2);
+  a.h.alpha1 = float(1.0 - p->beta1);
+  a.h.alpha2 = float(1.0 - p->beta2);
+  a.h.eps = float(p->eps);
+  a.h.weight_decay = float(p->weight_decay);
+  a.h.bias1 = float(1.0 - std::pow(p->beta1, t));
+  a.h.root2 = float(1.0 / std::sqrt(1.0 - std::pow(p->beta2, t)));
+  a.grad_scale = grad_scale;
+  a.hyper = hyper;
+  int cus = 0;
+  moe_status st;
+  if ((st = device_info(&cus)) != MOE_OK) return st;
+  static_assert(sizeof(AdamwTensor) == sizeof(moe_adamw_tensor), "the launcher takes the tensors as they are");
+  std::lock_guard<std::mutex> lk(g_timer_mu);
+  return launch_status(launch_adamw(a, reinterpret_cast<const AdamwTensor*>(tensors), count,
+                                    static_cast<hipStream_t>(stream), timer()));
 }
 
 moe_status moe_read_status(const void* fwd_ws, int32_t* out, void* stream) {

@@ -290,6 +290,61 @@ moe_status moe_route(const moe_shape* s, const float* logits, int32_t renorm, in
 moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t* topk_idx, const float* topk_w,
                          const float* d_topk_w, int32_t renorm, float* d_logits, void* stream);
 
+/* Choice of experts by scores, a bias for balance and groups (next to
+ * moe_route, whose softmax routing without them it contains; not on the pages, which keep the router
+ * outside). Per token, with z = logits[t]:
+ *   s[e]  softmax(z)[e], or 1 / (1 + exp(-z[e]))           (score)
+ *   c[e]  z[e] without a bias, s[e] + bias[e] with one: what the choice goes by
+ *   groups > 1: the E experts are `groups` groups of E / groups neighbours; a
+ *         group's score is the sum of its group_top largest c (of s, where there
+ *         is no bias and group_top is 2), and the experts of the groups_kept best
+ *         groups are chosen among
+ *   topk_idx  the k experts with the largest c, in descending order
+ *   topk_w    scale * s[topk_idx] (the bias bears on the choice alone), or with
+ *             renorm  scale * s[topk_idx] / (sum of the k chosen s)
+ * Scores are compared in 64 bits; ties go to the lower id, among groups too. An
+ * expert whose logit or bias is -inf is off: it is not chosen, and a group with
+ * no other is not kept. Where fewer than k are left the last slots get the id -1
+ * (which the layer drops) and the weight 0, as do all slots of a token whose
+ * mask byte is 0; its logits are not looked at. A NaN or +inf among a token's
+ * logits, or in the bias, gives the ids 0 .. k-1 and weights NaN. Finite logits of
+ * any magnitude have the weights the formulas give (renormalised sigmoid scores
+ * too, where every score underflows).
+ *   logits   fp32  [T, E]   4-byte aligned
+ *   bias     fp32  [E]      or NULL
+ *   mask     uint8 [T]      or NULL: every token counts
+ *   topk_idx int32 [T, k], topk_w fp32 [T, k]   written
+ * Uses s->T, E, k (check as moe_workspace_size). MOE_ERR_SHAPE unless 1 <= groups
+ * <= 64, E % groups == 0, 1 <= groups_kept <= groups, group_top 1 or 2, k <=
+ * groups_kept * E / groups, scale finite, reserved 0; MOE_ERR_PRECISION for an
+ * unknown score. */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct moe_gate_params {
+  int32_t score; /* moe_score */
+  int32_t renorm;
+  int32_t groups, groups_kept, group_top;
+  float scale;
+  int32_t reserved; /* 0 */
+} moe_gate_params;
+moe_status moe_gate(const moe_shape* s, const moe_gate_params* p, const float* logits, const float* bias,
+                    const uint8_t* mask, int32_t* topk_idx, float* topk_w, void* stream);
+
+/* Backward of moe_gate: d_logits fp32 [T, E] = dL/dlogits given d_topk_w =
+ * dL/dtopk_w and the topk_idx that moe_gate chose from these logits; with
+ * accumulate != 0 it is added to what d_logits holds, otherwise every element is
+ * written. The choice is piecewise constant and passes no gradient (the bias has
+ * none). Slots with an id outside [0, E) pass none and are no part of the
+ * renormalisation; an expert named twice by one token takes the sum of both slots.
+ *   sigmoid:          scale d_topk_w s (1 - s)
+ *   sigmoid, renorm:  scale p (1 - s) (d_topk_w - <p, d_topk_w>), p = s / sum of the chosen
+ *   softmax, renorm:  scale p (d_topk_w - <p, d_topk_w>)
+ *   softmax:          scale p (G - <p, G>), p over all experts, G = d_topk_w placed on the chosen
+ * Only the last has elements other than the chosen experts'. groups, groups_kept
+ * and group_top are checked, and otherwise not used. */
+moe_status moe_gate_bwd(const moe_shape* s, const moe_gate_params* p, const float* logits, const int32_t* topk_idx,
+                        const float* d_topk_w, int32_t accumulate, float* d_logits, void* stream);
+
 /* Balance of the routing, per sequence: a load-balance loss, the router
  * z-loss and the per-expert counts of a routed batch (not on the pages, which
  * keep the router outside; they name skewed routing as what their benchmark
@@ -489,6 +544,115 @@ typedef struct moe_muon_params {
 } moe_muon_params;
 moe_status moe_muon_step(const moe_ortho_shape* s, const moe_muon_params* p, const void* grad, float* momentum,
                          void* W, float* master, void* ws, size_t ws_bytes, void* stream);
+
+/* Dense products beside the routed experts: the router's logits (fp32 out, next to
+ * moe_gate), a shared expert (SwiGLU; the down product with the routed experts' y
+ * as its residual), from one token to a batch. With P = X W^T + bias:
+ *   Y = act(P) + residual
+ *   MOE_ACT_NONE  P                    MOE_ACT_RELU  max(P, 0)
+ *   MOE_ACT_SILU  P sigmoid(P)         MOE_ACT_GELU  P sigmoid(2 sqrt(2 / pi) (P + 0.044715 P^3))
+ *   MOE_ACT_SWIGLU  silu(P[:, :N]) * P[:, N:]   W has 2 N rows, gate rows first as in W13
+ * (the tanh form of GELU). N' below is 2 N for SwiGLU, N otherwise.
+ *   X        bf16 [M, K]
+ *   W        bf16 [N', K]
+ *   bias     fp32 [N'] or NULL
+ *   residual [M, N] of out_dtype or NULL; may be Y itself
+ *   Y        [M, N] of out_dtype (MOE_DT_BF16, MOE_DT_F32), written
+ *   pre      bf16 [M, N'] or NULL: P, which moe_linear_bwd needs for every act but NONE
+ *   ws       moe_linear_workspace_size().fwd_ws bytes; serves smaller M too
+ * Products are summed in fp32, act is taken of the fp32 P, one rounding each for Y
+ * and pre. Results are deterministic, but the sums' order goes with M, N and K. With
+ * M == 0 nothing is done. Rows of any length; every pointer 16-byte aligned. Limits:
+ * 0 <= M <= 2^24, 1 <= N, K, N' and K <= 2^20, M K < 2^36, M N' < 2^36, and N' times
+ * K rounded up to 8 at most 2^30. Calls that share `ws` must not overlap. */
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_SWIGLU = 4
+} moe_act;
+
+typedef struct moe_linear_shape {
+  int64_t M, N, K;
+  int32_t act;       /* moe_act */
+  int32_t out_dtype; /* moe_dtype of Y, residual and dY */
+  int64_t reserved;  /* 0 */
+} moe_linear_shape;
+
+/* Bytes of the scratch of moe_linear and moe_linear_bwd (either pointer may be
+ * NULL). Pure host function. */
+moe_status moe_linear_workspace_size(const moe_linear_shape* s, size_t* fwd_ws, size_t* bwd_ws);
+
+moe_status moe_linear(const moe_linear_shape* s, const void* X, const void* W, const float* bias, const void* residual,
+                      void* Y, void* pre, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of moe_linear for L with dL/dY = dY (dL/dresidual is dY itself). With
+ * dP = dY act'(P), P from `pre` (for MOE_ACT_NONE dP = dY and pre is not read):
+ *   dX    bf16 [M, K]   = dP W
+ *   dW    bf16 [N', K]  = dP^T X
+ *   dbias fp32 [N']     = sum over the rows of dP
+ * Each may be NULL and is then not computed (X is read for dW alone, W for dX
+ * alone; either may be NULL where it is not read). dP is rounded to bf16 for the
+ * two products, as they take bf16 operands; dbias is summed in fp32 before that
+ * rounding. With M == 0 dW and dbias are written as 0. relu has the slope 0 at 0.
+ *   dY   [M, N] of out_dtype     ws   moe_linear_workspace_size().bwd_ws bytes */
+moe_status moe_linear_bwd(const moe_linear_shape* s, const void* dY, const void* X, const void* W, const void* pre,
+                          void* dX, void* dW, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* One AdamW step over many tensors at once (next to moe_muon_step: what is not
+ * orthogonalised, or whole expert stacks with moments in 8 bits). Per element, with
+ * g = grad_scale * grad and t the step's number, counted from 1:
+ *   m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *   w <- (1 - lr weight_decay) w - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * with lr times the tensor's lr_mul and weight_decay times its decay_mul. All of it
+ * in fp32, the fresh m and v before they are rounded; w is `master` where that is
+ * given (param becomes its rounding and is not read), else param.
+ * Moments in 8 bits (MOE_STATE_8BIT): m and sqrt(v) as E4M3 codes in blocks of 128
+ * elements counted from the tensor's first, each block with one power-of-two scale 2^e by
+ * the rule of MOE_FP8_BLOCK (e the smallest integer, from -126 to 126, with 448 * 2^e at
+ * least the block's largest finite magnitude; 0 for a block of zeros), stored as the byte
+ * e + 127. Rounding is to nearest even, but that a sqrt(v) above 0 is held as the smallest
+ * code above 0 at least (the next steps divide by it); what is not finite is held as
+ * NaN. Buffers of zeros are moments of zero in either form.
+ *   tensors    host array, read at the call; `count` of them, any number
+ *   param      bf16 or fp32 [n]         grad  bf16 or fp32 [n]
+ *   master     fp32 [n] or NULL         (with an fp32 param NULL)
+ *   m, v       fp32 [n], or codes uint8 [n]
+ *   m_scale, v_scale   uint8 [ceil(n / 128)]; NULL with fp32 moments
+ *   n          0 <= n < 2^40; tensors of no elements are passed over
+ * Buffers may begin at any multiple of their element's size; none may overlap another
+ * of the same call. Host values (lr and the rest) are read at the call: a captured
+ * call replays them, unless `hyper` is given.
+ *   hyper      fp32 [4] in device memory or NULL: lr, 1 - beta1^t, 1 - beta2^t and
+ *              grad_scale, which then take the place of the host's (for captured steps)
+ *   grad_scale fp32 [1] in device memory or NULL (1): clipping or loss scaling; NULL
+ *              with hyper. Where it is not finite, nothing changes.
+ * MOE_ERR_SHAPE unless lr, eps, weight_decay and lr weight_decay are finite in fp32,
+ * eps >= 0, 0 <= beta1, beta2 < 1 - 2^-24, step >= 1, reserved 0. */
+typedef enum moe_state { MOE_STATE_F32 = 0, MOE_STATE_8BIT = 1 } moe_state;
+
+typedef struct moe_adamw_tensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t n;
+  float lr_mul, decay_mul;
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_params {
+  double lr, beta1, beta2, eps, weight_decay; /* 1 - beta is taken before the rounding to fp32 */
+  int32_t param_dtype, grad_dtype; /* moe_dtype */
+  int32_t state;                   /* moe_state */
+  int64_t step;
+  int64_t reserved; /* 0 */
+} moe_adamw_params;
+moe_status moe_adamw_step(const moe_adamw_params* p, const moe_adamw_tensor* tensors, int64_t count,
+                          const float* grad_scale, const float* hyper, void* stream);
 
 /* Copies the routing status word that moe_fwd left in `fwd_ws` (or that
  * moe_permute left in its scratch) to *out (MOE_OK or MOE_ERR_ROUTING).
