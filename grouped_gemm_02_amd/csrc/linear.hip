@@ -115,6 +115,20 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8], int cols) {
   }
 }
 
+__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
+  if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] > 0.f || v[i] != v[i] ? v[i] : 0.f;
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= sigmoid(v[i]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= gelu_gate(v[i]);
+  }
+}
+
+template <bool PAIR>
 __device__ __forceinline__ void finish8(const Out& o, int64_t r, int c, float (&v)[8], float (&u)[8]) {
   const int cols = o.N - c;
   float b[8];
@@ -123,7 +137,7 @@ __device__ __forceinline__ void finish8(const Out& o, int64_t r, int c, float (&
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += b[i];
   }
-  if (o.act == kActSwiglu) {
+  if constexpr (PAIR) {
     if (o.bias) {
       load8(o.bias + o.N + c, b, cols);
 #pragma unroll
@@ -137,16 +151,7 @@ __device__ __forceinline__ void finish8(const Out& o, int64_t r, int c, float (&
     for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
   } else {
     if (o.pre) store8(o.pre + r * int64_t(o.N) + c, v, cols);
-    if (o.act == kActRelu) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] > 0.f || v[i] != v[i] ? v[i] : 0.f;
-    } else if (o.act == kActSilu) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= sigmoid(v[i]);
-    } else if (o.act == kActGelu) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= gelu_gate(v[i]);
-    }
+    activate8(o.act, v);
   }
   const int64_t at = r * int64_t(o.N) + c;
   if (o.residual) {
@@ -197,7 +202,8 @@ struct KMajor {
       off[i] = uint32_t(row * op.ld * 2) + 16u * chunk;
     }
   }
-  __device__ __forceinline__ void load(int kt, uint16_t* lds) const {
+  // slab kt (one past the end: zeros) into `lds`
+  __device__ __forceinline__ void load(int kt, bool, uint16_t* lds) const {
     const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const uint32_t past = kt * BK + 8 * chunk < K ? 0u : kPast;
 #pragma unroll
@@ -227,13 +233,14 @@ struct MNMajor {
       off[i] = uint32_t((k * ld + 8 * c) * 2) | (8 * c < left ? 0u : kPast);
     }
   }
-  __device__ __forceinline__ void load(int kt, uint16_t* lds) const {
+  __device__ __forceinline__ void load(int kt, bool some, uint16_t* lds) const {
     const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const int64_t k0 = int64_t(kt) * BK;
+    const int64_t k0 = some ? int64_t(kt) * BK : 0;
     const int64_t rows = kend - k0 < BK ? kend - k0 : BK;
+    const int64_t bytes = some ? (rows * ld - e0) * 2 : 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      load_lds(base + k0 * ld + e0, (rows * ld - e0) * 2, lds + (64 * w + THREADS * i) * 8, off[i]);
+      load_lds(base + k0 * ld + e0, bytes, lds + (64 * w + THREADS * i) * 8, off[i]);
   }
 };
 
@@ -286,7 +293,7 @@ struct Problem {
   Out out;
 };
 
-// Block b's tile: the eight XCDs (b % 8) take contiguous ranges of tiles, and a range
+// The b-th tile: the eight XCDs (b % 8) take contiguous ranges of tiles, and a range
 // walks groups of eight row tiles column by column, so that tiles that run at once in
 // an XCD share rows of both operands in its L2.
 __device__ __forceinline__ void tile_of(const Problem& p, uint32_t b, uint32_t total, int* m, int* n, int* s) {
@@ -302,136 +309,435 @@ __device__ __forceinline__ void tile_of(const Problem& p, uint32_t b, uint32_t t
   *n = int(t / rows);
 }
 
-template <int BM, int BN, int WM, int WN, bool P_MN, bool Q_MN>
-__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const Problem p) {
+// Four columns of each half of the wave become eight of each lane: a holds columns 0..3
+// (lanes below 32) and 4..7, b columns 8..11 and 12..15; after it a lane below 32 has 0..7
+// in (a, b), one above 8..15.
+__device__ __forceinline__ void join_halves(float& a, float& b) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+
+// What a tile's sums go through: as they are (with bias, residual), an activation, SwiGLU,
+// or as a part of a split product into `partial`.
+enum { kPlain, kActs, kPair, kSplit };
+
+// The lane, as a value that the compiler does not know: what is computed from it is not
+// kept in registers through the products (it spilled).
+__device__ __forceinline__ int fresh_lane() {
+  int x = lane_id();
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// A wave's chunk of 16 bytes of the 32 staged rows.
+__device__ __forceinline__ uint16_t* staged(uint16_t* buf, int chunks, int row, int c) {
+  return buf + (row * chunks + (c ^ (row & (chunks - 1)))) * 8;
+}
+
+// Staged rows [32][CH chunks] of T out to a matrix of row length ld: `out` is the element
+// of the first row and chunk, of which `rows` rows and `cols` columns exist. A row's chunks
+// leave from neighbouring lanes.
+template <class T, int CH>
+__device__ __forceinline__ void copy_out(uint16_t* buf, T* out, int ld, int rows, int cols) {
+  constexpr int EC = 16 / sizeof(T), RP = 64 / CH;
+  const int lane = fresh_lane(), c = lane % CH;
+  const int n = min(EC, cols - EC * c);
+  if (n <= 0) return;
+  int r = lane / CH, off = r * ld + EC * c;
+#pragma unroll 1
+  for (int q = 0; q < 32 / RP; q += 2, r += 2 * RP, off += 2 * RP * ld) {
+    u32x4 v[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) v[w] = *reinterpret_cast<const u32x4*>(staged(buf, CH, r + w * RP, c));
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      T* dst = out + off + w * RP * ld;
+      if (r + w * RP >= rows) {
+      } else if (n == EC) {
+        __builtin_nontemporal_store(v[w], reinterpret_cast<u32x4u*>(dst));
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) dst[i] = T(sizeof(T) == 2 ? v[w][i / 2] >> (16 * (i & 1)) : v[w][i & 3]);
+      }
+    }
+  }
+}
+// The same inwards; what is not there is zero.
+template <class T, int CH>
+__device__ __forceinline__ void copy_in(uint16_t* buf, const T* in, int ld, int rows, int cols) {
+  constexpr int EC = 16 / sizeof(T), RP = 64 / CH, kLoads = 32 / RP;
+  const int lane = fresh_lane(), c = lane % CH, r0 = lane / CH;
+  const int n = min(EC, cols - EC * c);
+  u32x4 v[kLoads];
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    v[q] = u32x4{0u, 0u, 0u, 0u};
+    if (n == EC && r0 + q * RP < rows) v[q] = *reinterpret_cast<const u32x4u*>(in + (r0 + q * RP) * ld + EC * c);
+  }
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) *reinterpret_cast<u32x4*>(staged(buf, CH, r0 + q * RP, c)) = v[q];
+  if (n > 0 && n < EC) {
+#pragma unroll 1
+    for (int r = r0; r < min(32, rows); r += RP)
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) reinterpret_cast<T*>(staged(buf, CH, r, c))[i] = in[r * ld + EC * c + i];
+  }
+}
+
+// A wave's WTM x WTN sums at (m0, n0) of the product on their way out, 32 rows at a time:
+// bias, activation and residual in fp32 with eight columns of a row in a lane, then through
+// the wave's LDS, so that memory sees whole lines. A sub-tile at a time, and offsets of 32
+// bits from addresses that are the same in every lane: more of them at once would spill.
+template <int WTM, int WTN, int MODE>
+__device__ __forceinline__ void results(const Problem& p, f32x16 (&acc)[WTM / 32][WTN / 32], uint16_t* buf, int64_t m0,
+                                        int64_t n0, int part) {
+  constexpr int TM = WTM / 32, TN = WTN / 32;
+  constexpr bool kIsPair = MODE == kPair;
+  constexpr int kCols = kIsPair ? WTN / 2 : WTN;  // result columns of a wave
+  constexpr int CH16 = kCols / 8;                 // chunks of a staged row of bf16
+  constexpr int kHalves = kIsPair ? 1 : 2;        // fp32 rows are staged in this many parts
+  constexpr int CH32 = kCols / kHalves / 4;
+  constexpr int JS = kIsPair ? 2 : 1;             // sub-tiles that make 32 result columns
+  const Out& o = p.out;
+  const int64_t N = MODE == kSplit ? p.ldp : o.N;
+  const int64_t c0 = kIsPair ? n0 / 2 : n0;  // first result column
+  const int ld = int(N), cols = int(max(int64_t(0), min(int64_t(kCols), N - c0)));
+  const bool f32 = MODE == kSplit || o.f32;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int lane = fresh_lane(), row = lane & 31, up = lane >> 5;
+    const int64_t r0 = m0 + 32 * i;
+    const int rows = int(max(int64_t(0), min(int64_t(32), p.P.ents - r0)));
+    const int64_t at = r0 * N + c0;
+    __builtin_amdgcn_sched_barrier(0);
+    auto take = [&](const f32x16& x, int h, float (&y)[8]) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        y[r] = x[8 * h + r];
+        y[4 + r] = x[8 * h + 4 + r];
+        join_halves(y[r], y[4 + r]);
+      }
+    };
+    auto add = [&](float (&y)[8], int64_t c) {  // bias of eight columns from c of W's rows
+      float x[8];
+      load8(o.bias + c, x, int(min(int64_t(8), N - (c >= N && kIsPair ? c - N : c))));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] += x[q];
+    };
+    auto put16 = [&](int n, const float (&y)[8]) {
+      *reinterpret_cast<u32x4*>(staged(buf, CH16, row, 2 * n + up)) =
+          u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
+    };
+    // P itself first where it is kept: the gate part, then the up part of a pair
+    if (MODE != kSplit && o.pre) {
+#pragma unroll
+      for (int q = 0; q < JS; ++q) {
+#pragma unroll
+        for (int n = 0; n < kCols / 16; ++n) {
+          float v[8];
+          take(acc[i][n / 2 * JS + q], n % 2, v);
+          const int64_t c = c0 + 16 * n + 8 * up;
+          if (o.bias && c < N) add(v, c + q * N);
+          put16(n, v);
+        }
+        copy_out<uint16_t, CH16>(buf, o.pre + r0 * (JS * N) + q * N + c0, JS * ld, rows, cols);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // chunk n of this lane: its value before the residual
+    auto value = [&](int n, float (&v)[8]) {
+      take(acc[i][n / 2 * JS], n % 2, v);
+      if constexpr (MODE != kSplit) {
+        const int64_t c = c0 + 16 * n + 8 * up;
+        if (o.bias && c < N) add(v, c);
+        if constexpr (kIsPair) {
+          float u[8];
+          take(acc[i][n / 2 * JS + 1], n % 2, u);
+          if (o.bias && c < N) add(u, N + c);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = v[q] * sigmoid(v[q]) * u[q];
+        }
+        if constexpr (MODE == kActs) activate8(o.act, v);
+      }
+    };
+    if (f32) {
+      float* out = MODE == kSplit ? p.partial + int64_t(part) * p.P.ents * N : static_cast<float*>(o.Y);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        constexpr int kPart = kCols / kHalves;
+        const bool res = MODE != kSplit && o.residual;
+        if (res)
+          copy_in<uint32_t, CH32>(buf, static_cast<const uint32_t*>(o.residual) + at + h * kPart, ld, rows,
+                                  cols - h * kPart);
+#pragma unroll
+        for (int n = 0; n < kPart / 16; ++n) {
+          float v[8];
+          value(n + h * (kPart / 16), v);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            f32x4* s = reinterpret_cast<f32x4*>(staged(buf, CH32, row, 4 * n + 2 * up + q));
+            f32x4 x = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            if (res) x += *s;
+            *s = x;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        copy_out<uint32_t, CH32>(buf, reinterpret_cast<uint32_t*>(out) + at + h * kPart, ld, rows, cols - h * kPart);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      if (o.residual) copy_in<uint16_t, CH16>(buf, static_cast<const uint16_t*>(o.residual) + at, ld, rows, cols);
+#pragma unroll
+      for (int n = 0; n < kCols / 16; ++n) {
+        float v[8];
+        value(n, v);
+        if (o.residual) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(staged(buf, CH16, row, 2 * n + up));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[2 * q] += bf16_lo(x[q]);
+            v[2 * q + 1] += bf16_hi(x[q]);
+          }
+        }
+        put16(n, v);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      copy_out<uint16_t, CH16>(buf, static_cast<uint16_t*>(o.Y) + at, ld, rows, cols);
+    }
+  }
+}
+
+// A persistent walk: workgroup b takes the tiles b, b + grid, ... The slabs of all of
+// them are one stream, sent for two slabs ahead, across the tiles' ends too: results leave
+// through LDS of each wave's own, so the next tile's slabs are on their way meanwhile. The
+// number of a tile's slabs is made even (the last may be zeros), so that a stage is known
+// at compile time.
+template <int BM, int BN, int WM, int WN, bool P_MN, bool Q_MN, int MODE>
+__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const Problem p) {
   constexpr int kThreads = 64 * WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
   constexpr int kStage = (BM + BN) * BK;
+  static_assert(TN % 2 == 0, "a wave has gate and up columns of a pair");
   // two LDS objects, so that the compiler can tell reads of one stage from loads in
   // flight into the other
   __shared__ __attribute__((aligned(16))) uint16_t s0[kStage];
   __shared__ __attribute__((aligned(16))) uint16_t s1[kStage];
-  int mi, ni, si;
-  tile_of(p, blockIdx.x, gridDim.x, &mi, &ni, &si);
-  const int64_t m0 = int64_t(mi) * BM, n0 = int64_t(ni) * BN;
+  // 32 rows of a wave's results: WTN / 8 chunks of 16 bytes a row, chunk c at slot c ^ row
+  __shared__ __attribute__((aligned(16))) uint16_t s_out[WM * WN][32 * WTN];
   const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN, lane = lane_id();
+  const uint32_t total = uint32_t(p.mt) * uint32_t(p.nt) * uint32_t(p.splits);
+  const int all = int((p.kred + BK - 1) / BK);
   typename LoaderOf<P_MN, BM, kThreads>::type lp;
   typename LoaderOf<Q_MN, BN, kThreads>::type lq;
-  lp.init(p.P, m0, p.kred, p.Kp);
-  lq.init(p.Q, n0, p.kred, p.Kp);
-  const int all = int((p.kred + BK - 1) / BK);
-  const int k0 = si * p.slabs, nk = min(p.slabs, all - k0);
+  int mi, ni, si;
+  auto open = [&](uint32_t t) {
+    tile_of(p, t, total, &mi, &ni, &si);
+    mi = __builtin_amdgcn_readfirstlane(mi);
+    ni = __builtin_amdgcn_readfirstlane(ni);
+    si = __builtin_amdgcn_readfirstlane(si);
+    lp.init(p.P, int64_t(mi) * BM, p.kred, p.Kp);
+    lq.init(p.Q, int64_t(ni) * BN, p.kred, p.Kp);
+  };
   f32x16 acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  auto fetch = [&](int kt, uint16_t* s) {
-    lp.load(kt, s);
-    lq.load(kt, s + BM * BK);
+  struct Frags {
+    bf16x8 p[TM], q[TN];
   };
-  auto slab = [&](int kt, const uint16_t* cur, uint16_t* nxt) {
-    if (kt + 1 < nk) fetch(k0 + kt + 1, nxt);
-    __builtin_amdgcn_iglp_opt(0);
+  auto read = [&](const uint16_t* s, int kk, Frags& f) {
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      bf16x8 pf[TM], qf[TN];
+    for (int j = 0; j < TN; ++j) f.q[j] = frag<Q_MN, BN>(s + BM * BK, wn * WTN + 32 * j, kk);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) qf[j] = frag<Q_MN, BN>(cur + BM * BK, wn * WTN + 32 * j, kk);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) pf[i] = frag<P_MN, BM>(cur, wm * WTM + 32 * i, kk);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma_32x32x16(qf[j], pf[i], acc[i][j]);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the next slab is there
-    __syncthreads();
+    for (int i = 0; i < TM; ++i) f.p[i] = frag<P_MN, BM>(s, wm * WTM + 32 * i, kk);
   };
-  if (nk > 0) {
-    fetch(k0, s0);
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
-    int kt = 0;
-    for (; kt + 1 < nk; kt += 2) {
-      slab(kt, s0, s1);
-      slab(kt + 1, s1, s0);
+  auto multiply = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma_32x32x16(f.q[j], f.p[i], acc[i][j]);
+  };
+  // Which slab is sent for next: number f of the tile's nf (even), which end at fend. Past
+  // the last tile's end slabs of zeros are sent for.
+  uint32_t t = blockIdx.x;
+  int f = 0, nf, f0, fend;
+  bool more = true;
+  auto begin = [&]() {
+    f = 0;
+    f0 = si * p.slabs;
+    fend = min(f0 + p.slabs, all);
+    nf = (fend - f0 + 1) & ~1;
+  };
+  auto advance = [&]() {
+    if (more && f == nf) {
+      t += gridDim.x;
+      more = t < total;
+      if (more) {
+        open(t);
+        begin();
+      }
     }
-    if (kt < nk) slab(kt, s0, s1);
+  };
+  auto send = [&](uint16_t* s) {
+    const bool some = more && f0 + f < fend;
+    const int kt = some ? f0 + f : all;
+    lp.load(kt, some, s);
+    lq.load(kt, some, s + BM * BK);
+    ++f;
+  };
+  // The slab whose first fragments are in `a` and the next's are read: every step's
+  // products run while the next step's fragments come, in this order of issue: reads
+  // (and sends) spread over the products. Left to itself the compiler puts them behind the
+  // products, right before those that wait for them.
+  Frags a, b;
+  constexpr int kReads = (P_MN ? 2 : 1) * TM + (Q_MN ? 2 : 1) * TN, kMfmas = TM * TN;
+  constexpr int kBurst = (kReads + kMfmas - 2) / (kMfmas - 1);
+  constexpr int kSends = (BM + BN) * 8 / kThreads;
+  constexpr int kSendBurst = (kSends + kMfmas - 1) / kMfmas;
+  auto order = [&](bool sends) {
+#pragma unroll
+    for (int i = 0; i < kMfmas; ++i) {
+      if (i * kBurst < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kBurst, 0);
+      if (sends && i * kSendBurst < kSends) __builtin_amdgcn_sched_group_barrier(0x10, kSendBurst, 0);
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto step = [&](const uint16_t* s, int kk, Frags& next, const Frags& now) {
+    read(s, kk, next);
+    multiply(now);
+    order(false);
+  };
+  // the rest of a slab, then everybody has read it and the next one is there
+  auto steps = [&](const uint16_t* s) {
+    step(s, 1, b, a);
+    step(s, 2, a, b);
+    step(s, 3, b, a);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // its last products, while the slab after the next is sent for into its place
+  auto turn = [&](uint16_t* done, const uint16_t* nxt) {
+    advance();
+    __builtin_amdgcn_sched_barrier(0);
+    send(done);
+    read(nxt, 0, a);
+    multiply(b);
+    order(true);
+  };
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  };
+  open(t);
+  begin();
+  int64_t m0 = int64_t(mi) * BM, n0 = int64_t(ni) * BN;  // of the tile that is multiplied
+  int part = si, left = nf;
+  send(s0);
+  advance();
+  send(s1);
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  __syncthreads();
+  clear();
+  read(s0, 0, a);
+  steps(s0);
+  // At the top a slab in s0 lacks its last products, and nothing is under way: loads
+  // into LDS that crossed the loop's end would be waited for by the compiler.
+  while (true) {
+    turn(s0, s1);
+    steps(s1);
+    turn(s1, s0);
+    left -= 2;
+    if (left == 0) {
+      results<WTM, WTN, MODE>(p, acc, s_out[wave], m0 + wm * WTM, n0 + wn * WTN, part);
+      // two slabs of the next tile are there or under way, if there is one
+      if (!more) break;
+      m0 = int64_t(mi) * BM;
+      n0 = int64_t(ni) * BN;
+      part = si;
+      left = nf;
+      clear();
+      read(s0, 0, a);  // again, so that it takes no registers in between
+    }
+    steps(s0);
   }
-  // The accumulators go through LDS in fp32, HC columns at a time (rows [0, BM / 2) in
-  // the first stage), 16-byte chunk c of row m at slot c ^ m; then a thread takes eight
-  // columns of a row, so that stores and the loads of the epilogue are contiguous.
-  constexpr int kParts = BM * BN * 4 > 4 * kStage ? 2 : 1;
-  constexpr int HC = BN / kParts;
-  constexpr int kSlots = HC / 4;
-  static_assert(BM * HC * 4 <= 4 * kStage && WTN <= HC, "the tile's part fits both stages");
-  auto row = [&](int m) { return reinterpret_cast<float*>(m < BM / 2 ? s0 : s1) + (m % (BM / 2)) * HC; };
-  for (int h = 0; h < kParts; ++h) {
-    if (kParts == 1 || wn / (WN / kParts) == h) {
+}
+
+// Few rows (M <= 64): W is read once, straight into the fragments of
+// v_mfma_f32_16x16x32_bf16, and nothing waits for anything but its own loads. A workgroup
+// has 16 rows of W (a pair's: 8 gate rows and their 8 up rows); its waves take turns at
+// units of 64 k (a 128-byte line of each row), the sums meet in LDS. X comes from the
+// caches. MT: fragments of 16 rows of X.
+constexpr int kFewWaves = 8;
+constexpr int kFewUnits = 4;  // of a wave in flight
+
+// Eight k of a row, zeros past its end; rows begin anywhere.
+__device__ __forceinline__ u32x4 row8(const uint16_t* p, int k, int K) {
+  if (k + 8 <= K) return *reinterpret_cast<const u32x4u*>(p + k);
+  u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int m = wm * WTM + 32 * i + (lane & 31);
-        float* dst = row(m);
+  for (int i = 0; i < 8; ++i)
+    if (k + i < K) v[i / 2] |= uint32_t(p[k + i]) << (16 * (i & 1));
+  return v;
+}
+
+template <int MT>
+__global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const uint16_t* __restrict__ X,
+                                                                  const uint16_t* __restrict__ W, int M, int K,
+                                                                  bool pair, Out o) {
+  __shared__ float sums[kFewWaves][16 * MT][17];
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int e = lane & 15, kq = 8 * (lane >> 4);
+  const int n0 = int(blockIdx.x) * (pair ? 8 : 16);
+  const int n = pair ? n0 + (e & 7) : n0 + e;
+  const uint16_t* w = W + (int64_t(n < o.N ? n : o.N - 1) + (pair && e >= 8 ? o.N : 0)) * K;
+  const uint16_t* x[MT];
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+  for (int i = 0; i < MT; ++i) x[i] = X + int64_t(min(16 * i + e, M - 1)) * K;
+  f32x4 acc[MT];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int c = (wn * WTN + 32 * j + 8 * g + 4 * (lane >> 5) - h * HC) / 4;
-            const f32x16& a = acc[i][j];
-            *reinterpret_cast<f32x4*>(dst + ((c ^ (m & (kSlots - 1))) << 2)) =
-                f32x4{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
-          }
-      }
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 64 * wave; k0 < K; k0 += 64 * kFewWaves * kFewUnits) {
+    u32x4 wf[2 * kFewUnits], xf[2 * kFewUnits][MT];
+#pragma unroll
+    for (int q = 0; q < 2 * kFewUnits; ++q) {
+      const int k = k0 + (q / 2) * 64 * kFewWaves + 32 * (q & 1) + kq;
+      wf[q] = row8(w, k, K);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) xf[q][i] = row8(x[i], k, K);
     }
-    __syncthreads();
-    auto get = [&](int m, int c, float (&v)[8]) {
-      const float* src = row(m);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(src + (((c / 4 + q) ^ (m & (kSlots - 1))) << 2));
+    for (int q = 0; q < 2 * kFewUnits; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * q + i] = a[i];
+      for (int i = 0; i < MT; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wf[q]),
+                                                         __builtin_bit_cast(bf16x8, xf[q][i]), acc[i], 0, 0, 0);
+  }
+  // lane: row 16 i + lane % 16 of X, rows 4 (lane / 16) + r of the 16 of W
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sums[wave][16 * i + e][4 * (lane >> 4) + r] = acc[i][r];
+  __syncthreads();
+  const int chunks = pair ? 1 : 2;
+  for (int q = threadIdx.x; q < M * chunks; q += 64 * kFewWaves) {
+    const int m = q / chunks, c = 8 * (q % chunks);
+    if (n0 + c >= o.N) continue;
+    float v[8], u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+    for (int g = 0; g < kFewWaves; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] += sums[g][m][c + i];
+        if (pair) u[i] += sums[g][m][8 + i];
       }
-    };
-    const int rows = int(min(int64_t(BM), p.P.ents - m0));
-    if (p.splits > 1) {
-      constexpr int kPerRow = HC / 8;
-      for (int q = threadIdx.x; q < rows * kPerRow; q += kThreads) {
-        const int m = q / kPerRow, c = 8 * (q % kPerRow);
-        const int64_t col = n0 + h * HC + c;
-        if (col >= p.ldp) continue;
-        float v[8];
-        get(m, c, v);
-        float* dst = p.partial + (int64_t(si) * p.P.ents + m0 + m) * p.ldp + col;
-        *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
-      }
-    } else if (p.Q.pair) {
-      constexpr int kPerRow = HC / 16;
-      for (int q = threadIdx.x; q < rows * kPerRow; q += kThreads) {
-        const int m = q / kPerRow, o = 8 * (q % kPerRow), c = (o >> 5) * 64 + (o & 31);
-        const int col = int(n0 / 2) + h * (HC / 2) + o;
-        if (col >= p.out.N) continue;
-        float v[8], u[8];
-        get(m, c, v);
-        get(m, c + 32, u);
-        finish8(p.out, m0 + m, col, v, u);
-      }
-    } else {
-      constexpr int kPerRow = HC / 8;
-      for (int q = threadIdx.x; q < rows * kPerRow; q += kThreads) {
-        const int m = q / kPerRow, c = 8 * (q % kPerRow);
-        const int col = int(n0) + h * HC + c;
-        if (col >= p.out.N) continue;
-        float v[8], u[8];
-        get(m, c, v);
-        finish8(p.out, m0 + m, col, v, u);
-      }
-    }
-    if (kParts > 1) __syncthreads();
+    if (pair) finish8<true>(o, m, n0 + c, v, u);
+    else finish8<false>(o, m, n0 + c, v, u);
   }
 }
 
@@ -460,7 +766,8 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
         for (int i = 0; i < 8; ++i) u[i] += a[i];
       }
     }
-    finish8(o, m, c, v, u);
+    if (pair) finish8<true>(o, m, c, v, u);
+    else finish8<false>(o, m, c, v, u);
   }
 }
 
@@ -589,28 +896,29 @@ __global__ __launch_bounds__(256) void zero_kernel(uint16_t* __restrict__ p, int
 
 // How a product M x N over kred is cut.
 struct Plan {
-  int tile;    // 256, 128 or 64
+  int tile;    // rows of a tile: 256 (x 256), 128 (x 128) or 64 (x 128)
   int splits;  // parts of the k axis
 };
 
 constexpr int kMaxSplits = 16;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int tile_cols(int tile) { return tile == 256 ? 256 : 128; }
 
 Plan plan_of(int64_t M, int64_t N, int64_t kred) {
   const int64_t slabs = ceil_div(kred, BK);
   Plan best{64, 1};
   double least = 1e300;
   for (int tile : {256, 128, 64}) {
-    const int64_t tiles = ceil_div(M, tile) * ceil_div(N, tile);
+    const int64_t tiles = ceil_div(M, tile) * ceil_div(N, tile_cols(tile));
     if (tile < 256 && tiles > (1 << 20)) continue;  // a grid has less than 2^32 threads
-    const int64_t slots = tile == 256 ? 256 : tile == 128 ? 512 : 1024;  // workgroups that run at once
+    const int64_t slots = tile == 256 ? 256 : 512;  // workgroups that run at once
     for (int64_t s = 1; s <= kMaxSplits && s <= slabs; s *= 2) {
-      if (s > 1 && tiles * s > 2 * slots) break;
+      if (s > 1 && tiles * s > slots) break;
       const double rounds = double(ceil_div(tiles * s, slots));
-      // per slab and tile, with the slots full: 256 x 256 in 1.6 us, and so on
-      const double slab = tile == 256 ? 1.6 : tile == 128 ? 1.1 : 0.75;
-      const double join = s > 1 ? 4.0 + 2.0 * double(s) * double(M) * double(N) * 4e-6 / 4.0 : 0.0;
+      // per slab and tile, with the slots full
+      const double slab = tile == 256 ? 1.6 : tile == 128 ? 1.1 : 0.9;
+      const double join = s > 1 ? 5.0 + 2.0 * double(s) * double(M) * double(N) * 4e-6 / 4.0 : 0.0;
       const double t = rounds * (double(ceil_div(slabs, s)) * slab + 4.0) + join;
       if (t < least) {
         least = t;
@@ -623,13 +931,20 @@ Plan plan_of(int64_t M, int64_t N, int64_t kred) {
 
 int64_t pad8(int64_t n) { return (n + 7) & ~int64_t(7); }
 
-template <int T, int W>
-hipError_t launch_tiles(const Problem& p, bool pmn, bool qmn, hipStream_t st) {
-  const dim3 grid(unsigned(int64_t(p.mt) * p.nt * p.splits)), block(64 * W * (T == 256 ? 4 : W));
-  constexpr int WN = T == 256 ? 4 : W;
-  if (!pmn && !qmn) hipLaunchKernelGGL((tile_kernel<T, T, W, WN, false, false>), grid, block, 0, st, p);
-  else if (!pmn) hipLaunchKernelGGL((tile_kernel<T, T, W, WN, false, true>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((tile_kernel<T, T, W, WN, true, true>), grid, block, 0, st, p);
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_tiles(const Problem& p, bool pmn, bool qmn, int64_t slots, hipStream_t st) {
+  const int64_t tiles = int64_t(p.mt) * p.nt * p.splits;
+  const dim3 grid(unsigned(std::min(tiles, slots))), block(64 * WM * WN);
+  const bool split = p.splits > 1;
+  // gradients have no activation, bias or residual
+  auto kernel = pmn   ? (split ? tile_kernel<BM, BN, WM, WN, true, true, kSplit> : tile_kernel<BM, BN, WM, WN, true, true, kPlain>)
+                : qmn ? (split ? tile_kernel<BM, BN, WM, WN, false, true, kSplit>
+                               : tile_kernel<BM, BN, WM, WN, false, true, kPlain>)
+                : split                     ? tile_kernel<BM, BN, WM, WN, false, false, kSplit>
+                : p.Q.pair                  ? tile_kernel<BM, BN, WM, WN, false, false, kPair>
+                : p.out.act != kActNone     ? tile_kernel<BM, BN, WM, WN, false, false, kActs>
+                                            : tile_kernel<BM, BN, WM, WN, false, false, kPlain>;
+  hipLaunchKernelGGL(kernel, grid, block, 0, st, p);
   return hipGetLastError();
 }
 
@@ -651,7 +966,7 @@ hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64
   p.mt = int(ceil_div(P.ents, pl.tile));
   // a pair's columns come in groups of 64 with 32 of each part
   const int64_t ncols = Q.pair ? ceil_div(Q.ents / 2, 32) * 64 : Q.ents;
-  p.nt = int(ceil_div(ncols, pl.tile));
+  p.nt = int(ceil_div(ncols, tile_cols(pl.tile)));
   const int64_t slabs = ceil_div(kred, BK);
   p.slabs = int(ceil_div(slabs, pl.splits));
   p.splits = int(ceil_div(slabs, p.slabs));
@@ -661,8 +976,9 @@ hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64
   hipError_t e;
   {
     TimedLaunch tl(timer, name, st);
-    e = pl.tile == 256 ? launch_tiles<256, 2>(p, pmn, qmn, st)
-        : pl.tile == 128 ? launch_tiles<128, 2>(p, pmn, qmn, st) : launch_tiles<64, 2>(p, pmn, qmn, st);
+    e = pl.tile == 256 ? launch_tiles<256, 256, 2, 4>(p, pmn, qmn, 256, st)
+        : pl.tile == 128 ? launch_tiles<128, 128, 2, 2>(p, pmn, qmn, 512, st)
+                         : launch_tiles<64, 128, 2, 2>(p, pmn, qmn, 512, st);
   }
   if (e != hipSuccess || p.splits == 1) return e;
   TimedLaunch tl(timer, "linear_join", st);
@@ -683,9 +999,11 @@ hipError_t pad(const uint16_t* in, int64_t R, int64_t C, uint16_t* out, hipStrea
 constexpr size_t kAlign = 256;
 size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
-constexpr int64_t kDpRows = 64, kDpBlocks = 256;
+constexpr int64_t kDpRows = 16, kDpBlocks = 256;
 // rows of a block of dp_kernel: no more than kDpBlocks blocks
 int64_t dp_rows(int64_t M) { return std::max<int64_t>(kDpRows, ceil_div(M, kDpBlocks)); }
+
+constexpr int64_t kFewRows = 64;
 
 struct Layout {
   size_t x, w, dp, sums, partial, total;
@@ -722,6 +1040,15 @@ hipError_t launch_linear(const LinearArgs& a, const uint16_t* X, const uint16_t*
   const Layout L = layout(a, false);
   char* base = static_cast<char*>(ws);
   const int64_t R = a.act == kActSwiglu ? 2 * a.N : a.N;
+  const Out out{bias, residual, Y, pre, a.M, int(a.N), a.act, a.out_f32};
+  if (a.M <= kFewRows) {
+    TimedLaunch tl(timer, "linear_few", st);
+    const bool pair = a.act == kActSwiglu;
+    const dim3 grid(unsigned(ceil_div(a.N, pair ? 8 : 16))), block(64 * kFewWaves);
+    auto kernel = a.M <= 16 ? few_rows_kernel<1> : a.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, X, W, int(a.M), int(a.K), pair, out);
+    return hipGetLastError();
+  }
   if (a.K % 8 != 0) {
     uint16_t* xp = reinterpret_cast<uint16_t*>(base + L.x);
     uint16_t* wp = reinterpret_cast<uint16_t*>(base + L.w);
@@ -731,7 +1058,6 @@ hipError_t launch_linear(const LinearArgs& a, const uint16_t* X, const uint16_t*
     X = xp;
     W = wp;
   }
-  const Out out{bias, residual, Y, pre, a.M, int(a.N), a.act, a.out_f32};
   return product(Operand{X, pad8(a.K), a.M, false}, false, Operand{W, pad8(a.K), R, a.act == kActSwiglu}, false, a.K, out,
                  reinterpret_cast<float*>(base + L.partial), st, timer, "linear");
 }
