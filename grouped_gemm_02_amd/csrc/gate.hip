@@ -43,8 +43,9 @@ __device__ __forceinline__ void wave_argmaxd(double& v, int& id) {
   }
 }
 
-// The wave's token in 64 bits throughout: writes its k ids and weights.
-template <int PER>
+// The wave's token in 64 bits throughout: writes its k ids and weights. SLOTS: k / 64,
+// rounded up (as PER is for E).
+template <int PER, int SLOTS>
 __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32_t* __restrict__ idx,
                                              float* __restrict__ w) {
   const int lane = lane_id(), E = a.E, k = a.k;
@@ -59,7 +60,7 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
     return;
   }
   const double kOff = -__builtin_inf();
-  double c[PER], s[PER];
+  double c[PER];
   float zv[PER];
   bool bad = false;
   float m = -INFINITY;
@@ -81,35 +82,28 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
     return;
   }
   m = wave_maxf(m);
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    s[i] = 0.0;
-    if (zv[i] > -INFINITY) {
-      const double x = zv[i];
-      if (a.sigmoid) {
-        const double q = exp(-fabs(x));
-        s[i] = (x >= 0 ? 1.0 : q) / (1.0 + q);
-      } else {
-        s[i] = exp(x - double(m));
-      }
-    }
-    sum += s[i];
-  }
+  double sum = 1.0;
+  // s of a logit (0 of -inf); computed where it is needed, which takes fewer registers
+  auto score = [&](float x) {
+    if (x == -INFINITY) return 0.0;
+    if (!a.sigmoid) return exp(double(x) - double(m)) / sum;
+    const double q = exp(-fabs(double(x)));
+    return (x >= 0.f ? 1.0 : q) / (1.0 + q);
+  };
   if (!a.sigmoid) {
-    sum = wave_sumd(sum);
+    double part = 0.0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (zv[i] > -INFINITY) s[i] /= sum;
+    for (int i = 0; i < PER; ++i) part += score(zv[i]);
+    sum = wave_sumd(part);
   }
-  double by[PER];  // what groups are compared by
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const double b = c[i];
     const bool live = zv[i] > -INFINITY && b > kOff;
-    c[i] = !live ? kOff : (a.bias ? s[i] + b : double(zv[i]));
-    by[i] = !live ? kOff : (a.bias ? c[i] : (a.group_top == 2 ? s[i] : double(zv[i])));
+    c[i] = !live ? kOff : (a.bias ? score(zv[i]) + b : double(zv[i]));
   }
+  // what groups are compared by
+  auto by = [&](int i) { return a.bias || a.group_top == 1 || !(c[i] > kOff) ? c[i] : score(zv[i]); };
   if (a.groups > 1) {
     const int gs = E / a.groups;
     double mine = kOff;  // lane g: the score of group g
@@ -119,9 +113,12 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int e = lane + 64 * i;
-        if (e >= g * gs && e < (g + 1) * gs && (by[i] > v || (by[i] == v && e < id))) {
-          v = by[i];
-          id = e;
+        if (e >= g * gs && e < (g + 1) * gs) {
+          const double x = by(i);
+          if (x > v || (x == v && e < id)) {
+            v = x;
+            id = e;
+          }
         }
       }
       wave_argmaxd(v, id);
@@ -131,7 +128,7 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           const int e = lane + 64 * i;
-          if (e >= g * gs && e < (g + 1) * gs && e != id) u = fmax(u, by[i]);
+          if (e >= g * gs && e < (g + 1) * gs && e != id) u = fmax(u, by(i));
         }
         u = wave_maxd(u);
         if (u > kOff) score += u;
@@ -151,13 +148,13 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
     }
   }
   // slot j is kept by lane j % 64 in its register j / 64
-  int sel[PER];
-  double ss[PER];
-  float sz[PER];
+  int sel[SLOTS];
+  double ss[SLOTS];
+  float sz[SLOTS];
   int found = 0;
   float top = -INFINITY;  // the largest logit chosen
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
+  for (int i = 0; i < SLOTS; ++i) {
     sel[i] = -1;
     ss[i] = 0.0;
     sz[i] = -INFINITY;
@@ -175,22 +172,18 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
     }
     wave_argmaxd(v, id);
     if (!(v > kOff)) break;  // the same in every lane
-    double es = 0.0;
     float ez = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (id == lane + 64 * i) {
         c[i] = kOff;
-        es = s[i];
         ez = zv[i];
       }
-    es = __shfl(es, id & 63);
     ez = __shfl(ez, id & 63);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
+    for (int i = 0; i < SLOTS; ++i)
       if (j == lane + 64 * i) {
         sel[i] = id;
-        ss[i] = es;
         sz[i] = ez;
       }
     top = fmaxf(top, ez);
@@ -202,7 +195,7 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
     const double ref = a.sigmoid ? fmin(double(top), 0.0) : double(top);
     double d = 0.0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
+    for (int i = 0; i < SLOTS; ++i)
       if (lane + 64 * i < found) {
         const double x = sz[i];
         ss[i] = !a.sigmoid ? exp(x - ref) : (x >= 0 ? 1.0 / (1.0 + exp(-x)) : exp(x - ref) / (1.0 + exp(x)));
@@ -210,10 +203,13 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
       }
     d = wave_sumd(d);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) ss[i] = lane + 64 * i < found ? ss[i] / d : 0.0;
+    for (int i = 0; i < SLOTS; ++i) ss[i] = lane + 64 * i < found ? ss[i] / d : 0.0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) ss[i] = score(sz[i]);
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
+  for (int i = 0; i < SLOTS; ++i) {
     const int j = lane + 64 * i;
     if (j < k) {
       oi[j] = sel[i];
@@ -227,7 +223,412 @@ __global__ __launch_bounds__(64 * kWaves) void choose_kernel(GateArgs a, int32_t
                                                              float* __restrict__ w) {
   const int64_t t = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
   if (t >= a.T) return;  // the whole wave
-  choose_token<PER>(a, t, idx, w);
+  choose_token<PER, PER>(a, t, idx, w);
+}
+
+// ------------------------------------------------------------------ the quick way
+// k <= 16: LPT lanes a token (64 / LPT tokens a wave), V neighbouring experts a lane. What
+// the choice goes by is computed in fp32 with a known bound on its error and turned into
+// integers: a fixed-point number of its distance from the row's largest (up to 24 bits
+// over the row's range) above the expert's id, so that keys are different, their order
+// needs no second comparison, and a lane sorts its own with min and max. A round of the
+// choice takes the largest of the lanes' first keys (DPP) and moves its lane's list up.
+// Where two keys that have to be told apart are closer than twice the error, where
+// something is not finite, and where a group has too few experts, the wave takes the
+// token again in 64 bits; the ids are those of 64 bits always. Logits themselves (no
+// bias) map to keys in their order, so there only equal keys are taken again.
+
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+// the value of the lane that a butterfly over groups of W lanes meets
+template <int W>
+__device__ __forceinline__ uint32_t meet(uint32_t v) {
+  if constexpr (W == 2) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 15, 15, true));
+  if constexpr (W == 4) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 15, 15, true));
+  if constexpr (W == 8) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 15, 15, true));
+  if constexpr (W == 16) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 15, 15, true));
+  return 0;
+}
+// op over the LPT lanes of a token (16, 32 or 64), in every one of them
+template <int LPT, class Op>
+__device__ __forceinline__ uint32_t over(uint32_t v, Op op) {
+  v = op(v, meet<2>(v));
+  v = op(v, meet<4>(v));
+  v = op(v, meet<8>(v));
+  v = op(v, meet<16>(v));
+  if constexpr (LPT >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(r[0], r[1]);
+  }
+  if constexpr (LPT >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = op(r[0], r[1]);
+  }
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float over_max(float v) {
+  return __uint_as_float(over<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+template <int LPT>
+__device__ __forceinline__ float over_sum(float v) {
+  return __uint_as_float(over<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t over_umax(uint32_t v) {
+  return over<LPT>(v, [](uint32_t a, uint32_t b) { return umax(a, b); });
+}
+
+// Descending, by Batcher's odd-even merging (63 comparisons of 16). Every index is a
+// template's: as loops the compiler left some of them, and indexed registers by selects.
+template <int A, int B, int V>
+__device__ __forceinline__ void in_order(uint32_t (&s)[V]) {
+  const uint32_t a = s[A], b = s[B];
+  s[A] = umax(a, b);
+  s[B] = umin(a, b);
+}
+template <int LO, int N, int R, int I, int V>  // comparisons of I, I + 2 R, ... with their R-th next
+__device__ __forceinline__ void merge_pairs(uint32_t (&s)[V]) {
+  if constexpr (I + R < LO + N) {
+    in_order<I, I + R>(s);
+    merge_pairs<LO, N, R, I + 2 * R>(s);
+  }
+}
+template <int LO, int N, int R, int V>  // every R-th of N from LO on: two sorted halves into one
+__device__ __forceinline__ void merge_halves(uint32_t (&s)[V]) {
+  if constexpr (2 * R < N) {
+    merge_halves<LO, N, 2 * R>(s);
+    merge_halves<LO + R, N, 2 * R>(s);
+    merge_pairs<LO, N, R, LO + R>(s);
+  } else {
+    in_order<LO, LO + R>(s);
+  }
+}
+template <int LO, int N, int V>
+__device__ __forceinline__ void sort_down(uint32_t (&s)[V]) {
+  if constexpr (N > 1) {
+    sort_down<LO, N / 2>(s);
+    sort_down<LO + N / 2, N / 2>(s);
+    merge_halves<LO, N, 1>(s);
+  }
+}
+
+template <int LO, int H, int I, int V>
+__device__ __forceinline__ void halve(uint32_t (&s)[V]) {
+  if constexpr (I < H) {
+    in_order<LO + I, LO + I + H>(s);
+    halve<LO, H, I + 1>(s);
+  }
+}
+template <int LO, int N, int V>
+__device__ __forceinline__ void bitonic_down(uint32_t (&s)[V]) {
+  if constexpr (N > 1) {
+    halve<LO, N / 2, 0>(s);
+    bitonic_down<LO, N / 2>(s);
+    bitonic_down<LO + N / 2, N / 2>(s);
+  }
+}
+
+// The D largest of V in front, descending: both halves sorted, the larger of each pair
+// (the i-th largest of one, the i-th smallest of the other's D) and those in order again.
+template <int D, int V>
+__device__ __forceinline__ void largest_down(uint32_t (&s)[V]) {
+  if constexpr (D == V) {
+    sort_down<0, V>(s);
+  } else {
+    static_assert(2 * D == V, "halves");
+    sort_down<0, D>(s);
+    sort_down<D, D>(s);
+#pragma unroll
+    for (int i = 0; i < D; ++i) s[i] = umax(s[i], s[V - 1 - i]);
+    if constexpr (D > 4) bitonic_down<0, D>(s);
+    else sort_down<0, D>(s);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int e0, int E, bool there, float (&z)[V]) {
+  if (there && e0 + V <= E && V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4u*>(row + e0 + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < V) z[i + j] = x[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = there && e0 + i < E ? row[e0 + i] : -INFINITY;
+  }
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// e^x to two units, x <= 0 (0 below the normal range): 2^t on the transcendental unit, and
+// what t = x log2(e) lost in its rounding made good.
+__device__ __forceinline__ float power(float x) {
+  const float t = fmaxf(x, -200.f) * kLog2e;
+  const float r = fmaf(fmaxf(x, -200.f), kLog2e, -t) + x * 1.925963033500912e-8f;
+  const float p = __builtin_amdgcn_exp2f(t);
+  return x >= -200.f ? fmaf(p, r * 0.6931471805599453f, p) : 0.f;
+}
+constexpr float kWindow = 16.f;  // of a row's range that keys resolve at most
+
+// SLOW: PER of the path in 64 bits. D: keys of a lane that are kept in order (k <= D, or
+// all of them). batches: of 64 / LPT tokens a wave takes. lanes_group: lanes of a group.
+template <int LPT, int V, int D, int SLOW>
+__global__ __launch_bounds__(64 * kWaves, SLOW <= 2 ? 5 : SLOW <= 4 ? 4 : 2) void choose_quick_kernel(GateArgs a, int batches, int lanes_group,
+                                                                   int32_t* __restrict__ idx, float* __restrict__ w) {
+  constexpr int TPW = 64 / LPT;
+  constexpr int IB = LPT * V == 1024 ? 10 : LPT * V == 512 ? 9 : LPT * V == 256 ? 8 : LPT * V == 128 ? 7
+                   : LPT * V == 64 ? 6 : LPT * V == 32 ? 5 : 4;
+  static_assert((1 << IB) == LPT * V, "ids fill their bits");
+  constexpr int KB = 32 - IB < 24 ? 32 - IB : 24;
+  constexpr float kTop = float((1 << KB) - 1);
+  const int lane = lane_id(), l = lane % LPT, E = a.E, k = a.k, e0 = l * V;
+  const int64_t wave = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int64_t first = wave * batches * TPW;
+  if (first >= a.T) return;  // the whole wave
+  float bias[V];
+  bool bad_bias = false;
+  load_row<V>(a.bias, e0, E, a.bias != nullptr, bias);
+#pragma unroll
+  for (int i = 0; i < V; ++i) bad_bias |= !(bias[i] < INFINITY);
+  const bool spoilt = __any(bad_bias);
+  float c[V], zn[V];  // a batch's logits, then what the choice goes by; the next one's logits
+  bool live_token, next_live;  // there, and not masked
+  auto fetch = [&](int64_t t0, float (&x)[V], bool& live) {
+    const int64_t t = t0 + lane / LPT;
+    live = t < a.T && (!a.mask || a.mask[t] != 0);
+    // a masked row is read and not used: no load waits for the mask
+    load_row<V>(a.logits + t * E, e0, E, t < a.T, x);
+  };
+  uint64_t todo = 0;  // lane n: the lanes of batch n whose tokens are taken again
+  fetch(first, zn, next_live);
+  for (int n = 0; n < batches; ++n) {
+    const int64_t t0 = first + int64_t(n) * TPW, t = t0 + lane / LPT;
+    if (t0 >= a.T) break;
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = zn[i];
+    live_token = next_live;
+    if (n + 1 < batches && t0 + TPW < a.T) fetch(t0 + TPW, zn, next_live);
+
+    // an infinity or a NaN anywhere shows in the sum
+    bool odd = spoilt;
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) total += c[i];
+    uint32_t off = 0u;  // experts that are off
+    const bool uneven = __any(!(fabsf(total) < INFINITY));
+    if (uneven) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        odd |= !(c[i] < INFINITY);
+        off |= c[i] == -INFINITY ? 1u << i : 0u;
+      }
+    }
+    float zt = -INFINITY, sum = 0.f;  // the row's maximum, sum of exp(z - zt)
+    float error = 0.f;                // of what the choice goes by
+    if (!a.sigmoid && (a.bias || !a.renorm)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) zt = fmaxf(zt, c[i]);
+      zt = over_max<LPT>(zt);
+      float q[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        q[i] = __builtin_amdgcn_exp2f((c[i] - zt) * kLog2e);
+        if (uneven && c[i] == -INFINITY) q[i] = 0.f;
+        sum += q[i];
+      }
+      sum = over_sum<LPT>(sum);
+      if (a.bias) {
+        const float inv = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = q[i] * inv + bias[i];
+        // each power's argument and value, 22 sums, their weighted share of the arguments'
+        // errors: below 64 units of 2^-24 of the largest probability
+        error = 0x1p-18f * inv;
+      }
+    } else if (a.bias) {
+      // s (1 - s) (|z| 1.5 + 2) of the power, s of the sum, 2 s of the reciprocal: below
+      // 4 units of 2^-24
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * c[i])) + bias[i];
+      error = 0x1p-22f;
+    }
+    if (uneven) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = off >> i & 1u ? -INFINITY : c[i];
+    }
+    // Keys resolve twice the distance from the row's largest to the least of the lanes'
+    // largest, so LPT experts at least; what is below has the key 0.
+    float top = c[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = fmaxf(top, c[i]);
+    const float least = -over_max<LPT>(top > -INFINITY ? -top : -INFINITY);  // of live lanes
+    top = over_max<LPT>(top);
+    const float window = fminf(2.f * (top - least), kWindow);
+    float scale = (kTop - 2.f) * __builtin_amdgcn_rcpf(window);
+    if (!(window > 0.f && scale < 1e30f)) scale = 1.f;  // equal ones have equal keys, and are taken again
+    if (a.bias) error += 0x1p-23f * (fabsf(top) + window);
+    const float close = a.bias ? 2.f * error * scale + 1.f : 0.f;
+    odd |= !(close < 0x1p+22f);
+    const uint32_t near = uint32_t(fminf(close, 0x1p+22f));
+    uint32_t s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float h = fmaxf((c[i] - top) * scale + kTop, 0.f);
+      s[i] = (uint32_t(h) << IB) | uint32_t(LPT * V - 1 - e0 - i);
+    }
+    largest_down<D>(s);
+
+    if (a.groups > 1) {
+      // the group's two largest keys in each of its lanes
+      uint32_t g0 = s[0], g1 = V > 1 ? s[V > 1 ? 1 : 0] : 0u;
+      auto join = [&](uint32_t b0, uint32_t b1) {
+        g1 = umax(umin(g0, b0), umax(g1, b1));
+        g0 = umax(g0, b0);
+      };
+      if (lanes_group >= 2) join(meet<2>(g0), meet<2>(g1));
+      if (lanes_group >= 4) join(meet<4>(g0), meet<4>(g1));
+      if (lanes_group >= 8) join(meet<8>(g0), meet<8>(g1));
+      if (lanes_group >= 16) join(meet<16>(g0), meet<16>(g1));
+      const uint32_t group = uint32_t(l / lanes_group);
+      uint32_t score = g0 >> IB;
+      uint32_t far = near;
+      if (a.group_top == 2) {
+        // a sum needs both of its keys: none below the window or off
+        odd |= e0 < E && (g1 >> IB) == 0u;
+        score += g1 >> IB;
+        far = 2u * near + 4u;
+      }
+      score = score ? (score << 6) | (63u - group) : 0u;
+      uint32_t last = 0u;
+      uint32_t kept = 0u;
+      for (int r = 0; r <= a.groups_kept; ++r) {
+        const uint32_t m = over_umax<LPT>(score);
+        if (r == a.groups_kept) {  // the best group that is left out
+          odd |= r < a.groups && (last >> 6) - (m >> 6) <= far;
+        } else {
+          odd |= m == 0u;  // a group with nothing above the window
+          const uint32_t hit = score == m ? ~0u : 0u;
+          kept |= hit;
+          score &= ~hit;
+        }
+        last = m;
+      }
+#pragma unroll
+      for (int i = 0; i < D; ++i) s[i] &= kept;
+    }
+
+    // the k largest keys, key j in lane j; and the next one
+    uint32_t mine = 0u, next = 0u, won = 0u;
+    for (int j = 0; j <= k; ++j) {
+      const uint32_t m = over_umax<LPT>(s[0]);
+      mine = l == j ? m : mine;
+      next = m;
+      // by masks: a choice between two elements becomes an index the compiler cannot resolve
+      const uint32_t win = s[0] == m ? ~0u : 0u;
+#pragma unroll
+      for (int i = 0; i + 1 < D; ++i) s[i] = (s[i + 1] & win) | (s[i] & ~win);
+      s[D - 1] &= ~win;
+      won -= win;
+    }
+    if (D < V) odd |= won >= uint32_t(D);  // the lane had more than its list held
+    // lane j's follower: key j + 1
+    uint32_t follow = uint32_t(__builtin_amdgcn_update_dpp(0, int(mine), 0x101, 15, 15, true));  // row_shl:1
+    if (l == k - 1) follow = next;
+    // (a key of 0 where one is wanted: all that is left is off, or below the window)
+    const uint32_t hm = mine >> IB, hf = follow >> IB;
+    odd |= l < k && hm - hf <= near;
+
+    const int e = LPT * V - 1 - int(mine & uint32_t(LPT * V - 1));
+    const bool some = l < k && hm != 0u;
+    const float x = some ? a.logits[t * E + e] : -INFINITY;
+    float v = 0.f;
+    if (!a.sigmoid) {
+      if (a.renorm) zt = over_max<LPT>(x);
+      if (some) v = power(x - zt);
+      if (a.renorm) sum = over_sum<LPT>(v);
+    } else {
+      const float q = power(-fabsf(x));
+      v = (x >= 0.f ? 1.f : q) * __builtin_amdgcn_rcpf(1.f + q);
+      if (a.renorm) {
+        // scores below e^ref, all of them, in units of it
+        const float ref = over_max<LPT>(x);
+        if (__any(ref < 0.f)) v = ref < 0.f ? power(x - ref) * __builtin_amdgcn_rcpf(1.f + q) : v;
+        v = some ? v : 0.f;
+        sum = over_sum<LPT>(v);
+      }
+    }
+    if (a.renorm || !a.sigmoid) v *= __builtin_amdgcn_rcpf(sum);
+    const uint64_t again = __ballot(odd && live_token);
+    const uint64_t own = LPT == 64 ? ~uint64_t(0) : ((uint64_t(1) << (LPT & 63)) - 1) << (lane / LPT * (LPT & 63));
+    if (t < a.T && l < k && !(again & own)) {
+      idx[t * k + l] = live_token ? e : -1;
+      w[t * k + l] = live_token ? a.scale * v : 0.f;
+    }
+    if (lane == n) todo = again;
+  }
+  // after the batches, so that their registers are free
+  if (!__any(todo != 0)) return;
+#pragma unroll 1
+  for (int n = 0; n < batches; ++n) {
+    const uint64_t again = __shfl(todo, n);
+#pragma unroll 1
+    for (int q = 0; q < TPW; ++q)
+      if ((again >> (q * (LPT & 63))) & (LPT == 64 ? ~uint64_t(0) : (uint64_t(1) << (LPT & 63)) - 1))
+        choose_token<SLOW, 1>(a, first + int64_t(n) * TPW + q, idx, w);
+  }
+}
+
+// Lanes of a group in the quick way, or 0 where it does not serve: the groups' ends are
+// lanes' ends, two, four, ... of them; without a bias groups compared by sums of scores
+// and experts by logits would take two kinds of keys.
+int quick_group_lanes(const GateArgs& a, int V) {
+  if (a.k > 16) return 0;
+  if (a.groups == 1) return 1;
+  if (!a.bias && a.group_top == 2) return 0;
+  const int gs = a.E / a.groups;
+  if (gs % V != 0) return 0;
+  const int n = gs / V;
+  return n <= 16 && (n & (n - 1)) == 0 ? n : 0;
+}
+
+template <int LPT, int V, int D, int SLOW>
+bool launch_quick(const GateArgs& a, int32_t* idx, float* w, hipStream_t st) {
+  const int lanes = quick_group_lanes(a, V);
+  if (lanes == 0) return false;
+  constexpr int TPW = 64 / LPT;
+  // several batches a wave where there are many: the next one's logits come meanwhile
+  const int64_t waves = (a.T + TPW - 1) / TPW;
+  const int batches = int(waves >= 16384 ? 4 : 1);
+  const int64_t blocks = (waves + int64_t(batches) * kWaves - 1) / (int64_t(batches) * kWaves);
+  hipLaunchKernelGGL((choose_quick_kernel<LPT, V, D, SLOW>), dim3(unsigned(blocks)), dim3(64 * kWaves), 0, st, a,
+                     batches, lanes, idx, w);
+  return true;
+}
+
+bool launch_quick(const GateArgs& a, int32_t* idx, float* w, hipStream_t st) {
+  if (a.E <= 16) return launch_quick<16, 1, 1, 1>(a, idx, w, st);
+  if (a.E <= 32) return launch_quick<16, 2, 2, 1>(a, idx, w, st);
+  if (a.E <= 64) return launch_quick<16, 4, 4, 1>(a, idx, w, st);
+  if (a.E <= 128) return launch_quick<16, 8, 8, 2>(a, idx, w, st);
+  if (a.k <= 8) {
+    if (a.E <= 256) return launch_quick<16, 16, 8, 4>(a, idx, w, st);
+    if (a.E <= 512) return launch_quick<32, 16, 8, 8>(a, idx, w, st);
+    return launch_quick<64, 16, 8, 16>(a, idx, w, st);
+  }
+  if (a.E <= 256) return launch_quick<16, 16, 16, 4>(a, idx, w, st);
+  if (a.E <= 512) return launch_quick<32, 16, 16, 8>(a, idx, w, st);
+  return launch_quick<64, 16, 16, 16>(a, idx, w, st);
 }
 
 // The gradient of one token (one wave): slot j's value goes to the lane of its
@@ -329,6 +730,7 @@ __global__ __launch_bounds__(64 * kWaves) void bwd_kernel(GateArgs a, const int3
 hipError_t launch_gate(const GateArgs& a, int32_t* idx, float* w, hipStream_t st, KernelTimer* timer) {
   if (a.T <= 0) return hipSuccess;
   TimedLaunch tl(timer, "gate", st);
+  if (gate::launch_quick(a, idx, w, st)) return hipGetLastError();
   const dim3 grid(unsigned((a.T + gate::kWaves - 1) / gate::kWaves)), block(64 * gate::kWaves);
   if (a.E <= 128)
     hipLaunchKernelGGL(gate::choose_kernel<2>, grid, block, 0, st, a, idx, w);
