@@ -725,6 +725,139 @@ __global__ __launch_bounds__(64 * kWaves) void bwd_kernel(GateArgs a, const int3
   }
 }
 
+// ------------------------------------------------------------------ the quick way back
+// k <= 16, LPT lanes a token as above, slot j in lane j. The row is put together in LDS:
+// zeros, the slots' values at their experts (one after the other only where an expert is
+// named twice), and for the dense form p (G - <p, G>) with lane l at the experts l + LPT i;
+// then a wave's rows, which lie one after the other in memory, leave as one run.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int LPT, int V, bool DENSE>
+__global__ __launch_bounds__(64 * kWaves) void bwd_quick_kernel(GateArgs a, const int32_t* __restrict__ idx,
+                                                                const float* __restrict__ dw, int accumulate,
+                                                                float* __restrict__ dz) {
+  constexpr int TPW = 64 / LPT;
+  __shared__ __attribute__((aligned(16))) float s_rows[kWaves][LPT * V * TPW + 4];
+  const int lane = lane_id(), l = lane % LPT, E = a.E, k = a.k;
+  const int64_t t0 = (int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6)) * TPW, t = t0 + lane / LPT;
+  if (t0 >= a.T) return;  // the whole wave
+  float* rows = s_rows[threadIdx.x >> 6];
+  float* row = rows + lane / LPT * E;
+  const int n = int(min(int64_t(TPW), a.T - t0)) * E;  // elements of the wave's rows
+  const bool slot = l < k && t < a.T;
+  int e = slot ? idx[t * k + l] : -1;
+  if (e >= E) e = -1;
+  const float d = e >= 0 ? dw[t * k + l] : 0.f;
+  float p[V];
+  float x = 0.f, sum = 0.f;
+  if constexpr (DENSE) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int o = l + LPT * i;
+      p[i] = t < a.T && o < E ? a.logits[t * E + o] : -INFINITY;
+      top = fmaxf(top, p[i]);
+    }
+    top = over_max<LPT>(top);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      // a row of -inf alone has no probabilities; a NaN stays one
+      p[i] = p[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((p[i] - top) * kLog2e);
+      sum += p[i];
+    }
+    sum = over_sum<LPT>(sum);
+  } else if (e >= 0) {
+    x = a.logits[t * E + e];
+  }
+  for (int i = 4 * lane; i < n; i += 256) *reinterpret_cast<f32x4*>(rows + i) = f32x4{0.f, 0.f, 0.f, 0.f};
+  float val = d;
+  if constexpr (!DENSE) {
+    const bool some = e >= 0 && x != -INFINITY;
+    float v = 0.f, slope = 1.f;
+    if (a.sigmoid) {
+      const float q = power(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.f + q);
+      v = (x >= 0.f ? 1.f : q) * r;
+      slope = (x >= 0.f ? q : 1.f) * r;
+      if (a.renorm) {
+        const float ref = over_max<LPT>(some ? x : -INFINITY);
+        if (__any(ref < 0.f)) v = ref < 0.f ? power(x - ref) * r : v;
+      }
+    } else {
+      const float top = over_max<LPT>(some ? x : -INFINITY);
+      v = power(x - top);
+    }
+    if (x != x) v = x;
+    v = some ? v : 0.f;
+    float g = d;
+    if (a.renorm) {
+      v *= __builtin_amdgcn_rcpf(over_sum<LPT>(v));
+      g = d - over_sum<LPT>(some ? v * d : 0.f);
+    }
+    val = some ? v * slope * g : 0.f;
+  }
+  // is an expert named twice? Every slot against those behind it, in the token's row of lanes
+  bool twice = false;
+  for (int j = 1; j < k; ++j) {
+    const int o = __shfl(e, (lane & ~(LPT - 1)) + ((l + j) & (LPT - 1)));
+    twice |= l + j < k && e >= 0 && o == e;
+  }
+  wave_sync();
+  if (!__any(twice)) {
+    if (e >= 0) row[e] = val;
+  } else {
+    for (int j = 0; j < k; ++j) {
+      if (l == j && e >= 0) row[e] += val;
+      wave_sync();
+    }
+  }
+  wave_sync();
+  if constexpr (DENSE) {
+    float g[V];
+    float pg = 0.f;
+    const float inv = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int o = l + LPT * i;
+      g[i] = o < E ? row[o] : 0.f;
+      pg += p[i] * g[i];
+    }
+    pg = over_sum<LPT>(pg) * inv;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int o = l + LPT * i;
+      if (o < E) row[o] = p[i] == 0.f ? 0.f : p[i] * inv * (g[i] - pg);
+    }
+    wave_sync();
+  }
+  float* out = dz + t0 * E;
+  for (int i = 4 * lane; i < n; i += 256) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(rows + i);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] *= a.scale;
+    if (i + 4 <= n) {
+      if (accumulate) v += *reinterpret_cast<const f32x4u*>(out + i);
+      *reinterpret_cast<f32x4u*>(out + i) = v;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i + q < n) out[i + q] = accumulate ? out[i + q] + v[q] : v[q];
+    }
+  }
+}
+
+template <int LPT, int V>
+void launch_bwd_quick(const GateArgs& a, const int32_t* idx, const float* dw, int accumulate, float* dz, hipStream_t st) {
+  const int64_t per = int64_t(kWaves) * (64 / LPT);
+  const dim3 grid(unsigned((a.T + per - 1) / per)), block(64 * kWaves);
+  if (!a.sigmoid && !a.renorm)
+    hipLaunchKernelGGL((bwd_quick_kernel<LPT, V, true>), grid, block, 0, st, a, idx, dw, accumulate, dz);
+  else
+    hipLaunchKernelGGL((bwd_quick_kernel<LPT, V, false>), grid, block, 0, st, a, idx, dw, accumulate, dz);
+}
+
 }  // namespace gate
 
 hipError_t launch_gate(const GateArgs& a, int32_t* idx, float* w, hipStream_t st, KernelTimer* timer) {
@@ -745,6 +878,16 @@ hipError_t launch_gate_bwd(const GateArgs& a, const int32_t* idx, const float* d
                            hipStream_t st, KernelTimer* timer) {
   if (a.T <= 0) return hipSuccess;
   TimedLaunch tl(timer, "gate_bwd", st);
+  if (a.k <= 16) {
+    if (a.E <= 16) gate::launch_bwd_quick<16, 1>(a, idx, dw, accumulate, dz, st);
+    else if (a.E <= 32) gate::launch_bwd_quick<16, 2>(a, idx, dw, accumulate, dz, st);
+    else if (a.E <= 64) gate::launch_bwd_quick<16, 4>(a, idx, dw, accumulate, dz, st);
+    else if (a.E <= 128) gate::launch_bwd_quick<16, 8>(a, idx, dw, accumulate, dz, st);
+    else if (a.E <= 256) gate::launch_bwd_quick<16, 16>(a, idx, dw, accumulate, dz, st);
+    else if (a.E <= 512) gate::launch_bwd_quick<32, 16>(a, idx, dw, accumulate, dz, st);
+    else gate::launch_bwd_quick<64, 16>(a, idx, dw, accumulate, dz, st);
+    return hipGetLastError();
+  }
   const dim3 grid(unsigned((a.T + gate::kWaves - 1) / gate::kWaves)), block(64 * gate::kWaves);
   if (a.E <= 128)
     hipLaunchKernelGGL(gate::bwd_kernel<2>, grid, block, 0, st, a, idx, dw, accumulate, dz);
