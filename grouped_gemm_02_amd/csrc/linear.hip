@@ -293,6 +293,17 @@ struct Problem {
   Out out;
 };
 
+// A barrier that waits for nothing by itself (__syncthreads waits for every load into
+// LDS); memory accesses stay on their side of it.
+__device__ __forceinline__ void meet_all() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The operand of s_waitcnt for lgkmcnt(0) and vmcnt(n)
+constexpr int wait_code(int n) { return (n & 15) | (n >> 4) << 14 | 0x0070; }
+
 // The b-th tile: the eight XCDs (b % 8) take contiguous ranges of tiles, and a range
 // walks groups of eight row tiles column by column, so that tiles that run at once in
 // an XCD share rows of both operands in its L2.
@@ -514,16 +525,20 @@ __device__ __forceinline__ void results(const Problem& p, f32x16 (&acc)[WTM / 32
 // through LDS of each wave's own, so the next tile's slabs are on their way meanwhile. The
 // number of a tile's slabs is made even (the last may be zeros), so that a stage is known
 // at compile time.
-template <int BM, int BN, int WM, int WN, bool P_MN, bool Q_MN, int MODE>
-__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const Problem p) {
+// NS: stages, that is how many slabs ahead are sent for.
+template <int BM, int BN, int WM, int WN, int NS, bool P_MN, bool Q_MN, int MODE>
+__global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(const Problem p) {
   constexpr int kThreads = 64 * WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
   constexpr int kStage = (BM + BN) * BK;
   static_assert(TN % 2 == 0, "a wave has gate and up columns of a pair");
-  // two LDS objects, so that the compiler can tell reads of one stage from loads in
-  // flight into the other
+  static_assert(NS == 2 || NS == 4, "stages");
+  // an LDS object for each stage, so that the compiler can tell reads of one from loads in
+  // flight into another
   __shared__ __attribute__((aligned(16))) uint16_t s0[kStage];
   __shared__ __attribute__((aligned(16))) uint16_t s1[kStage];
+  __shared__ __attribute__((aligned(16))) uint16_t s2[NS > 2 ? kStage : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t s3[NS > 2 ? kStage : 8];
   // 32 rows of a wave's results: WTN / 8 chunks of 16 bytes a row, chunk c at slot c ^ row
   __shared__ __attribute__((aligned(16))) uint16_t s_out[WM * WN][32 * WTN];
   const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN, lane = lane_id();
@@ -556,7 +571,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const Problem p) 
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mfma_32x32x16(f.q[j], f.p[i], acc[i][j]);
   };
-  // Which slab is sent for next: number f of the tile's nf (even), which end at fend. Past
+  // Which slab is sent for next: number f of the tile's nf (a multiple of NS), which end at fend. Past
   // the last tile's end slabs of zeros are sent for.
   uint32_t t = blockIdx.x;
   int f = 0, nf, f0, fend;
@@ -565,7 +580,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const Problem p) 
     f = 0;
     f0 = si * p.slabs;
     fend = min(f0 + p.slabs, all);
-    nf = (fend - f0 + 1) & ~1;
+    nf = (fend - f0 + NS - 1) & ~(NS - 1);
   };
   auto advance = [&]() {
     if (more && f == nf) {
@@ -612,11 +627,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const Problem p) 
     step(s, 1, b, a);
     step(s, 2, a, b);
     step(s, 3, b, a);
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-    __syncthreads();
+    // lgkmcnt(0), and all loads but those of the NS - 2 slabs after the next
+    __builtin_amdgcn_s_waitcnt(wait_code((NS - 2) * kSends));
+    meet_all();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // its last products, while the slab after the next is sent for into its place
+  // its last products, while another slab is sent for into its place
   auto turn = [&](uint16_t* done, const uint16_t* nxt) {
     advance();
     __builtin_amdgcn_sched_barrier(0);
@@ -640,21 +656,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const Problem p) 
   send(s0);
   advance();
   send(s1);
-  __builtin_amdgcn_s_waitcnt(0x0F70);
-  __syncthreads();
+  if constexpr (NS > 2) {
+    advance();
+    send(s2);
+    advance();
+    send(s3);
+  }
+  __builtin_amdgcn_s_waitcnt(wait_code((NS - 1) * kSends));
+  meet_all();
   clear();
   read(s0, 0, a);
   steps(s0);
-  // At the top a slab in s0 lacks its last products, and nothing is under way: loads
-  // into LDS that crossed the loop's end would be waited for by the compiler.
+  // At the top a slab in s0 lacks its last products.
   while (true) {
     turn(s0, s1);
     steps(s1);
-    turn(s1, s0);
-    left -= 2;
+    if constexpr (NS > 2) {
+      turn(s1, s2);
+      steps(s2);
+      turn(s2, s3);
+      steps(s3);
+      turn(s3, s0);
+    } else {
+      turn(s1, s0);
+    }
+    left -= NS;
     if (left == 0) {
       results<WTM, WTN, MODE>(p, acc, s_out[wave], m0 + wm * WTM, n0 + wn * WTN, part);
-      // two slabs of the next tile are there or under way, if there is one
+      // slabs of the next tile are there or under way, if there is one
       if (!more) break;
       m0 = int64_t(mi) * BM;
       n0 = int64_t(ni) * BN;
@@ -904,7 +933,14 @@ constexpr int kMaxSplits = 16;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int tile_cols(int tile) { return tile == 256 ? 256 : 128; }
+int slots_of(int tile) { return tile == 128 ? 512 : 256; }  // workgroups that run at once
 
+// The least of an estimate in microseconds, from products of 25 shapes in each of the three
+// forms with every tile and splits of 1, 2, 4, 8 and 16 (the choice was the fastest, or
+// within 10 % of it): a slab takes 1.6 us in a 256 x 256 tile (one a CU), 0.74 in a 128 x 128
+// one alone on its CU and 1.0 with a second beside it, 0.37 in a 64 x 128 one (one a CU:
+// four stages take its LDS); a tile's start and results 8, 3 and 2; joining parts a launch
+// and their sums written and read.
 Plan plan_of(int64_t M, int64_t N, int64_t kred) {
   const int64_t slabs = ceil_div(kred, BK);
   Plan best{64, 1};
@@ -912,14 +948,16 @@ Plan plan_of(int64_t M, int64_t N, int64_t kred) {
   for (int tile : {256, 128, 64}) {
     const int64_t tiles = ceil_div(M, tile) * ceil_div(N, tile_cols(tile));
     if (tile < 256 && tiles > (1 << 20)) continue;  // a grid has less than 2^32 threads
-    const int64_t slots = tile == 256 ? 256 : 512;  // workgroups that run at once
-    for (int64_t s = 1; s <= kMaxSplits && s <= slabs; s *= 2) {
+    const int64_t slots = slots_of(tile);
+    for (int64_t s = 1; s <= kMaxSplits && s <= slabs; ++s) {
       if (s > 1 && tiles * s > slots) break;
-      const double rounds = double(ceil_div(tiles * s, slots));
-      // per slab and tile, with the slots full
-      const double slab = tile == 256 ? 1.6 : tile == 128 ? 1.1 : 0.9;
-      const double join = s > 1 ? 5.0 + 2.0 * double(s) * double(M) * double(N) * 4e-6 / 4.0 : 0.0;
-      const double t = rounds * (double(ceil_div(slabs, s)) * slab + 4.0) + join;
+      const int64_t n = tiles * s, part = ceil_div(slabs, s), rest = n % slots;
+      const double results = tile == 256 ? 8.0 : tile == 128 ? 3.0 : 2.0;
+      const double slab = tile == 256 ? 1.6 : tile == 128 ? 1.0 : 0.37;
+      const double last = tile == 128 && rest <= 256 ? 0.74 : slab;
+      double t = double(n / slots) * (double(part) * slab + results);
+      if (rest) t += double(part) * last + results;
+      if (s > 1) t += 5.0 + 0.3 * double(s) + double(s) * double(M) * double(N) * 8.0 / 12e6;
       if (t < least) {
         least = t;
         best = Plan{tile, int(s)};
@@ -931,28 +969,28 @@ Plan plan_of(int64_t M, int64_t N, int64_t kred) {
 
 int64_t pad8(int64_t n) { return (n + 7) & ~int64_t(7); }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int NS>
 hipError_t launch_tiles(const Problem& p, bool pmn, bool qmn, int64_t slots, hipStream_t st) {
   const int64_t tiles = int64_t(p.mt) * p.nt * p.splits;
   const dim3 grid(unsigned(std::min(tiles, slots))), block(64 * WM * WN);
   const bool split = p.splits > 1;
   // gradients have no activation, bias or residual
-  auto kernel = pmn   ? (split ? tile_kernel<BM, BN, WM, WN, true, true, kSplit> : tile_kernel<BM, BN, WM, WN, true, true, kPlain>)
-                : qmn ? (split ? tile_kernel<BM, BN, WM, WN, false, true, kSplit>
-                               : tile_kernel<BM, BN, WM, WN, false, true, kPlain>)
-                : split                     ? tile_kernel<BM, BN, WM, WN, false, false, kSplit>
-                : p.Q.pair                  ? tile_kernel<BM, BN, WM, WN, false, false, kPair>
-                : p.out.act != kActNone     ? tile_kernel<BM, BN, WM, WN, false, false, kActs>
-                                            : tile_kernel<BM, BN, WM, WN, false, false, kPlain>;
+  auto kernel = pmn   ? (split ? tile_kernel<BM, BN, WM, WN, NS, true, true, kSplit> : tile_kernel<BM, BN, WM, WN, NS, true, true, kPlain>)
+                : qmn ? (split ? tile_kernel<BM, BN, WM, WN, NS, false, true, kSplit>
+                               : tile_kernel<BM, BN, WM, WN, NS, false, true, kPlain>)
+                : split                     ? tile_kernel<BM, BN, WM, WN, NS, false, false, kSplit>
+                : p.Q.pair                  ? tile_kernel<BM, BN, WM, WN, NS, false, false, kPair>
+                : p.out.act != kActNone     ? tile_kernel<BM, BN, WM, WN, NS, false, false, kActs>
+                                            : tile_kernel<BM, BN, WM, WN, NS, false, false, kPlain>;
   hipLaunchKernelGGL(kernel, grid, block, 0, st, p);
   return hipGetLastError();
 }
 
-// What the parts of a split product M x N may take at most: kMaxSplits of them, and
-// twice as many tiles as run at once. Grows with M, so a scratch serves smaller M.
+// What the parts of a split product M x N may take at most: kMaxSplits of them, and as
+// many tiles as run at once. Grows with M, so a scratch serves smaller M.
 size_t partial_bytes(int64_t M, int64_t N) {
   const size_t all = size_t(kMaxSplits) * size_t(M) * size_t(ceil_div(N, 64) * 64) * 4;
-  return std::min(all, size_t(2 * 256) * 256 * 256 * 4);
+  return std::min(all, size_t(256) * 256 * 256 * 4);
 }
 
 hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64_t kred, const Out& out, float* partial,
@@ -976,9 +1014,9 @@ hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64
   hipError_t e;
   {
     TimedLaunch tl(timer, name, st);
-    e = pl.tile == 256 ? launch_tiles<256, 256, 2, 4>(p, pmn, qmn, 256, st)
-        : pl.tile == 128 ? launch_tiles<128, 128, 2, 2>(p, pmn, qmn, 512, st)
-                         : launch_tiles<64, 128, 2, 2>(p, pmn, qmn, 512, st);
+    e = pl.tile == 256 ? launch_tiles<256, 256, 2, 4, 2>(p, pmn, qmn, slots_of(256), st)
+        : pl.tile == 128 ? launch_tiles<128, 128, 2, 2, 2>(p, pmn, qmn, slots_of(128), st)
+                         : launch_tiles<64, 128, 2, 2, 4>(p, pmn, qmn, slots_of(64), st);
   }
   if (e != hipSuccess || p.splits == 1) return e;
   TimedLaunch tl(timer, "linear_join", st);
