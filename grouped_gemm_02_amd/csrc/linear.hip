@@ -525,23 +525,16 @@ __device__ __forceinline__ void results(const Problem& p, f32x16 (&acc)[WTM / 32
 // through LDS of each wave's own, so the next tile's slabs are on their way meanwhile. The
 // number of a tile's slabs is made even (the last may be zeros), so that a stage is known
 // at compile time.
-// NS: stages, that is how many slabs ahead are sent for.
+// NS: stages, that is how many slabs ahead are sent for. s0 .. s3: the stages' LDS; out: 32
+// rows of each wave's results, WTN / 8 chunks of 16 bytes a row, chunk c at slot c ^ row.
 template <int BM, int BN, int WM, int WN, int NS, bool P_MN, bool Q_MN, int MODE>
-__global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(const Problem p) {
+__device__ __forceinline__ void walk(const Problem& p, uint32_t first, uint32_t grid, uint16_t* s0, uint16_t* s1,
+                                     uint16_t* s2, uint16_t* s3, uint16_t* out) {
   constexpr int kThreads = 64 * WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
-  constexpr int kStage = (BM + BN) * BK;
   static_assert(TN % 2 == 0, "a wave has gate and up columns of a pair");
   static_assert(NS == 2 || NS == 4, "stages");
-  // an LDS object for each stage, so that the compiler can tell reads of one from loads in
-  // flight into another
-  __shared__ __attribute__((aligned(16))) uint16_t s0[kStage];
-  __shared__ __attribute__((aligned(16))) uint16_t s1[kStage];
-  __shared__ __attribute__((aligned(16))) uint16_t s2[NS > 2 ? kStage : 8];
-  __shared__ __attribute__((aligned(16))) uint16_t s3[NS > 2 ? kStage : 8];
-  // 32 rows of a wave's results: WTN / 8 chunks of 16 bytes a row, chunk c at slot c ^ row
-  __shared__ __attribute__((aligned(16))) uint16_t s_out[WM * WN][32 * WTN];
-  const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN, lane = lane_id();
+  const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
   const uint32_t total = uint32_t(p.mt) * uint32_t(p.nt) * uint32_t(p.splits);
   const int all = int((p.kred + BK - 1) / BK);
   typename LoaderOf<P_MN, BM, kThreads>::type lp;
@@ -573,7 +566,7 @@ __global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(con
   };
   // Which slab is sent for next: number f of the tile's nf (a multiple of NS), which end at fend. Past
   // the last tile's end slabs of zeros are sent for.
-  uint32_t t = blockIdx.x;
+  uint32_t t = first;
   int f = 0, nf, f0, fend;
   bool more = true;
   auto begin = [&]() {
@@ -584,7 +577,7 @@ __global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(con
   };
   auto advance = [&]() {
     if (more && f == nf) {
-      t += gridDim.x;
+      t += grid;
       more = t < total;
       if (more) {
         open(t);
@@ -682,7 +675,7 @@ __global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(con
     }
     left -= NS;
     if (left == 0) {
-      results<WTM, WTN, MODE>(p, acc, s_out[wave], m0 + wm * WTM, n0 + wn * WTN, part);
+      results<WTM, WTN, MODE>(p, acc, out + wave * 32 * WTN, m0 + wm * WTM, n0 + wn * WTN, part);
       // slabs of the next tile are there or under way, if there is one
       if (!more) break;
       m0 = int64_t(mi) * BM;
@@ -694,6 +687,33 @@ __global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(con
     }
     steps(s0);
   }
+}
+
+// An LDS object for each stage, so that the compiler can tell reads of one from loads in
+// flight into another.
+#define MOE_LINEAR_LDS                                                                  \
+  constexpr int kStage = (BM + BN) * BK, kMore = NS > 2 ? kStage : 8;                   \
+  __shared__ __attribute__((aligned(16))) uint16_t s0[kStage];                          \
+  __shared__ __attribute__((aligned(16))) uint16_t s1[kStage];                          \
+  __shared__ __attribute__((aligned(16))) uint16_t s2[kMore];                           \
+  __shared__ __attribute__((aligned(16))) uint16_t s3[kMore];                           \
+  __shared__ __attribute__((aligned(16))) uint16_t s_out[WM * 32 * BN];
+
+template <int BM, int BN, int WM, int WN, int NS, bool P_MN, bool Q_MN, int MODE>
+__global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(const Problem p) {
+  MOE_LINEAR_LDS
+  walk<BM, BN, WM, WN, NS, P_MN, Q_MN, MODE>(p, blockIdx.x, gridDim.x, s0, s1, s2, s3, s_out);
+}
+
+// dX and dW at once where neither fills the CUs: the first `nx` workgroups have dX's tiles,
+// one each, the others dW's (1003 x 777 x 1001: 12 us for both instead of 11 and 12).
+template <int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void both_kernel(const Problem x, const Problem w, uint32_t nx) {
+  MOE_LINEAR_LDS
+  if (blockIdx.x < nx)
+    walk<BM, BN, WM, WN, NS, false, true, kPlain>(x, blockIdx.x, nx, s0, s1, s2, s3, s_out);
+  else
+    walk<BM, BN, WM, WN, NS, true, true, kPlain>(w, blockIdx.x - nx, gridDim.x - nx, s0, s1, s2, s3, s_out);
 }
 
 // Few rows (M <= 64): W is read once, straight into the fragments of
@@ -803,22 +823,29 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 // ------------------------------------------------------------------ passes around the products
 
 // rows [R, C] -> [R, ld], the columns past C zero
-__global__ __launch_bounds__(256) void pad_kernel(const uint16_t* __restrict__ in, int64_t R, int C, int64_t ld,
-                                                  uint16_t* __restrict__ out) {
-  const int per = int(ld / 8);
-  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < R * per; q += int64_t(gridDim.x) * 256) {
+struct PadJob {
+  const uint16_t* in;
+  uint16_t* out;
+  int64_t R;
+  int C;
+  int64_t ld;
+  int blocks;
+};
+__device__ void pad_rows(const PadJob& a, int block) {
+  const int per = int(a.ld / 8);
+  for (int64_t q = int64_t(block) * 256 + threadIdx.x; q < a.R * per; q += int64_t(a.blocks) * 256) {
     const int64_t r = q / per;
     const int c = int(q % per) * 8;
-    const uint16_t* src = in + r * C + c;
+    const uint16_t* src = a.in + r * a.C + c;
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (c + 8 <= C) {
+    if (c + 8 <= a.C) {
       v = *reinterpret_cast<const u32x4u*>(src);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c + i < C) v[i / 2] |= uint32_t(src[i]) << (16 * (i & 1));
+        if (c + i < a.C) v[i / 2] |= uint32_t(src[i]) << (16 * (i & 1));
     }
-    *reinterpret_cast<u32x4*>(out + r * ld + c) = v;
+    *reinterpret_cast<u32x4*>(a.out + r * a.ld + c) = v;
   }
 }
 
@@ -834,15 +861,16 @@ struct DpArgs {
   float* sums;  // [blocks][cols] column sums of dP, or NULL
   int cols;     // N'
   int rows;     // rows of a block
+  int blocks;   // along the rows; as many for every 256 columns of dY
 };
 
 // dP = dY act'(P), and its column sums. A workgroup takes `rows` rows of 8 x 32 = 256
 // columns; thread t the columns 8 (t % 32) of rows t / 32, + 8, ...
-__global__ __launch_bounds__(256) void dp_kernel(const DpArgs a) {
-  __shared__ float red[8][256];
+__device__ void slope_rows(const DpArgs& a, int block, float (&red)[8][256]) {
   const int tr = threadIdx.x >> 5, tc = threadIdx.x & 31;
-  const int c = int(blockIdx.y) * 256 + 8 * tc;
-  const int64_t r0 = int64_t(blockIdx.x) * a.rows;
+  const int by = block / a.blocks, bx = block % a.blocks;
+  const int c = by * 256 + 8 * tc;
+  const int64_t r0 = int64_t(bx) * a.rows;
   const bool pair = a.act == kActSwiglu;
   const int cols = a.N - c;
   float sv[8], su[8];
@@ -898,9 +926,20 @@ __global__ __launch_bounds__(256) void dp_kernel(const DpArgs a) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-    const int col = int(blockIdx.y) * 256 + int(threadIdx.x);
-    if (col < a.N) a.sums[int64_t(blockIdx.x) * a.cols + part * a.N + col] = s;
+    const int col = by * 256 + int(threadIdx.x);
+    if (col < a.N) a.sums[int64_t(bx) * a.cols + part * a.N + col] = s;
   }
+}
+
+// What has to be done before the products, in one launch: dP, and rows made a multiple of
+// 16 bytes.
+__global__ __launch_bounds__(256) void before_kernel(const DpArgs d, int slopes, const PadJob a, const PadJob b) {
+  __shared__ float red[8][256];
+  int block = int(blockIdx.x);
+  if (block < slopes) return slope_rows(d, block, red);
+  block -= slopes;
+  if (block < a.blocks) return pad_rows(a, block);
+  pad_rows(b, block - a.blocks);
 }
 
 // dbias from the blocks' sums; no blocks: zeros
@@ -910,8 +949,17 @@ __global__ __launch_bounds__(256) void bias_kernel(const float* __restrict__ sum
   const int lane = lane_id(), w = threadIdx.x >> 6;
   const int c = int(blockIdx.x) * 64 + lane;
   float s = 0.f;
-  if (c < cols)
-    for (int b = w; b < blocks; b += 4) s += sums[int64_t(b) * cols + c];
+  if (c < cols) {
+    int b = w;
+    for (; b + 28 < blocks; b += 32) {  // eight loads under way
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = sums[int64_t(b + 4 * i) * cols + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[i];
+    }
+    for (; b < blocks; b += 4) s += sums[int64_t(b) * cols + c];
+  }
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < cols) out[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
@@ -993,9 +1041,7 @@ size_t partial_bytes(int64_t M, int64_t N) {
   return std::min(all, size_t(256) * 256 * 256 * 4);
 }
 
-hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64_t kred, const Out& out, float* partial,
-                   hipStream_t st, KernelTimer* timer, const char* name) {
-  const Plan pl = plan_of(P.ents, Q.ents, kred);
+Problem problem(const Plan& pl, const Operand& P, const Operand& Q, int64_t kred, const Out& out, float* partial) {
   Problem p;
   p.P = P;
   p.Q = Q;
@@ -1011,6 +1057,13 @@ hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64
   p.partial = partial;
   p.ldp = ceil_div(ncols, 64) * 64;
   p.out = out;
+  return p;
+}
+
+hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64_t kred, const Out& out, float* partial,
+                   hipStream_t st, KernelTimer* timer, const char* name) {
+  const Plan pl = plan_of(P.ents, Q.ents, kred);
+  const Problem p = problem(pl, P, Q, kred, out, partial);
   hipError_t e;
   {
     TimedLaunch tl(timer, name, st);
@@ -1026,11 +1079,16 @@ hipError_t product(const Operand& P, bool pmn, const Operand& Q, bool qmn, int64
   return hipGetLastError();
 }
 
-hipError_t pad(const uint16_t* in, int64_t R, int64_t C, uint16_t* out, hipStream_t st, KernelTimer* timer) {
-  TimedLaunch tl(timer, "linear_pad", st);
-  const int64_t blocks = ceil_div(R * (pad8(C) / 8), 256);
-  hipLaunchKernelGGL(pad_kernel, dim3(unsigned(std::min<int64_t>(blocks, 8192))), dim3(256), 0, st, in, R, int(C),
-                     pad8(C), out);
+PadJob pad_job(const uint16_t* in, int64_t R, int64_t C, uint16_t* out) {
+  return PadJob{in, out, R, int(C), pad8(C), int(std::min<int64_t>(ceil_div(R * (pad8(C) / 8), 256), 8192))};
+}
+
+hipError_t before(const DpArgs& d, bool slopes, const PadJob& a, const PadJob& b, hipStream_t st, KernelTimer* timer) {
+  const int64_t n = slopes ? int64_t(d.blocks) * ceil_div(d.N, 256) : 0;
+  const int64_t grid = n + a.blocks + b.blocks;
+  if (grid == 0) return hipSuccess;
+  TimedLaunch tl(timer, "linear_before", st);
+  hipLaunchKernelGGL(before_kernel, dim3(unsigned(grid)), dim3(256), 0, st, d, int(n), a, b);
   return hipGetLastError();
 }
 
@@ -1090,8 +1148,7 @@ hipError_t launch_linear(const LinearArgs& a, const uint16_t* X, const uint16_t*
   if (a.K % 8 != 0) {
     uint16_t* xp = reinterpret_cast<uint16_t*>(base + L.x);
     uint16_t* wp = reinterpret_cast<uint16_t*>(base + L.w);
-    hipError_t e = pad(X, a.M, a.K, xp, st, timer);
-    if (e == hipSuccess) e = pad(W, R, a.K, wp, st, timer);
+    const hipError_t e = before(DpArgs{}, false, pad_job(X, a.M, a.K, xp), pad_job(W, R, a.K, wp), st, timer);
     if (e != hipSuccess) return e;
     X = xp;
     W = wp;
@@ -1124,9 +1181,9 @@ hipError_t launch_linear_bwd(const LinearArgs& a, const void* dY, const uint16_t
   char* base = static_cast<char*>(ws);
   const bool as_is = a.act == kActNone && !a.out_f32 && R % 8 == 0;  // dY is dP already
   const uint16_t* dP = static_cast<const uint16_t*>(dY);
-  const bool products = dX || dW;
-  if (dbias || (products && !as_is)) {
-    DpArgs d;
+  const bool products = dX || dW, slopes = dbias || (products && !as_is), odd = a.K % 8 != 0;
+  DpArgs d{};
+  if (slopes) {
     d.dY = dY;
     d.pre = pre;
     d.M = a.M;
@@ -1137,43 +1194,44 @@ hipError_t launch_linear_bwd(const LinearArgs& a, const void* dY, const uint16_t
     d.ld = pad8(R);
     d.sums = dbias ? reinterpret_cast<float*>(base + L.sums) : nullptr;
     d.cols = int(R);
-    d.rows = int(dp_rows(a.M));
-    const int blocks = int(ceil_div(a.M, d.rows));
-    {
-      TimedLaunch tl(timer, "linear_dp", st);
-      hipLaunchKernelGGL(dp_kernel, dim3(unsigned(blocks), unsigned(ceil_div(a.N, 256))), dim3(256), 0, st, d);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (dbias) {
-      TimedLaunch tl(timer, "linear_dbias", st);
-      hipLaunchKernelGGL(bias_kernel, dim3(unsigned(ceil_div(R, 64))), dim3(256), 0, st, d.sums, blocks, int(R), dbias);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    // (a grid has less than 2^32 threads)
+    d.rows = int(dbias ? dp_rows(a.M) : std::max(kDpRows, ceil_div(a.M * ceil_div(a.N, 256), int64_t(1) << 20)));
+    d.blocks = int(ceil_div(a.M, d.rows));
     if (d.dP) dP = d.dP;
+  }
+  uint16_t* wp = reinterpret_cast<uint16_t*>(base + L.w);
+  uint16_t* xp = reinterpret_cast<uint16_t*>(base + L.x);
+  e = before(d, slopes, dX && odd ? pad_job(W, R, a.K, wp) : PadJob{}, dW && odd ? pad_job(X, a.M, a.K, xp) : PadJob{},
+             st, timer);
+  if (e != hipSuccess) return e;
+  if (odd) {
+    W = wp;
+    X = xp;
+  }
+  if (dbias) {
+    TimedLaunch tl(timer, "linear_dbias", st);
+    hipLaunchKernelGGL(bias_kernel, dim3(unsigned(ceil_div(R, 64))), dim3(256), 0, st, d.sums, d.blocks, int(R), dbias);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const int64_t ldr = pad8(R), ldk = pad8(a.K);
   float* partial = reinterpret_cast<float*>(base + L.partial);
-  if (dX) {
-    if (a.K % 8 != 0) {
-      uint16_t* wp = reinterpret_cast<uint16_t*>(base + L.w);
-      if ((e = pad(W, R, a.K, wp, st, timer)) != hipSuccess) return e;
-      W = wp;
+  const Out ox{nullptr, nullptr, dX, nullptr, a.M, int(a.K), kActNone, false};
+  const Out ow{nullptr, nullptr, dW, nullptr, R, int(a.K), kActNone, false};
+  const Operand px{dP, ldr, a.M, false}, qx{W, ldk, a.K, false}, pw{dP, ldr, R, false}, qw{X, ldk, a.K, false};
+  if (dX && dW) {
+    const Plan plx = plan_of(a.M, a.K, R), plw = plan_of(R, a.K, a.M);
+    if (plx.tile == 64 && plw.tile == 64 && plx.splits == 1 && plw.splits == 1) {
+      const Problem x = problem(plx, px, qx, R, ox, partial), w = problem(plw, pw, qw, a.M, ow, partial);
+      const int64_t nx = int64_t(x.mt) * x.nt, nw = int64_t(w.mt) * w.nt;
+      if (nx + nw <= slots_of(64)) {
+        TimedLaunch tl(timer, "linear_dx_dw", st);
+        hipLaunchKernelGGL((both_kernel<64, 128, 2, 2, 4>), dim3(unsigned(nx + nw)), dim3(256), 0, st, x, w, uint32_t(nx));
+        return hipGetLastError();
+      }
     }
-    const Out out{nullptr, nullptr, dX, nullptr, a.M, int(a.K), kActNone, false};
-    e = product(Operand{dP, ldr, a.M, false}, false, Operand{W, ldk, a.K, false}, true, R, out, partial, st, timer,
-                "linear_dx");
-    if (e != hipSuccess) return e;
   }
-  if (dW) {
-    if (a.K % 8 != 0) {
-      uint16_t* xp = reinterpret_cast<uint16_t*>(base + L.x);
-      if ((e = pad(X, a.M, a.K, xp, st, timer)) != hipSuccess) return e;
-      X = xp;
-    }
-    const Out out{nullptr, nullptr, dW, nullptr, R, int(a.K), kActNone, false};
-    e = product(Operand{dP, ldr, R, false}, true, Operand{X, ldk, a.K, false}, true, a.M, out, partial, st, timer,
-                "linear_dw");
-  }
+  if (dX && (e = product(px, false, qx, true, R, ox, partial, st, timer, "linear_dx")) != hipSuccess) return e;
+  if (dW) e = product(pw, true, qw, true, a.M, ow, partial, st, timer, "linear_dw");
   return e;
 }
 
