@@ -12,6 +12,7 @@ import ctypes
 import dataclasses
 import os
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -787,16 +788,17 @@ class AdamWBuffers:
     (bf16 or fp32, one type for all), m and v (fp32 of the parameter's size, or
     uint8 codes with a scale byte per 128 elements), optionally fp32 masters of bf16
     parameters (an entry may be None) and multipliers of the learning rate and the
-    weight decay per tensor. It holds the tensors, so that they outlive it."""
+    weight decay per tensor. It holds the tensors; the moments and masters are taken at
+    the places they have now, parameters and gradients are looked up at every step."""
 
     def __init__(self, params, m, v, m_scale=None, v_scale=None, master=None, lr_mul=None, decay_mul=None):
         n = len(params)
         none = [None] * n
-        self.params, self.m, self.v = list(params), list(m), list(v)
-        self.m_scale, self.v_scale = list(m_scale or none), list(v_scale or none)
-        self.master = list(master or none)
+        self.params, self.m, self.v = tuple(params), tuple(m), tuple(v)
+        self.m_scale, self.v_scale = tuple(m_scale or none), tuple(v_scale or none)
+        self.master = tuple(master or none)
         self.state = "f32" if m_scale is None else "8bit"
-        self.lr_mul, self.decay_mul = list(lr_mul or [1.0] * n), list(decay_mul or [1.0] * n)
+        self.lr_mul, self.decay_mul = tuple(lr_mul or [1.0] * n), tuple(decay_mul or [1.0] * n)
         for name in ("m", "v", "m_scale", "v_scale", "master", "lr_mul", "decay_mul"):
             if len(getattr(self, name)) != n:
                 raise MoEError(MOE_ERR_SHAPE, f"{n} parameters and {len(getattr(self, name))} of {name}")
@@ -820,11 +822,16 @@ class AdamWBuffers:
                     raise MoEError(MOE_ERR_SHAPE, f"{name}[{i}] is on {t.device}, param[0] on {self.device}")
         self._refuse_overlap()
         self._table = (moe_adamw_tensor * max(n, 1))()
+        self._sizes, self._at = [p.numel() for p in self.params], [p.data_ptr() for p in self.params]
         for i in range(n):
             e = self._table[i]
-            e.n, e.lr_mul, e.decay_mul = self.params[i].numel(), float(self.lr_mul[i]), float(self.decay_mul[i])
+            e.n, e.lr_mul, e.decay_mul = self._sizes[i], float(self.lr_mul[i]), float(self.decay_mul[i])
+            e.m, e.v, e.master = self.m[i].data_ptr(), self.v[i].data_ptr(), _ptr(self.master[i])
+            e.m_scale, e.v_scale = _ptr(self.m_scale[i]), _ptr(self.v_scale[i])
+        # columns of the table: param 0, grad 1, n 7
+        self._words = np.frombuffer(self._table, dtype=np.int64).reshape(-1, ctypes.sizeof(moe_adamw_tensor) // 8)
 
-    def _refuse_overlap(self, grads=()) -> None:
+    def _refuse_overlap(self) -> None:
         """No buffer that a step writes may share memory with another of its buffers."""
         spans = []
         for name in ("params", "m", "v", "m_scale", "v_scale", "master"):
@@ -855,7 +862,7 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
                grad_scale=None, hyper=None, stream=None) -> None:
     """One AdamW step on the parameters in place (see moe_adamw_step). grads: one tensor
     per parameter, bf16 or fp32, one type for all; None passes a parameter over."""
-    n = len(buf.params)
+    n, grads = len(buf.params), list(grads)
     if len(grads) != n:
         raise MoEError(MOE_ERR_SHAPE, f"{n} parameters and {len(grads)} gradients")
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
@@ -864,20 +871,30 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
     gt = next((g.dtype for g in grads if g is not None), _F32)
     if gt not in (_BF16, _F32):
         raise MoEError(MOE_ERR_SHAPE, f"gradients are {gt}, expected bf16 or fp32")
-    table = buf._table
-    for i, g in enumerate(grads):
-        e, p = table[i], buf.params[i]
-        if g is None:
-            e.n = 0
-            continue
-        k = p.numel()
-        if g.get_device() != dev or g.dtype is not gt or g.numel() != k or not g.is_contiguous():
-            _want(g, f"grads[{i}]", gt, k)
-            raise MoEError(MOE_ERR_SHAPE, f"grads[{i}] holds {g.numel()} elements on {g.device}, needs {k} on cuda:{dev}")
-        e.n, e.param, e.grad = k, p.data_ptr(), g.data_ptr()
-        e.m, e.v = buf.m[i].data_ptr(), buf.v[i].data_ptr()
-        e.m_scale, e.v_scale, e.master = _ptr(buf.m_scale[i]), _ptr(buf.v_scale[i]), _ptr(buf.master[i])
+    # all at once: a call for many small tensors is bound by these lines
+    sizes, some = buf._sizes, [g is not None for g in grads]
+    if all(some):
+        there = grads
+    else:
+        there, sizes = [g for g in grads if g is not None], [k if y else 0 for k, y in zip(sizes, some)]
+    at = [t.data_ptr() for t in buf.params]
+    # parameters where they were and as long are what was checked then
+    moved = at != buf._at or [t.numel() for t in buf.params] != buf._sizes
+    for what, have, dt in (("grads", there, gt), ("params", buf.params, buf.dtype))[:2 if moved else 1]:
+        want = [k for k, y in zip(buf._sizes, some) if y] if have is there and there is not grads else buf._sizes
+        if ([t.numel() for t in have] != want or not all([t.dtype is dt and t.is_contiguous() for t in have])
+                or any([t.get_device() != dev for t in have])):
+            for i, t in enumerate(have):
+                _want(t, f"{what}[{i}]", dt, want[i])
+                if t.numel() != want[i] or t.get_device() != dev:
+                    raise MoEError(MOE_ERR_SHAPE, f"{what}[{i}] holds {t.numel()} elements on {t.device}, needs "
+                                   f"{want[i]} on cuda:{dev}")
+    if n:
+        w = buf._words
+        w[:, 0] = buf._at = at
+        w[:, 1] = [0 if g is None else g.data_ptr() for g in grads]
+        w[:, 7] = sizes
     p = moe_adamw_params(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
                          MOE_DT["bf16"] if buf.dtype is _BF16 else MOE_DT["f32"],
                          MOE_DT["bf16"] if gt is _BF16 else MOE_DT["f32"], MOE_STATES[buf.state], int(step), 0)
-    moe_adamw_step(p, table, n, grad_scale, hyper, stream)
+    moe_adamw_step(p, buf._table, n, grad_scale, hyper, stream)

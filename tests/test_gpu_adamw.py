@@ -248,3 +248,25 @@ def test_captured_steps_follow_the_device_values(B):
         B.adamw_step(ref, [h], hyper=x, **H)
         torch.cuda.synchronize()
         assert torch.equal(p, q) and torch.equal(buf.m[0], ref.m[0]) and torch.equal(buf.v[0], ref.v[0])
+
+
+def test_parameters_that_moved(B):
+    """A parameter whose storage was exchanged is stepped where it is now, and refused where it no
+    longer fits."""
+    p, g, buf = _one(B, "f32", 400)
+    old = p.data.clone()
+    elsewhere = old.clone()
+    first = p.data
+    p.data = elsewhere
+    B.adamw_step(buf, [g], step=1, **H)
+    assert torch.equal(first, old) and not torch.equal(elsewhere, old)
+    for bad in (elsewhere[:300], elsewhere.bfloat16(), elsewhere.cpu(), torch.zeros(800, device=DEV)[::2]):
+        p.data = bad
+        with pytest.raises(B.MoEError) as ei:
+            B.adamw_step(buf, [g], step=2, **H)
+        assert ei.value.status == 2
+    p.data = elsewhere
+    for bad in (g[:300], g.bfloat16().double(), g.cpu(), torch.zeros(800, device=DEV)[::2]):
+        with pytest.raises(B.MoEError) as ei:
+            B.adamw_step(buf, [bad], step=2, **H)
+        assert ei.value.status == 2
