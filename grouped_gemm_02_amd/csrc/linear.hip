@@ -375,20 +375,27 @@ __device__ __forceinline__ void copy_out(uint16_t* buf, T* out, int ld, int rows
     }
   }
 }
-// The same inwards; what is not there is zero.
+// The same inwards, in two halves, so that the loads can be on their way early; what is not
+// there is zero.
 template <class T, int CH>
-__device__ __forceinline__ void copy_in(uint16_t* buf, const T* in, int ld, int rows, int cols) {
-  constexpr int EC = 16 / sizeof(T), RP = 64 / CH, kLoads = 32 / RP;
+__device__ __forceinline__ void copy_in_load(u32x4 (&v)[CH / 2], const T* in, int ld, int rows, int cols) {
+  constexpr int EC = 16 / sizeof(T), RP = 64 / CH;
   const int lane = fresh_lane(), c = lane % CH, r0 = lane / CH;
   const int n = min(EC, cols - EC * c);
-  u32x4 v[kLoads];
 #pragma unroll
-  for (int q = 0; q < kLoads; ++q) {
+  for (int q = 0; q < CH / 2; ++q) {
     v[q] = u32x4{0u, 0u, 0u, 0u};
     if (n == EC && r0 + q * RP < rows) v[q] = *reinterpret_cast<const u32x4u*>(in + (r0 + q * RP) * ld + EC * c);
   }
+}
+template <class T, int CH>
+__device__ __forceinline__ void copy_in_put(uint16_t* buf, const u32x4 (&v)[CH / 2], const T* in, int ld, int rows,
+                                            int cols) {
+  constexpr int EC = 16 / sizeof(T), RP = 64 / CH;
+  const int lane = fresh_lane(), c = lane % CH, r0 = lane / CH;
+  const int n = min(EC, cols - EC * c);
 #pragma unroll
-  for (int q = 0; q < kLoads; ++q) *reinterpret_cast<u32x4*>(staged(buf, CH, r0 + q * RP, c)) = v[q];
+  for (int q = 0; q < CH / 2; ++q) *reinterpret_cast<u32x4*>(staged(buf, CH, r0 + q * RP, c)) = v[q];
   if (n > 0 && n < EC) {
 #pragma unroll 1
     for (int r = r0; r < min(32, rows); r += RP)
@@ -416,6 +423,10 @@ __device__ __forceinline__ void results(const Problem& p, f32x16 (&acc)[WTM / 32
   const int64_t c0 = kIsPair ? n0 / 2 : n0;  // first result column
   const int ld = int(N), cols = int(max(int64_t(0), min(int64_t(kCols), N - c0)));
   const bool f32 = MODE == kSplit || o.f32;
+  u32x4 ahead[CH16 / 2];
+  if (MODE != kSplit && !f32 && o.residual)
+    copy_in_load<uint16_t, CH16>(ahead, static_cast<const uint16_t*>(o.residual) + m0 * N + c0, ld,
+                                 int(max(int64_t(0), min(int64_t(32), p.P.ents - m0))), cols);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int lane = fresh_lane(), row = lane & 31, up = lane >> 5;
@@ -479,9 +490,12 @@ __device__ __forceinline__ void results(const Problem& p, f32x16 (&acc)[WTM / 32
       for (int h = 0; h < kHalves; ++h) {
         constexpr int kPart = kCols / kHalves;
         const bool res = MODE != kSplit && o.residual;
-        if (res)
-          copy_in<uint32_t, CH32>(buf, static_cast<const uint32_t*>(o.residual) + at + h * kPart, ld, rows,
-                                  cols - h * kPart);
+        if (res) {
+          const uint32_t* in = static_cast<const uint32_t*>(o.residual) + at + h * kPart;
+          u32x4 x[CH32 / 2];
+          copy_in_load<uint32_t, CH32>(x, in, ld, rows, cols - h * kPart);
+          copy_in_put<uint32_t, CH32>(buf, x, in, ld, rows, cols - h * kPart);
+        }
 #pragma unroll
         for (int n = 0; n < kPart / 16; ++n) {
           float v[8];
@@ -499,7 +513,16 @@ __device__ __forceinline__ void results(const Problem& p, f32x16 (&acc)[WTM / 32
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      if (o.residual) copy_in<uint16_t, CH16>(buf, static_cast<const uint16_t*>(o.residual) + at, ld, rows, cols);
+      if (o.residual) {
+        const uint16_t* in = static_cast<const uint16_t*>(o.residual) + at;
+        copy_in_put<uint16_t, CH16>(buf, ahead, in, ld, rows, cols);
+        __builtin_amdgcn_sched_barrier(0);
+        // the next rows' part, while these are worked on
+        if (i + 1 < TM)
+          copy_in_load<uint16_t, CH16>(ahead, in + 32 * N, ld, int(max(int64_t(0), min(int64_t(32), p.P.ents - r0 - 32))),
+                                       cols);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int n = 0; n < kCols / 16; ++n) {
         float v[8];
@@ -705,15 +728,49 @@ __global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void tile_kernel(con
   walk<BM, BN, WM, WN, NS, P_MN, Q_MN, MODE>(p, blockIdx.x, gridDim.x, s0, s1, s2, s3, s_out);
 }
 
-// dX and dW at once where neither fills the CUs: the first `nx` workgroups have dX's tiles,
-// one each, the others dW's (1003 x 777 x 1001: 12 us for both instead of 11 and 12).
+// out[c] = sum over the blocks of sums[block][c], of 64 columns; no blocks: zeros
+__device__ void bias_sums(const float* __restrict__ sums, int blocks, int cols, float* __restrict__ out, int block,
+                          float (&red)[4][64]) {
+  const int lane = lane_id(), w = threadIdx.x >> 6;
+  const int c = block * 64 + lane;
+  float s = 0.f;
+  if (c < cols) {
+    int b = w;
+    for (; b + 28 < blocks; b += 32) {  // eight loads under way
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = sums[int64_t(b + 4 * i) * cols + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[i];
+    }
+    for (; b < blocks; b += 4) s += sums[int64_t(b) * cols + c];
+  }
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < cols) out[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+// What both_kernel's last workgroups add up: dbias, or nothing.
+struct BiasArgs {
+  const float* sums;
+  int blocks, cols;
+  float* out;
+};
+
+// dX and dW at once where neither fills the CUs, and dbias: the first `nx` workgroups have
+// dX's tiles, one each, the next `nw` dW's, the last dbias (1003 x 777 x 1001: 12 us for
+// the products instead of 11 and 12, and dbias's 4 us within them).
 template <int BM, int BN, int WM, int WN, int NS>
-__global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void both_kernel(const Problem x, const Problem w, uint32_t nx) {
+__global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void both_kernel(const Problem x, const Problem w, uint32_t nx,
+                                                                             uint32_t nw, const BiasArgs bias) {
   MOE_LINEAR_LDS
+  __shared__ float red[4][64];
   if (blockIdx.x < nx)
     walk<BM, BN, WM, WN, NS, false, true, kPlain>(x, blockIdx.x, nx, s0, s1, s2, s3, s_out);
+  else if (blockIdx.x < nx + nw)
+    walk<BM, BN, WM, WN, NS, true, true, kPlain>(w, blockIdx.x - nx, nw, s0, s1, s2, s3, s_out);
   else
-    walk<BM, BN, WM, WN, NS, true, true, kPlain>(w, blockIdx.x - nx, gridDim.x - nx, s0, s1, s2, s3, s_out);
+    bias_sums(bias.sums, bias.blocks, bias.cols, bias.out, int(blockIdx.x - nx - nw), red);
 }
 
 // Few rows (M <= 64): W is read once, straight into the fragments of
@@ -946,23 +1003,7 @@ __global__ __launch_bounds__(256) void before_kernel(const DpArgs d, int slopes,
 __global__ __launch_bounds__(256) void bias_kernel(const float* __restrict__ sums, int blocks, int cols,
                                                    float* __restrict__ out) {
   __shared__ float red[4][64];
-  const int lane = lane_id(), w = threadIdx.x >> 6;
-  const int c = int(blockIdx.x) * 64 + lane;
-  float s = 0.f;
-  if (c < cols) {
-    int b = w;
-    for (; b + 28 < blocks; b += 32) {  // eight loads under way
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = sums[int64_t(b + 4 * i) * cols + c];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += x[i];
-    }
-    for (; b < blocks; b += 4) s += sums[int64_t(b) * cols + c];
-  }
-  red[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && c < cols) out[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  bias_sums(sums, blocks, cols, out, int(blockIdx.x), red);
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(uint16_t* __restrict__ p, int64_t n) {
@@ -1208,27 +1249,29 @@ hipError_t launch_linear_bwd(const LinearArgs& a, const void* dY, const uint16_t
     W = wp;
     X = xp;
   }
-  if (dbias) {
-    TimedLaunch tl(timer, "linear_dbias", st);
-    hipLaunchKernelGGL(bias_kernel, dim3(unsigned(ceil_div(R, 64))), dim3(256), 0, st, d.sums, d.blocks, int(R), dbias);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   const int64_t ldr = pad8(R), ldk = pad8(a.K);
   float* partial = reinterpret_cast<float*>(base + L.partial);
   const Out ox{nullptr, nullptr, dX, nullptr, a.M, int(a.K), kActNone, false};
   const Out ow{nullptr, nullptr, dW, nullptr, R, int(a.K), kActNone, false};
   const Operand px{dP, ldr, a.M, false}, qx{W, ldk, a.K, false}, pw{dP, ldr, R, false}, qw{X, ldk, a.K, false};
+  const int64_t nb = dbias ? ceil_div(R, 64) : 0;
   if (dX && dW) {
     const Plan plx = plan_of(a.M, a.K, R), plw = plan_of(R, a.K, a.M);
     if (plx.tile == 64 && plw.tile == 64 && plx.splits == 1 && plw.splits == 1) {
       const Problem x = problem(plx, px, qx, R, ox, partial), w = problem(plw, pw, qw, a.M, ow, partial);
       const int64_t nx = int64_t(x.mt) * x.nt, nw = int64_t(w.mt) * w.nt;
-      if (nx + nw <= slots_of(64)) {
+      if (nx + nw + nb <= slots_of(64)) {
         TimedLaunch tl(timer, "linear_dx_dw", st);
-        hipLaunchKernelGGL((both_kernel<64, 128, 2, 2, 4>), dim3(unsigned(nx + nw)), dim3(256), 0, st, x, w, uint32_t(nx));
+        hipLaunchKernelGGL((both_kernel<64, 128, 2, 2, 4>), dim3(unsigned(nx + nw + nb)), dim3(256), 0, st, x, w,
+                           uint32_t(nx), uint32_t(nw), BiasArgs{d.sums, d.blocks, int(R), dbias});
         return hipGetLastError();
       }
     }
+  }
+  if (dbias) {
+    TimedLaunch tl(timer, "linear_dbias", st);
+    hipLaunchKernelGGL(bias_kernel, dim3(unsigned(nb)), dim3(256), 0, st, d.sums, d.blocks, int(R), dbias);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (dX && (e = product(px, false, qx, true, R, ox, partial, st, timer, "linear_dx")) != hipSuccess) return e;
   if (dW) e = product(pw, true, qw, true, a.M, ow, partial, st, timer, "linear_dw");
