@@ -674,8 +674,10 @@ __global__ __launch_bounds__(64 * kWaves) void bwd_kernel(GateArgs a, const int3
     total = wave_sumf(total);
     pd = wave_sumf(pd) / total;
   }
+  bool some = false;
   for (int j0 = 0; j0 < k; j0 += 64) {
     const int j = j0 + lane, ej = expert(j);
+    some |= ej >= 0;
     float val = 0.f;
     if (ej >= 0 && (dense || z[ej] != -INFINITY)) {
       const float d = dw[t * k + j], x = z[ej];
@@ -705,10 +707,11 @@ __global__ __launch_bounds__(64 * kWaves) void bwd_kernel(GateArgs a, const int3
       m = fmaxf(m, v[i]);
     }
     m = wave_maxf(m);
+    const bool none = !__any(some);  // no choice, no gradient, whatever the logits are
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       // a row of -inf alone has no probabilities; a NaN stays one
-      v[i] = v[i] == -INFINITY ? 0.f : expf(v[i] - m);
+      v[i] = none || v[i] == -INFINITY ? 0.f : expf(v[i] - m);
       sum += v[i];
       pg += v[i] * g[i];
     }
@@ -762,10 +765,13 @@ __global__ __launch_bounds__(64 * kWaves) void bwd_quick_kernel(GateArgs a, cons
       top = fmaxf(top, p[i]);
     }
     top = over_max<LPT>(top);
+    // a token without a choice has no gradient, whatever its logits are
+    const uint64_t chosen = __ballot(e >= 0) >> (lane & ~(LPT - 1));
+    const bool none = (LPT == 64 ? chosen : chosen & ((uint64_t(1) << (LPT & 63)) - 1)) == 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       // a row of -inf alone has no probabilities; a NaN stays one
-      p[i] = p[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((p[i] - top) * kLog2e);
+      p[i] = none || p[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((p[i] - top) * kLog2e);
       sum += p[i];
     }
     sum = over_sum<LPT>(sum);

@@ -254,3 +254,31 @@ def test_empty_batch(B):
     shape = B.make_shape(0, 256, 128, 8, 2)
     i, w = B.gate(shape, B.make_gate_params(), torch.empty((0, 8), device=DEV))
     assert i.shape == (0, 2) and w.shape == (0, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k", [(41, 60, 4), (30, 256, 8), (19, 600, 3), (9, 1000, 20)])
+def test_masked_rows_hold_anything(B, score, renorm, T, E, k):
+    """NaN, infinities and the type's lowest in the logits of masked tokens, NaN in their
+    gradient: they have no choice, no weight and no gradient, and the others do not notice."""
+    print(f"case masked rows T={T} E={E} k={k} {score} {renorm}", flush=True)
+    z = inputs.make_router_logits(T, E, 4, DEV, 0.5)
+    mask = (torch.arange(T, device=DEV) % 3 != 1).to(torch.uint8)
+    out = mask == 0
+    wild = z.clone()
+    for at, v in ((0, torch.nan), (1, torch.inf), (2, -torch.inf), (3, torch.finfo(torch.float32).min)):
+        wild[out, at] = v
+    wild[1] = torch.nan
+    dw = torch.randn((T, k), generator=torch.Generator().manual_seed(3)).to(DEV)
+    dw_wild = dw.clone()
+    dw_wild[out] = torch.nan
+    shape, p = B.make_shape(T, 256, 128, E, k), B.make_gate_params(score, renorm=renorm)
+    idx, w = B.gate(shape, p, z, None, mask)
+    i2, w2 = B.gate(shape, p, wild, None, mask)
+    assert torch.equal(idx, i2) and torch.equal(w, w2) and (idx[out] == -1).all() and not w[out].any()
+    d, d2 = B.gate_bwd(shape, p, z, idx, dw), B.gate_bwd(shape, p, wild, idx, dw_wild)
+    assert torch.equal(d, d2) and not d2[out].any() and torch.isfinite(d2).all()
+    acc = torch.full((T, E), 2.0, device=DEV)
+    B.gate_bwd(shape, p, wild, idx, dw_wild, acc, accumulate=True)
+    assert (acc[out] == 2).all() and torch.isfinite(acc).all()
