@@ -23,6 +23,7 @@ namespace adamw {
 constexpr int kThreads = 256;
 constexpr int kChunk = 8 * kThreads;  // elements of a workgroup
 constexpr int kMaxTensors = 48;
+constexpr uint32_t kMaxChunks = uint32_t(1) << 22;  // of a launch, which has less than 2^32 threads
 
 // Vectors at any address of their elements: a tensor begins anywhere.
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
@@ -303,8 +304,8 @@ hipError_t launch_adamw(const AdamwArgs& a, const AdamwTensor* tensors, int64_t 
           at = 0;
           if (i < count) continue;
         } else {
-          // a launch has at most 2^30 chunks; a longer tensor goes on in the next
-          const int64_t room = (int64_t(1) << 30) - b.first[b.count];
+          // a longer tensor goes on in the next launch
+          const int64_t room = int64_t(kMaxChunks) - b.first[b.count];
           const int64_t n = std::min(t.n - at, room * kChunk);
           const int64_t psz = a.param_bf16 ? 2 : 4, gsz = a.grad_bf16 ? 2 : 4, ssz = a.eight ? 1 : 4;
           Entry& e = b.e[b.count];
@@ -325,7 +326,7 @@ hipError_t launch_adamw(const AdamwArgs& a, const AdamwTensor* tensors, int64_t 
             ++i;
             at = 0;
           }
-          if (b.count < kMaxTensors && b.first[b.count] < (uint32_t(1) << 30) && i < count) continue;
+          if (b.count < kMaxTensors && b.first[b.count] < kMaxChunks && i < count) continue;
         }
       }
       if (b.count > 0) {

@@ -265,8 +265,45 @@ def test_parameters_that_moved(B):
         with pytest.raises(B.MoEError) as ei:
             B.adamw_step(buf, [g], step=2, **H)
         assert ei.value.status == 2
+    p.data = buf.m[0]
+    with pytest.raises(B.MoEError):     # over the step's own moments
+        B.adamw_step(buf, [g], step=2, **H)
     p.data = elsewhere
     for bad in (g[:300], g.bfloat16().double(), g.cpu(), torch.zeros(800, device=DEV)[::2]):
         with pytest.raises(B.MoEError) as ei:
             B.adamw_step(buf, [bad], step=2, **H)
         assert ei.value.status == 2
+
+
+def test_a_tensor_longer_than_a_launch(B):
+    """2^33 elements fill a launch; what is behind goes on in another, with the next tensor.
+    Codes, scales and offsets past 32 bits, looked at round the ends."""
+    n, more = (1 << 33) + 1000, 300
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of device memory")
+    print("case adamw 2^33 elements", flush=True)
+    at = [0, 4_000_000_000, (1 << 32) - 500, (1 << 33) - 500, n - 700]
+    P = [torch.full((s,), 0.5, dtype=torch.bfloat16, device=DEV) for s in (n, more)]
+    G = [torch.zeros(s, dtype=torch.bfloat16, device=DEV) for s in (n, more)]
+    r = torch.randn(700, generator=torch.Generator().manual_seed(5)).bfloat16().to(DEV)
+    for a in at:
+        G[0][a:a + 700] = r
+    G[1][:] = r[:more]
+    buf = B.AdamWBuffers.allocate(P, state="8bit")
+    B.adamw_step(buf, G, step=1, **H)
+    old = np.full(700, 0.5)
+    w, m, v = oa.step(old, _n(r), 0 * old, 0 * old, t=1, **H)
+    for a in at:
+        _check_w(_n(P[0][a:a + 700]), w, old, torch.bfloat16)
+    _check_w(_n(P[1]), w[:more], old[:more], torch.bfloat16)
+    # without a gradient: the decay alone, moments of zero
+    rest = P[0][100_000]
+    assert abs(float(rest) - 0.5 * (1 - H["lr"] * H["weight_decay"])) <= 2.0 ** -8 * 0.5
+    for a, b in zip(at, at[1:]):
+        assert (P[0][a + 700:b] == rest).all() and not buf.m[0][a + 700:b].any()
+    for a in at:   # a block's 128 elements share a scale; one wholly inside
+        i = -(-a // 128) * 128
+        k = slice(i - a, i - a + 128)
+        _near_code(buf.m[0][i:i + 128].cpu().numpy(), buf.m_scale[0][i // 128:i // 128 + 1].cpu().numpy(), m[k], False)
+        _near_code(buf.v[0][i:i + 128].cpu().numpy(), buf.v_scale[0][i // 128:i // 128 + 1].cpu().numpy(),
+                   np.sqrt(v[k]), True)
