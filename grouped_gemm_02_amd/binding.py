@@ -751,18 +751,18 @@ class LinearBuffers:
         mk = lambda n: torch.empty(max(n, 256), dtype=_U8, device=device)  # noqa: E731
         return cls(shape, mk(f), mk(b) if training else None)
 
-    def _of(self, X) -> moe_linear_shape:
-        s = self.shape
-        if X.shape[0] == s.M:
+    def _of(self, X, cols: int) -> moe_linear_shape:
+        s, size = self.shape, tuple(X.shape)
+        if size == (s.M, cols):
             return s
-        if X.shape[0] > s.M:
-            raise MoEError(MOE_ERR_SHAPE, f"X has {X.shape[0]} rows, the buffers are for {s.M}")
-        return moe_linear_shape(X.shape[0], s.N, s.K, s.act, s.out_dtype, 0)
+        if len(size) != 2 or size[1] != cols or size[0] > s.M:
+            raise MoEError(MOE_ERR_SHAPE, f"rows are {list(size)}, the buffers are for up to {s.M} of {cols}")
+        return moe_linear_shape(size[0], s.N, s.K, s.act, s.out_dtype, 0)
 
 
 def linear(buf: LinearBuffers, X, W, bias=None, residual=None, Y=None, pre=None, stream=None):
     """act(X W^T + bias) + residual for the rows X has (see moe_linear)."""
-    s = buf._of(X)
+    s = buf._of(X, buf.shape.K)
     if Y is None:
         Y = _result(stream, (s.M, s.N), _BF16 if s.out_dtype == 0 else _F32, X.device)
     moe_linear(s, X, W, bias, residual, Y, pre, buf.fwd_ws, stream)
@@ -773,7 +773,7 @@ def linear_bwd(buf: LinearBuffers, dY, X, W, pre=None, bias=False, dX=None, dW=N
                need_dW=True, stream=None):
     """(dX, dW, dbias) of linear; dbias is None unless `bias` (or a dbias) is
     given, dX and dW are None where they are not needed."""
-    s, dev = buf._of(dY), dY.device
+    s, dev = buf._of(dY, buf.shape.N), dY.device
     R = linear_rows(s)
     if dX is None and need_dX:
         dX = _result(stream, (s.M, s.K), _BF16, dev)
@@ -891,6 +891,8 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
                 if t.numel() != want[i] or t.get_device() != dev:
                     raise MoEError(MOE_ERR_SHAPE, f"{what}[{i}] holds {t.numel()} elements on {t.device}, needs "
                                    f"{want[i]} on cuda:{dev}")
+    if moved:
+        buf._refuse_overlap()
     if n:
         w = buf._words
         w[:, 0] = buf._at = at

@@ -335,7 +335,8 @@ moe_status moe_gate(const moe_shape* s, const moe_gate_params* p, const float* l
  * accumulate != 0 it is added to what d_logits holds, otherwise every element is
  * written. The choice is piecewise constant and passes no gradient (the bias has
  * none). Slots with an id outside [0, E) pass none and are no part of the
- * renormalisation; an expert named twice by one token takes the sum of both slots.
+ * renormalisation; an expert named twice by one token takes the sum of both slots. A
+ * token without such a slot (masked out) has no gradient, whatever its logits hold.
  *   sigmoid:          scale d_topk_w s (1 - s)
  *   sigmoid, renorm:  scale p (1 - s) (d_topk_w - <p, d_topk_w>), p = s / sum of the chosen
  *   softmax, renorm:  scale p (d_topk_w - <p, d_topk_w>)
@@ -564,7 +565,8 @@ moe_status moe_muon_step(const moe_ortho_shape* s, const moe_muon_params* p, con
  * and pre. Results are deterministic, but the sums' order goes with M, N and K. With
  * M == 0 nothing is done. Rows of any length; every pointer 16-byte aligned. Limits:
  * 0 <= M <= 2^24, 1 <= N, K, N' and K <= 2^20, M K < 2^36, M N' < 2^36, and N' times
- * K rounded up to 8 at most 2^30. Calls that share `ws` must not overlap. */
+ * K rounded up to 8 at most 2^30. Calls that share `ws` must not overlap, and what is
+ * written overlaps nothing else of the call (but Y its residual). */
 typedef enum moe_act {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,

@@ -264,3 +264,20 @@ def test_captured_and_on_other_streams(B, M, N, K):
             torch.cuda.synchronize()
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+def test_rows_of_another_shape_are_refused(B):
+    """Rows in three dimensions or of another length are no batch of fewer rows."""
+    M, N, K = 24, 40, 16
+    buf = B.LinearBuffers.allocate(B.make_linear_shape(M, N, K))
+    W = torch.ones((N, K), dtype=torch.bfloat16, device=DEV)
+    mk = lambda *s: torch.ones(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    for X in (mk(2, 12, K), mk(M * K), mk(12, 2 * K), mk(K, M), mk(M + 1, K)):
+        with pytest.raises(B.MoEError) as ei:
+            B.linear(buf, X, W)
+        assert ei.value.status == 2
+    for dY in (mk(2, 12, N), mk(M * N), mk(12, 2 * N), mk(M + 1, N)):
+        with pytest.raises(B.MoEError) as ei:
+            B.linear_bwd(buf, dY, mk(M, K), W)
+        assert ei.value.status == 2
+    assert B.linear(buf, mk(3, K), W).shape == (3, N)
