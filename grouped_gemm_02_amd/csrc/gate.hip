@@ -481,13 +481,19 @@ __global__ __launch_bounds__(64 * kWaves, SLOW <= 2 ? 5 : SLOW <= 4 ? 4 : 2) voi
     const float close = a.bias ? 2.f * error * scale + 1.f : 0.f;
     odd |= !(close < 0x1p+22f);
     const uint32_t near = uint32_t(fminf(close, 0x1p+22f));
+    // (the shift is rounded alike for all; where it is off by much the first keys meet at the
+    // top and are taken again)
+    const float shift = fmaf(-top, scale, kTop);
     uint32_t s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float h = fmaxf((c[i] - top) * scale + kTop, 0.f);
-      s[i] = (uint32_t(h) << IB) | uint32_t(LPT * V - 1 - e0 - i);
+      const float h = __builtin_amdgcn_fmed3f(fmaf(c[i], scale, shift), 0.f, kTop);
+      s[i] = (uint32_t(h) << IB) | uint32_t(V - 1 - i);
     }
     largest_down<D>(s);
+    // the id's other bits, which the lane's experts share
+#pragma unroll
+    for (int i = 0; i < D; ++i) s[i] |= uint32_t((LPT - 1 - l) * V);
 
     if (a.groups > 1) {
       // the group's two largest keys in each of its lanes
