@@ -43,6 +43,12 @@ __device__ __forceinline__ void wave_argmaxd(double& v, int& id) {
   }
 }
 
+// 1 / (1 + e^-x), 0 of -inf
+__device__ __forceinline__ double sigmoid64(float x) {
+  const double q = exp(-fabs(double(x)));
+  return x == -INFINITY ? 0.0 : (x >= 0.f ? 1.0 : q) / (1.0 + q);
+}
+
 // The wave's token in 64 bits throughout: writes its k ids and weights. SLOTS: k / 64,
 // rounded up (as PER is for E).
 template <int PER, int SLOTS>
@@ -86,9 +92,7 @@ __device__ __forceinline__ void choose_token(const GateArgs& a, int64_t t, int32
   // s of a logit (0 of -inf); computed where it is needed, which takes fewer registers
   auto score = [&](float x) {
     if (x == -INFINITY) return 0.0;
-    if (!a.sigmoid) return exp(double(x) - double(m)) / sum;
-    const double q = exp(-fabs(double(x)));
-    return (x >= 0.f ? 1.0 : q) / (1.0 + q);
+    return a.sigmoid ? sigmoid64(x) : exp(double(x) - double(m)) / sum;
   };
   if (!a.sigmoid) {
     double part = 0.0;
@@ -233,10 +237,12 @@ __global__ __launch_bounds__(64 * kWaves) void choose_kernel(GateArgs a, int32_t
 // over the row's range) above the expert's id, so that keys are different, their order
 // needs no second comparison, and a lane sorts its own with min and max. A round of the
 // choice takes the largest of the lanes' first keys (DPP) and moves its lane's list up.
-// Where two keys that have to be told apart are closer than twice the error, where
-// something is not finite, and where a group has too few experts, the wave takes the
-// token again in 64 bits; the ids are those of 64 bits always. Logits themselves (no
-// bias) map to keys in their order, so there only equal keys are taken again.
+// Where two keys of the choice are closer than twice the error, what they stand for is
+// computed in 64 bits and put in order (softmax scores with a bias need the whole row for
+// that); where that does not settle it, where groups are too close, where something is
+// not finite and where a group has too few experts, the wave takes the token again in 64
+// bits. The ids are those of 64 bits always. Logits themselves (no bias) map to keys in
+// their order, so there only equal keys are too close.
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -402,6 +408,7 @@ __global__ __launch_bounds__(64 * kWaves, SLOW <= 2 ? 5 : SLOW <= 4 ? 4 : 2) voi
 #pragma unroll
   for (int i = 0; i < V; ++i) bad_bias |= !(bias[i] < INFINITY);
   const bool spoilt = __any(bad_bias);
+  const bool few = (a.sigmoid || !a.bias) && k < 16;  // close keys are told apart by themselves
   float c[V], zn[V];  // a batch's logits, then what the choice goes by; the next one's logits
   bool live_token, next_live;  // there, and not masked
   auto fetch = [&](int64_t t0, float (&x)[V], bool& live) {
@@ -553,10 +560,38 @@ __global__ __launch_bounds__(64 * kWaves, SLOW <= 2 ? 5 : SLOW <= 4 ? 4 : 2) voi
     if (l == k - 1) follow = next;
     // (a key of 0 where one is wanted: all that is left is off, or below the window)
     const uint32_t hm = mine >> IB, hf = follow >> IB;
-    odd |= l < k && hm - hf <= near;
+    bool tight = l < k && hm - hf <= near;
+    odd |= tight && (!few || hf == 0u);
+    tight &= few && live_token;
+    if (__any(tight)) {
+      // Whatever else there is is below these k keys, or below the next one too where that is
+      // as close: their order in 64 bits is all that is missing.
+      const uint32_t after = over_umax<LPT>(s[0]);
+      odd |= tight && l == k - 1 && (next >> IB) - (after >> IB) <= near;
+      const int base = lane & ~(LPT - 1);
+      const uint32_t key = l == k ? next : mine;
+      const int id = LPT * V - 1 - int(key & uint32_t(LPT * V - 1));
+      double value = -__builtin_inf();
+      if (l <= k && (key >> IB) != 0u) {
+        const float x = a.logits[t * E + id];
+        value = a.bias ? sigmoid64(x) + double(a.bias[id]) : double(x);
+      }
+      int rank = 0;
+      for (int j = 0; j <= k; ++j) {
+        const double o = __shfl(value, base + j);
+        const int oi = __shfl(id, base + j);
+        rank += o > value || (o == value && oi < id) ? 1 : 0;
+      }
+      int from = l;
+      for (int j = 0; j <= k; ++j)
+        if (__shfl(l <= k ? rank : -1, base + j) == l) from = j;
+      const uint32_t sorted = __shfl(key, base + from);
+      const uint64_t mark = __ballot(tight) >> base;
+      if (l < k && (LPT == 64 ? mark : mark & ((uint64_t(1) << (LPT & 63)) - 1)) != 0) mine = sorted;
+    }
 
     const int e = LPT * V - 1 - int(mine & uint32_t(LPT * V - 1));
-    const bool some = l < k && hm != 0u;
+    const bool some = l < k && (mine >> IB) != 0u;
     const float x = some ? a.logits[t * E + e] : -INFINITY;
     float v = 0.f;
     if (!a.sigmoid) {
@@ -615,7 +650,7 @@ bool launch_quick(const GateArgs& a, int32_t* idx, float* w, hipStream_t st) {
   constexpr int TPW = 64 / LPT;
   // several batches a wave where there are many: the next one's logits come meanwhile
   const int64_t waves = (a.T + TPW - 1) / TPW;
-  const int batches = int(waves >= 16384 ? 4 : 1);
+  const int batches = int(waves >= 16384 ? 2 : 1);
   const int64_t blocks = (waves + int64_t(batches) * kWaves - 1) / (int64_t(batches) * kWaves);
   hipLaunchKernelGGL((choose_quick_kernel<LPT, V, D, SLOW>), dim3(unsigned(blocks)), dim3(64 * kWaves), 0, st, a,
                      batches, lanes, idx, w);
