@@ -215,7 +215,7 @@ def _here(stream, *wanted) -> list:
     """_want for each (tensor, name, dtype, numel), and the tensor must be on the
     current device, whose stream the call is enqueued on. Returns their
     addresses and the stream's handle."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None  # without it there is no GPU tensor
+    dev = _current_device() if torch.cuda.is_initialized() else None  # without it there is no GPU tensor
     at = []
     for t, name, dtype, numel in wanted:
         if t is None or type(t) is int:
@@ -236,6 +236,9 @@ _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 # Stream object, where this torch has it.
 _current_handle = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                    or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream) -> int | None:
@@ -719,22 +722,28 @@ def muon_step(buf: OrthoBuffers, grad, momentum, W, *, lr, momentum_coef=0.95, w
 def gate(shape: moe_shape, params: moe_gate_params, logits, bias=None, mask=None, topk_idx=None, topk_w=None,
          stream=None):
     """(topk_idx, topk_w) of the experts chosen for each token (see moe_gate)."""
-    if topk_idx is None:
+    i, w = topk_idx, topk_w
+    # (addresses of results made here need no checks)
+    if i is None:
         topk_idx = _result(stream, (shape.T, shape.k), _I32, logits.device)
-    if topk_w is None:
+        i = topk_idx.data_ptr()
+    if w is None:
         topk_w = _result(stream, (shape.T, shape.k), _F32, logits.device)
-    moe_gate(shape, params, logits, bias, mask, topk_idx, topk_w, stream)
+        w = topk_w.data_ptr()
+    moe_gate(shape, params, logits, bias, mask, i, w, stream)
     return topk_idx, topk_w
 
 
 def gate_bwd(shape: moe_shape, params: moe_gate_params, logits, topk_idx, d_topk_w, d_logits=None, accumulate=False,
              stream=None):
     """d_logits of the chosen weights' gradient; accumulate adds to the d_logits given."""
-    if d_logits is None:
+    d = d_logits
+    if d is None:
         if accumulate:
             raise MoEError(MOE_ERR_SHAPE, "accumulate needs a d_logits to add to")
         d_logits = _result(stream, (shape.T, shape.E), _F32, logits.device)
-    moe_gate_bwd(shape, params, logits, topk_idx, d_topk_w, accumulate, d_logits, stream)
+        d = d_logits.data_ptr()
+    moe_gate_bwd(shape, params, logits, topk_idx, d_topk_w, accumulate, d, stream)
     return d_logits
 
 
@@ -763,9 +772,11 @@ class LinearBuffers:
 def linear(buf: LinearBuffers, X, W, bias=None, residual=None, Y=None, pre=None, stream=None):
     """act(X W^T + bias) + residual for the rows X has (see moe_linear)."""
     s = buf._of(X, buf.shape.K)
-    if Y is None:
+    y = Y
+    if y is None:
         Y = _result(stream, (s.M, s.N), _BF16 if s.out_dtype == 0 else _F32, X.device)
-    moe_linear(s, X, W, bias, residual, Y, pre, buf.fwd_ws, stream)
+        y = Y.data_ptr()
+    moe_linear(s, X, W, bias, residual, y, pre, buf.fwd_ws, stream)
     return Y
 
 
@@ -867,7 +878,7 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
     n, grads = len(buf.params), list(grads)
     if len(grads) != n:
         raise MoEError(MOE_ERR_SHAPE, f"{n} parameters and {len(grads)} gradients")
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    dev = _current_device() if torch.cuda.is_initialized() else None
     if n and buf.device.type == "cuda" and buf.device.index != dev:
         raise MoEError(MOE_ERR_SHAPE, f"the parameters are on {buf.device}, the current device is cuda:{dev}")
     gt = next((g.dtype for g in grads if g is not None), _F32)
