@@ -6,16 +6,25 @@
 //   forward  P = X, Q = W                    both with k along their rows (k-major)
 //   dX       P = dP, Q = W^T                 W has one memory row per k (mn-major)
 //   dW       P = dP^T, Q = X^T               both mn-major, k the token
-// Tiles of BM x BN, slabs of 64 k staged in LDS in two stages by loads that go there
-// directly (buffer_load ... lds): while one slab is multiplied the next one is on its
-// way. Waves take 32 x 32 sub-tiles with v_mfma_f32_32x32x16_bf16, Q's fragment as the A
-// operand, so that a lane holds one row m and runs of four columns n.
+// Tiles of BM x BN, slabs of 64 k staged in LDS by loads that go there directly
+// (buffer_load ... lds), sent for as many slabs ahead as there are stages: 256 x 256 by
+// eight waves with two stages (128 KiB, one workgroup a CU), 128 x 128 by four with two, 64 x
+// 128 by four with four. Waves take 32 x 32 sub-tiles with v_mfma_f32_32x32x16_bf16, Q's
+// fragment as the A operand, so that a lane holds one row m and runs of four columns n.
 //   k-major operand in LDS: rows of 64 k, 16-byte chunk c of row r at slot c ^ (r / 2) % 8:
 //     fragment reads (16 rows, one chunk) then touch 16 different bank groups.
 //   mn-major operand: k-rows of the tile's entities, chunk c of k-row k at slot
 //     c ^ 4 (k % 4) (64 entities: c ^ 4 ((k / 2) % 2)); a fragment comes from two
 //     transpose reads (ds_read_b64_tr_b16), whose 16 (row, chunk) pairs lie in
 //     different bank groups.
+// Measured: 16384 x 4096 x 1536 186 us (1.11 PFLOP/s; a library product of that size takes
+// 153 to 164), with a residual 193, with operands and results that come from HBM and not from the
+// last-level cache 215 to 230. A slab of a 256 x 256 tile takes 1.5 us, the MFMAs alone would
+// 0.86 (they are busy 46 % of the cycles): the fragments' reads and the slabs' arrival
+// take the LDS as long as the products take the MFMAs, and the next slab is all that fits
+// beside the one at work. Lines fetched into L2 a slab earlier made it slower (206 us), as
+// did tiles whose results wait for memory one after the other. Waves of 128 x 128, which
+// would read a third less from LDS, need all 512 registers, and the compiler spilled.
 // Rows and columns past the matrix are read from a valid row or as zeros and not
 // stored; k past the end is zero in both operands. Rows that are no multiple of 16 bytes
 // are first copied to rows that are.
@@ -544,10 +553,10 @@ __device__ __forceinline__ void results(const Problem& p, f32x16 (&acc)[WTM / 32
 }
 
 // A persistent walk: workgroup b takes the tiles b, b + grid, ... The slabs of all of
-// them are one stream, sent for two slabs ahead, across the tiles' ends too: results leave
+// them are one stream, sent for NS slabs ahead, across the tiles' ends too: results leave
 // through LDS of each wave's own, so the next tile's slabs are on their way meanwhile. The
-// number of a tile's slabs is made even (the last may be zeros), so that a stage is known
-// at compile time.
+// number of a tile's slabs is made a multiple of NS (the last may be zeros), so that a stage
+// is known at compile time.
 // NS: stages, that is how many slabs ahead are sent for. s0 .. s3: the stages' LDS; out: 32
 // rows of each wave's results, WTN / 8 chunks of 16 bytes a row, chunk c at slot c ^ row.
 template <int BM, int BN, int WM, int WN, int NS, bool P_MN, bool Q_MN, int MODE>
@@ -773,11 +782,12 @@ __global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void both_kernel(con
     bias_sums(bias.sums, bias.blocks, bias.cols, bias.out, int(blockIdx.x - nx - nw), red);
 }
 
-// Few rows (M <= 64): W is read once, straight into the fragments of
+// Few rows (M <= 32): W is read once, straight into the fragments of
 // v_mfma_f32_16x16x32_bf16, and nothing waits for anything but its own loads. A workgroup
 // has 16 rows of W (a pair's: 8 gate rows and their 8 up rows); its waves take turns at
 // units of 64 k (a 128-byte line of each row), the sums meet in LDS. X comes from the
-// caches. MT: fragments of 16 rows of X.
+// caches. MT: fragments of 16 rows of X. One token, 1536 rows of 2048 (SwiGLU): 7.4 us,
+// most of it latency (a launch takes 2.7, the 6.3 MB of W 1.3 at the memory's rate).
 constexpr int kFewWaves = 8;
 constexpr int kFewUnits = 4;  // of a wave in flight
 
@@ -848,7 +858,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const uint16_t
 }
 
 // The parts of a split product added in their order, and on through the epilogue. A
-// paired product's columns stand in the order its tiles have them.
+// paired product's columns stand in the order its tiles have them. Five parts of 1536 x 2048:
+// 13 us (69 MB, mostly from the last-level cache).
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, int splits, int64_t ldp, bool pair,
                                                    Out o) {
   const int per = (o.N + 7) / 8;
@@ -989,7 +1000,8 @@ __device__ void slope_rows(const DpArgs& a, int block, float (&red)[8][256]) {
 }
 
 // What has to be done before the products, in one launch: dP, and rows made a multiple of
-// 16 bytes.
+// 16 bytes. 16384 x 768 SwiGLU: 29 us for 126 MB (4.3 TB/s); 1003 x 777 with X and W of
+// 1001 columns: 8.4 us, latency and launch.
 __global__ __launch_bounds__(256) void before_kernel(const DpArgs d, int slopes, const PadJob a, const PadJob b) {
   __shared__ float red[8][256];
   int block = int(blockIdx.x);
@@ -1137,10 +1149,13 @@ constexpr size_t kAlign = 256;
 size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 constexpr int64_t kDpRows = 16, kDpBlocks = 256;
-// rows of a block of dp_kernel: no more than kDpBlocks blocks
+// rows of a block of slope_rows: no more than kDpBlocks blocks
 int64_t dp_rows(int64_t M) { return std::max<int64_t>(kDpRows, ceil_div(M, kDpBlocks)); }
 
-constexpr int64_t kFewRows = 64;
+// Rows that few_rows_kernel takes: whole calls of 1, 32 and 48 rows take 7.6, 10.7 and 12.8 us in
+// it for N' = 1536, K = 2048 (SwiGLU) and 12.7, 13.8, 14.1 in tiles; for 4096 x 4096 9.3, 15.5, 20.2
+// and 15.5, 15.9, 16.3; for 1001 x 777 8.1, 12.1, 16.4 and 14.3, 14.8, 14.9.
+constexpr int64_t kFewRows = 32;
 
 struct Layout {
   size_t x, w, dp, sums, partial, total;
@@ -1182,7 +1197,7 @@ hipError_t launch_linear(const LinearArgs& a, const uint16_t* X, const uint16_t*
     TimedLaunch tl(timer, "linear_few", st);
     const bool pair = a.act == kActSwiglu;
     const dim3 grid(unsigned(ceil_div(a.N, pair ? 8 : 16))), block(64 * kFewWaves);
-    auto kernel = a.M <= 16 ? few_rows_kernel<1> : a.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
+    auto kernel = a.M <= 16 ? few_rows_kernel<1> : few_rows_kernel<2>;
     hipLaunchKernelGGL(kernel, grid, block, 0, st, X, W, int(a.M), int(a.K), pair, out);
     return hipGetLastError();
   }

@@ -282,3 +282,30 @@ def test_masked_rows_hold_anything(B, score, renorm, T, E, k):
     acc = torch.full((T, E), 2.0, device=DEV)
     B.gate_bwd(shape, p, wild, idx, dw_wild, acc, accumulate=True)
     assert (acc[out] == 2).all() and torch.isfinite(acc).all()
+
+
+def test_offsets_past_32_bits(B):
+    """Logits of more than 2^31 elements: tokens at the ends and round the border against the oracle."""
+    T, E, k = 2_200_001, 1024, 3
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    print("case gate past 32 bits", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    z = torch.empty((T, E), device=DEV)
+    for at in range(0, T, 200_000):
+        z[at:at + 200_000] = torch.randn(z[at:at + 200_000].shape, generator=g, device=DEV)
+    border = (1 << 31) // E
+    rows = torch.tensor([0, 1, border // 2, border - 1, border, border + 1, T - 2, T - 1], device=DEV)
+    shape = B.make_shape(T, 256, 128, E, k)
+    for score, renorm in (("sigmoid", True), ("softmax", False)):
+        p, b = B.make_gate_params(score, renorm=renorm), _bias(E, 3, 0.2 if score == "sigmoid" else 0.5 / E)
+        idx, w = B.gate(shape, p, z, b)
+        zr = z[rows].cpu().numpy()
+        ri, rw = og.choose(zr, k, score, renorm, b.cpu().numpy())
+        assert np.array_equal(idx[rows].cpu().numpy(), ri)
+        assert np.all(np.abs(w[rows].cpu().numpy() - rw) <= TOL * rw.max(1, keepdims=True))
+        dw = torch.randn((T, k), generator=g, device=DEV)
+        d = B.gate_bwd(shape, p, z, idx, dw)
+        _compare_bwd(d[rows].cpu().numpy(), og.choose_backward(zr, ri, dw[rows].cpu().numpy(), score, renorm),
+                     dw[rows].cpu().numpy(), 1.0)
+        del d

@@ -281,3 +281,51 @@ def test_rows_of_another_shape_are_refused(B):
             B.linear_bwd(buf, dY, mk(M, K), W)
         assert ei.value.status == 2
     assert B.linear(buf, mk(3, K), W).shape == (3, N)
+
+
+def test_offsets_past_32_bits(B):
+    """Results and operands of more than 2^31 elements: rows at the ends, round the border and
+    between them against the oracle, the row behind them left alone."""
+    M, L, S = 600_001, 4096, 64
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    print("case linear past 32 bits", flush=True)
+    border = (1 << 31) // L
+    rows = torch.tensor([0, 1, border // 2, border - 1, border, border + 1, M - 2, M - 1], device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    n = lambda *sz: torch.randn(sz, generator=g, device=DEV)  # noqa: E731
+    # a long row out, a residual in place
+    X, W, b = n(M, S).bfloat16(), (n(L, S) / 8).bfloat16(), n(L)
+    Y = torch.empty((M + 1, L), dtype=torch.bfloat16, device=DEV)
+    for at in range(0, M + 1, 50_000):
+        Y[at:at + 50_000] = n(*Y[at:at + 50_000].shape).bfloat16()
+    old, behind = Y[rows].clone(), Y[M].clone()
+    buf = B.LinearBuffers.allocate(B.make_linear_shape(M, L, S))
+    B.linear(buf, X, W, b, Y[:M], Y=Y[:M])
+    want, _ = ol.linear(_n(X[rows]), _n(W), _n(b), _n(old))
+    e = (S + 4) * 2.0 ** -24 * (np.abs(_n(X[rows])) @ np.abs(_n(W)).T + np.abs(_n(b)) + np.abs(_n(old)))
+    assert np.all(np.abs(_n(Y[rows]) - want) <= e + 2.0 ** -8 * (np.abs(want) + e))
+    assert torch.equal(Y[M], behind)
+    # backwards from such rows: dX from dY of that size, dW and dbias over all of them
+    dY = Y[:M]
+    dX, dW, db = B.linear_bwd(buf, dY, X, W, bias=True)
+    w = _n(dY[rows]) @ _n(W)
+    e = (L + 2) * 2.0 ** -24 * (np.abs(_n(dY[rows])) @ np.abs(_n(W)))
+    assert np.all(np.abs(_n(dX[rows]) - w) <= e + 2.0 ** -8 * (np.abs(w) + e))
+    cols = torch.tensor([0, 1, L // 2, L - 1], device=DEV)
+    d = torch.cat([dY[at:at + 50_000, cols].double() for at in range(0, M, 50_000)]).cpu().numpy()
+    x = _n(X)
+    e = (M + 2) * 2.0 ** -24 * (np.abs(d).T @ np.abs(x))
+    w = d.T @ x
+    assert np.all(np.abs(_n(dW[cols]) - w) <= e + 2.0 ** -8 * (np.abs(w) + e))
+    assert np.all(np.abs(_n(db[cols]) - d.sum(0)) <= (M + 2) * 2.0 ** -24 * np.abs(d).sum(0))
+    # and long rows in, of an odd length (they are copied first)
+    del Y, dY, dX
+    buf = B.LinearBuffers.allocate(B.make_linear_shape(M, S, L - 3, act="relu"), training=False)
+    X, W = torch.empty((M, L - 3), dtype=torch.bfloat16, device=DEV), (n(S, L - 3) / 64).bfloat16()
+    for at in range(0, M, 50_000):
+        X[at:at + 50_000] = n(*X[at:at + 50_000].shape).bfloat16()
+    Y = B.linear(buf, X, W)
+    want, _ = ol.linear(_n(X[rows]), _n(W), act="relu")
+    e = (L + 2) * 2.0 ** -24 * (np.abs(_n(X[rows])) @ np.abs(_n(W)).T)
+    assert np.all(np.abs(_n(Y[rows]) - want) <= e + 2.0 ** -8 * (np.abs(want) + e))
