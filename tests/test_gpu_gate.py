@@ -309,3 +309,34 @@ def test_offsets_past_32_bits(B):
         _compare_bwd(d[rows].cpu().numpy(), og.choose_backward(zr, ri, dw[rows].cpu().numpy(), score, renorm),
                      dw[rows].cpu().numpy(), 1.0)
         del d
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,L,top", [(128, 8, 1, 1, 1), (256, 8, 8, 4, 2), (60, 4, 1, 1, 1), (512, 15, 1, 1, 1), (512, 16, 1, 1, 1),
+                                         (1000, 6, 1, 1, 1), (16, 1, 1, 1, 1), (16, 15, 1, 1, 1), (16, 16, 1, 1, 1),
+                                         (256, 8, 8, 2, 1)])
+def test_close_pairs_among_spread_scores(B, score, E, k, G, L, top):
+    """Well spread rows in which two, three or more of the best k + 3 are equal or a unit or two
+    apart, inside the choice, across its end and behind it; biases of few values, so that
+    some such pairs stay close and some do not."""
+    T = 600
+    r = np.random.default_rng(E + k)
+    z = (1.5 * r.standard_normal((T, E))).astype(np.float32)
+    order = np.argsort(-z, axis=1)
+    for t in range(T):
+        best = order[t, :min(E, k + 3)]
+        n = len(best)
+        for _ in range(r.integers(1, 4)):
+            at, size = r.integers(0, n), r.integers(2, 5)
+            run = best[at:at + size]
+            v = z[t, run[0]]
+            for e in run[1:]:
+                z[t, e] = v
+                for _ in range(r.integers(0, 3)):
+                    z[t, e] = np.nextafter(z[t, e], np.float32(-10 if r.random() < 0.5 else 10))
+    z = torch.from_numpy(z).to(DEV)
+    coarse = (torch.arange(E, device=DEV) % 3).float() * 0.03125
+    _check(B, z, k, score, True, None, G, L, top)
+    _check(B, z, k, score, True, torch.zeros(E, device=DEV), G, L, top)
+    _check(B, z, k, score, False, coarse, G, L, top)
+    _check(B, z, k, score, True, coarse + _bias(E, 1, 1e-7), G, L, top)
