@@ -1001,7 +1001,7 @@ __device__ void slope_rows(const DpArgs& a, int block, float (&red)[8][256]) {
 
 // What has to be done before the products, in one launch: dP, and rows made a multiple of
 // 16 bytes. 16384 x 768 SwiGLU: 29 us for 126 MB (4.3 TB/s); 1003 x 777 with X and W of
-// 1001 columns: 8.4 us, latency and launch.
+// 1001 columns: 6.7 us, latency and launch (9.5 with 16 rows a block).
 __global__ __launch_bounds__(256) void before_kernel(const DpArgs d, int slopes, const PadJob a, const PadJob b) {
   __shared__ float red[8][256];
   int block = int(blockIdx.x);
@@ -1148,7 +1148,7 @@ hipError_t before(const DpArgs& d, bool slopes, const PadJob& a, const PadJob& b
 constexpr size_t kAlign = 256;
 size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
-constexpr int64_t kDpRows = 16, kDpBlocks = 256;
+constexpr int64_t kDpRows = 8, kDpBlocks = 256;
 // rows of a block of slope_rows: no more than kDpBlocks blocks
 int64_t dp_rows(int64_t M) { return std::max<int64_t>(kDpRows, ceil_div(M, kDpBlocks)); }
 
