@@ -329,3 +329,37 @@ def test_offsets_past_32_bits(B):
     want, _ = ol.linear(_n(X[rows]), _n(W), act="relu")
     e = (L + 2) * 2.0 ** -24 * (np.abs(_n(X[rows])) @ np.abs(_n(W)).T)
     assert np.all(np.abs(_n(Y[rows]) - want) <= e + 2.0 ** -8 * (np.abs(want) + e))
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 640, 4096), (1003, 257, 1001), (3000, 96, 203)])   # parts, copies, both
+def test_two_graphs_share_a_scratch(B, M, N, K):
+    """Two captured passes over one scratch, replayed in turn and between eager calls on it, with
+    inputs that change: nothing is left in it that a later call relies on."""
+    print(f"case two graphs, one scratch {M} {N} {K}", flush=True)
+    buf = B.LinearBuffers.allocate(B.make_linear_shape(M, N, K, act="silu"))
+    own = B.LinearBuffers.allocate(B.make_linear_shape(M, N, K, act="silu"))
+    sets = []
+    for s, rows in ((1, M), (2, M // 2 + 1)):
+        r = _rand(s)
+        sets.append([r(rows, K).bfloat16().to(DEV), (r(N, K) / K ** 0.5).bfloat16().to(DEV), r(rows, N).bfloat16().to(DEV),
+                     r(rows, N).bfloat16().to(DEV)])
+    both = lambda b, X, W, dY, P: [B.linear(b, X, W)] + list(B.linear_bwd(b, dY, X, W, P, bias=True))  # noqa: E731
+    both(buf, *sets[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for a in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = both(buf, *a)
+        graphs.append((g, out))
+    for _ in range(3):
+        for a in sets:
+            for t in a:
+                t.copy_(t.roll(1, 0))
+        for i in (0, 1, 0):
+            graphs[i][0].replay()
+        both(buf, *sets[1])
+        torch.cuda.synchronize()
+        for (_, out), a in zip(graphs, sets):
+            for x, y in zip(out, both(own, *a)):
+                assert torch.equal(x, y)
