@@ -958,8 +958,10 @@ __device__ void slope_rows(const DpArgs& a, int block, float (&red)[8][256]) {
         if (a.act == kActRelu) {
           o[i] = g[i] > 0.f ? d[i] : (g[i] != g[i] ? g[i] : 0.f);
         } else if (a.act == kActGelu) {
-          const float s = gelu_gate(g[i]);
-          o[i] = d[i] * (s + g[i] * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * g[i] * g[i]));
+          // far from 0 the gate is 0 or 1 and constant, and g^2 may be past fp32's range
+          const float s = gelu_gate(g[i]), q = s * (1.f - s);
+          const float bend = q == 0.f ? 0.f : g[i] * q * 1.5957691216057308f * (1.f + 0.134145f * g[i] * g[i]);
+          o[i] = d[i] * (s + bend);
         } else if (a.act == kActSilu || pair) {
           const float s = sigmoid(g[i]);
           const float slope = s * (1.f + g[i] * (1.f - s));
