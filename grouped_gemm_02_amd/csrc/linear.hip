@@ -965,8 +965,10 @@ __device__ void slope_rows(const DpArgs& a, int block, float (&red)[8][256]) {
         } else if (a.act == kActSilu || pair) {
           const float s = sigmoid(g[i]);
           const float slope = s * (1.f + g[i] * (1.f - s));
-          o[i] = pair ? d[i] * u[i] * slope : d[i] * slope;
-          if (pair) up[i] = d[i] * g[i] * s;
+          // what may be 0 first: d u and d g may be past fp32's range where dP is not. (The
+          // slope is up to 1.1, so half of it: u slope stays in the range)
+          o[i] = pair ? u[i] * (0.5f * slope) * d[i] * 2.f : d[i] * slope;
+          if (pair) up[i] = g[i] * s * d[i];
         }
         sv[i] += o[i];
         su[i] += up[i];

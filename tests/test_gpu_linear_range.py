@@ -69,3 +69,32 @@ def test_slopes_of_finite_p(B, act, out):
     assert np.all(np.abs(_n(rows) - want) <= e + 2.0 ** -24 * np.abs(want))
     assert np.all(np.abs(_n(dX) - want) <= e + 2.0 ** -8 * (np.abs(want) + e))
     assert np.all(np.abs(_n(db) - want.sum(0)) <= e.sum(0) + 8 * 2.0 ** -24 * np.abs(want).sum(0))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_pairs_of_finite_p(B, out):
+    """Gate and up parts whose products with dY leave fp32's range before a factor of 0 meets
+    them, or where the gradient itself does not."""
+    print(f"case far pairs {out}", flush=True)
+    v = FAR + [1.0, 4.0]
+    g = np.array(v + [-x for x in v] + [0.0])
+    u = np.array([1.0, -1e19, 1e25, -1e38, 3.3e38, 0.0])
+    G, U = (torch.tensor(t.ravel()).bfloat16() for t in np.meshgrid(g, u))
+    d = torch.tensor([1.0, -100.0, 1e-3, 1e5, 0.25]).to(torch.bfloat16 if out == "bf16" else torch.float32)
+    P = torch.cat([G, U])[None, :].expand(len(d), -1).contiguous().to(DEV)
+    dY = d[:, None].expand(-1, len(G)).contiguous().to(DEV)
+    dX, rows, _ = _dp(B, "swiglu", dY, P)
+    x, (gg, uu) = np.abs(_n(dY)), np.split(_n(P), 2, axis=1)
+    want = ol.slope_times(_n(dY), _n(P), "swiglu")
+    e = np.concatenate([x * np.abs(uu) * _slope_error(gg, "silu"), 2.0 ** -16 * x * np.abs(gg) * ol._sigmoid(gg)], axis=1)
+    # the largest number of bf16 is 2^-8 of itself below fp32's
+    big = float(torch.finfo(torch.float32).max)
+    inside, beyond = np.abs(want) < big * (1 - 2.0 ** -7), np.abs(want) > big * (1 + 2.0 ** -7)
+    off = np.abs(_n(rows) - want)[inside]
+    assert np.all(off <= (e + 3 * 2.0 ** -24 * np.abs(want))[inside] + 1e-37)
+    assert beyond.any() and np.all(_n(rows)[beyond] == np.sign(want[beyond]) * np.inf)
+    # an infinity in dP meets the unit matrix' zeros: rows without one
+    whole = inside.all(1)
+    assert whole.sum() >= 2
+    off = np.abs(_n(dX) - want)[whole]
+    assert np.all(off <= (e + 2.0 ** -8 * (np.abs(want) + e) + 3 * 2.0 ** -24 * np.abs(want))[whole] + 1e-37)
