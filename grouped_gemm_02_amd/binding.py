@@ -891,8 +891,9 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
     else:
         there, sizes = [g for g in grads if g is not None], [k if y else 0 for k, y in zip(sizes, some)]
     at = [t.data_ptr() for t in buf.params]
-    # parameters where they were and as long are what was checked then
-    moved = at != buf._at or [t.numel() for t in buf.params] != buf._sizes
+    # parameters where they were, as long, of their type and dense are what was checked then
+    moved = (at != buf._at or [t.numel() for t in buf.params] != buf._sizes
+             or not all([t.dtype is buf.dtype and t.is_contiguous() for t in buf.params]))
     for what, have, dt in (("grads", there, gt), ("params", buf.params, buf.dtype))[:2 if moved else 1]:
         want = [k for k, y in zip(buf._sizes, some) if y] if have is there and there is not grads else buf._sizes
         if ([t.numel() for t in have] != want or not all([t.dtype is dt and t.is_contiguous() for t in have])
