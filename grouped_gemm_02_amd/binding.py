@@ -796,13 +796,17 @@ def linear_bwd(buf: LinearBuffers, dY, X, W, pre=None, bias=False, dX=None, dW=N
     return dX, dW, dbias
 
 
+_addresses = torch.Tensor.data_ptr  # with map: half of what the same in a comprehension costs
+
+
 class AdamWBuffers:
     """The tensors of an AdamW step with their moments: lists of the parameters
     (bf16 or fp32, one type for all), m and v (fp32 of the parameter's size, or
     uint8 codes with a scale byte per 128 elements), optionally fp32 masters of bf16
     parameters (an entry may be None) and multipliers of the learning rate and the
-    weight decay per tensor. It holds the tensors; the moments and masters are taken at
-    the places they have now, parameters and gradients are looked up at every step."""
+    weight decay per tensor. It holds the tensors and looks up at every step where they
+    are: one whose storage was exchanged (`t.data = loaded`) is checked anew and taken
+    where it is now."""
 
     def __init__(self, params, m, v, m_scale=None, v_scale=None, master=None, lr_mul=None, decay_mul=None):
         n = len(params)
@@ -820,11 +824,24 @@ class AdamWBuffers:
         self.dtype = self.params[0].dtype if n else _F32
         if self.dtype not in (_BF16, _F32):
             raise MoEError(MOE_ERR_SHAPE, f"parameters are {self.dtype}, expected bf16 or fp32")
-        mt = _F32 if self.state == "f32" else _U8
         self.device = self.params[0].device if n else None
-        for i, p in enumerate(self.params):
-            k = p.numel()
+        self._sizes = [p.numel() for p in self.params]
+        self._table = (moe_adamw_tensor * max(n, 1))()
+        for e, k, lr, decay in zip(self._table, self._sizes, self.lr_mul, self.decay_mul):
+            e.n, e.lr_mul, e.decay_mul = k, float(lr), float(decay)
+        # columns of the table: param 0, grad 1, n 7
+        self._words = np.frombuffer(self._table, dtype=np.int64).reshape(-1, ctypes.sizeof(moe_adamw_tensor) // 8)
+        # what the step reads and writes beside parameters and gradients
+        self._state = [t for ts in (self.m, self.v, self.m_scale, self.v_scale, self.master) for t in ts if t is not None]
+        self._look()
+
+    def _look(self) -> None:
+        """Checks all tensors and takes their addresses."""
+        mt = _F32 if self.state == "f32" else _U8
+        for i, (p, k) in enumerate(zip(self.params, self._sizes)):
             b = -(-k // STATE_BLOCK)
+            if p.numel() != k:
+                raise MoEError(MOE_ERR_SHAPE, f"param[{i}] holds {p.numel()} elements, had {k}")
             for t, name, dt, size in ((p, "param", self.dtype, k), (self.m[i], "m", mt, k), (self.v[i], "v", mt, k),
                                       (self.m_scale[i], "m_scale", _U8, b), (self.v_scale[i], "v_scale", _U8, b),
                                       (self.master[i], "master", _F32, k)):
@@ -832,17 +849,22 @@ class AdamWBuffers:
                     continue
                 _want(t, f"{name}[{i}]", dt, size)
                 if t.device != self.device:
-                    raise MoEError(MOE_ERR_SHAPE, f"{name}[{i}] is on {t.device}, param[0] on {self.device}")
+                    raise MoEError(MOE_ERR_SHAPE, f"{name}[{i}] is on {t.device}, param[0] was on {self.device}")
         self._refuse_overlap()
-        self._table = (moe_adamw_tensor * max(n, 1))()
-        self._sizes, self._at = [p.numel() for p in self.params], [p.data_ptr() for p in self.params]
-        for i in range(n):
-            e = self._table[i]
-            e.n, e.lr_mul, e.decay_mul = self._sizes[i], float(self.lr_mul[i]), float(self.decay_mul[i])
-            e.m, e.v, e.master = self.m[i].data_ptr(), self.v[i].data_ptr(), _ptr(self.master[i])
+        for i, e in enumerate(self._table[:len(self.params)]):
+            e.param, e.m, e.v, e.master = (_ptr(t[i]) for t in (self.params, self.m, self.v, self.master))
             e.m_scale, e.v_scale = _ptr(self.m_scale[i]), _ptr(self.v_scale[i])
-        # columns of the table: param 0, grad 1, n 7
-        self._words = np.frombuffer(self._table, dtype=np.int64).reshape(-1, ctypes.sizeof(moe_adamw_tensor) // 8)
+        self._at, self._state_at = list(map(_addresses, self.params)), list(map(_addresses, self._state))
+        # Other names of the moments' memory: while they live no other tensor's can be at these
+        # addresses, so a moment at its address has that memory.
+        self._held = [t.detach() for t in self._state]
+
+    def _moved(self) -> bool:
+        """Is a tensor no longer what was looked at?"""
+        return (list(map(_addresses, self.params)) != self._at or list(map(_addresses, self._state)) != self._state_at
+                or list(map(torch.Tensor.numel, self.params)) != self._sizes
+                or not all(map(torch.Tensor.is_contiguous, self.params))
+                or not all([t.dtype is self.dtype for t in self.params]))
 
     def _refuse_overlap(self) -> None:
         """No buffer that a step writes may share memory with another of its buffers."""
@@ -890,26 +912,19 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
         there = grads
     else:
         there, sizes = [g for g in grads if g is not None], [k if y else 0 for k, y in zip(sizes, some)]
-    at = [t.data_ptr() for t in buf.params]
-    # parameters where they were, as long, of their type and dense are what was checked then
-    moved = (at != buf._at or [t.numel() for t in buf.params] != buf._sizes
-             or not all([t.dtype is buf.dtype and t.is_contiguous() for t in buf.params]))
-    for what, have, dt in (("grads", there, gt), ("params", buf.params, buf.dtype))[:2 if moved else 1]:
-        want = [k for k, y in zip(buf._sizes, some) if y] if have is there and there is not grads else buf._sizes
-        if ([t.numel() for t in have] != want or not all([t.dtype is dt and t.is_contiguous() for t in have])
-                or any([t.get_device() != dev for t in have])):
-            for i, t in enumerate(have):
-                _want(t, f"{what}[{i}]", dt, want[i])
-                if t.numel() != want[i] or t.get_device() != dev:
-                    raise MoEError(MOE_ERR_SHAPE, f"{what}[{i}] holds {t.numel()} elements on {t.device}, needs "
-                                   f"{want[i]} on cuda:{dev}")
-    if moved:
-        buf._refuse_overlap()
+    want = sizes if there is grads else [k for k, y in zip(buf._sizes, some) if y]
+    if (list(map(torch.Tensor.numel, there)) != want or not all([t.dtype is gt for t in there])
+            or not all(map(torch.Tensor.is_contiguous, there)) or any([t.get_device() != dev for t in there])):
+        for i, t in enumerate(there):
+            _want(t, f"grads[{i}]", gt, want[i])
+            if t.numel() != want[i] or t.get_device() != dev:
+                raise MoEError(MOE_ERR_SHAPE, f"grads[{i}] holds {t.numel()} elements on {t.device}, needs "
+                               f"{want[i]} on cuda:{dev}")
+    if buf._moved():
+        buf._look()
     if n:
-        w = buf._words
-        w[:, 0] = buf._at = at
-        w[:, 1] = [0 if g is None else g.data_ptr() for g in grads]
-        w[:, 7] = sizes
+        buf._words[:, 1] = [0 if g is None else g.data_ptr() for g in grads]
+        buf._words[:, 7] = sizes
     p = moe_adamw_params(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
                          MOE_DT["bf16"] if buf.dtype is _BF16 else MOE_DT["f32"],
                          MOE_DT["bf16"] if gt is _BF16 else MOE_DT["f32"], MOE_STATES[buf.state], int(step), 0)

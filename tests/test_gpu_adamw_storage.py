@@ -1,9 +1,6 @@
 """The tensors of an AdamW step where their storage, type or strides change between steps."""
-import numpy as np
 import pytest
 import torch
-
-from oracle import moe_adamw as oa
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -42,3 +39,66 @@ def test_another_view_of_a_parameters_memory_is_refused(B):
         p.data = whole
         B.adamw_step(buf, [_rand(100), _rand(24, 40)], step=1, **H)
         assert not torch.equal(p, keep)
+
+
+@pytest.mark.parametrize("state", ["f32", "8bit"])
+def test_moments_and_masters_that_moved(B, state):
+    """What a loaded checkpoint exchanges is stepped where it is now, and what was there is left
+    alone; what no longer fits is refused."""
+    print(f"case moved moments {state}", flush=True)
+    n = 700
+    mk = lambda: B.AdamWBuffers.allocate([_rand(n).bfloat16(), _rand(60, seed=2).bfloat16()], state=state, master=True)  # noqa: E731
+    buf, ref = mk(), mk()
+    names = ["m", "v", "master"] + (["m_scale", "v_scale"] if state == "8bit" else [])
+    G = [_rand(n, seed=3), _rand(60, seed=4)]
+    for b in (buf, ref):
+        B.adamw_step(b, G, step=1, **H)
+    first = [(getattr(buf, name)[0].data, getattr(ref, name)[0].clone()) for name in names]
+    for name in names:
+        t = getattr(buf, name)[0]
+        t.data = t.data.clone()
+    for b in (buf, ref):
+        B.adamw_step(b, G, step=2, **H)
+    for old, was in first:
+        assert torch.equal(old, was)
+    for name in ["params"] + names:
+        for a, b in zip(getattr(buf, name), getattr(ref, name)):
+            assert torch.equal(a, b), name
+    assert not torch.equal(buf.m[0], first[0][0])
+    for name in names:
+        t = getattr(buf, name)[0]
+        good = t.data
+        other = torch.float16 if t.dtype == torch.float32 else torch.float32
+        for bad in (good[:-1].clone(), good.to(other), good.cpu(), torch.zeros(2 * len(good), dtype=good.dtype, device=DEV)[::2]):
+            t.data = bad
+            with pytest.raises(B.MoEError) as ei:
+                B.adamw_step(buf, G, step=3, **H)
+            assert ei.value.status == 2
+        t.data = good
+    v = buf.v[0].data
+    buf.v[0].data = buf.m[0].data   # one over the other
+    with pytest.raises(B.MoEError):
+        B.adamw_step(buf, G, step=3, **H)
+    buf.v[0].data = v
+    for b in (buf, ref):
+        B.adamw_step(b, G, step=3, **H)
+    for name in ["params"] + names:
+        for a, b in zip(getattr(buf, name), getattr(ref, name)):
+            assert torch.equal(a, b), name
+
+
+def test_moments_at_an_address_keep_their_memory(B):
+    """Memory that a moment left is not given away before the step has looked again: a shorter
+    tensor cannot stand at the same address unseen."""
+    n = 1 << 20
+    p = _rand(n)
+    buf = B.AdamWBuffers.allocate([p])
+    B.adamw_step(buf, [_rand(n)], step=1, **H)
+    at = buf.m[0].data_ptr()
+    buf.m[0].data = torch.empty(0, device=DEV)
+    short = torch.zeros(n - 1000, device=DEV)
+    assert short.data_ptr() != at
+    buf.m[0].data = short
+    with pytest.raises(B.MoEError):
+        B.adamw_step(buf, [_rand(n)], step=2, **H)
+    assert not short.any()
