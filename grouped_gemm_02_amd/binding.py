@@ -8,8 +8,10 @@ falls back to another implementation.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import dataclasses
+import itertools
 import os
 
 import numpy as np
@@ -850,6 +852,7 @@ class AdamWBuffers:
                 _want(t, f"{name}[{i}]", dt, size)
                 if t.device != self.device:
                     raise MoEError(MOE_ERR_SHAPE, f"{name}[{i}] is on {t.device}, param[0] was on {self.device}")
+        self._grads_at = None
         self._refuse_overlap()
         for i, e in enumerate(self._table[:len(self.params)]):
             e.param, e.m, e.v, e.master = (_ptr(t[i]) for t in (self.params, self.m, self.v, self.master))
@@ -876,6 +879,17 @@ class AdamWBuffers:
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise MoEError(MOE_ERR_SHAPE, f"buffers of {a[2]} and {b[2]} overlap")
+        # where they end and begin, in order, with room before the first and behind the last
+        self._ends, self._starts = [0] + [s[1] for s in spans], [s[0] for s in spans] + [1 << 64]
+
+    def _refuse_grads(self, at, sizes, dtype) -> None:
+        """Nor may a gradient lie where the step writes."""
+        width = dtype.itemsize
+        below = map(bisect.bisect_right, itertools.repeat(self._starts), at)   # how many begin no later
+        for i, (a, k, j) in enumerate(zip(at, sizes, below)):
+            if k and (self._ends[j] > a or self._starts[j] < a + k * width):
+                raise MoEError(MOE_ERR_SHAPE, f"grads[{i}] overlaps a buffer that the step writes")
+        self._grads_at = (at, dtype)
 
     @classmethod
     def allocate(cls, params, state="f32", master=False, lr_mul=None, decay_mul=None) -> "AdamWBuffers":
@@ -923,7 +937,11 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
     if buf._moved():
         buf._look()
     if n:
-        buf._words[:, 1] = [0 if g is None else g.data_ptr() for g in grads]
+        at = [0 if g is None else g.data_ptr() for g in grads]
+        # (gradients of these addresses, sizes and type were looked over)
+        if (at, gt) != buf._grads_at:
+            buf._refuse_grads(at, sizes, gt)
+        buf._words[:, 1] = at
         buf._words[:, 7] = sizes
     p = moe_adamw_params(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
                          MOE_DT["bf16"] if buf.dtype is _BF16 else MOE_DT["f32"],

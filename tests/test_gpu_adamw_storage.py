@@ -102,3 +102,55 @@ def test_moments_at_an_address_keep_their_memory(B):
     with pytest.raises(B.MoEError):
         B.adamw_step(buf, [_rand(n)], step=2, **H)
     assert not short.any()
+
+
+@pytest.mark.parametrize("state", ["f32", "8bit"])
+def test_gradients_over_what_a_step_writes_are_refused(B, state):
+    """A gradient that shares an element with a parameter, a moment, a scale or a master, from
+    either side; gradients that touch them only, or share among themselves, are served."""
+    print(f"case gradients over buffers {state}", flush=True)
+    n = 384
+    dt = torch.float32 if state == "f32" else torch.uint8
+    w = 4 if state == "f32" else 1
+    pool = torch.zeros(64 * n, dtype=torch.uint8, device=DEV)   # one allocation, cut by hand
+    at = 0
+
+    def take(count, dtype):
+        nonlocal at
+        size = count * (torch.finfo(dtype).bits // 8 if dtype.is_floating_point else 1)
+        t = pool[at:at + size].view(dtype)
+        at += size
+        return t
+    g0 = take(n, torch.float32)
+    p, m, g1, v, master = (take(n, d) for d in (torch.bfloat16, dt, torch.float32, dt, torch.float32))
+    ms, vs = (take(4, torch.uint8)[:3] for _ in range(2))
+    g2 = take(n, torch.float32)
+    buf = B.AdamWBuffers([p], [m], [v], None if state == "f32" else [ms], None if state == "f32" else [vs], [master])
+    whole = pool.clone()
+    begin = pool.data_ptr()
+    for name, t in (("p", p), ("m", m), ("v", v), ("master", master)) + ((("ms", ms), ("vs", vs)) if state == "8bit" else ()):
+        first, last = t.data_ptr() - begin, t.data_ptr() - begin + t.numel() * t.element_size()
+        for byte in (first, first // 4 * 4 - 4 * n + 4, (last - 1) // 4 * 4):
+            if byte < 0:
+                continue
+            bad = pool[byte:byte + 4 * n].view(torch.float32)
+            with pytest.raises(B.MoEError) as ei:
+                B.adamw_step(buf, [bad], step=1, **H)
+            assert ei.value.status == 2, (name, byte)
+    assert torch.equal(pool, whole)
+    for g in (g0, g1, g2, g0):   # right before, between and behind them
+        g.fill_(1.0)
+        B.adamw_step(buf, [g], step=1, **H)
+    # the same place in turn with moved moments: looked over again
+    g = _rand(n)
+    B.adamw_step(buf, [g], step=2, **H)
+    keep = g.clone()
+    if state == "f32":
+        buf.m[0].data = g
+        with pytest.raises(B.MoEError):
+            B.adamw_step(buf, [g], step=2, **H)
+        assert torch.equal(g, keep)
+    two = B.AdamWBuffers.allocate([_rand(n), _rand(n)])
+    B.adamw_step(two, [g, g], step=1, **H)   # read alone
+    B.adamw_step(two, [None, g], step=1, **H)
+    assert torch.equal(g, keep)
