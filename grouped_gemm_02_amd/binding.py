@@ -8,13 +8,13 @@ falls back to another implementation.
 """
 from __future__ import annotations
 
+import array
 import bisect
 import ctypes
 import dataclasses
 import itertools
 import os
 
-import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -831,8 +831,11 @@ class AdamWBuffers:
         self._table = (moe_adamw_tensor * max(n, 1))()
         for e, k, lr, decay in zip(self._table, self._sizes, self.lr_mul, self.decay_mul):
             e.n, e.lr_mul, e.decay_mul = k, float(lr), float(decay)
-        # columns of the table: param 0, grad 1, n 7
-        self._words = np.frombuffer(self._table, dtype=np.int64).reshape(-1, ctypes.sizeof(moe_adamw_tensor) // 8)
+        # the table's words of 8 bytes, and its columns of gradients and sizes
+        words = memoryview(self._table).cast("B").cast("q")
+        width = ctypes.sizeof(moe_adamw_tensor) // 8
+        self._grad_words, self._size_words = (words[getattr(moe_adamw_tensor, name).offset // 8::width][:n]
+                                              for name in ("grad", "n"))
         # what the step reads and writes beside parameters and gradients
         self._state = [t for ts in (self.m, self.v, self.m_scale, self.v_scale, self.master) for t in ts if t is not None]
         self._look()
@@ -941,8 +944,7 @@ def adamw_step(buf: AdamWBuffers, grads, *, lr, beta1=0.9, beta2=0.999, eps=1e-8
         # (gradients of these addresses, sizes and type were looked over)
         if (at, gt) != buf._grads_at:
             buf._refuse_grads(at, sizes, gt)
-        buf._words[:, 1] = at
-        buf._words[:, 7] = sizes
+        buf._grad_words[:], buf._size_words[:] = array.array("q", at), array.array("q", sizes)
     p = moe_adamw_params(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
                          MOE_DT["bf16"] if buf.dtype is _BF16 else MOE_DT["f32"],
                          MOE_DT["bf16"] if gt is _BF16 else MOE_DT["f32"], MOE_STATES[buf.state], int(step), 0)
