@@ -154,3 +154,23 @@ def test_gradients_over_what_a_step_writes_are_refused(B, state):
     B.adamw_step(two, [g, g], step=1, **H)   # read alone
     B.adamw_step(two, [None, g], step=1, **H)
     assert torch.equal(g, keep)
+
+
+def test_steps_without_torchs_own_comparisons(B, monkeypatch):
+    """Where this torch lacks them the tensors are looked at one by one, with the same results and
+    refusals."""
+    P, G = [_rand(300), _rand(5, 7, seed=1)], [_rand(300, seed=2), _rand(5, 7, seed=3)]
+    ref = B.AdamWBuffers.allocate([p.clone() for p in P])
+    B.adamw_step(ref, G, step=1, **H)
+    monkeypatch.setattr(B, "_are_at", lambda ts, at, _: [t.data_ptr() for t in ts] == at)
+    monkeypatch.setattr(B._Like, "__call__", lambda self, ts: False)
+    buf = B.AdamWBuffers.allocate(P)
+    B.adamw_step(buf, G, step=1, **H)
+    for a, b in zip(buf.params + buf.m + buf.v, ref.params + ref.m + ref.v):
+        assert torch.equal(a, b)
+    for bad in ([G[0], G[1].t()], [G[0], G[1].bfloat16()], [G[0][:-1], G[1]], [G[0], G[1].cpu()], [buf.m[0], G[1]]):
+        with pytest.raises(B.MoEError) as ei:
+            B.adamw_step(buf, bad, step=2, **H)
+        assert ei.value.status == 2
+    B.adamw_step(buf, [None, G[1]], step=2, **H)
+    assert torch.equal(buf.params[0], ref.params[0]) and not torch.equal(buf.params[1], ref.params[1])
