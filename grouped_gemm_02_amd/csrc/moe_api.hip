@@ -933,7 +933,11 @@ moe_status moe_adamw_step(const moe_adamw_params* p, const moe_adamw_tensor* ten
       (p->state != MOE_STATE_F32 && p->state != MOE_STATE_8BIT))
     return MOE_ERR_PRECISION;
   const double most = 3.4028234e38;  // of fp32, and false for NaN
-  if (!(std::fabs(p->lr) <= most) || !(p->eps >= 0.0 && p->eps <= most) || !(std::fabs(p->weight_decay) <= most) ||
+  // the kernel takes a reciprocal, which knows no numbers below the normal range: a smaller eps would
+  // make 0 / eps a NaN, a larger one every update 0
+  const float eps = float(p->eps);
+  const bool eps_ok = p->eps == 0.0 || (eps >= 0x1p-126f && eps <= 0x1p+100f);
+  if (!(std::fabs(p->lr) <= most) || !eps_ok || !(std::fabs(p->weight_decay) <= most) ||
       !(std::fabs(p->lr * p->weight_decay) <= most))
     return MOE_ERR_SHAPE;
   const double below = 1.0 - 0x1p-24;  // what rounds to 1 in fp32 is no average
@@ -964,7 +968,7 @@ moe_status moe_adamw_step(const moe_adamw_params* p, const moe_adamw_tensor* ten
   a.h.beta2 = float(p->beta2);
   a.h.alpha1 = float(1.0 - p->beta1);
   a.h.alpha2 = float(1.0 - p->beta2);
-  a.h.eps = float(p->eps);
+  a.h.eps = eps;
   a.h.weight_decay = float(p->weight_decay);
   a.h.bias1 = float(1.0 - std::pow(p->beta1, t));
   a.h.root2 = float(1.0 / std::sqrt(1.0 - std::pow(p->beta2, t)));

@@ -630,8 +630,8 @@ moe_status moe_linear_bwd(const moe_linear_shape* s, const void* dY, const void*
  *              grad_scale, which then take the place of the host's (for captured steps)
  *   grad_scale fp32 [1] in device memory or NULL (1): clipping or loss scaling; NULL
  *              with hyper. Where it is not finite, nothing changes.
- * MOE_ERR_SHAPE unless lr, eps, weight_decay and lr weight_decay are finite in fp32,
- * eps >= 0, 0 <= beta1, beta2 < 1 - 2^-24, step >= 1, reserved 0. */
+ * MOE_ERR_SHAPE unless lr, weight_decay and lr weight_decay are finite in fp32, eps is 0
+ * or from 2^-126 to 2^100, 0 <= beta1, beta2 < 1 - 2^-24, step >= 1, reserved 0. */
 typedef enum moe_state { MOE_STATE_F32 = 0, MOE_STATE_8BIT = 1 } moe_state;
 
 typedef struct moe_adamw_tensor {
