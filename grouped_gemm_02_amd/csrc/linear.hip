@@ -211,13 +211,14 @@ struct KMajor {
       off[i] = uint32_t(row * op.ld * 2) + 16u * chunk;
     }
   }
-  // slab kt (one past the end: zeros) into `lds`
-  __device__ __forceinline__ void load(int kt, bool, uint16_t* lds) const {
+  // slab kt into `lds`, zeros if there is none. (Past the end of a row a lane's own offset is
+  // past every extent; the slab's is added to a row that has it, or is 0.)
+  __device__ __forceinline__ void load(int kt, bool some, uint16_t* lds) const {
     const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int at = some ? kt * 2 * BK : 0;
     const uint32_t past = kt * BK + 8 * chunk < K ? 0u : kPast;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      load_lds(data, lds + (64 * w + THREADS * i) * 8, off[i] | past, kt * 2 * BK);
+    for (int i = 0; i < kPer; ++i) load_lds(data, lds + (64 * w + THREADS * i) * 8, off[i] | past, at);
   }
 };
 
