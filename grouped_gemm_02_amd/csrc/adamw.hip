@@ -30,24 +30,13 @@ typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
 
-struct Entry {
-  void* param;
-  const void* grad;
-  float* master;
-  void* m;
-  void* v;
-  uint8_t* m_scale;
-  uint8_t* v_scale;
-  int64_t n;
-  float lr_mul, decay_mul;
-};
 struct Batch {
   AdamwHyper h;
   const float* grad_scale;
   const float* hyper;
   int count;
   uint32_t first[kMaxTensors + 1];  // a tensor's first chunk
-  Entry e[kMaxTensors];
+  AdamwTensor e[kMaxTensors];
 };
 static_assert(sizeof(Batch) <= 4096, "kernel arguments");
 
@@ -221,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(const Batch b) {
     const int mid = (lo + hi) >> 1;
     if (b.first[mid] <= blockIdx.x) lo = mid; else hi = mid;
   }
-  const Entry& en = b.e[lo];
+  const AdamwTensor& en = b.e[lo];
   const int64_t n = en.n;
   float lr = b.h.lr, bias1 = b.h.bias1, root2 = b.h.root2, gs = 1.f;
   if (b.hyper) {
@@ -308,17 +297,16 @@ hipError_t launch_adamw(const AdamwArgs& a, const AdamwTensor* tensors, int64_t 
           const int64_t room = int64_t(kMaxChunks) - b.first[b.count];
           const int64_t n = std::min(t.n - at, room * kChunk);
           const int64_t psz = a.param_bf16 ? 2 : 4, gsz = a.grad_bf16 ? 2 : 4, ssz = a.eight ? 1 : 4;
-          Entry& e = b.e[b.count];
+          AdamwTensor& e = b.e[b.count];
+          e = t;
           e.param = static_cast<char*>(t.param) + at * psz;
           e.grad = static_cast<const char*>(t.grad) + at * gsz;
-          e.master = t.master ? t.master + at : nullptr;
+          if (t.master) e.master = t.master + at;
           e.m = static_cast<char*>(t.m) + at * ssz;
           e.v = static_cast<char*>(t.v) + at * ssz;
-          e.m_scale = t.m_scale ? t.m_scale + at / 128 : nullptr;
-          e.v_scale = t.v_scale ? t.v_scale + at / 128 : nullptr;
+          if (t.m_scale) e.m_scale = t.m_scale + at / 128;
+          if (t.v_scale) e.v_scale = t.v_scale + at / 128;
           e.n = n;
-          e.lr_mul = t.lr_mul;
-          e.decay_mul = t.decay_mul;
           b.first[b.count + 1] = b.first[b.count] + uint32_t((n + kChunk - 1) / kChunk);
           ++b.count;
           at += n;
