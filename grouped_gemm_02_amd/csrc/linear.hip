@@ -211,14 +211,13 @@ struct KMajor {
       off[i] = uint32_t(row * op.ld * 2) + 16u * chunk;
     }
   }
-  // slab kt into `lds`, zeros if there is none. (Past the end of a row a lane's own offset is
-  // past every extent; the slab's is added to a row that has it, or is 0.)
+  // slab kt into `lds`, zeros if there is none (kt is 0 then). Past the end of a row a lane's own
+  // offset is past every extent; the slab's is within every row.
   __device__ __forceinline__ void load(int kt, bool some, uint16_t* lds) const {
     const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const int at = some ? kt * 2 * BK : 0;
-    const uint32_t past = kt * BK + 8 * chunk < K ? 0u : kPast;
+    const uint32_t past = some && kt * BK + 8 * chunk < K ? 0u : kPast;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) load_lds(data, lds + (64 * w + THREADS * i) * 8, off[i] | past, at);
+    for (int i = 0; i < kPer; ++i) load_lds(data, lds + (64 * w + THREADS * i) * 8, off[i] | past, kt * 2 * BK);
   }
 };
 
@@ -620,7 +619,7 @@ __device__ __forceinline__ void walk(const Problem& p, uint32_t first, uint32_t 
   };
   auto send = [&](uint16_t* s) {
     const bool some = more && f0 + f < fend;
-    const int kt = some ? f0 + f : all;
+    const int kt = some ? f0 + f : 0;
     lp.load(kt, some, s);
     lq.load(kt, some, s + BM * BK);
     ++f;
