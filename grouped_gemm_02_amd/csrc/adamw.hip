@@ -7,7 +7,7 @@
 // replays them); a workgroup takes kChunk elements of one tensor, found by bisecting the
 // tensors' first chunks. A thread takes eight neighbouring elements and is done: with two
 // or four such pieces one after the other the 8-bit step of 604 M bf16 weights took 1.15
-// and 1.20 ms instead of 1.06 (6.05 GB at 5.7 TB/s), 12.6 M fp32 ones 84 and 97 us
+// and 1.20 ms instead of 1.06 (now 1.02: 6.05 GB at 5.9 TB/s), 12.6 M fp32 ones 84 and 97 us
 // instead of 78. Sixteen threads hold the 128 elements that share a scale where moments are
 // held in 8 bits; what is rare there (numbers that are not finite, roots that would round
 // to 0) is looked for in all eight at once, as the arithmetic of a piece comes near the

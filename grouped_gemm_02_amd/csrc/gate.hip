@@ -8,12 +8,17 @@
 //   k <= 16 (and groups that end where lanes do): several tokens a wave, fp32 scores as
 //   integer keys, and 64 bits only where keys are too close ("the quick way" below).
 //   16,384 tokens of 128 experts, k = 8, sigmoid and bias: 7.4 us, of which 2.7 are a
-//   launch; 131,072 of 256 in 8 groups: 60 to 70 us (134 MB; the memory's time is 29). It is
-//   bound by its vector instructions, about 700 for four tokens of 256 experts: two
-//   transcendentals an expert, the keys, the lanes' sorts (108), nine rounds of 17.
+//   launch; 131,072 of 256 in 8 groups: 54 to 65 us (134 MB; the memory's time is 29). Its
+//   vector instructions take 46 of them, 835 for four tokens of 256 experts: two
+//   transcendentals an expert, the keys, the lanes' sorts (108), nine rounds of 17; the rest
+//   is waiting that 2.3 waves a SIMD do not cover.
+//   Rows of equal keys (logits all alike) are all taken again: 48 and 819 us.
 //   Otherwise: one wave per token, lane l at the experts l + 64 i (E <= 1024: at most 16 a
 //   lane; instantiated for 2, 4 and 16), everything in 64 bits, experts taken one at a time
-//   by a wave-wide arg-max. The same sizes in this way: 41 and 601 us.
+//   by a wave-wide arg-max. The same sizes in this way: 41 and 601 us; 131,072 tokens of 160
+//   experts in 8 groups of 20, k = 6: 413.
+// Weights come from the chosen logits in fp32 in the quick way (1e-7 of a row's largest) and
+// in 64 bits in the other: both within 1e-5, and ids are the same in both.
 // The gradient for k <= 16 puts rows together in LDS and is bound by memory: 100,007
 // tokens of 60 experts through a whole softmax 11.9 us (51 MB at 4.3 TB/s; 39.9 with a wave
 // a token), 16,384 of 128 5.2 us (14.6).

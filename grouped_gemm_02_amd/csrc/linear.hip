@@ -787,7 +787,8 @@ __global__ __launch_bounds__(64 * WM * WN, NS == 2 ? 2 : 1) void both_kernel(con
 // has 16 rows of W (a pair's: 8 gate rows and their 8 up rows); its waves take turns at
 // units of 64 k (a 128-byte line of each row), the sums meet in LDS. X comes from the
 // caches. MT: fragments of 16 rows of X. One token, 1536 rows of 2048 (SwiGLU): 7.4 us,
-// most of it latency (a launch takes 2.7, the 6.3 MB of W 1.3 at the memory's rate).
+// where a launch takes 2.7 and the 6.3 MB of W 1.3 at the memory's rate: its 96 workgroups
+// leave 160 CUs without loads, and the rest is latency.
 constexpr int kFewWaves = 8;
 constexpr int kFewUnits = 4;  // of a wave in flight
 
@@ -932,7 +933,10 @@ struct DpArgs {
   int blocks;   // along the rows; as many for every 256 columns of dY
 };
 
-// dP = dY act'(P), and its column sums. A workgroup takes `rows` rows of 8 x 32 = 256
+// dP = dY act'(P), and its column sums. dP is held in bf16, also where dY is fp32: the
+// matrix instructions take 16 bits, and the bits beyond would be a second product of the same size.
+// It costs dX and dW 0.0023 of their norm against 0.0017 with dP in fp32 (their own rounding);
+// the column sums are of dP before it. A workgroup takes `rows` rows of 8 x 32 = 256
 // columns; thread t the columns 8 (t % 32) of rows t / 32, + 8, ...
 __device__ void slope_rows(const DpArgs& a, int block, float (&red)[8][256]) {
   const int tr = threadIdx.x >> 5, tc = threadIdx.x & 31;
@@ -1161,7 +1165,8 @@ int64_t dp_rows(int64_t M) { return std::max<int64_t>(kDpRows, ceil_div(M, kDpBl
 
 // Rows that few_rows_kernel takes: whole calls of 1, 32 and 48 rows take 7.6, 10.7 and 12.8 us in
 // it for N' = 1536, K = 2048 (SwiGLU) and 12.7, 13.8, 14.1 in tiles; for 4096 x 4096 9.3, 15.5, 20.2
-// and 15.5, 15.9, 16.3; for 1001 x 777 8.1, 12.1, 16.4 and 14.3, 14.8, 14.9.
+// and 15.5, 15.9, 16.3; for 1001 x 777 8.1, 12.1, 16.4 and 14.3, 14.8, 14.9. One border for all
+// sizes: at 48 rows the first would gain a tenth, the others lose a tenth and a quarter.
 constexpr int64_t kFewRows = 32;
 
 struct Layout {

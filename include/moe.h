@@ -309,7 +309,8 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
  * mask byte is 0; its logits are not looked at. A NaN or +inf among a token's
  * logits, or in the bias, gives the ids 0 .. k-1 and weights NaN. Finite logits of
  * any magnitude have the weights the formulas give (renormalised sigmoid scores
- * too, where every score underflows).
+ * too, where every score underflows; without renorm a score below 2^-126 may count as 0
+ * before it is scaled).
  *   logits   fp32  [T, E]   4-byte aligned
  *   bias     fp32  [E]      or NULL
  *   mask     uint8 [T]      or NULL: every token counts
